@@ -16,7 +16,7 @@ __all__ = [
     "MoeError", "Dims", "QMat", "BlobLayout", "LayerWeights", "Moe", "load_library", "header_symbols",
     "MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED", "MOE_ERR_CUDA", "MOE_ERR_BAD_EXPERT_ID",
     "MOE_ERR_TIMEOUT", "MOE_ERR_NONFINITE", "MOE_ERR_WORKSPACE", "build_library", "static_get_error",
-    "layer_forward_static", "ExpertCache",
+    "layer_forward_static", "ExpertCache", "QdenseWeights", "LogitRules", "make_qdense_weights", "make_logit_rules",
 ]
 
 MOE_OK = 0
@@ -57,6 +57,19 @@ class LayerWeights(ctypes.Structure):
 
 class HeadWeights(ctypes.Structure):
     _fields_ = [("vocab", ctypes.c_int), ("hidden", ctypes.c_int), ("w", QMat)]
+
+
+class QdenseWeights(ctypes.Structure):
+    _fields_ = [("channels", ctypes.c_int), ("width", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
+
+
+class LogitRules(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("history_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p),
+                ("history_stride", ctypes.c_int), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("bias_len", ctypes.c_void_p), ("bias_stride", ctypes.c_int), ("mask", ctypes.c_void_p),
+                ("mask_stride", ctypes.c_int)]
 
 
 class MoeError(RuntimeError):
@@ -105,6 +118,10 @@ def load_library(path: str = LIB_PATH):
         "moe_cache_slot_expert": (I, [V, I, I]),
         "moe_cache_slots": (I, [V]),
         "moe_layer_forward_offload": (I, [V, V, I, V, P(LayerWeights), V, V, Z, V]),
+        "moe_norm_quant": (I, [V, V, V, I, I, V, ctypes.c_float, V, V, V, V, V]),
+        "moe_qdense_workspace_bytes": (Z, [P(QdenseWeights), I]),
+        "moe_qdense_forward": (I, [V, V, V, I, P(QdenseWeights), ctypes.c_float, V, V, V, Z, V]),
+        "moe_logits_process": (I, [V, V, Z, I, I, P(LogitRules), V, Z, V, V]),
         "moe_prompt_workspace_bytes": (Z, [P(Dims), I]),
         "moe_layer_forward_prompt": (I, [V, V, I, P(LayerWeights), V, V, V, V, V, Z, V]),
     }
@@ -170,6 +187,81 @@ def make_layer_weights(dims: Dims, router_q: int, router_s: int, router_b: int, 
 def make_head_weights(vocab: int, hidden: int, q: int, scales: int, biases: int) -> HeadWeights:
     """HeadWeights from device addresses (or CUDA tensors) of the tied head."""
     return HeadWeights(vocab, hidden, QMat(_ptr(q), _ptr(scales), _ptr(biases)))
+
+
+def _data(t, what: str, kind: str, numel: int):
+    """Device address of a tensor that a call of the batched path takes (None
+    stays None), after a check of its type, size and layout.  kind: "b16"
+    (bf16, or its bits as 16-bit integers), "f32", "i32" or "i8"."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous CUDA tensor is wanted")
+    if t.dtype not in (_DTYPES or _fill_dtypes())[kind]:
+        raise ValueError(f"{what}: {t.dtype} given, {_DTYPES[kind][0]} wanted")
+    if t.numel() < numel:
+        raise ValueError(f"{what}: {t.numel()} elements given, {numel} wanted")
+    return t.data_ptr()
+
+
+_DTYPES = {}
+
+
+def _fill_dtypes():
+    import torch
+    _DTYPES.update(b16=(torch.bfloat16, torch.int16, torch.uint16), f32=(torch.float32,),
+                   i32=(torch.int32, torch.uint32), i8=(torch.int8,), u8=(torch.uint8,))
+    return _DTYPES
+
+
+def _rows(t, what: str, n_rows: int, width: int):
+    """Device address and row stride of an fp32 matrix of at least n_rows rows
+    and `width` columns."""
+    if not t.is_cuda or t.dtype not in (_DTYPES or _fill_dtypes())["f32"] or t.dim() != 2 or t.shape[0] < n_rows or t.shape[1] < width \
+            or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a float32 CUDA matrix of at least {n_rows} x {width} with adjacent columns is wanted")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(width, t.stride(0))
+
+
+def make_qdense_weights(channels: int, width: int, q, scales) -> QdenseWeights:
+    """QdenseWeights from CUDA tensors: q int8 [channels, width], scales fp32
+    [channels].  The result keeps the tensors alive."""
+    w = QdenseWeights(channels, width, _data(q, "q", "i8", channels * width), _data(scales, "scales", "f32", channels))
+    w.keep = (q, scales)
+    return w
+
+
+def make_logit_rules(history=None, history_len=None, prompt_len=None, repetition=None, presence=None, frequency=None,
+                     bias_ids=None, bias_values=None, bias_len=None, mask=None) -> LogitRules:
+    """LogitRules from CUDA tensors, any of which may be left out with what
+    belongs to it: history int32 [T, L] with history_len (and prompt_len)
+    int32 [T] and the penalties fp32 [T]; bias_ids int32 and bias_values fp32
+    [T, B] with bias_len int32 [T]; mask int32 words [T, W], or [W] for one
+    mask of every row.  The result keeps the tensors alive."""
+    rows = []
+    for name, t in (("history", history), ("bias_ids", bias_ids)):
+        if t is not None:
+            if t.dim() != 2:
+                raise ValueError(f"{name}: a matrix is wanted")
+            rows.append(t.shape[0])
+    if mask is not None:
+        if mask.dim() not in (1, 2):
+            raise ValueError("mask: a vector or a matrix is wanted")
+        if mask.dim() == 2:
+            rows.append(mask.shape[0])
+    T = min(rows) if rows else None
+    n = T or 0
+    L = history.shape[1] if history is not None else 0
+    B = bias_ids.shape[1] if bias_ids is not None else 0
+    r = LogitRules(_data(history, "history", "i32", n * L), _data(history_len, "history_len", "i32", n),
+                   _data(prompt_len, "prompt_len", "i32", n), L, _data(repetition, "repetition", "f32", n),
+                   _data(presence, "presence", "f32", n), _data(frequency, "frequency", "f32", n),
+                   _data(bias_ids, "bias_ids", "i32", n * B), _data(bias_values, "bias_values", "f32", n * B),
+                   _data(bias_len, "bias_len", "i32", n), B, _data(mask, "mask", "i32", 0),
+                   mask.shape[1] if mask is not None and mask.dim() == 2 else 0)
+    r.rows, r.words = T, mask.shape[-1] if mask is not None else None
+    r.keep = (history, history_len, prompt_len, repetition, presence, frequency, bias_ids, bias_values, bias_len, mask)
+    return r
 
 
 def layer_forward_static(x, w: LayerWeights, y, ids_out=None, logits_out=None, weights_out=None, stream=None):
@@ -343,6 +435,51 @@ class Moe:
         bf16 [T, N] and/or fp32 [T, N] outputs."""
         self._check(self.lib.moe_dense_forward(self.h, _ptr(x), n_tokens, ctypes.byref(w), _ptr(y), _ptr(y32),
                                                _stream(stream)), "moe_dense_forward")
+
+    def norm_quant(self, hidden, n_rows, q, scales, y=None, norm=None, eps: float = 1e-6, hidden_out=None, x_out=None,
+                   stream=None):
+        """Residual addition, root-mean-square norm and 8-bit rows of n_rows
+        rows (moe_norm_quant): q int8 [T, H] and scales fp32 [T] of the
+        normalised hidden (+ y) bf16 [T, H], whose sum goes to hidden_out and
+        whose bf16 rows go to x_out where these are given.  H is q's last
+        dimension."""
+        H = q.shape[-1]
+        n = n_rows * H
+        self._check(self.lib.moe_norm_quant(self.h, _data(hidden, "hidden", "b16", n), _data(y, "y", "b16", n), n_rows,
+                                            H, _data(norm, "norm", "b16", H), eps,
+                                            _data(hidden_out, "hidden_out", "b16", n), _data(q, "q", "i8", n),
+                                            _data(scales, "scales", "f32", n_rows), _data(x_out, "x_out", "b16", n),
+                                            _stream(stream)), "moe_norm_quant")
+
+    def qdense_workspace_bytes(self, w: QdenseWeights, n_rows: int) -> int:
+        return int(self.lib.moe_qdense_workspace_bytes(ctypes.byref(w), n_rows))
+
+    def qdense_forward(self, x, x_scales, n_rows, w: QdenseWeights, ws=None, y=None, y32=None, softcap: float = 0.0,
+                       stream=None):
+        """A dense 8-bit projection of n_rows 8-bit rows (moe_qdense_forward):
+        x int8 [T, K] with x_scales fp32 [T]; outputs y bf16 and/or y32 fp32
+        [T, N], through a softcap if one is given; ws of
+        qdense_workspace_bytes(w, n_rows) bytes."""
+        n = n_rows * w.channels
+        self._check(self.lib.moe_qdense_forward(self.h, _data(x, "x", "i8", n_rows * w.width),
+                                                _data(x_scales, "x_scales", "f32", n_rows), n_rows, ctypes.byref(w),
+                                                softcap, _data(y, "y", "b16", n), _data(y32, "y32", "f32", n),
+                                                _data(ws, "ws", "u8", 0), 0 if ws is None else ws.numel(),
+                                                _stream(stream)), "moe_qdense_forward")
+
+    def logits_process(self, logits, n_rows, vocab, rules: LogitRules, out=None, tokens=None, stream=None):
+        """Penalties, biases, a mask (rules: make_logit_rules) and the greedy
+        token of n_rows rows of logits (moe_logits_process): fp32 matrices
+        whose rows may lie apart (out may be logits itself), tokens int32."""
+        if rules.rows is not None and rules.rows < n_rows:
+            raise ValueError(f"rules for {rules.rows} rows given, {n_rows} wanted")
+        if rules.words is not None and rules.words < (vocab + 31) // 32:
+            raise ValueError(f"mask: {rules.words} words given, {(vocab + 31) // 32} wanted")
+        at, ld = _rows(logits, "logits", n_rows, vocab)
+        to, ld_out = _rows(out, "out", n_rows, vocab) if out is not None else (None, 0)
+        self._check(self.lib.moe_logits_process(self.h, at, ld, n_rows, vocab, ctypes.byref(rules), to, ld_out,
+                                                _data(tokens, "tokens", "i32", n_rows), _stream(stream)),
+                    "moe_logits_process")
 
     def embed(self, ids, n, hw: HeadWeights, out, stream=None):
         """Tied embedding rows (bf16 [n, H]) of int32 token ids on the device."""

@@ -23,6 +23,7 @@ struct moe_handle {
   bool prefill;               // multi-token layer calls use the fused prefill kernel
   int prefill_key[4], prefill_ok;  // cached check (hidden, inter, n_experts, top_k) -> usable
   bool head_ready;            // the head kernel's attributes are set (first head call)
+  bool qdense_ready;          // the same for the 8-bit projection's kernels
   bool prefill_dense;         // multi-token calls may run dense slots on the tensor cores (tcgen05)
   // failure-detection hook, consumed by the next fused single-token launch
   int skip_block_next;                  // -1: none
@@ -64,7 +65,10 @@ constexpr size_t kDeviceWords = kSyncOffset + 64 + 1024;
 // 64-bit words (each launch tags its logits with its epoch; zero at start)
 constexpr size_t kMboxOffset = 1536;
 static_assert(kDeviceWords <= kMboxOffset, "mailboxes overlap the device words");
-size_t device_words(int n_sm) { return kMboxOffset + (size_t)n_sm * moe::kMaxExperts * 2; }
+// after the mailboxes: the processed logits' greedy state, a 64-bit maximum
+// per row, then a finished-block ticket per row (zero between launches)
+size_t logits_state_offset(int n_sm) { return kMboxOffset + (size_t)n_sm * moe::kMaxExperts * 2; }
+size_t device_words(int n_sm) { return logits_state_offset(n_sm) + 3 * (size_t)moe::kLogitsMaxRows; }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
@@ -246,6 +250,20 @@ int check_head(const moe_head_weights *w) {
   const void *p[3] = {w->w.q, w->w.scales, w->w.biases};
   for (const void *q : p)
     if (!q || !aligned(q, 16)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// The batched path's calls launch on the current device, which has to be the handle's.
+bool on_device(const moe_handle *h) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+int check_qdense(const moe_qdense_weights *w) {
+  if (!w) return MOE_ERR_INVALID_ARG;
+  if (w->width < 16 || w->width % 16 || w->width > moe::kQdenseMaxK) return MOE_ERR_UNSUPPORTED;
+  if (w->channels < 1 || w->channels > (1 << 28)) return MOE_ERR_UNSUPPORTED;
+  if (!w->q || !aligned(w->q, 16) || !w->scales || !aligned(w->scales, 4)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
@@ -813,6 +831,133 @@ int moe_dense_forward(moe_handle *h, const void *x, int n_tokens, const moe_head
   a.err = h->dwords;
   a.trace = take_trace(h, 1);
   return cuda_status(moe::launch_head(a, (int)((warps + 7) / 8), (cudaStream_t)stream, h->pdl));
+}
+
+int moe_norm_quant(moe_handle *h, const void *hidden, const void *y, int n_rows, int width, const void *norm,
+                   float eps, void *hidden_out, int8_t *q, float *scales, void *x_out, moe_stream_t stream) {
+  if (!h || !hidden || !q || !scales) return MOE_ERR_INVALID_ARG;
+  if (width < 16 || width % 16 || width > moe::kNormMaxWidth) return MOE_ERR_UNSUPPORTED;
+  if (n_rows < 1 || n_rows > MOE_NORM_MAX_ROWS) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || eps > 1.0f) return MOE_ERR_INVALID_ARG;
+  if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  const void *p16[6] = {hidden, y, norm, hidden_out, q, x_out};
+  for (const void *p : p16)
+    if (p && !aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+  if (hidden_out && !y) return MOE_ERR_INVALID_ARG;
+  moe::NormQuantArgs a;
+  a.h = (const uint16_t *)hidden;
+  a.y = (const uint16_t *)y;
+  a.g = (const uint16_t *)norm;
+  a.h_out = (uint16_t *)hidden_out;
+  a.q = q;
+  a.scales = scales;
+  a.x_out = (uint16_t *)x_out;
+  a.T = n_rows;
+  a.H = width;
+  a.eps = eps;
+  a.err = h->dwords;
+  a.trace = take_trace(h, 1);
+  return cuda_status(moe::launch_norm_quant(a, (cudaStream_t)stream, h->pdl));
+}
+
+size_t moe_qdense_workspace_bytes(const moe_qdense_weights *w, int n_rows) {
+  if (check_qdense(w) != MOE_OK || n_rows < 1 || n_rows > moe::kQdenseMaxRows) return 0;
+  return moe::qdense_ws_bytes(n_rows, w->width);
+}
+
+int moe_qdense_forward(moe_handle *h, const int8_t *x, const float *x_scales, int n_rows, const moe_qdense_weights *w,
+                       float softcap, void *y, float *y32, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  if (!h || !x || !x_scales || (!y && !y32)) return MOE_ERR_INVALID_ARG;
+  int st = check_qdense(w);
+  if (st) return st;
+  if (n_rows < 1 || n_rows > moe::kQdenseMaxRows) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(x_scales, 4) || (y && !aligned(y, 2)) || (y32 && !aligned(y32, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (!(softcap == softcap)) return MOE_ERR_INVALID_ARG;
+  if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::qdense_ws_bytes(n_rows, w->width);
+  if (need) {
+    if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  }
+  if (!h->qdense_ready) {
+    if (moe::qdense_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    h->qdense_ready = true;
+  }
+  moe::QdenseArgs a;
+  a.x = x;
+  a.xs = x_scales;
+  a.w = w->q;
+  a.ws = w->scales;
+  a.y = (uint16_t *)y;
+  a.y32 = y32;
+  a.work = (uint8_t *)ws;
+  a.softcap = softcap;
+  a.T = n_rows;
+  a.N = w->channels;
+  a.K = w->width;
+  a.err = h->dwords;
+  a.trace = take_trace(h, 1);
+  return cuda_status(moe::launch_qdense(a, h->n_sm, (cudaStream_t)stream, h->pdl));
+}
+
+int moe_logits_process(moe_handle *h, const float *logits, size_t logits_stride, int n_rows, int vocab,
+                       const moe_logit_rules *r, float *out, size_t out_stride, int32_t *tokens, moe_stream_t stream) {
+  if (!h || !logits || !r || (!out && !tokens)) return MOE_ERR_INVALID_ARG;
+  if (n_rows < 1 || n_rows > moe::kLogitsMaxRows) return MOE_ERR_INVALID_ARG;
+  if (vocab < 1 || vocab > (1 << 28)) return MOE_ERR_UNSUPPORTED;
+  if (logits_stride < (size_t)vocab || (out && out_stride < (size_t)vocab)) return MOE_ERR_INVALID_ARG;
+  if (logits_stride > ((size_t)1 << 32) || (out && out_stride > ((size_t)1 << 32))) return MOE_ERR_UNSUPPORTED;
+  if (out == logits && out_stride != logits_stride) return MOE_ERR_INVALID_ARG;
+  const void *p4[11] = {logits,        out,         tokens,       r->history,  r->history_len,   r->prompt_len,
+                        r->repetition, r->presence, r->frequency, r->bias_len, r->mask};
+  for (const void *p : p4)
+    if (p && !aligned(p, 4)) return MOE_ERR_INVALID_ARG;
+  if ((r->bias_ids && !aligned(r->bias_ids, 4)) || (r->bias_values && !aligned(r->bias_values, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (r->history) {
+    if (!r->history_len || r->history_stride < 1) return MOE_ERR_INVALID_ARG;
+    if (r->history_stride > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  } else if (r->history_len || r->prompt_len || r->repetition || r->presence || r->frequency) {
+    return MOE_ERR_INVALID_ARG;  // penalties without a history to take them from
+  }
+  if (r->bias_ids) {
+    if (!r->bias_values || !r->bias_len || r->bias_stride < 1) return MOE_ERR_INVALID_ARG;
+    if (r->bias_stride > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  } else if (r->bias_values || r->bias_len) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (r->mask && r->mask_stride != 0 && r->mask_stride < (vocab + 31) / 32) return MOE_ERR_INVALID_ARG;
+  if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  moe::LogitsArgs a;
+  a.logits = logits;
+  a.ld = logits_stride;
+  a.out = out;
+  a.ld_out = out_stride;
+  a.tokens = tokens;
+  a.history = r->history;
+  a.history_len = r->history_len;
+  a.prompt_len = r->prompt_len;
+  a.history_stride = r->history_stride;
+  a.repetition = r->repetition;
+  a.presence = r->presence;
+  a.frequency = r->frequency;
+  a.bias_ids = r->bias_ids;
+  a.bias_values = r->bias_values;
+  a.bias_len = r->bias_len;
+  a.bias_stride = r->bias_stride;
+  a.mask = r->mask;
+  a.mask_stride = r->mask_stride;
+  unsigned *state = h->dwords + logits_state_offset(h->n_sm);
+  a.best = reinterpret_cast<unsigned long long *>(state);
+  a.tickets = state + 2 * moe::kLogitsMaxRows;
+  a.T = n_rows;
+  a.V = vocab;
+  a.slice = 0;
+  a.err = h->dwords;
+  a.trace = take_trace(h, 1);
+  return cuda_status(moe::launch_logits(a, (cudaStream_t)stream, h->pdl));
 }
 
 int moe_embed(moe_handle *h, const int32_t *ids, int n, const moe_head_weights *w, void *out, moe_stream_t stream) {

@@ -191,6 +191,71 @@ cudaError_t prompt_set_attributes();
 // the combine writes y (nullable) and, if add_residual, hres <- bf16(hres + y)
 cudaError_t launch_prompt(const PromptArgs &a, uint16_t *y, bool add_residual, int n_sm, cudaStream_t st, bool pdl);
 
+// Residual, norm and 8-bit rows (norm_quant.cu); one block per row.
+constexpr int kNormMaxWidth = 16384;
+struct NormQuantArgs {
+  const uint16_t *h;          // bf16 [T, H]
+  const uint16_t *y;          // nullable bf16 [T, H], added to h
+  const uint16_t *g;          // nullable bf16 [H]: norm weight
+  uint16_t *h_out;            // nullable bf16 [T, H]: bf16(h + y); may be h
+  int8_t *q;                  // [T, H] codes
+  float *scales;              // [T]
+  uint16_t *x_out;            // nullable bf16 [T, H]: the normalised rows
+  int T, H;
+  float eps;
+  unsigned *err;
+  unsigned long long *trace;
+};
+cudaError_t launch_norm_quant(const NormQuantArgs &a, cudaStream_t st, bool pdl);
+
+// Penalties, biases, masks and the greedy token on logits (logits.cu).
+constexpr int kLogitsMaxRows = 4096;
+struct LogitsArgs {
+  const float *logits;        // fp32 [T, ld]
+  size_t ld;
+  float *out;                 // nullable fp32 [T, ld_out]; may be logits
+  size_t ld_out;
+  int32_t *tokens;            // nullable [T]
+  const int32_t *history;     // nullable [T, history_stride]
+  const int32_t *history_len; // [T]
+  const int32_t *prompt_len;  // nullable [T]
+  int history_stride;
+  const float *repetition, *presence, *frequency;  // nullable [T]
+  const int32_t *bias_ids;    // nullable [T, bias_stride]
+  const float *bias_values;   // [T, bias_stride]
+  const int32_t *bias_len;    // [T]
+  int bias_stride;
+  const uint32_t *mask;       // nullable [T, mask_stride] words
+  int mask_stride;
+  unsigned long long *best;   // [kLogitsMaxRows] packed (logit, id) maxima: zero between launches
+  unsigned *tickets;          // [kLogitsMaxRows] finished blocks per row: zero between launches
+  int T, V;
+  int slice;                  // tokens per block (set by the launcher)
+  unsigned *err;
+  unsigned long long *trace;
+};
+cudaError_t launch_logits(const LogitsArgs &a, cudaStream_t st, bool pdl);
+
+// Dense 8-bit projection (qdense.cu).
+constexpr int kQdenseMaxK = 16384;
+constexpr int kQdenseMaxRows = 65536;
+struct QdenseArgs {
+  const int8_t *x;            // [T, K] codes
+  const float *xs;            // [T]
+  const int8_t *w;            // [N, K] codes
+  const float *ws;            // [N]
+  uint16_t *y;                // nullable bf16 [T, N]
+  float *y32;                 // nullable fp32 [T, N]
+  uint8_t *work;              // qdense_ws_bytes(T, K) bytes
+  float softcap;              // <= 0: none
+  int T, N, K;
+  unsigned *err;
+  unsigned long long *trace;
+};
+size_t qdense_ws_bytes(int T, int K);
+cudaError_t qdense_set_attributes();
+cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl);
+
 // smem budgets (bytes) for a given shape; 0 = shape not supported by that kernel
 size_t router_smem(const Dims &d, int tb);
 size_t gateup_smem(const Dims &d, int tt);

@@ -400,6 +400,109 @@ int moe_dense_forward(moe_handle *h, const void *x, int n_tokens, const moe_head
 int moe_embed(moe_handle *h, const int32_t *ids, int n, const moe_head_weights *w, void *out,
               moe_stream_t stream);
 
+/* ---- From the residual stream to the next token, for a batch of rows.
+ * Three calls that a decode loop over many sequences makes around the layers:
+ * the residual addition and norm with 8-bit rows, the 8-bit projection that
+ * takes them (an attention-like projection, or a head with its softcap for
+ * more rows than moe_head_forward takes), and the processing of the logits.
+ * Each is one or two launches, allocates nothing, and can be captured in a
+ * CUDA graph.  The handle's device has to be the current one. */
+
+/* Residual addition, root-mean-square norm and 8-bit rows.  Per row:
+ *   s = bf16(hidden + y)                   (s = hidden without y)
+ *   u = s * norm                           (u = s without norm)
+ *   r = 1 / sqrt(mean(s^2) + eps),  m = max |u|
+ *   q = rint(127 u / m)  (ties to even; zero for m = 0),  scale = m r / 127
+ * so q * scale stands for the normalised row u r.  The codes are those of
+ * exact arithmetic on the stored bf16 values.
+ *   hidden      bf16 [n_rows, width];  y nullable bf16 [n_rows, width]
+ *   norm        nullable bf16 [width]
+ *   eps         0 .. 1 (the layers use 1e-6)
+ *   hidden_out  nullable bf16 [n_rows, width]: s; may be hidden itself;
+ *               only with y
+ *   q           int8 [n_rows, width], -127 .. 127;  scales fp32 [n_rows]
+ *   x_out       nullable bf16 [n_rows, width]: bf16(u r)
+ * width: a multiple of 16, 16 .. 16384; n_rows 1 .. MOE_NORM_MAX_ROWS;
+ * matrices and norm 16-byte aligned.  Other outputs must not overlap an
+ * input.  A row with a NaN or an infinity in s or u, or whose sum of squares
+ * passes the range of fp32, gets codes 0, scale NaN and x_out NaN (s is
+ * written all the same) and records MOE_ERR_NONFINITE. */
+#define MOE_NORM_MAX_ROWS (1 << 20)
+int moe_norm_quant(moe_handle *h, const void *hidden, const void *y, int n_rows, int width, const void *norm,
+                   float eps, void *hidden_out, int8_t *q, float *scales, void *x_out, moe_stream_t stream);
+
+/* An 8-bit matrix with a scale per output channel: W[n, k] = q[n, k] * scales[n]. */
+typedef struct {
+  int channels;         /* N: 1 .. 2^28                                        */
+  int width;            /* K: a multiple of 16, 16 .. 16384                    */
+  const int8_t *q;      /* [N, K] row-major, 16-byte aligned                   */
+  const float *scales;  /* [N]                                                 */
+} moe_qdense_weights;
+
+/* Workspace of moe_qdense_forward for n_rows rows (0: none needed, and for
+ * arguments that the call refuses). */
+size_t moe_qdense_workspace_bytes(const moe_qdense_weights *w, int n_rows);
+
+/* Dense projection of 8-bit rows:
+ *   y[t, n] = cap(x_scales[t] * scales[n] * sum_k x[t, k] q[n, k])
+ *   cap(z) = softcap * tanh(z / softcap), or z for softcap <= 0
+ *   x         int8 [n_rows, K], 16-byte aligned;  x_scales fp32 [n_rows]
+ *   n_rows    1 .. MOE_QDENSE_MAX_ROWS
+ *   y         nullable bf16 [n_rows, N];  y32 nullable fp32 [n_rows, N];
+ *             not both null
+ *   ws        moe_qdense_workspace_bytes(w, n_rows) bytes, 256-byte aligned
+ *             (null where that is 0)
+ * Up to 8 rows the sums are exact 32-bit integers. */
+#define MOE_QDENSE_MAX_ROWS 65536
+int moe_qdense_forward(moe_handle *h, const int8_t *x, const float *x_scales, int n_rows, const moe_qdense_weights *w,
+                       float softcap, void *y, float *y32, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The rules of moe_logits_process (all device pointers; a part whose first
+ * pointer is null is left out). */
+typedef struct {
+  /* Tokens of each row so far, prompt first: history [n_rows, history_stride],
+   * of which the first history_len[t] count (clamped to 0 .. history_stride;
+   * history_stride 1 .. 2^24), the first prompt_len[t] of those (null: 0) the
+   * prompt.  The penalties are per row, null: none. */
+  const int32_t *history;
+  const int32_t *history_len;
+  const int32_t *prompt_len;
+  int history_stride;
+  const float *repetition;  /* of tokens anywhere in the history: l > 0 ? l / p : l * p  */
+  const float *presence;    /* subtracted once from tokens after the prompt              */
+  const float *frequency;   /* subtracted per occurrence after the prompt                */
+  /* Added to single logits: [n_rows, bias_stride], the first bias_len[t] of a
+   * row (clamped to 0 .. bias_stride; bias_stride 1 .. 2^24).  Of several
+   * entries for one token the last counts. */
+  const int32_t *bias_ids;
+  const float *bias_values;
+  const int32_t *bias_len;
+  int bias_stride;
+  /* Allowed tokens: bit v % 32 of word v / 32, [n_rows, mask_stride] words;
+   * mask_stride 0: one mask for every row. */
+  const uint32_t *mask;
+  int mask_stride;
+} moe_logit_rules;
+
+/* Penalties, biases and a mask on logits, and the greedy token of the result.
+ * In this order, each rounded to fp32: repetition; frequency times the count;
+ * presence; bias; -inf where the mask does not allow the token.
+ *   logits   fp32 [n_rows, logits_stride], the first vocab (1 .. 2^28) of a
+ *            row; n_rows 1 .. MOE_LOGITS_MAX_ROWS; logits_stride >= vocab
+ *   out      nullable fp32 [n_rows, out_stride]; may be logits itself (with
+ *            the same stride); columns from vocab on are left as they are
+ *   tokens   nullable int32 [n_rows]: argmax, ties to the lower id; -1 where
+ *            no logit is above -inf;  out and tokens not both null
+ * A NaN or +inf that the mask does not remove is passed on, skipped by the
+ * argmax and records MOE_ERR_NONFINITE; ids outside the vocabulary are
+ * skipped and record MOE_ERR_BAD_EXPERT_ID.  One launch.  The greedy state
+ * lives in the handle (cleared by the launch that used it), so calls on one
+ * handle must not overlap on the GPU. */
+#define MOE_LOGITS_MAX_ROWS 4096
+int moe_logits_process(moe_handle *h, const float *logits, size_t logits_stride, int n_rows, int vocab,
+                       const moe_logit_rules *rules, float *out, size_t out_stride, int32_t *tokens,
+                       moe_stream_t stream);
+
 /* Launch tracing (diagnostics).  With a non-null device buffer of
  * 4 * n_launches u64, each subsequent kernel launch by this handle takes the
  * next 4 slots (wrapping) and records %globaltimer values, combined with

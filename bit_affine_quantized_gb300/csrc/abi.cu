@@ -898,7 +898,7 @@ int moe_qdense_forward(moe_handle *h, const int8_t *x, const float *x_scales, in
   a.N = w->channels;
   a.K = w->width;
   a.err = h->dwords;
-  a.trace = take_trace(h, 1);
+  a.trace = take_trace(h, need ? 2 : 1);
   return cuda_status(moe::launch_qdense(a, h->n_sm, (cudaStream_t)stream, h->pdl));
 }
 

@@ -46,6 +46,7 @@
 #include "dense.cuh"
 #include "fused.cuh"
 #include "kernels.h"
+#include "tma_maps.h"
 
 namespace moe {
 namespace {
@@ -956,31 +957,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) prompt_gemm_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ host side
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return (EncodeTiledFn) nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
-
-// A tensor map over a row-major tensor (dims[0] innermost, byte strides of
-// dims 1..); elements outside the tensor read as zero.
-bool encode_map(EncodeTiledFn f, CUtensorMap *m, CUtensorMapDataType dt, int rank, const void *ptr,
-                const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle sw) {
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return f(m, dt, (cuuint32_t)rank, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           sw, sw == CU_TENSOR_MAP_SWIZZLE_NONE ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Operand rows of x and h per sorted position (fp16, boxes of 64 elements x
 // kNmax rows with the 128-byte swizzle), the codes of gate, up and down
 // (boxes of 32 bytes x 128 rows of one expert) for the routed experts (3-D

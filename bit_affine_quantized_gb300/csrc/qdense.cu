@@ -8,15 +8,40 @@
 // run per warp and channel) and multiplies them with the rows' codes in
 // shared memory by dp4a, so the sums are exact 32-bit integers (at most
 // 128 * 128 * 16384 = 2^28 in magnitude).
+//
+// qdense_mma_kernel: more rows, on the 5th-generation tensor cores.  sm_103a
+// has no 8-bit integer form of tcgen05.mma; 8-bit codes are exact in fp16, so
+// the products run as fp16 with fp32 sums (exact while the partial sums stay
+// below 2^24).  The rows are widened to fp16 once per call by
+// qdense_widen_kernel; the matrix, the larger operand, is read as 8-bit codes
+// and widened on its way into the tensor cores:
+//   weights warp   TMA: 128 channels x 128 codes per stage
+//   rows warp      TMA: up to 256 rows x 64 fp16 per stage
+//   8 widen warps  a channel per thread: 64 codes from shared memory to fp16
+//                  pairs in registers to the A operand in tensor memory (two
+//                  groups of 4 warps take alternate 64-wide steps)
+//   MMA warp       tcgen05.mma, M = 128 channels (A in tensor memory),
+//                  N = rows (B in shared memory), fp32 sums in tensor memory
+//   4 finish warps the sums times both scales, the softcap, the store
+// A in tensor memory keeps the widened codes out of shared memory, whose
+// bandwidth is what a 128 x 256 fp16 tile asks most of.
+// Few tiles: the blocks of a cluster share a tile, each takes a part of K, and
+// the parts are added through distributed shared memory in rank order.
+#include <cuda.h>
 #include <math.h>
+#include <string.h>
 
+#include "dense.cuh"
+#include "fused.cuh"
 #include "kernels.h"
+#include "tma_maps.h"
 
 namespace moe {
 
 namespace {
 constexpr int kQdWarps = 8;
 constexpr int kQdThreads = kQdWarps * 32;
+constexpr int kQdRowsMax = 8;  // rows that the dp4a kernel takes
 
 __device__ __forceinline__ int4 qd_stream(const int8_t *p) {
   int4 v;
@@ -115,26 +140,462 @@ cudaError_t set_rows_attr() {
   return cudaFuncSetAttribute(qdense_rows_kernel<kT, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kT * kQdenseMaxK);
 }
+// ------------------------------------------------------------------ rows to fp16
+constexpr int kWidenThreads = 256;
+
+// Four 8-bit codes as two exact fp16 pairs: the code + 128 goes under the
+// exponent of 1024 (1024 + c is exact for c < 1024), then 1152 is subtracted.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+}
+
+__global__ void __launch_bounds__(kWidenThreads) qdense_widen_kernel(const QdenseArgs a) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) trace_min(a.trace, kTrEntry);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) trace_min(a.trace, kTrWaited);
+  const size_t n = (size_t)a.T * (a.K / 16);
+  const uint4 *src = reinterpret_cast<const uint4 *>(a.x);
+  uint4 *dst = reinterpret_cast<uint4 *>(a.work);
+  for (size_t i = (size_t)blockIdx.x * kWidenThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kWidenThreads) {
+    const uint4 v = __ldcs(src + i);
+    uint4 o0, o1;
+    widen4(v.x, o0.x, o0.y);
+    widen4(v.y, o0.z, o0.w);
+    widen4(v.z, o1.x, o1.y);
+    widen4(v.w, o1.z, o1.w);
+    dst[2 * i] = o0;
+    dst[2 * i + 1] = o1;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) trace_max(a.trace, kTrExit);
+}
+
+// ------------------------------------------------------------------ tensor cores
+constexpr int kMmM = 128;                  // channels per tile
+constexpr int kMmWiden = 8;                // widen warps
+constexpr int kMmFin0 = kMmWiden;          // 4 finish warps
+constexpr int kMmWts = kMmFin0 + 4;        // weights warp
+constexpr int kMmRows = kMmWts + 1;        // rows warp
+constexpr int kMmMma = kMmRows + 1;        // MMA warp
+constexpr int kMmThreads = (kMmMma + 1) * 32;
+constexpr int kMmABufs = 8;                // A tiles (32 tensor-memory columns of 128 x 64 fp16 each)
+constexpr uint32_t kMmACol = 256;          // first column of the A tiles; the sums lie below
+constexpr int kMmWStage = kMmM * 128;      // bytes of a weight stage
+constexpr int kMmMaxN = 256;
+constexpr int kMmMaxSplit = 8;
+constexpr int kMmBarBytes = 512;
+
+struct MmPlan {
+  int n;            // rows per tile (the MMA N): a multiple of 16
+  int wst, rst;     // stages of weights and of rows
+  int dbufs;        // sets of sums in tensor memory
+  int split;        // blocks of a cluster that share a tile along K
+  int ntile, ttile; // tiles of channels, of rows
+  int smem;
+};
+
+struct MmParams {
+  CUtensorMap w;    // 8-bit codes {K, N}, box {128, 128}, 128-byte swizzle
+  CUtensorMap x;    // fp16 rows {K, T}, box {64, n}, 128-byte swizzle
+  QdenseArgs a;
+  MmPlan p;
+};
+
+__device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity) {
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    if (global_ns() - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// D (tensor memory) += A (tensor memory, 128 x 16) * B (shared memory, n x 16)^T
+__device__ __forceinline__ void mm_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+          d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// 32 registers of each lane to 32 tensor-memory columns of the warp's lanes.
+__device__ __forceinline__ void mm_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void mm_store(const QdenseArgs &a, int t, int n, float acc, float xs, float ws) {
+  float v = __fmul_rn(__fmul_rn(acc, xs), ws);
+  if (a.softcap > 0.f) v = a.softcap * tanhf(v / a.softcap);
+  const size_t o = (size_t)t * a.N + n;
+  if (a.y32) a.y32[o] = v;
+  if (a.y) a.y[o] = float_to_bf16_bits(v);
+}
+
+__global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_constant__ MmParams prm) {
+  extern __shared__ __align__(1024) uint8_t msm[];
+  const QdenseArgs &a = prm.a;
+  const MmPlan &P = prm.p;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t *base = msm + ((1024u - (smem_addr(msm) & 1023u)) & 1023u);
+  const int rstage = P.n * 128;
+  uint8_t *wbuf = base, *rbuf = base + P.wst * kMmWStage;
+  uint64_t *bar = reinterpret_cast<uint64_t *>(rbuf + P.rst * rstage);
+  uint64_t *wfull = bar, *wempty = wfull + P.wst, *rfull = wempty + P.wst, *rempty = rfull + P.rst;
+  uint64_t *afull = rempty + P.rst, *aempty = afull + kMmABufs, *dfull = aempty + kMmABufs, *dempty = dfull + 2;
+  uint64_t *tready = dempty + 2;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(tready + 1);
+  const bool tracer = blockIdx.x == 0 && tid == 0;
+
+  if (tid == 0) {
+    for (int i = 0; i < P.wst; ++i) {
+      mbar_init(&wfull[i], 1);
+      mbar_init(&wempty[i], kMmWiden);
+    }
+    for (int i = 0; i < P.rst; ++i) {
+      mbar_init(&rfull[i], 1);
+      mbar_init(&rempty[i], 1);
+    }
+    for (int i = 0; i < kMmABufs; ++i) {
+      mbar_init(&afull[i], kMmWiden / 2);
+      mbar_init(&aempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&dfull[i], 1);
+      mbar_init(&dempty[i], 4);
+    }
+    mbar_init(tready, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (tracer) trace_min(a.trace, kTrEntry);
+  pdl_launch_dependents();
+
+  const int split = P.split;
+  const int part = split > 1 ? (int)cluster_rank() : 0;
+  const int first = blockIdx.x / split, stride = gridDim.x / split;  // units of this block
+  const int units = P.ntile * P.ttile;
+  // K in stages of 128; this block's part of them, and its 64-wide steps
+  const int nst = (a.K + 127) / 128, st0 = nst * part / split, st1 = nst * (part + 1) / split;
+  const int steps = min(2 * (st1 - st0), (a.K + 63) / 64 - 2 * st0);
+  const uint32_t idesc = dense::idesc_f16(kMmM, P.n);
+
+  if (warp == kMmWts) {
+    // ============================================================ weights
+    // nothing that an earlier launch still writes is read here: the launch
+    // before this one (the widening of the rows) waited for those
+    bool ok = true;
+    int st = 0, ph = 0, issued = 0;
+    for (int u = first; u < units && ok; u += stride) {
+      const int n0 = u / P.ttile * kMmM;
+      for (int s = st0; s < st1 && ok; ++s, ++issued) {
+        if (issued >= P.wst) ok = __all_sync(0xffffffffu, mm_wait(&wempty[st], ph ^ 1));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&wfull[st], kMmWStage);
+          dense::tma_load_2d(wbuf + st * kMmWStage, &prm.w, 128 * s, n0, &wfull[st]);
+        }
+        __syncwarp();
+        if (++st == P.wst) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+    // copies in flight land before the block's shared memory is released
+    for (int j = max(0, issued - P.wst); j < issued; ++j) mm_wait(&wfull[j % P.wst], (j / P.wst) & 1);
+  } else if (warp == kMmRows) {
+    // ============================================================ rows
+    pdl_wait();  // the widened rows
+    if (tracer) trace_min(a.trace, kTrWaited);
+    fused::fence_proxy_async_global();
+    bool ok = true;
+    int st = 0, ph = 0, issued = 0;
+    for (int u = first; u < units && ok; u += stride) {
+      const int t0 = u % P.ttile * P.n;
+      for (int g = 0; g < steps && ok; ++g, ++issued) {
+        if (issued >= P.rst) ok = __all_sync(0xffffffffu, mm_wait(&rempty[st], ph ^ 1));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&rfull[st], (uint32_t)rstage);
+          dense::tma_load_2d(rbuf + st * rstage, &prm.x, 128 * st0 + 64 * g, t0, &rfull[st]);
+        }
+        __syncwarp();
+        if (++st == P.rst) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+    for (int j = max(0, issued - P.rst); j < issued; ++j) mm_wait(&rfull[j % P.rst], (j / P.rst) & 1);
+  } else if (warp == kMmMma) {
+    // ============================================================ MMA
+    dense::tc_alloc(s_tmem, 512);
+    dense::tc_fence_before();
+    __syncwarp();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
+    if (lane == 0) mbar_arrive_expect_tx(tready, 0);
+    const uint64_t bdesc0 = dense::sdesc(smem_addr(rbuf), 16, 1024, 2);
+    bool ok = true;
+    int gi = 0, du = 0, st = 0, ph = 0, ab = 0, aph = 0;
+    for (int u = first; u < units && ok; u += stride) {
+      const int db = du % P.dbufs;
+      if (du >= P.dbufs) ok = __all_sync(0xffffffffu, mm_wait(&dempty[db], ((du / P.dbufs) - 1) & 1));
+      ++du;
+      dense::tc_fence_after();
+      const uint32_t acc = tmem + db * 128;
+      for (int g = 0; g < steps && ok; ++g, ++gi) {
+        ok = __all_sync(0xffffffffu, mm_wait(&rfull[st], ph) && mm_wait(&afull[ab], aph));
+        if (!ok) break;
+        dense::tc_fence_after();
+        if (lane == 0) {
+          const uint64_t bd = bdesc0 + (uint64_t)((st * rstage) >> 4);
+          const uint32_t ad = tmem + kMmACol + 32 * ab;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)  // K = 16 per MMA: 8 columns of A, 32 bytes of B's rows
+            mm_mma(acc, ad + 8 * ks, bd + 2 * ks, idesc, (g > 0 || ks > 0) ? 1u : 0u);
+          dense::tc_commit(&rempty[st]);
+          dense::tc_commit(&aempty[ab]);
+          if (g == steps - 1) dense::tc_commit(&dfull[db]);
+        }
+        __syncwarp();
+        if (++st == P.rst) {
+          st = 0;
+          ph ^= 1;
+        }
+        if (++ab == kMmABufs) {
+          ab = 0;
+          aph ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+    // the last MMAs are complete and the sums read before the memory goes back (bounded waits)
+    if (gi > 0) mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1);
+    if (du > 0) mm_wait(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
+    dense::tc_fence_after();
+    __syncwarp();
+    dense::tc_dealloc(tmem, 512);
+  } else if (warp >= kMmFin0) {
+    // ============================================================ finish
+    // Warp w reads tensor-memory lanes 32 (w % 4) .. +31: channels n0 + rr.
+    // A register per lane and column: 32 neighbouring channels of one row are
+    // one store instruction.
+    bool ok = mm_wait(tready, 0);
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
+    const int rr = 32 * (warp & 3) + lane;
+    float *partial = reinterpret_cast<float *>(base);  // [n][128], over the stages
+    int du = 0;
+    for (int u = first; u < units && ok; u += stride, ++du) {
+      const int n = u / P.ttile * kMmM + rr, t0 = u % P.ttile * P.n, cnt = min(P.n, a.T - t0);
+      const int db = du % P.dbufs;
+      const float ws = split == 1 && n < a.N ? __ldg(a.ws + n) : 0.f;
+      ok = __all_sync(0xffffffffu, mm_wait(&dfull[db], (du / P.dbufs) & 1));
+      if (!ok) break;
+      dense::tc_fence_after();
+      const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + db * 128;
+      for (int c0 = 0; c0 < cnt; c0 += 16) {
+        float v[16];
+        dense::tc_ld16(ta + c0, v);
+        const float xl = split == 1 && lane < 16 && c0 + lane < cnt ? __ldcg(a.xs + t0 + c0 + lane) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float xs = __shfl_sync(0xffffffffu, xl, j);
+          if (split > 1)
+            partial[(c0 + j) * kMmM + rr] = v[j];
+          else if (c0 + j < cnt && n < a.N)
+            mm_store(a, t0 + c0 + j, n, v[j], xs, ws);
+        }
+      }
+      dense::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&dempty[db], 0);
+    }
+    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+  } else {
+    // ============================================================ widen
+    // Thread: channel rr of the tile; 64 of a stage's 128 codes.  Its 16-byte
+    // chunk j lies at j ^ (rr % 8) of the row (128-byte swizzle).
+    const int grp = warp >> 2, rr = 32 * (warp & 3) + lane, sw = rr & 7;
+    bool ok = mm_wait(tready, 0);
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem) + ((uint32_t)(32 * (warp & 3)) << 16) + kMmACol;
+    int st = 0, ph = 0, gu = 0;  // weight stage; steps before this unit
+    for (int u = first; u < units && ok; u += stride) {
+      for (int g = grp; g < 2 * (st1 - st0) && ok; g += 2) {
+        ok = mm_wait(&wfull[st], ph);
+        const uint8_t *row = wbuf + st * kMmWStage + rr * 128;
+        uint4 c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4 *>(row + (((4 * grp + j) ^ sw) << 4));
+        uint32_t o[32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          widen4(c[j].x, o[8 * j], o[8 * j + 1]);
+          widen4(c[j].y, o[8 * j + 2], o[8 * j + 3]);
+          widen4(c[j].z, o[8 * j + 4], o[8 * j + 5]);
+          widen4(c[j].w, o[8 * j + 6], o[8 * j + 7]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&wempty[st], 0);
+        if (++st == P.wst) {
+          st = 0;
+          ph ^= 1;
+        }
+        if (g < steps) {  // the last stage may hold one step only
+          const int gi = gu + g, ab = gi % kMmABufs;
+          if (gi >= kMmABufs) ok = ok && mm_wait(&aempty[ab], ((gi / kMmABufs) - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            dense::tc_fence_after();
+            mm_st32(tmem + 32 * ab, o);
+            dense::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&afull[ab], 0);
+          }
+        }
+      }
+      gu += steps;
+    }
+    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+  }
+
+  if (split > 1) {
+    // One tile per cluster: every block's sums lie in its shared memory; block
+    // r adds and stores every split-th row of the tile.
+    __syncwarp();
+    cluster_sync_all();
+    const int n0 = first / P.ttile * kMmM, t0 = first % P.ttile * P.n, cnt = min(P.n, a.T - t0);
+    const int rr = tid & (kMmM - 1), n = n0 + rr;
+    if (tid < 3 * kMmM && n < a.N) {
+      const float ws = __ldg(a.ws + n);
+      for (int c = part + split * (tid / kMmM); c < cnt; c += 3 * split) {
+        const uint32_t at = smem_addr(base) + (uint32_t)(c * kMmM + rr) * 4u;
+        float v[kMmMaxSplit];
+#pragma unroll
+        for (int r = 0; r < kMmMaxSplit; ++r) v[r] = r < split ? cluster_ld(at, r) : 0.f;
+        float sum = v[0];
+#pragma unroll
+        for (int r = 1; r < kMmMaxSplit; ++r) sum += v[r];
+        mm_store(a, t0 + c, n, sum, __ldcg(a.xs + t0 + c), ws);
+      }
+    }
+    cluster_sync_all();  // no block leaves while another reads its sums
+  }
+  if (tracer) trace_max(a.trace, kTrExit);
+}
+
+MmPlan mm_plan(int T, int N, int K, int n_sm) {
+  MmPlan p;
+  p.ttile = (T + kMmMaxN - 1) / kMmMaxN;
+  p.n = ((T + p.ttile - 1) / p.ttile + 15) / 16 * 16;
+  p.ntile = (N + kMmM - 1) / kMmM;
+  p.dbufs = p.n <= 128 ? 2 : 1;
+  p.wst = p.n <= 64 ? 10 : p.n <= 128 ? 7 : 5;
+  p.rst = p.n <= 128 ? 6 : 4;
+  const int units = p.ntile * p.ttile, nst = (K + 127) / 128;
+  p.split = 1;
+  if (units * 2 <= n_sm) {
+    p.split = n_sm / units;
+    if (p.split > kMmMaxSplit) p.split = kMmMaxSplit;
+    if (p.split > nst) p.split = nst;
+  }
+  p.smem = p.wst * kMmWStage + p.rst * p.n * 128 + kMmBarBytes + 1024;
+  return p;
+}
+
+cudaError_t launch_mma(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
+  const EncodeTiledFn f = encode_tiled();
+  if (!f) return cudaErrorNotSupported;
+  MmParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.a = a;
+  const MmPlan &p = prm.p = mm_plan(a.T, a.N, a.K, n_sm);
+  const cuuint64_t dw[2] = {(cuuint64_t)a.K, (cuuint64_t)a.N}, sw[1] = {(cuuint64_t)a.K};
+  const cuuint64_t dx[2] = {(cuuint64_t)a.K, (cuuint64_t)a.T}, sx[1] = {(cuuint64_t)a.K * 2};
+  const cuuint32_t bw[2] = {128, kMmM}, bx[2] = {64, (cuuint32_t)p.n};
+  if (!encode_map(f, &prm.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.w, dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(f, &prm.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const size_t pieces = (size_t)a.T * (a.K / 16), blocks = (pieces + kWidenThreads - 1) / kWidenThreads;
+  const size_t most = (size_t)n_sm * 8;
+  cudaError_t e = launch_k(qdense_widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kWidenThreads), 0,
+                           st, pdl, a);
+  if (e != cudaSuccess) return e;
+  if (prm.a.trace) prm.a.trace += 4;
+  const int units = p.ntile * p.ttile;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.split > 1 ? units * p.split : (units < n_sm ? units : n_sm));
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (p.split > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = p.split;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, qdense_mma_kernel, prm);
+}
 }  // namespace
 
 cudaError_t qdense_set_attributes() {
   cudaError_t e;
   if ((e = set_rows_attr<1>()) || (e = set_rows_attr<2>()) || (e = set_rows_attr<4>()) || (e = set_rows_attr<8>()))
     return e;
-  return cudaSuccess;
+  return cudaFuncSetAttribute(qdense_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
 }
 
-size_t qdense_ws_bytes(int T, int K) {
-  (void)T;
-  (void)K;
-  return 0;
-}
+// The widened rows of the tensor-core path.
+size_t qdense_ws_bytes(int T, int K) { return T <= kQdRowsMax ? 0 : ((size_t)T * K * 2 + 255) / 256 * 256; }
 
 cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
   if (a.T <= 1) return launch_rows_t<1>(a, n_sm, st, pdl);
   if (a.T <= 2) return launch_rows_t<2>(a, n_sm, st, pdl);
   if (a.T <= 4) return launch_rows_t<4>(a, n_sm, st, pdl);
-  return launch_rows_t<8>(a, n_sm, st, pdl);
+  if (a.T <= kQdRowsMax) return launch_rows_t<8>(a, n_sm, st, pdl);
+  return launch_mma(a, n_sm, st, pdl);
 }
 
 }  // namespace moe

@@ -157,13 +157,27 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return (_raw_stream or _find_raw_stream())()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _find_raw_stream():
+    """Sets _raw_stream, the handle of the current device's current stream:
+    torch's own getter where there is one (a Stream object costs several times
+    as much as a small call), else through torch.cuda."""
+    global _raw_stream
+    import torch
+    torch.cuda.current_stream()  # torch's device state is set up
+    get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    _raw_stream = (lambda: get(dev())) if get and dev else lambda: torch.cuda.current_stream().cuda_stream
+    return _raw_stream
 
 
 def make_dims(hidden: int, inter: int, n_experts: int, top_k: int, group: int = 64) -> Dims:

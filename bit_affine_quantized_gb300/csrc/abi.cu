@@ -24,6 +24,7 @@ struct moe_handle {
   int prefill_key[4], prefill_ok;  // cached check (hidden, inter, n_experts, top_k) -> usable
   bool head_ready;            // the head kernel's attributes are set (first head call)
   bool qdense_ready;          // the same for the 8-bit projection's kernels
+  bool logits_ready;          // and for the logits kernel
   bool prefill_dense;         // multi-token calls may run dense slots on the tensor cores (tcgen05)
   // failure-detection hook, consumed by the next fused single-token launch
   int skip_block_next;                  // -1: none
@@ -858,7 +859,7 @@ int moe_norm_quant(moe_handle *h, const void *hidden, const void *y, int n_rows,
   a.eps = eps;
   a.err = h->dwords;
   a.trace = take_trace(h, 1);
-  return cuda_status(moe::launch_norm_quant(a, (cudaStream_t)stream, h->pdl));
+  return cuda_status(moe::launch_norm_quant(a, h->n_sm, (cudaStream_t)stream, h->pdl));
 }
 
 size_t moe_qdense_workspace_bytes(const moe_qdense_weights *w, int n_rows) {
@@ -930,6 +931,10 @@ int moe_logits_process(moe_handle *h, const float *logits, size_t logits_stride,
   }
   if (r->mask && r->mask_stride != 0 && r->mask_stride < (vocab + 31) / 32) return MOE_ERR_INVALID_ARG;
   if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  if (!h->logits_ready) {
+    if (moe::logits_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    h->logits_ready = true;
+  }
   moe::LogitsArgs a;
   a.logits = logits;
   a.ld = logits_stride;
@@ -954,10 +959,9 @@ int moe_logits_process(moe_handle *h, const float *logits, size_t logits_stride,
   a.tickets = state + 2 * moe::kLogitsMaxRows;
   a.T = n_rows;
   a.V = vocab;
-  a.slice = 0;
   a.err = h->dwords;
   a.trace = take_trace(h, 1);
-  return cuda_status(moe::launch_logits(a, (cudaStream_t)stream, h->pdl));
+  return cuda_status(moe::launch_logits(a, h->n_sm, (cudaStream_t)stream, h->pdl));
 }
 
 int moe_embed(moe_handle *h, const int32_t *ids, int n, const moe_head_weights *w, void *out, moe_stream_t stream) {

@@ -206,7 +206,7 @@ struct NormQuantArgs {
   unsigned *err;
   unsigned long long *trace;
 };
-cudaError_t launch_norm_quant(const NormQuantArgs &a, cudaStream_t st, bool pdl);
+cudaError_t launch_norm_quant(const NormQuantArgs &a, int n_sm, cudaStream_t st, bool pdl);
 
 // Penalties, biases, masks and the greedy token on logits (logits.cu).
 constexpr int kLogitsMaxRows = 4096;
@@ -230,11 +230,12 @@ struct LogitsArgs {
   unsigned long long *best;   // [kLogitsMaxRows] packed (logit, id) maxima: zero between launches
   unsigned *tickets;          // [kLogitsMaxRows] finished blocks per row: zero between launches
   int T, V;
-  int slice;                  // tokens per block (set by the launcher)
+  int seg;                    // slices per segment (set by the launcher)
   unsigned *err;
   unsigned long long *trace;
 };
-cudaError_t launch_logits(const LogitsArgs &a, cudaStream_t st, bool pdl);
+cudaError_t logits_set_attributes();
+cudaError_t launch_logits(const LogitsArgs &a, int n_sm, cudaStream_t st, bool pdl);
 
 // Dense 8-bit projection (qdense.cu).
 constexpr int kQdenseMaxK = 16384;

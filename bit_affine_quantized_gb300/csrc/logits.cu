@@ -9,15 +9,22 @@
 //   v not allowed by the mask:  l <- -inf
 //   token = argmax l, ties to the lower id, -1 if nothing is left
 //
-// A block takes one slice of a row's vocabulary.  It scans the row's whole
-// history and counts the tokens of its slice in shared memory (integer
-// atomics: the result does not depend on their order), which needs no table
-// in global memory and no clearing of one; the history comes from L2 after
-// its first reader.  A table word holds the count after the prompt in its low
-// 31 bits and "occurs in the prompt" in bit 31.  A second table holds, per
-// token of the slice, the number of its last bias entry.
+// The rows' vocabularies go in segments; a block takes a run of consecutive
+// segments.  Per segment it counts the history's tokens in a table in shared
+// memory (integer atomics: the result does not depend on their order), so no
+// table in global memory has to be kept or cleared; the start of a row's
+// history stays in registers over the block's segments.  A table word holds
+// the count after the prompt in its low 31 bits and "occurs in the prompt" in
+// bit 31.  A second table holds, per token of the segment, the number of its
+// last bias entry.  A segment is up to four slices of four tokens per thread:
+// every token of the history is looked at once per segment, which at
+// 4096-token segments and as many history tokens was a third of the time.
+// The logits are copied slices ahead into a ring in shared memory (cp.async)
+// in which every thread has places of its own, so that tables are built while
+// logits are on their way and only a segment's ends need barriers.
 // The blocks of a row merge their best (logit, id) with one 64-bit atomicMax
-// each; the last of them writes the token and clears the row's state.
+// each; the one that adds the row's last segments writes the token and clears
+// the row's state.
 #include <math.h>
 
 #include "kernels.h"
@@ -25,7 +32,12 @@
 namespace moe {
 
 namespace {
-constexpr int kLgThreads = 256;
+constexpr int kLgThreads = 1024;
+constexpr int kLgSlice = 4 * kLgThreads;
+constexpr int kLgRing = 4;       // slices of logits in shared memory
+constexpr int kMaskSlice = kLgSlice / 32;  // mask words of a slice
+constexpr int kLgSegMax = 4;     // slices per segment, at most
+constexpr int kHistRegs = 4;     // history entries per thread that stay in registers
 constexpr unsigned kInPrompt = 0x80000000u;
 
 // Orders finite floats as unsigned integers (larger float, larger key; both
@@ -42,115 +54,368 @@ struct RowRules {
 };
 
 // One logit through the rules; c, b: its words of the two tables.
-__device__ __forceinline__ float lg_apply(float l, unsigned c, unsigned b, bool allowed, const RowRules &r) {
+__device__ __forceinline__ float lg_apply(float l, unsigned c, unsigned b, const RowRules &r) {
   if (c != 0u) {
     l = l > 0.f ? __fdiv_rn(l, r.rep) : __fmul_rn(l, r.rep);
     const unsigned n = c & ~kInPrompt;
     if (n != 0u) l = __fsub_rn(__fsub_rn(l, __fmul_rn(r.freq, (float)n)), r.pres);
   }
   if (b != 0u) l = __fadd_rn(l, __ldg(r.bias + b - 1));
-  return allowed ? l : -INFINITY;
+  return l;
 }
 
-template <bool kHist, bool kBias>
-__global__ void __launch_bounds__(kLgThreads) logits_kernel(const LogitsArgs a) {
+// The rules on the few of four neighbouring logits that one of them names:
+// most groups have none, and a loop over those that are keeps the division
+// and the branches off the others.
+__device__ __forceinline__ void lg_touched(float (&x)[4], uint4 c, uint4 b, const RowRules &r) {
+  unsigned todo = ((c.x | b.x) ? 1u : 0u) | ((c.y | b.y) ? 2u : 0u) | ((c.z | b.z) ? 4u : 0u) | ((c.w | b.w) ? 8u : 0u);
+  while (todo) {
+    const int k = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const float l = k == 0 ? x[0] : k == 1 ? x[1] : k == 2 ? x[2] : x[3];
+    const unsigned ck = k == 0 ? c.x : k == 1 ? c.y : k == 2 ? c.z : c.w;
+    const unsigned bk = k == 0 ? b.x : k == 1 ? b.y : k == 2 ? b.z : b.w;
+    const float v = lg_apply(l, ck, bk, r);
+    x[0] = k == 0 ? v : x[0];
+    x[1] = k == 1 ? v : x[1];
+    x[2] = k == 2 ? v : x[2];
+    x[3] = k == 3 ? v : x[3];
+  }
+}
+
+__device__ __forceinline__ void lg_copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void lg_copy4(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void lg_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void lg_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// kQuad: rows start on 16-byte boundaries, and a thread's tokens of a slice are
+// four neighbours, 4 tid + k; else tid + k threads.
+template <bool kHist, bool kBias, bool kMask, bool kQuad>
+__global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs a) {
   extern __shared__ __align__(16) unsigned lsm[];
   __shared__ unsigned long long s_best[kLgThreads / 32];
-  const int tid = threadIdx.x, t = blockIdx.y, V = a.V;
-  const int v0 = blockIdx.x * a.slice, n = min(a.slice, V - v0);
-  unsigned *cnt = lsm, *bix = lsm + (kHist ? a.slice : 0);
-  const bool tracer = blockIdx.x == 0 && t == 0 && tid == 0;
+  const int tid = threadIdx.x, V = a.V;
+  constexpr int kStep = kQuad ? 1 : kLgThreads;  // distance of a thread's tokens
+  const int own = kQuad ? 4 * tid : tid;         // its first token of a slice
+  const int seg = a.seg * kLgSlice;
+  float *const ring = reinterpret_cast<float *>(lsm) + own, *const ring_end = ring + kLgRing * kLgSlice;
+  unsigned *const cnt = lsm + kLgRing * kLgSlice, *const bix = cnt + (kHist ? seg : 0);
+  // mask words of the slices in the ring, four for the 128 tokens of a warp
+  uint32_t *const mring = bix + (kBias ? seg : 0) + (tid >> 5) * 4, *const mend = mring + kLgRing * kMaskSlice;
+  const bool tracer = blockIdx.x == 0 && tid == 0;
   if (tracer) trace_min(a.trace, kTrEntry);
+  const int ns = (V + seg - 1) / seg;  // segments per row
+  const long long units = (long long)ns * a.T;
+  const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  if (kHist || kBias)
+    for (int i = tid; i < ((kHist ? 1 : 0) + (kBias ? 1 : 0)) * seg / 4; i += kLgThreads)
+      reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
   pdl_wait();
   pdl_launch_dependents();
   if (tracer) trace_min(a.trace, kTrWaited);
 
-  bool bad_id = false, bad = false;
-  RowRules rr = {1.f, 0.f, 0.f, nullptr};
-  if (kHist || kBias) {
-    for (int i = tid; i < ((kHist ? a.slice : 0) + (kBias ? a.slice : 0)); i += kLgThreads) lsm[i] = 0u;
-    __syncthreads();
-  }
-  if (kHist) {
-    const int len = max(0, min(__ldcg(a.history_len + t), a.history_stride));
-    const int p = a.prompt_len ? __ldcg(a.prompt_len + t) : 0;
-    const int32_t *hist = a.history + (size_t)t * a.history_stride;
-    for (int i = tid; i < len; i += kLgThreads) {
-      const int id = __ldcg(hist + i);
-      const unsigned d = (unsigned)(id - v0);
-      if (d < (unsigned)n) {
-        if (i < p)
-          atomicOr(cnt + d, kInPrompt);
-        else
-          atomicAdd(cnt + d, 1u);
+  int t = (int)(u0 / ns), sg = (int)(u0 % ns);
+  // Copies run ahead.  cin: this thread's first token of the next slice to
+  // copy; cleft: tokens from the slice's start to the row's end; the block's
+  // part ends cend tokens before the end of row et.
+  const float *cin = a.logits + (size_t)t * a.ld + (size_t)sg * seg + own;
+  float *cto = ring;
+  const int mown = kQuad ? (tid & ~31) * 4 + (tid & 3) * 32 : (tid & ~31) + (tid & 3) * kStep;  // first token of the lane's word
+  const uint32_t *cmask = kMask ? a.mask + (size_t)t * a.mask_stride + ((sg * seg + mown) >> 5) : nullptr;
+  uint32_t *mto = mring;
+  int ct = t, cleft = V - sg * seg;
+  const int et = (int)((u1 - 1) / ns), cend = max(0, V - ((int)((u1 - 1) % ns) + 1) * seg);
+  auto copy_next = [&]() {
+    if (ct < et || (ct == et && cleft > cend)) {
+      if (kQuad && own + 4 <= cleft) {
+        lg_copy16(cto, cin);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (own + k * kStep < cleft) lg_copy4(cto + k * kStep, cin + k * kStep);
       }
-      bad_id = bad_id || id < 0 || id >= V;
+      if (kMask) {
+        if ((tid & 31) < 4 && mown < cleft) lg_copy4(mto + (tid & 3), cmask);
+        mto += kMaskSlice;
+        if (mto == mend) mto = mring;
+        cmask += kLgSlice / 32;
+      }
+      cto += kLgSlice;
+      if (cto == ring_end) cto = ring;
+      cin += kLgSlice;
+      cleft -= kLgSlice;
+      if (cleft <= 0) {  // the next row
+        ++ct;
+        cin = a.logits + (size_t)ct * a.ld + own;
+        if (kMask) cmask = a.mask + (size_t)ct * a.mask_stride + (mown >> 5);
+        cleft = V;
+      }
     }
-    if (a.repetition) rr.rep = __ldcg(a.repetition + t);
-    if (a.presence) rr.pres = __ldcg(a.presence + t);
-    if (a.frequency) rr.freq = __ldcg(a.frequency + t);
-  }
-  if (kBias) {
-    const int len = max(0, min(__ldcg(a.bias_len + t), a.bias_stride));
-    const int32_t *ids = a.bias_ids + (size_t)t * a.bias_stride;
-    rr.bias = a.bias_values + (size_t)t * a.bias_stride;
-    for (int i = tid; i < len; i += kLgThreads) {
-      const int id = __ldcg(ids + i);
-      const unsigned d = (unsigned)(id - v0);
-      if (d < (unsigned)n) atomicMax(bix + d, (unsigned)(i + 1));
-      bad_id = bad_id || id < 0 || id >= V;
-    }
-  }
-  if (kHist || kBias) __syncthreads();
-  if (bad_id) set_error(a.err, kErrBadId);
+    lg_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kLgRing - 1; ++i) copy_next();
 
-  const float *in = a.logits + (size_t)t * a.ld + v0;
-  float *out = a.out ? a.out + (size_t)t * a.ld_out + v0 : nullptr;
-  const uint32_t *mask = a.mask ? a.mask + (size_t)t * a.mask_stride + (v0 >> 5) : nullptr;
-  unsigned long long best = 0ull;
-  for (int i = tid; i < n; i += kLgThreads) {
-    const bool allowed = !mask || ((__ldcg(mask + (i >> 5)) >> (i & 31)) & 1u);
-    const float l = lg_apply(__ldcs(in + i), kHist ? cnt[i] : 0u, kBias ? bix[i] : 0u, allowed, rr);
-    if (out) out[i] = l;
-    if (l < INFINITY) {  // not NaN, not +inf
-      if (l > -INFINITY) best = max(best, lg_key(l, (unsigned)(v0 + i)));
-    } else {
-      bad = true;
-    }
-  }
-  if (bad) set_error(a.err, kErrNonFinite);
-  if (a.tokens) {
+  bool fresh = true, bad_id = false, bad = false;
+  RowRules rr = {1.f, 0.f, 0.f, nullptr};
+  int hlen = 0, plen = 0, blen = 0, hv[kHistRegs], bv = 0, done = 0;
+  float best = -INFINITY;  // the thread's best of the row so far
+  int best_id = 0;
+  const float *in = ring;
+  const uint32_t *mslice = mring;
+  for (long long u = u0; u < u1; ++u) {
+    const int v0 = sg * seg, n = min(seg, V - v0);
+    // this thread's places of the segment's first slice
+    float *out = a.out ? a.out + (size_t)t * a.ld_out + v0 + own : nullptr;
+    if (kHist || kBias) {
+      const int32_t *hist = a.history + (size_t)t * a.history_stride, *bids = a.bias_ids + (size_t)t * a.bias_stride;
+      if (fresh) {  // a row begins: its rules and its lists' first entries (a list's buffer is a stride long whatever its length)
+        fresh = false;
+        if (kHist) {
+          hlen = __ldcg(a.history_len + t);
+          plen = a.prompt_len ? __ldcg(a.prompt_len + t) : 0;
+          if (a.repetition) rr.rep = __ldcg(a.repetition + t);
+          if (a.presence) rr.pres = __ldcg(a.presence + t);
+          if (a.frequency) rr.freq = __ldcg(a.frequency + t);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, off));
-    if ((tid & 31) == 0) s_best[tid >> 5] = best;
-    __syncthreads();
-    if (tid == 0) {
-#pragma unroll
-      for (int w = 1; w < kLgThreads / 32; ++w) best = max(best, s_best[w]);
-      if (best != 0ull) atomicMax(a.best + t, best);
-      __threadfence();  // this block's maximum is visible before it takes its ticket
-      if (atomicAdd(a.tickets + t, 1u) == gridDim.x - 1) {  // the row's last block
-        __threadfence();
-        const unsigned long long v = atomicExch(a.best + t, 0ull);
-        atomicExch(a.tickets + t, 0u);
-        a.tokens[t] = v ? (int32_t)(0xFFFFFFFFu - (unsigned)(v & 0xFFFFFFFFull)) : -1;
+          for (int k = 0; k < kHistRegs; ++k)
+            hv[k] = tid + k * kLgThreads < a.history_stride ? __ldcg(hist + tid + k * kLgThreads) : 0;
+        }
+        if (kBias) {
+          blen = __ldcg(a.bias_len + t);
+          rr.bias = a.bias_values + (size_t)t * a.bias_stride;
+          bv = tid < a.bias_stride ? __ldcg(bids + tid) : 0;
+        }
+        hlen = max(0, min(hlen, a.history_stride));
+        blen = max(0, min(blen, a.bias_stride));
       }
+      __syncthreads();  // every thread is done with the segment before: the tables are clear
+      if (kHist) {
+        auto count = [&](int id, int i) {
+          const unsigned d = (unsigned)(id - v0);
+          if (d < (unsigned)n) {
+            if (i < plen)
+              atomicOr(cnt + d, kInPrompt);
+            else
+              atomicAdd(cnt + d, 1u);
+          }
+          bad_id = bad_id || (unsigned)id >= (unsigned)V;
+        };
+#pragma unroll
+        for (int k = 0; k < kHistRegs; ++k)
+          if (tid + k * kLgThreads < hlen) count(hv[k], tid + k * kLgThreads);
+        int i = kHistRegs * kLgThreads;
+        if ((reinterpret_cast<uintptr_t>(hist) & 15u) == 0) {
+#pragma unroll 4
+          for (i += 4 * tid; i + 3 < hlen; i += 4 * kLgThreads) {
+            const int4 q = __ldcg(reinterpret_cast<const int4 *>(hist + i));
+            count(q.x, i);
+            count(q.y, i + 1);
+            count(q.z, i + 2);
+            count(q.w, i + 3);
+          }
+          for (; i < hlen; ++i) count(__ldcg(hist + i), i);  // the last one to three (their thread's loop ended there)
+        } else {
+#pragma unroll 8
+          for (i += tid; i < hlen; i += kLgThreads) count(__ldcg(hist + i), i);
+        }
+      }
+      if (kBias) {
+        auto enter = [&](int id, int i) {
+          const unsigned d = (unsigned)(id - v0);
+          if (d < (unsigned)n) atomicMax(bix + d, (unsigned)(i + 1));
+          bad_id = bad_id || (unsigned)id >= (unsigned)V;
+        };
+        if (tid < blen) enter(bv, tid);
+#pragma unroll 4
+        for (int i = kLgThreads + tid; i < blen; i += kLgThreads) enter(__ldcg(bids + i), i);
+      }
+      __syncthreads();  // the tables are complete
+    }
+    unsigned *ci = cnt + own, *bi = bix + own;
+    int v = v0 + own;
+    for (int left = n; left > 0; left -= kLgSlice) {  // the segment's slices
+      lg_wait<kLgRing - 2>();  // the thread's part of the slice has landed
+      uint32_t m = 15u;
+      if (kMask) {
+        __syncwarp();  // and its warp's mask words
+        if (kQuad) {
+          m = mslice[(tid & 31) >> 3] >> (4 * (tid & 7));
+        } else {
+          const uint4 w = *reinterpret_cast<const uint4 *>(mslice);
+          const int i = tid & 31;
+          m = ((w.x >> i) & 1u) | (((w.y >> i) & 1u) << 1) | (((w.z >> i) & 1u) << 2) | (((w.w >> i) & 1u) << 3);
+        }
+        __syncwarp();  // every lane has its bits before the place is filled again
+        mslice += kMaskSlice;
+        if (mslice == mend) mslice = mring;
+      }
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      uint4 c = none, b = none;
+      float l[4];
+      if (kQuad) {
+        const float4 f = *reinterpret_cast<const float4 *>(in);
+        l[0] = f.x;
+        l[1] = f.y;
+        l[2] = f.z;
+        l[3] = f.w;
+        if (kHist) c = *reinterpret_cast<const uint4 *>(ci);
+        if (kBias) b = *reinterpret_cast<const uint4 *>(bi);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l[k] = in[k * kStep];
+        if (kHist) c = make_uint4(ci[0], ci[kStep], ci[2 * kStep], ci[3 * kStep]);
+        if (kBias) b = make_uint4(bi[0], bi[kStep], bi[2 * kStep], bi[3 * kStep]);
+      }
+      copy_next();  // into the place before this one, which the thread has read
+      in += kLgSlice;
+      if (in == ring_end) in = ring;
+      if ((kHist || kBias) && (c.x | c.y | c.z | c.w | b.x | b.y | b.z | b.w) != 0u) {
+        lg_touched(l, c, b, rr);
+        if (kQuad) {
+          if (kHist) *reinterpret_cast<uint4 *>(ci) = none;
+          if (kBias) *reinterpret_cast<uint4 *>(bi) = none;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (kHist) ci[k * kStep] = 0u;
+            if (kBias) bi[k * kStep] = 0u;
+          }
+        }
+      }
+      if (kMask) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l[k] = m & (1u << k) ? l[k] : -INFINITY;
+      }
+      if (left >= kLgSlice) {
+        if (out) {
+          if (kQuad) {
+            __stcs(reinterpret_cast<float4 *>(out), make_float4(l[0], l[1], l[2], l[3]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) __stcs(out + k * kStep, l[k]);
+          }
+        }
+      } else {  // the row's end
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bool there = own + k * kStep < left;
+          l[k] = there ? l[k] : -INFINITY;
+          if (out && there) __stcs(out + k * kStep, l[k]);
+        }
+      }
+      if (!(l[0] < INFINITY && l[1] < INFINITY && l[2] < INFINITY && l[3] < INFINITY)) {
+        bad = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (!(l[k] < INFINITY)) l[k] = -INFINITY;  // NaN and +inf are not for the token
+      }
+      const float top = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+      if (top > best) {
+        best = top;
+        best_id = v + kStep * (l[0] == top ? 0 : l[1] == top ? 1 : l[2] == top ? 2 : 3);  // the first of them
+      }
+      if (out) out += kLgSlice;
+      v += kLgSlice;
+      ci += kLgSlice;
+      bi += kLgSlice;
+    }
+    ++done;
+    if (++sg == ns || u + 1 == u1) {  // the row ends, or the block's part of it
+      if (a.tokens) {
+        unsigned long long key = best > -INFINITY ? lg_key(best, (unsigned)best_id) : 0ull;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
+        if ((tid & 31) == 0) s_best[tid >> 5] = key;
+        __syncthreads();
+        if (tid < 32) {
+          key = s_best[tid];
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, off));
+        }
+        if (tid == 0) {
+          bool last = done == ns;  // the whole row was this block's
+          if (!last) {
+            if (key != 0ull) atomicMax(a.best + t, key);
+            __threadfence();  // this block's maximum is visible before it takes its ticket
+            last = atomicAdd(a.tickets + t, (unsigned)done) + done == (unsigned)ns;
+            if (last) {
+              __threadfence();
+              key = atomicExch(a.best + t, 0ull);
+              atomicExch(a.tickets + t, 0u);
+            }
+          }
+          if (last) a.tokens[t] = key ? (int32_t)(0xFFFFFFFFu - (unsigned)(key & 0xFFFFFFFFull)) : -1;
+        }
+        __syncthreads();  // s_best is free again
+      }
+      best = -INFINITY;
+      done = 0;
+      sg = 0;
+      ++t;
+      fresh = true;
     }
   }
+  lg_wait<0>();
+  if (bad_id) set_error(a.err, kErrBadId);
+  if (bad) set_error(a.err, kErrNonFinite);
   if (tracer) trace_max(a.trace, kTrExit);
+}
+
+size_t lg_smem(bool h, bool b, int seg) {
+  return (size_t)kLgSlice * 4 * (kLgRing + seg * ((h ? 1 : 0) + (b ? 1 : 0))) + (size_t)kLgRing * kMaskSlice * 4;
+}
+
+using LgKernel = void (*)(const LogitsArgs);
+template <bool kHist, bool kBias>
+LgKernel lg_pick(bool mask, bool quad) {
+  if (mask) return quad ? logits_kernel<kHist, kBias, true, true> : logits_kernel<kHist, kBias, true, false>;
+  return quad ? logits_kernel<kHist, kBias, false, true> : logits_kernel<kHist, kBias, false, false>;
+}
+LgKernel lg_kernel(bool h, bool b, bool mask, bool quad) {
+  if (h) return b ? lg_pick<true, true>(mask, quad) : lg_pick<true, false>(mask, quad);
+  return b ? lg_pick<false, true>(mask, quad) : lg_pick<false, false>(mask, quad);
 }
 }  // namespace
 
-cudaError_t launch_logits(const LogitsArgs &a0, cudaStream_t st, bool pdl) {
+cudaError_t logits_set_attributes() {
+  for (int i = 0; i < 16; ++i) {
+    const cudaError_t e = cudaFuncSetAttribute(lg_kernel(i & 1, i & 2, i & 4, i & 8),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)lg_smem(i & 1, i & 2, kLgSegMax));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_logits(const LogitsArgs &a0, int n_sm, cudaStream_t st, bool pdl) {
   LogitsArgs a = a0;
-  a.slice = 4096;
   const bool h = a.history != nullptr, b = a.bias_ids != nullptr;
-  const dim3 grid((a.V + a.slice - 1) / a.slice, a.T), block(kLgThreads);
-  const size_t smem = (size_t)a.slice * 4 * ((h ? 1 : 0) + (b ? 1 : 0));
-  if (h && b) return launch_k(logits_kernel<true, true>, grid, block, smem, st, pdl, a);
-  if (h) return launch_k(logits_kernel<true, false>, grid, block, smem, st, pdl, a);
-  if (b) return launch_k(logits_kernel<false, true>, grid, block, smem, st, pdl, a);
-  return launch_k(logits_kernel<false, false>, grid, block, smem, st, pdl, a);
+  const bool quad = (((uintptr_t)a.logits | (uintptr_t)a.out) & 15u) == 0 && a.ld % 4 == 0 && (!a.out || a.ld_out % 4 == 0);
+  // Slices per segment: the fewest slices for the block that has most of them,
+  // a segment's own work counted as half a slice and one per 6000 tokens of
+  // history.
+  const double own = 0.5 + (h ? a.history_stride / 6000.0 : 0.0);
+  double least = 0.0;
+  long long blocks = 0;
+  for (int s = 1; s <= kLgSegMax; s *= 2) {
+    const long long segs = ((long long)a.V + (long long)s * kLgSlice - 1) / ((long long)s * kLgSlice) * a.T;
+    const long long n = segs < n_sm ? segs : n_sm;
+    const double cost = (double)((segs + n - 1) / n) * (s + own);
+    if (s == 1 || cost < least) {
+      least = cost;
+      a.seg = s;
+      blocks = n;
+    }
+  }
+  return launch_k(lg_kernel(h, b, a.mask != nullptr, quad), dim3((unsigned)blocks), dim3(kLgThreads), lg_smem(h, b, a.seg), st, pdl, a);
 }
 
 }  // namespace moe

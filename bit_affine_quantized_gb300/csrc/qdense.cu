@@ -204,16 +204,23 @@ struct MmParams {
   MmPlan p;
 };
 
+// Bounded wait that suspends in hardware; the timer is read only once a wait
+// is not over at its first look (reading it costs more than most waits).
+__device__ __forceinline__ bool mm_try(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity) {
+  if (mm_try(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
   for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
-    if (ok) return true;
+    for (int i = 0; i < 64; ++i)
+      if (mm_try(bar, parity)) return true;
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
 }

@@ -41,7 +41,8 @@ namespace moe {
 namespace {
 constexpr int kQdWarps = 8;
 constexpr int kQdThreads = kQdWarps * 32;
-constexpr int kQdRowsMax = 8;  // rows that the dp4a kernel takes
+constexpr int kQdRowsMax = 8;   // rows that the dp4a kernel takes
+constexpr int kQdFewMax = 32;   // rows that the mma.sync kernel takes, where they fit
 
 __device__ __forceinline__ int4 qd_stream(const int8_t *p) {
   int4 v;
@@ -51,46 +52,68 @@ __device__ __forceinline__ int4 qd_stream(const int8_t *p) {
   return v;
 }
 
-__device__ __forceinline__ float qd_finish(int acc, float xs, float ws, float cap) {
-  const float v = __fmul_rn(__fmul_rn((float)acc, xs), ws);
-  return cap > 0.f ? cap * tanhf(v / cap) : v;
+__device__ __forceinline__ void qd_put(const QdenseArgs &a, int t, int n, float acc, float xs, float ws) {
+  float v = __fmul_rn(__fmul_rn(acc, xs), ws);
+  if (a.softcap > 0.f) v = a.softcap * tanhf(v / a.softcap);
+  const size_t o = (size_t)t * a.N + n;
+  if (a.y32) a.y32[o] = v;
+  if (a.y) a.y[o] = float_to_bf16_bits(v);
+}
+// The same of an integer sum.
+__device__ __forceinline__ void qd_store(const QdenseArgs &a, int t, int n, int acc, float xs, float ws) {
+  qd_put(a, t, n, (float)acc, xs, ws);
 }
 
-template <int kT, int kR>
+// kT rows, kR channels per warp; kAhead 16-byte pieces of each channel's row
+// are requested before the first is used (those of a warp's first channels
+// before the rows' codes have arrived).
+template <int kT, int kR, int kAhead>
 __global__ void __launch_bounds__(kQdThreads) qdense_rows_kernel(const QdenseArgs a) {
   extern __shared__ __align__(16) int4 qsm[];  // [kT][K / 16]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int K = a.K, nck = K / 16, t0 = blockIdx.y * kT, nt = min(kT, a.T - t0);
-  const bool tracer = blockIdx.x == 0 && blockIdx.y == 0 && tid == 0;
+  const int K = a.K, nck = K / 16, nt = min(kT, a.T);
+  const bool tracer = blockIdx.x == 0 && tid == 0;
   if (tracer) trace_min(a.trace, kTrEntry);
   pdl_wait();
   pdl_launch_dependents();
   if (tracer) trace_min(a.trace, kTrWaited);
-  const int4 *x4 = reinterpret_cast<const int4 *>(a.x + (size_t)t0 * K);
+  const int units = (a.N + kR - 1) / kR;
+  int u = blockIdx.x * kQdWarps + warp;
+  int4 w[kR][kAhead];
+  auto request = [&](int n0, int c0) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int c = c0 + 32 * j + lane;
+#pragma unroll
+      for (int r = 0; r < kR; ++r)  // channels past N: discarded below
+        w[r][j] = c < nck ? qd_stream(a.w + (size_t)min(n0 + r, a.N - 1) * K + 16 * c) : make_int4(0, 0, 0, 0);
+    }
+  };
+  if (u < units) request(u * kR, 0);
+  const int4 *x4 = reinterpret_cast<const int4 *>(a.x);
   for (int i = tid; i < kT * nck; i += kQdThreads) qsm[i] = i < nt * nck ? __ldcg(x4 + i) : make_int4(0, 0, 0, 0);
   __syncthreads();
-  const int units = (a.N + kR - 1) / kR;
-  for (int u = blockIdx.x * kQdWarps + warp; u < units; u += gridDim.x * kQdWarps) {
+  for (bool first = true; u < units; u += gridDim.x * kQdWarps, first = false) {
     const int n0 = u * kR;
-    const int8_t *wr[kR];
-#pragma unroll
-    for (int r = 0; r < kR; ++r) wr[r] = a.w + (size_t)min(n0 + r, a.N - 1) * K;  // past N: discarded below
+    if (!first) request(n0, 0);
     int acc[kR][kT];
 #pragma unroll
     for (int r = 0; r < kR; ++r)
 #pragma unroll
       for (int t = 0; t < kT; ++t) acc[r][t] = 0;
-#pragma unroll 2
-    for (int c = lane; c < nck; c += 32) {
-      int4 w[kR];
+    for (int c0 = 0; c0 < nck; c0 += 32 * kAhead) {
+      if (c0 > 0) request(n0, c0);
 #pragma unroll
-      for (int r = 0; r < kR; ++r) w[r] = qd_stream(wr[r] + 16 * c);
+      for (int j = 0; j < kAhead; ++j) {
+        const int c = min(c0 + 32 * j + lane, nck - 1);  // past the row: the weights are zero
 #pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        const int4 x = qsm[t * nck + c];
+        for (int t = 0; t < kT; ++t) {
+          const int4 x = qsm[t * nck + c];
 #pragma unroll
-        for (int r = 0; r < kR; ++r)
-          acc[r][t] = __dp4a(w[r].w, x.w, __dp4a(w[r].z, x.z, __dp4a(w[r].y, x.y, __dp4a(w[r].x, x.x, acc[r][t]))));
+          for (int r = 0; r < kR; ++r)
+            acc[r][t] = __dp4a(w[r][j].w, x.w,
+                               __dp4a(w[r][j].z, x.z, __dp4a(w[r][j].y, x.y, __dp4a(w[r][j].x, x.x, acc[r][t]))));
+        }
       }
     }
     // lane r * kT + t ends with sum (r, t)
@@ -103,45 +126,45 @@ __global__ void __launch_bounds__(kQdThreads) qdense_rows_kernel(const QdenseArg
         if (lane == r * kT + t) mine = s;
       }
     const int r = lane / kT, t = lane % kT;
-    if (r < kR && t < nt && n0 + r < a.N) {
-      const float v = qd_finish(mine, __ldcg(a.xs + t0 + t), __ldg(a.ws + n0 + r), a.softcap);
-      const size_t o = (size_t)(t0 + t) * a.N + n0 + r;
-      if (a.y32) a.y32[o] = v;
-      if (a.y) a.y[o] = float_to_bf16_bits(v);
-    }
+    if (r < kR && t < nt && n0 + r < a.N) qd_store(a, t, n0 + r, mine, __ldcg(a.xs + t), __ldg(a.ws + n0 + r));
   }
   if (tracer) trace_max(a.trace, kTrExit);
 }
 
-template <int kT, int kR>
+template <int kT, int kR, int kAhead>
 cudaError_t launch_rows(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
   const size_t smem = (size_t)kT * a.K;
   int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, qdense_rows_kernel<kT, kR>, kQdThreads, smem);
+  cudaError_t e =
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, qdense_rows_kernel<kT, kR, kAhead>, kQdThreads, smem);
   if (e != cudaSuccess) return e;
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   const int units = (a.N + kR - 1) / kR, blocks = (units + kQdWarps - 1) / kQdWarps;
   const int most = n_sm * per_sm;
-  return launch_k(qdense_rows_kernel<kT, kR>, dim3(blocks < most ? blocks : most, (a.T + kT - 1) / kT),
-                  dim3(kQdThreads), smem, st, pdl, a);
+  return launch_k(qdense_rows_kernel<kT, kR, kAhead>, dim3(blocks < most ? blocks : most), dim3(kQdThreads), smem, st,
+                  pdl, a);
 }
 
+#ifndef QA1
+#define QA1 6
+#endif
+#ifndef QA4
+#define QA4 3
+#endif
 template <int kT>
 cudaError_t launch_rows_t(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
-  if (a.N >= 4 * kQdWarps * 4 * n_sm) return launch_rows<kT, 4>(a, n_sm, st, pdl);
-  return launch_rows<kT, 1>(a, n_sm, st, pdl);
+  if (a.N >= 4 * kQdWarps * 4 * n_sm) return launch_rows<kT, 4, QA4>(a, n_sm, st, pdl);
+  return launch_rows<kT, 1, QA1>(a, n_sm, st, pdl);
 }
 
 template <int kT>
 cudaError_t set_rows_attr() {
-  cudaError_t e = cudaFuncSetAttribute(qdense_rows_kernel<kT, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(qdense_rows_kernel<kT, 4, QA4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kT * kQdenseMaxK);
   if (e) return e;
-  return cudaFuncSetAttribute(qdense_rows_kernel<kT, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(qdense_rows_kernel<kT, 1, QA1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kT * kQdenseMaxK);
 }
-// ------------------------------------------------------------------ rows to fp16
-constexpr int kWidenThreads = 256;
 
 // Four 8-bit codes as two exact fp16 pairs: the code + 128 goes under the
 // exponent of 1024 (1024 + c is exact for c < 1024), then 1152 is subtracted.
@@ -151,6 +174,203 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
+
+// ------------------------------------------------------------------ few rows, mma.sync
+constexpr int kQfWarps = 16;
+constexpr int kQfThreads = kQfWarps * 32;
+constexpr int kQfAhead = 4;          // 64-wide K blocks whose codes a warp has in flight
+constexpr int kQfFlush = 1024 / 64;  // blocks after which the fp32 sums go to integers: 128 * 128 * 1024 = 2^24
+constexpr size_t kQfSmemMax = 200 * 1024;
+__host__ __device__ constexpr int qf_pitch(int K) { return 2 * K + 16; }  // bytes of a row: consecutive rows 4 banks apart
+
+// kNt: groups of 8 rows.  A warp takes a tile of 16 channels (or, where tiles
+// are few, a part of a tile's K: split parts by neighbouring warps).  K comes
+// in 64-wide blocks; lane (r, c) = (lane / 4, lane % 4) loads the codes 16 c
+// .. 16 c + 15 of channels r and r + 8, and multiplication j of a block takes
+// codes 4 j .. 4 j + 3 of those for the k positions that mma.m16n8k16 gives
+// the lane; the rows, widened to fp16 in shared memory, follow the same order.
+template <int kNt>
+__global__ void __launch_bounds__(kQfThreads, 1) qdense_few_kernel(const QdenseArgs a, const int split) {
+  extern __shared__ __align__(16) uint8_t fsm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const int K = a.K, nb = (K + 63) / 64, pitch = qf_pitch(K);
+  const bool tracer = blockIdx.x == 0 && tid == 0;
+  if (tracer) trace_min(a.trace, kTrEntry);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tracer) trace_min(a.trace, kTrWaited);
+
+  const int tiles = (a.N + 15) / 16, per_block = kQfWarps / split;
+  const int part = warp % split;
+  const int b0 = nb * part / split, b1 = nb * (part + 1) / split;  // this warp's blocks
+  int tile = blockIdx.x * per_block + warp / split;
+  int4 w0[kQfAhead], w1[kQfAhead];
+  auto request = [&](int n0, int b) {
+    const int8_t *p0 = a.w + (size_t)min(n0 + r, a.N - 1) * K + 16 * c;  // channels past N: discarded below
+    const int8_t *p1 = a.w + (size_t)min(n0 + r + 8, a.N - 1) * K + 16 * c;
+#pragma unroll
+    for (int j = 0; j < kQfAhead; ++j) {
+      const bool there = b + j < b1 && 64 * (b + j) + 16 * c < K;
+      w0[j] = there ? qd_stream(p0 + 64 * (b + j)) : make_int4(0, 0, 0, 0);
+      w1[j] = there ? qd_stream(p1 + 64 * (b + j)) : make_int4(0, 0, 0, 0);
+    }
+  };
+  if (tile < tiles) request(tile * 16, b0);
+  // the rows, widened (those past T: zero)
+  const int nck = K / 16;
+  for (int i = tid; i < 8 * kNt * nck; i += kQfThreads) {
+    const int t = i / nck, k = i - t * nck;
+    const uint4 v = t < a.T ? __ldcg(reinterpret_cast<const uint4 *>(a.x + (size_t)t * K) + k) : make_uint4(0u, 0u, 0u, 0u);
+    uint4 o0, o1;
+    widen4(v.x, o0.x, o0.y);
+    widen4(v.y, o0.z, o0.w);
+    widen4(v.z, o1.x, o1.y);
+    widen4(v.w, o1.z, o1.w);
+    uint4 *dst = reinterpret_cast<uint4 *>(fsm + (size_t)t * pitch + 32 * k);
+    dst[0] = o0;
+    dst[1] = o1;
+  }
+  __syncthreads();
+  int *parts = reinterpret_cast<int *>(fsm + (size_t)8 * kNt * pitch);  // [warp][4 kNt][32], split > 1
+  // (every warp of a block makes the same number of rounds: barriers below)
+  const int rounds = (tiles + gridDim.x * per_block - 1) / (gridDim.x * per_block);
+  for (int round = 0; round < rounds; ++round, tile += gridDim.x * per_block) {
+    const int n0 = tile * 16;
+    int sum[kNt][4];
+#pragma unroll
+    for (int n = 0; n < kNt; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[n][i] = 0;
+    if (tile < tiles) {
+      if (round > 0) request(n0, b0);
+      for (int f = b0; f < b1; f += kQfFlush) {  // exact in fp32
+        float acc[kNt][4];
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+        const int fe = min(b1, f + kQfFlush);
+        for (int b = f; b < fe; b += kQfAhead) {
+          int4 x0[kQfAhead], x1[kQfAhead];
+#pragma unroll
+          for (int j = 0; j < kQfAhead; ++j) {
+            x0[j] = w0[j];
+            x1[j] = w1[j];
+          }
+          request(n0, b + kQfAhead);
+#pragma unroll
+          for (int j = 0; j < kQfAhead; ++j) {
+            if (b + j >= fe) break;  // (warp-uniform)
+            const int k = min(64 * (b + j) + 16 * c, K - 16);  // past the row: the weights are zero
+            const uint32_t *q0 = reinterpret_cast<const uint32_t *>(&x0[j]), *q1 = reinterpret_cast<const uint32_t *>(&x1[j]);
+            uint32_t A[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              widen4(q0[i], A[i][0], A[i][2]);
+              widen4(q1[i], A[i][1], A[i][3]);
+            }
+#pragma unroll
+            for (int n = 0; n < kNt; ++n) {
+              const uint4 *bx = reinterpret_cast<const uint4 *>(fsm + (size_t)(8 * n + r) * pitch + 2 * k);
+              const uint4 v0 = bx[0], v1 = bx[1];
+              mma_f16(acc[n], A[0], v0.x, v0.y);
+              mma_f16(acc[n], A[1], v0.z, v0.w);
+              mma_f16(acc[n], A[2], v1.x, v1.y);
+              mma_f16(acc[n], A[3], v1.z, v1.w);
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[n][i] += __float2int_rn(acc[n][i]);
+      }
+    }
+    if (split > 1) {
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) parts[(warp * kNt * 4 + n * 4 + i) * 32 + lane] = sum[n][i];
+      __syncthreads();
+      if (part == 0) {
+        for (int p = 1; p < split; ++p)
+#pragma unroll
+          for (int n = 0; n < kNt; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[n][i] += parts[((warp + p) * kNt * 4 + n * 4 + i) * 32 + lane];
+      }
+      __syncthreads();
+    }
+    if (part == 0 && tile < tiles) {
+      // sum[n][i]: channel n0 + r + 8 (i / 2), row 8 n + 2 c + i % 2
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int ch = n0 + r + 8 * (i >> 1);
+        const float ws = ch < a.N ? __ldg(a.ws + ch) : 0.f;
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+          const int t = 8 * n + 2 * c + (i & 1);
+          if (t < a.T && ch < a.N) qd_store(a, t, ch, sum[n][i], __ldcg(a.xs + t), ws);
+        }
+      }
+    }
+  }
+  if (tracer) trace_max(a.trace, kTrExit);
+}
+
+template <int kNt>
+size_t few_smem(int K) {
+  return (size_t)8 * kNt * qf_pitch(K) + (size_t)kQfWarps * kNt * 4 * 32 * 4;
+}
+
+template <int kNt>
+cudaError_t launch_few_n(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
+  const int tiles = (a.N + 15) / 16, nb = (a.K + 63) / 64;
+  // parts of K per tile while whole tiles would leave warps without work
+  int split = 1;
+  while (split < kQfWarps && 2 * split * tiles <= n_sm * kQfWarps && 2 * split <= nb) split *= 2;
+  const int per_block = kQfWarps / split, blocks = (tiles + per_block - 1) / per_block;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks < n_sm ? blocks : n_sm);
+  cfg.blockDim = dim3(kQfThreads);
+  cfg.dynamicSmemBytes = few_smem<kNt>(a.K);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, qdense_few_kernel<kNt>, a, split);
+}
+
+// Whether the rows, widened, fit a block's shared memory.
+bool few_fits(int T, int K) {
+  const int nt = (T + 7) / 8;
+  return T <= kQdFewMax && (size_t)8 * nt * qf_pitch(K) + (size_t)kQfWarps * nt * 4 * 32 * 4 <= kQfSmemMax;
+}
+
+cudaError_t launch_few(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
+  switch ((a.T + 7) / 8) {
+    case 1: return launch_few_n<1>(a, n_sm, st, pdl);
+    case 2: return launch_few_n<2>(a, n_sm, st, pdl);
+    case 3: return launch_few_n<3>(a, n_sm, st, pdl);
+    default: return launch_few_n<4>(a, n_sm, st, pdl);
+  }
+}
+
+cudaError_t set_few_attr() {
+  const cudaFuncAttribute f = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(qdense_few_kernel<1>, f, (int)kQfSmemMax)) ||
+      (e = cudaFuncSetAttribute(qdense_few_kernel<2>, f, (int)kQfSmemMax)) ||
+      (e = cudaFuncSetAttribute(qdense_few_kernel<3>, f, (int)kQfSmemMax)))
+    return e;
+  return cudaFuncSetAttribute(qdense_few_kernel<4>, f, (int)kQfSmemMax);
+}
+
+// ------------------------------------------------------------------ rows to fp16
+constexpr int kWidenThreads = 256;
 
 __global__ void __launch_bounds__(kWidenThreads) qdense_widen_kernel(const QdenseArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0) trace_min(a.trace, kTrEntry);
@@ -209,9 +429,9 @@ struct MmParams {
 __device__ __forceinline__ bool mm_try(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
       : "memory");
   return ok != 0;
 }
@@ -219,8 +439,7 @@ __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity) {
   if (mm_try(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
   for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (mm_try(bar, parity)) return true;
+    if (mm_try(bar, parity)) return true;
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
 }
@@ -261,14 +480,6 @@ __device__ __forceinline__ float cluster_ld(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
-}
-
-__device__ __forceinline__ void mm_store(const QdenseArgs &a, int t, int n, float acc, float xs, float ws) {
-  float v = __fmul_rn(__fmul_rn(acc, xs), ws);
-  if (a.softcap > 0.f) v = a.softcap * tanhf(v / a.softcap);
-  const size_t o = (size_t)t * a.N + n;
-  if (a.y32) a.y32[o] = v;
-  if (a.y) a.y[o] = float_to_bf16_bits(v);
 }
 
 __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_constant__ MmParams prm) {
@@ -445,7 +656,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
           if (split > 1)
             partial[(c0 + j) * kMmM + rr] = v[j];
           else if (c0 + j < cnt && n < a.N)
-            mm_store(a, t0 + c0 + j, n, v[j], xs, ws);
+            qd_put(a, t0 + c0 + j, n, v[j], xs, ws);
         }
       }
       dense::tc_fence_before();
@@ -506,19 +717,25 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     __syncwarp();
     cluster_sync_all();
     const int n0 = first / P.ttile * kMmM, t0 = first % P.ttile * P.n, cnt = min(P.n, a.T - t0);
-    const int rr = tid & (kMmM - 1), n = n0 + rr;
-    if (tid < 3 * kMmM && n < a.N) {
-      const float ws = __ldg(a.ws + n);
-      for (int c = part + split * (tid / kMmM); c < cnt; c += 3 * split) {
-        const uint32_t at = smem_addr(base) + (uint32_t)(c * kMmM + rr) * 4u;
-        float v[kMmMaxSplit];
+    // a warp per row, four channels per lane: 4 * split remote loads in flight
+    float ws[4];
 #pragma unroll
-        for (int r = 0; r < kMmMaxSplit; ++r) v[r] = r < split ? cluster_ld(at, r) : 0.f;
-        float sum = v[0];
+    for (int i = 0; i < 4; ++i) ws[i] = n0 + lane + 32 * i < a.N ? __ldg(a.ws + n0 + lane + 32 * i) : 0.f;
+    for (int c = part + split * warp; c < cnt; c += split * (kMmThreads / 32)) {
+      const uint32_t at = smem_addr(base) + (uint32_t)(c * kMmM + lane) * 4u;
+      const float xs = __ldcg(a.xs + t0 + c);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f}, v[kMmMaxSplit][4];
 #pragma unroll
-        for (int r = 1; r < kMmMaxSplit; ++r) sum += v[r];
-        mm_store(a, t0 + c, n, sum, __ldcg(a.xs + t0 + c), ws);
-      }
+      for (int r = 0; r < kMmMaxSplit; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[r][i] = r < split ? cluster_ld(at + 128u * i, r) : 0.f;
+#pragma unroll
+      for (int r = 0; r < kMmMaxSplit; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += v[r][i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n0 + lane + 32 * i < a.N) qd_put(a, t0 + c, n0 + lane + 32 * i, sum[i], xs, ws[i]);
     }
     cluster_sync_all();  // no block leaves while another reads its sums
   }
@@ -589,15 +806,22 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl)
 
 cudaError_t qdense_set_attributes() {
   cudaError_t e;
-  if ((e = set_rows_attr<1>()) || (e = set_rows_attr<2>()) || (e = set_rows_attr<4>()) || (e = set_rows_attr<8>()))
+  if ((e = set_rows_attr<1>()) || (e = set_rows_attr<2>()) || (e = set_rows_attr<4>()) || (e = set_rows_attr<8>()) ||
+      (e = set_few_attr()))
     return e;
   return cudaFuncSetAttribute(qdense_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
 }
 
 // The widened rows of the tensor-core path.
-size_t qdense_ws_bytes(int T, int K) { return T <= kQdRowsMax ? 0 : ((size_t)T * K * 2 + 255) / 256 * 256; }
+size_t qdense_ws_bytes(int T, int K) {
+  return T <= kQdRowsMax || few_fits(T, K) ? 0 : ((size_t)T * K * 2 + 255) / 256 * 256;
+}
 
+#ifndef QFMIN
+#define QFMIN 3
+#endif
 cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
+  if (a.T >= QFMIN && few_fits(a.T, a.K)) return launch_few(a, n_sm, st, pdl);
   if (a.T <= 1) return launch_rows_t<1>(a, n_sm, st, pdl);
   if (a.T <= 2) return launch_rows_t<2>(a, n_sm, st, pdl);
   if (a.T <= 4) return launch_rows_t<4>(a, n_sm, st, pdl);

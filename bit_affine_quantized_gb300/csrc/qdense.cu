@@ -495,6 +495,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   uint64_t *afull = rempty + P.rst, *aempty = afull + kMmABufs, *dfull = aempty + kMmABufs, *dempty = dfull + 2;
   uint64_t *tready = dempty + 2;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(tready + 1);
+  float *s_xs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bar) + kMmBarBytes);  // [256] row scales
   const bool tracer = blockIdx.x == 0 && tid == 0;
 
   if (tid == 0) {
@@ -635,33 +636,63 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     // one store instruction.
     bool ok = mm_wait(tready, 0);
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
-    const int rr = 32 * (warp & 3) + lane;
+    const int rr = 32 * (warp & 3) + lane, ft = tid - kMmFin0 * 32;
     float *partial = reinterpret_cast<float *>(base);  // [n][128], over the stages
     int du = 0;
-    for (int u = first; u < units && ok; u += stride, ++du) {
+    for (int u = first; u < units; u += stride, ++du) {
       const int n = u / P.ttile * kMmM + rr, t0 = u % P.ttile * P.n, cnt = min(P.n, a.T - t0);
       const int db = du % P.dbufs;
-      const float ws = split == 1 && n < a.N ? __ldg(a.ws + n) : 0.f;
-      ok = __all_sync(0xffffffffu, mm_wait(&dfull[db], (du / P.dbufs) & 1));
-      if (!ok) break;
-      dense::tc_fence_after();
-      const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + db * 128;
-      for (int c0 = 0; c0 < cnt; c0 += 16) {
-        float v[16];
-        dense::tc_ld16(ta + c0, v);
-        const float xl = split == 1 && lane < 16 && c0 + lane < cnt ? __ldcg(a.xs + t0 + c0 + lane) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float xs = __shfl_sync(0xffffffffu, xl, j);
-          if (split > 1)
-            partial[(c0 + j) * kMmM + rr] = v[j];
-          else if (c0 + j < cnt && n < a.N)
-            qd_put(a, t0 + c0 + j, n, v[j], xs, ws);
-        }
+      float ws = 0.f;
+      if (split == 1) {  // the tile's row scales to shared memory while its sums are made
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // every finish warp is done with the tile before
+        for (int i = ft; i < P.n; i += 128) s_xs[i] = i < cnt ? __ldcg(a.xs + t0 + i) : 0.f;
+        ws = n < a.N ? __ldg(a.ws + n) : 0.f;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
       }
-      dense::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&dempty[db], 0);
+      ok = __all_sync(0xffffffffu, ok && mm_wait(&dfull[db], (du / P.dbufs) & 1));
+      if (ok) {
+        dense::tc_fence_after();
+        const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + db * 128;
+        for (int c0 = 0; c0 < cnt; c0 += 32) {
+          float v[32];
+          dense::tc_ld32(ta + c0, v);  // (columns past the tile's: not used)
+          const int m = min(32, cnt - c0);
+          if (split > 1) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < m) partial[(c0 + j) * kMmM + rr] = v[j];
+          } else if (n < a.N) {
+            const size_t o = (size_t)(t0 + c0) * a.N + n;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 xs = *reinterpret_cast<const float4 *>(s_xs + c0 + j);
+              v[j] = __fmul_rn(__fmul_rn(v[j], xs.x), ws);
+              v[j + 1] = __fmul_rn(__fmul_rn(v[j + 1], xs.y), ws);
+              v[j + 2] = __fmul_rn(__fmul_rn(v[j + 2], xs.z), ws);
+              v[j + 3] = __fmul_rn(__fmul_rn(v[j + 3], xs.w), ws);
+            }
+            if (a.softcap > 0.f) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = a.softcap * tanhf(v[j] / a.softcap);
+            }
+            if (a.y32) {
+              float *p = a.y32 + o;
+#pragma unroll
+              for (int j = 0; j < 32; ++j, p += a.N)
+                if (j < m) *p = v[j];
+            }
+            if (a.y) {
+              uint16_t *p = a.y + o;
+#pragma unroll
+              for (int j = 0; j < 32; ++j, p += a.N)
+                if (j < m) *p = float_to_bf16_bits(v[j]);
+            }
+          }
+        }
+        dense::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&dempty[db], 0);
+      }
     }
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
   } else {
@@ -757,7 +788,7 @@ MmPlan mm_plan(int T, int N, int K, int n_sm) {
     if (p.split > kMmMaxSplit) p.split = kMmMaxSplit;
     if (p.split > nst) p.split = nst;
   }
-  p.smem = p.wst * kMmWStage + p.rst * p.n * 128 + kMmBarBytes + 1024;
+  p.smem = p.wst * kMmWStage + p.rst * p.n * 128 + kMmBarBytes + 1024 + 1024;
   return p;
 }
 

@@ -401,12 +401,15 @@ constexpr int kMmWts = kMmFin0 + 4;        // weights warp
 constexpr int kMmRows = kMmWts + 1;        // rows warp
 constexpr int kMmMma = kMmRows + 1;        // MMA warp
 constexpr int kMmThreads = (kMmMma + 1) * 32;
-constexpr int kMmABufs = 8;                // A tiles (32 tensor-memory columns of 128 x 64 fp16 each)
+constexpr int kMmK = 128;                  // K of a stage
+constexpr int kMmABufs = 4;                // A tiles in tensor memory (64 columns: 128 x 128 fp16)
 constexpr uint32_t kMmACol = 256;          // first column of the A tiles; the sums lie below
-constexpr int kMmWStage = kMmM * 128;      // bytes of a weight stage
+constexpr int kMmWStage = kMmM * kMmK;     // bytes of a weight stage
 constexpr int kMmMaxN = 256;
+constexpr int kMmSplitN = 128;             // rows per tile, at most, where a cluster shares a tile
 constexpr int kMmMaxSplit = 8;
 constexpr int kMmBarBytes = 512;
+constexpr int kMmXsBytes = kMmMaxN * 4;
 
 struct MmPlan {
   int n;            // rows per tile (the MMA N): a multiple of 16
@@ -443,6 +446,9 @@ __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity) {
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
 }
+__device__ __forceinline__ void mm_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
 
 // D (tensor memory) += A (tensor memory, 128 x 16) * B (shared memory, n x 16)^T
 __device__ __forceinline__ void mm_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -453,7 +459,8 @@ __device__ __forceinline__ void mm_mma(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 
-// 32 registers of each lane to 32 tensor-memory columns of the warp's lanes.
+// 32 registers of each lane to 32 tensor-memory columns of the warp's lanes
+// (complete after mm_st_wait).
 __device__ __forceinline__ void mm_st32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -463,8 +470,8 @@ __device__ __forceinline__ void mm_st32(uint32_t taddr, const uint32_t (&r)[32])
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void mm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -474,13 +481,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float cluster_ld(uint32_t addr, uint32_t rank) {
+// The address of this block's shared memory `addr` in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
   uint32_t at;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
+  return at;
 }
+__device__ __forceinline__ void cluster_st(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Rows per block of a shared tile.
+__host__ __device__ inline int mm_quota(const MmPlan &p) { return (p.n + p.split - 1) / p.split; }
 
 __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_constant__ MmParams prm) {
   extern __shared__ __align__(1024) uint8_t msm[];
@@ -488,35 +500,25 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   const MmPlan &P = prm.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *base = msm + ((1024u - (smem_addr(msm) & 1023u)) & 1023u);
-  const int rstage = P.n * 128;
+  const int rhalf = P.n * 128, rstage = 2 * rhalf;  // a rows stage: two halves of 64 of K
   uint8_t *wbuf = base, *rbuf = base + P.wst * kMmWStage;
   uint64_t *bar = reinterpret_cast<uint64_t *>(rbuf + P.rst * rstage);
   uint64_t *wfull = bar, *wempty = wfull + P.wst, *rfull = wempty + P.wst, *rempty = rfull + P.rst;
   uint64_t *afull = rempty + P.rst, *aempty = afull + kMmABufs, *dfull = aempty + kMmABufs, *dempty = dfull + 2;
   uint64_t *tready = dempty + 2;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(tready + 1);
-  float *s_xs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bar) + kMmBarBytes);  // [256] row scales
+  float *s_xs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bar) + kMmBarBytes);  // [n] row scales
+  float *s_part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(s_xs) + kMmXsBytes);  // [split][quota][128]
   const bool tracer = blockIdx.x == 0 && tid == 0;
 
-  if (tid == 0) {
-    for (int i = 0; i < P.wst; ++i) {
-      mbar_init(&wfull[i], 1);
-      mbar_init(&wempty[i], kMmWiden);
+  {
+    // arrivals per phase, in the order of the barriers
+    const int nb = 2 * P.wst + 2 * P.rst + 2 * kMmABufs + 5;
+    if (tid < nb) {
+      uint64_t *b = bar + tid;
+      mbar_init(b, b >= wempty && b < rfull ? kMmWiden : b >= afull && b < aempty ? kMmWiden : b >= dempty && b < tready ? 4 : 1);
+      fence_mbar_init();
     }
-    for (int i = 0; i < P.rst; ++i) {
-      mbar_init(&rfull[i], 1);
-      mbar_init(&rempty[i], 1);
-    }
-    for (int i = 0; i < kMmABufs; ++i) {
-      mbar_init(&afull[i], kMmWiden / 2);
-      mbar_init(&aempty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&dfull[i], 1);
-      mbar_init(&dempty[i], 4);
-    }
-    mbar_init(tready, 1);
-    fence_mbar_init();
   }
   __syncthreads();
   if (tracer) trace_min(a.trace, kTrEntry);
@@ -524,109 +526,107 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
 
   const int split = P.split;
   const int part = split > 1 ? (int)cluster_rank() : 0;
+  if (split > 1) cluster_sync_all();  // every block of the cluster runs: its shared memory can be written
   const int first = blockIdx.x / split, stride = gridDim.x / split;  // units of this block
   const int units = P.ntile * P.ttile;
-  // K in stages of 128; this block's part of them, and its 64-wide steps
-  const int nst = (a.K + 127) / 128, st0 = nst * part / split, st1 = nst * (part + 1) / split;
-  const int steps = min(2 * (st1 - st0), (a.K + 63) / 64 - 2 * st0);
+  const int nst = (a.K + kMmK - 1) / kMmK, st0 = nst * part / split, st1 = nst * (part + 1) / split;  // its part of K
   const uint32_t idesc = dense::idesc_f16(kMmM, P.n);
+  auto halves = [&](int s) { return a.K - s * kMmK > 64 ? 2 : 1; };  // 64-wide halves of stage s with codes
 
   if (warp == kMmWts) {
     // ============================================================ weights
-    // nothing that an earlier launch still writes is read here: the launch
-    // before this one (the widening of the rows) waited for those
-    bool ok = true;
-    int st = 0, ph = 0, issued = 0;
-    for (int u = first; u < units && ok; u += stride) {
-      const int n0 = u / P.ttile * kMmM;
-      for (int s = st0; s < st1 && ok; ++s, ++issued) {
-        if (issued >= P.wst) ok = __all_sync(0xffffffffu, mm_wait(&wempty[st], ph ^ 1));
-        if (!ok) break;
-        if (lane == 0) {
+    // Nothing that an earlier launch still writes is read here: the launch
+    // before this one (the widening of the rows) waited for those.
+    if (lane == 0) {
+      bool ok = true;
+      int st = 0, ph = 0, issued = 0;
+      for (int u = first; u < units && ok; u += stride) {
+        const int n0 = u / P.ttile * kMmM;
+        for (int s = st0; s < st1; ++s, ++issued) {
+          if (issued >= P.wst && !(ok = mm_wait(&wempty[st], ph ^ 1))) break;
           mbar_arrive_expect_tx(&wfull[st], kMmWStage);
-          dense::tma_load_2d(wbuf + st * kMmWStage, &prm.w, 128 * s, n0, &wfull[st]);
-        }
-        __syncwarp();
-        if (++st == P.wst) {
-          st = 0;
-          ph ^= 1;
+          dense::tma_load_2d(wbuf + st * kMmWStage, &prm.w, kMmK * s, n0, &wfull[st]);
+          if (++st == P.wst) {
+            st = 0;
+            ph ^= 1;
+          }
         }
       }
+      if (!ok) set_error(a.err, kErrTimeout);
+      // copies in flight land before the block's shared memory is released
+      for (int j = max(0, issued - P.wst); j < issued; ++j) mm_wait(&wfull[j % P.wst], (j / P.wst) & 1);
     }
-    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
-    // copies in flight land before the block's shared memory is released
-    for (int j = max(0, issued - P.wst); j < issued; ++j) mm_wait(&wfull[j % P.wst], (j / P.wst) & 1);
   } else if (warp == kMmRows) {
     // ============================================================ rows
     pdl_wait();  // the widened rows
     if (tracer) trace_min(a.trace, kTrWaited);
-    fused::fence_proxy_async_global();
-    bool ok = true;
-    int st = 0, ph = 0, issued = 0;
-    for (int u = first; u < units && ok; u += stride) {
-      const int t0 = u % P.ttile * P.n;
-      for (int g = 0; g < steps && ok; ++g, ++issued) {
-        if (issued >= P.rst) ok = __all_sync(0xffffffffu, mm_wait(&rempty[st], ph ^ 1));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&rfull[st], (uint32_t)rstage);
-          dense::tma_load_2d(rbuf + st * rstage, &prm.x, 128 * st0 + 64 * g, t0, &rfull[st]);
-        }
-        __syncwarp();
-        if (++st == P.rst) {
-          st = 0;
-          ph ^= 1;
+    if (lane == 0) {
+      fused::fence_proxy_async_global();
+      bool ok = true;
+      int st = 0, ph = 0, issued = 0;
+      for (int u = first; u < units && ok; u += stride) {
+        const int t0 = u % P.ttile * P.n;
+        for (int s = st0; s < st1; ++s, ++issued) {
+          if (issued >= P.rst && !(ok = mm_wait(&rempty[st], ph ^ 1))) break;
+          const int h = halves(s);
+          mbar_arrive_expect_tx(&rfull[st], (uint32_t)(h * rhalf));
+          for (int i = 0; i < h; ++i)
+            dense::tma_load_2d(rbuf + st * rstage + i * rhalf, &prm.x, kMmK * s + 64 * i, t0, &rfull[st]);
+          if (++st == P.rst) {
+            st = 0;
+            ph ^= 1;
+          }
         }
       }
+      if (!ok) set_error(a.err, kErrTimeout);
+      for (int j = max(0, issued - P.rst); j < issued; ++j) mm_wait(&rfull[j % P.rst], (j / P.rst) & 1);
     }
-    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
-    for (int j = max(0, issued - P.rst); j < issued; ++j) mm_wait(&rfull[j % P.rst], (j / P.rst) & 1);
   } else if (warp == kMmMma) {
     // ============================================================ MMA
     dense::tc_alloc(s_tmem, 512);
     dense::tc_fence_before();
     __syncwarp();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
-    if (lane == 0) mbar_arrive_expect_tx(tready, 0);
-    const uint64_t bdesc0 = dense::sdesc(smem_addr(rbuf), 16, 1024, 2);
-    bool ok = true;
-    int gi = 0, du = 0, st = 0, ph = 0, ab = 0, aph = 0;
-    for (int u = first; u < units && ok; u += stride) {
-      const int db = du % P.dbufs;
-      if (du >= P.dbufs) ok = __all_sync(0xffffffffu, mm_wait(&dempty[db], ((du / P.dbufs) - 1) & 1));
-      ++du;
-      dense::tc_fence_after();
-      const uint32_t acc = tmem + db * 128;
-      for (int g = 0; g < steps && ok; ++g, ++gi) {
-        ok = __all_sync(0xffffffffu, mm_wait(&rfull[st], ph) && mm_wait(&afull[ab], aph));
-        if (!ok) break;
-        dense::tc_fence_after();
-        if (lane == 0) {
+    if (lane == 0) {
+      mm_arrive(tready);
+      const uint64_t bdesc0 = dense::sdesc(smem_addr(rbuf), 16, 1024, 2);
+      bool ok = true;
+      int gi = 0, du = 0, st = 0, ph = 0, ab = 0, aph = 0;
+      for (int u = first; u < units && ok; u += stride) {
+        const int db = du % P.dbufs;
+        if (du >= P.dbufs && !(ok = mm_wait(&dempty[db], ((du / P.dbufs) - 1) & 1))) break;
+        ++du;
+        const uint32_t acc = tmem + db * 128;
+        for (int s = st0; s < st1; ++s, ++gi) {
+          if (!(ok = mm_wait(&rfull[st], ph) && mm_wait(&afull[ab], aph))) break;
+          dense::tc_fence_after();
           const uint64_t bd = bdesc0 + (uint64_t)((st * rstage) >> 4);
-          const uint32_t ad = tmem + kMmACol + 32 * ab;
+          const uint32_t ad = tmem + kMmACol + 64 * ab;
+          const int h = halves(s);
+          for (int i = 0; i < h; ++i)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)  // K = 16 per MMA: 8 columns of A, 32 bytes of B's rows
-            mm_mma(acc, ad + 8 * ks, bd + 2 * ks, idesc, (g > 0 || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < 4; ++ks)  // K = 16 per MMA: 8 columns of A, 32 bytes of B's rows
+              mm_mma(acc, ad + 32 * i + 8 * ks, bd + (uint64_t)((i * rhalf) >> 4) + 2 * ks, idesc,
+                     (s > st0 || i > 0 || ks > 0) ? 1u : 0u);
           dense::tc_commit(&rempty[st]);
           dense::tc_commit(&aempty[ab]);
-          if (g == steps - 1) dense::tc_commit(&dfull[db]);
-        }
-        __syncwarp();
-        if (++st == P.rst) {
-          st = 0;
-          ph ^= 1;
-        }
-        if (++ab == kMmABufs) {
-          ab = 0;
-          aph ^= 1;
+          if (s == st1 - 1) dense::tc_commit(&dfull[db]);
+          if (++st == P.rst) {
+            st = 0;
+            ph ^= 1;
+          }
+          if (++ab == kMmABufs) {
+            ab = 0;
+            aph ^= 1;
+          }
         }
       }
+      if (!ok) set_error(a.err, kErrTimeout);
+      // the last MMAs are complete and the sums read before the memory goes back (bounded waits)
+      if (gi > 0) mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1);
+      if (du > 0) mm_wait(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
+      dense::tc_fence_after();
     }
-    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
-    // the last MMAs are complete and the sums read before the memory goes back (bounded waits)
-    if (gi > 0) mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1);
-    if (du > 0) mm_wait(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
-    dense::tc_fence_after();
     __syncwarp();
     dense::tc_dealloc(tmem, 512);
   } else if (warp >= kMmFin0) {
@@ -637,7 +637,6 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     bool ok = mm_wait(tready, 0);
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
     const int rr = 32 * (warp & 3) + lane, ft = tid - kMmFin0 * 32;
-    float *partial = reinterpret_cast<float *>(base);  // [n][128], over the stages
     int du = 0;
     for (int u = first; u < units; u += stride, ++du) {
       const int n = u / P.ttile * kMmM + rr, t0 = u % P.ttile * P.n, cnt = min(P.n, a.T - t0);
@@ -653,63 +652,84 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       if (ok) {
         dense::tc_fence_after();
         const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + db * 128;
-        for (int c0 = 0; c0 < cnt; c0 += 32) {
-          float v[32];
-          dense::tc_ld32(ta + c0, v);  // (columns past the tile's: not used)
-          const int m = min(32, cnt - c0);
-          if (split > 1) {
+        if (split > 1) {
+          // rows o * quota .. of the tile are added up in block o of the cluster
+          const int quota = mm_quota(P);
+          for (int o = 0; o < split; ++o) {
+            const uint32_t to = cluster_map(smem_addr(s_part + (size_t)(part * quota) * kMmM + rr), o);
+            for (int c0 = 0; c0 < quota && o * quota + c0 < cnt; c0 += 16) {
+              float v[16];
+              dense::tc_ld16(ta + o * quota + c0, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < m) partial[(c0 + j) * kMmM + rr] = v[j];
-          } else if (n < a.N) {
-            const size_t o = (size_t)(t0 + c0) * a.N + n;
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 xs = *reinterpret_cast<const float4 *>(s_xs + c0 + j);
-              v[j] = __fmul_rn(__fmul_rn(v[j], xs.x), ws);
-              v[j + 1] = __fmul_rn(__fmul_rn(v[j + 1], xs.y), ws);
-              v[j + 2] = __fmul_rn(__fmul_rn(v[j + 2], xs.z), ws);
-              v[j + 3] = __fmul_rn(__fmul_rn(v[j + 3], xs.w), ws);
+              for (int j = 0; j < 16; ++j)
+                if (c0 + j < quota) cluster_st(to + (uint32_t)((c0 + j) * kMmM) * 4u, v[j]);
             }
-            if (a.softcap > 0.f) {
+          }
+        } else {
+          for (int c0 = 0; c0 < cnt; c0 += 32) {
+            float v[32];
+            dense::tc_ld32(ta + c0, v);  // (columns past the tile's: not used)
+            const int m = min(32, cnt - c0);
+            if (n < a.N) {
+              const size_t o = (size_t)(t0 + c0) * a.N + n;
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = a.softcap * tanhf(v[j] / a.softcap);
-            }
-            if (a.y32) {
-              float *p = a.y32 + o;
+              for (int j = 0; j < 32; j += 4) {
+                const float4 xs = *reinterpret_cast<const float4 *>(s_xs + c0 + j);
+                v[j] = __fmul_rn(__fmul_rn(v[j], xs.x), ws);
+                v[j + 1] = __fmul_rn(__fmul_rn(v[j + 1], xs.y), ws);
+                v[j + 2] = __fmul_rn(__fmul_rn(v[j + 2], xs.z), ws);
+                v[j + 3] = __fmul_rn(__fmul_rn(v[j + 3], xs.w), ws);
+              }
+              if (a.softcap > 0.f) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j, p += a.N)
-                if (j < m) *p = v[j];
-            }
-            if (a.y) {
-              uint16_t *p = a.y + o;
+                for (int j = 0; j < 32; ++j) v[j] = a.softcap * tanhf(v[j] / a.softcap);
+              }
+              if (a.y32) {
+                float *p = a.y32 + o;
 #pragma unroll
-              for (int j = 0; j < 32; ++j, p += a.N)
-                if (j < m) *p = float_to_bf16_bits(v[j]);
+                for (int j = 0; j < 32; ++j, p += a.N)
+                  if (j < m) *p = v[j];
+              }
+              if (a.y) {
+                uint16_t *p = a.y + o;
+#pragma unroll
+                for (int j = 0; j < 32; ++j, p += a.N)
+                  if (j < m) *p = float_to_bf16_bits(v[j]);
+              }
             }
           }
         }
         dense::tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&dempty[db], 0);
+        if (lane == 0) mm_arrive(&dempty[db]);
       }
     }
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
   } else {
     // ============================================================ widen
-    // Thread: channel rr of the tile; 64 of a stage's 128 codes.  Its 16-byte
-    // chunk j lies at j ^ (rr % 8) of the row (128-byte swizzle).
-    const int grp = warp >> 2, rr = 32 * (warp & 3) + lane, sw = rr & 7;
+    // Thread: channel rr of the tile, 64 of a stage's 128 codes.  Its 16-byte
+    // chunk j lies at j ^ (rr % 8) of the row (128-byte swizzle).  A stage's
+    // tile is announced one stage later, when its store into tensor memory is
+    // long complete.
+    const int half = warp >> 2, rr = 32 * (warp & 3) + lane, sw = rr & 7;
     bool ok = mm_wait(tready, 0);
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem) + ((uint32_t)(32 * (warp & 3)) << 16) + kMmACol;
-    int st = 0, ph = 0, gu = 0;  // weight stage; steps before this unit
+    const uint32_t tmem =
+        *reinterpret_cast<volatile uint32_t *>(s_tmem) + ((uint32_t)(32 * (warp & 3)) << 16) + kMmACol + 32 * half;
+    int st = 0, ph = 0, gi = 0, told = 0;
+    auto tell = [&]() {  // stage `told` is in tensor memory
+      mm_st_wait();
+      dense::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mm_arrive(&afull[told % kMmABufs]);
+      ++told;
+    };
     for (int u = first; u < units && ok; u += stride) {
-      for (int g = grp; g < 2 * (st1 - st0) && ok; g += 2) {
+      for (int s = st0; s < st1 && ok; ++s, ++gi) {
         ok = mm_wait(&wfull[st], ph);
         const uint8_t *row = wbuf + st * kMmWStage + rr * 128;
         uint4 c[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4 *>(row + (((4 * grp + j) ^ sw) << 4));
+        for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4 *>(row + (((4 * half + j) ^ sw) << 4));
         uint32_t o[32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -719,76 +739,76 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
           widen4(c[j].w, o[8 * j + 6], o[8 * j + 7]);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&wempty[st], 0);
+        if (lane == 0) mm_arrive(&wempty[st]);
         if (++st == P.wst) {
           st = 0;
           ph ^= 1;
         }
-        if (g < steps) {  // the last stage may hold one step only
-          const int gi = gu + g, ab = gi % kMmABufs;
-          if (gi >= kMmABufs) ok = ok && mm_wait(&aempty[ab], ((gi / kMmABufs) - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            dense::tc_fence_after();
-            mm_st32(tmem + 32 * ab, o);
-            dense::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&afull[ab], 0);
-          }
+        if (told < gi) tell();
+        const int ab = gi % kMmABufs;
+        if (gi >= kMmABufs) ok = ok && mm_wait(&aempty[ab], ((gi / kMmABufs) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          dense::tc_fence_after();
+          mm_st32(tmem + 64 * ab, o);
         }
       }
-      gu += steps;
+      // a unit's last stage is not kept waiting for the next unit's weights
+      if (ok && told < gi) tell();
     }
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
   }
 
   if (split > 1) {
-    // One tile per cluster: every block's sums lie in its shared memory; block
-    // r adds and stores every split-th row of the tile.
+    // One tile per cluster; the parts of this block's rows are here.
     __syncwarp();
     cluster_sync_all();
-    const int n0 = first / P.ttile * kMmM, t0 = first % P.ttile * P.n, cnt = min(P.n, a.T - t0);
-    // a warp per row, four channels per lane: 4 * split remote loads in flight
+    const int n0 = first / P.ttile * kMmM, t0 = first % P.ttile * P.n, cnt = min(P.n, a.T - t0), quota = mm_quota(P);
     float ws[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) ws[i] = n0 + lane + 32 * i < a.N ? __ldg(a.ws + n0 + lane + 32 * i) : 0.f;
-    for (int c = part + split * warp; c < cnt; c += split * (kMmThreads / 32)) {
-      const uint32_t at = smem_addr(base) + (uint32_t)(c * kMmM + lane) * 4u;
-      const float xs = __ldcg(a.xs + t0 + c);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f}, v[kMmMaxSplit][4];
+    for (int c = warp; c < quota && part * quota + c < cnt; c += kMmThreads / 32) {
+      const int t = t0 + part * quota + c;
+      const float xs = __ldcg(a.xs + t);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < split; ++r)  // in rank order
 #pragma unroll
-      for (int r = 0; r < kMmMaxSplit; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[r][i] = r < split ? cluster_ld(at + 128u * i, r) : 0.f;
-#pragma unroll
-      for (int r = 0; r < kMmMaxSplit; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += v[r][i];
+        for (int i = 0; i < 4; ++i) sum[i] += s_part[(size_t)(r * quota + c) * kMmM + lane + 32 * i];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (n0 + lane + 32 * i < a.N) qd_put(a, t0 + c, n0 + lane + 32 * i, sum[i], xs, ws[i]);
+        if (n0 + lane + 32 * i < a.N) qd_put(a, t, n0 + lane + 32 * i, sum[i], xs, ws[i]);
     }
-    cluster_sync_all();  // no block leaves while another reads its sums
   }
   if (tracer) trace_max(a.trace, kTrExit);
 }
 
 MmPlan mm_plan(int T, int N, int K, int n_sm) {
   MmPlan p;
-  p.ttile = (T + kMmMaxN - 1) / kMmMaxN;
-  p.n = ((T + p.ttile - 1) / p.ttile + 15) / 16 * 16;
+  auto tiles = [&](int most) {
+    p.ttile = (T + most - 1) / most;
+    p.n = ((T + p.ttile - 1) / p.ttile + 15) / 16 * 16;
+  };
   p.ntile = (N + kMmM - 1) / kMmM;
-  p.dbufs = p.n <= 128 ? 2 : 1;
-  p.wst = p.n <= 64 ? 10 : p.n <= 128 ? 7 : 5;
-  p.rst = p.n <= 128 ? 6 : 4;
-  const int units = p.ntile * p.ttile, nst = (K + 127) / 128;
   p.split = 1;
-  if (units * 2 <= n_sm) {
+  tiles(kMmMaxN);
+  const int nst = (K + kMmK - 1) / kMmK;
+  if (2 * p.ntile * p.ttile <= n_sm) {
+    tiles(kMmSplitN);
+    const int units = p.ntile * p.ttile;
     p.split = n_sm / units;
     if (p.split > kMmMaxSplit) p.split = kMmMaxSplit;
     if (p.split > nst) p.split = nst;
+    if (p.split < 1) p.split = 1;
   }
-  p.smem = p.wst * kMmWStage + p.rst * p.n * 128 + kMmBarBytes + 1024 + 1024;
+  p.dbufs = p.n <= 128 ? 2 : 1;
+  p.wst = p.n <= 64 ? 8 : 5;
+  p.rst = p.n <= 64 ? 4 : p.n <= 128 ? 3 : 2;
+  if (p.split > 1) {
+    p.wst = 5;
+    p.rst = 2;
+  }
+  p.smem = p.wst * kMmWStage + p.rst * p.n * 256 + kMmBarBytes + kMmXsBytes + 1024 +
+           (p.split > 1 ? p.split * mm_quota(p) * kMmM * 4 : 0);
   return p;
 }
 

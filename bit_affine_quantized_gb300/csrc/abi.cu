@@ -24,6 +24,7 @@ struct moe_handle {
   int prefill_key[4], prefill_ok;  // cached check (hidden, inter, n_experts, top_k) -> usable
   bool head_ready;            // the head kernel's attributes are set (first head call)
   bool qdense_ready;          // the same for the 8-bit projection's kernels
+  int qdense_clusters[moe::kQdenseMaxCluster + 1];  // clusters that fit the device, by their blocks
   bool logits_ready;          // and for the logits kernel
   bool prefill_dense;         // multi-token calls may run dense slots on the tensor cores (tcgen05)
   // failure-detection hook, consumed by the next fused single-token launch
@@ -883,7 +884,7 @@ int moe_qdense_forward(moe_handle *h, const int8_t *x, const float *x_scales, in
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   }
   if (!h->qdense_ready) {
-    if (moe::qdense_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    if (moe::qdense_set_attributes(h->qdense_clusters) != cudaSuccess) return MOE_ERR_CUDA;
     h->qdense_ready = true;
   }
   moe::QdenseArgs a;
@@ -900,7 +901,7 @@ int moe_qdense_forward(moe_handle *h, const int8_t *x, const float *x_scales, in
   a.K = w->width;
   a.err = h->dwords;
   a.trace = take_trace(h, need ? 2 : 1);
-  return cuda_status(moe::launch_qdense(a, h->n_sm, (cudaStream_t)stream, h->pdl));
+  return cuda_status(moe::launch_qdense(a, h->n_sm, h->qdense_clusters, (cudaStream_t)stream, h->pdl));
 }
 
 int moe_logits_process(moe_handle *h, const float *logits, size_t logits_stride, int n_rows, int vocab,

@@ -254,8 +254,11 @@ struct QdenseArgs {
   unsigned long long *trace;
 };
 size_t qdense_ws_bytes(int T, int K);
-cudaError_t qdense_set_attributes();
-cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl);
+constexpr int kQdenseMaxCluster = 8;
+// clusters[s], s <= kQdenseMaxCluster: clusters of s blocks of the tensor-core
+// kernel that the device holds at once
+cudaError_t qdense_set_attributes(int *clusters);
+cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, const int *clusters, cudaStream_t st, bool pdl);
 
 // smem budgets (bytes) for a given shape; 0 = shape not supported by that kernel
 size_t router_smem(const Dims &d, int tb);

@@ -3,11 +3,18 @@
 //
 //   y[t, n] = cap(xs[t] * ws[n] * sum_k x[t, k] w[n, k]),  cap(z) = c tanh(z / c) or z
 //
-// qdense_rows_kernel: up to 8 rows per block row of the grid.  A warp takes
-// kR channels; each lane loads 16 bytes of every channel's row (one 512-byte
-// run per warp and channel) and multiplies them with the rows' codes in
-// shared memory by dp4a, so the sums are exact 32-bit integers (at most
-// 128 * 128 * 16384 = 2^28 in magnitude).
+// qdense_rows_kernel: one or two rows (and up to 8 that the next kernel has no
+// room for).  A warp takes kR channels; each lane loads 16 bytes of every
+// channel's row (one 512-byte run per warp and channel) and multiplies them
+// with the rows' codes in shared memory by dp4a, so the sums are exact 32-bit
+// integers (at most 128 * 128 * 16384 = 2^28 in magnitude).  HBM bound: 1 x
+// 262144 x 2816 in 107 us, 6.9 TB/s of codes; 1 x 4096 x 2816 in 3.3 us.
+//
+// qdense_few_kernel: 3 to 16 rows, mma.sync with the codes widened to fp16 in
+// registers on their way from global memory; the fp32 sums go to integers
+// every 1024 of K, so they stay exact.  Up to 8 rows HBM bound (8 x 262144 x
+// 2816: 117 us; dp4a took 186), from 9 to 16 by mma.sync's rate (155 us; 24
+// rows would take 186, no less than the next kernel).
 //
 // qdense_mma_kernel: more rows, on the 5th-generation tensor cores.  sm_103a
 // has no 8-bit integer form of tcgen05.mma; 8-bit codes are exact in fp16, so
@@ -16,15 +23,22 @@
 // qdense_widen_kernel; the matrix, the larger operand, is read as 8-bit codes
 // and widened on its way into the tensor cores:
 //   weights warp   TMA: 128 channels x 128 codes per stage
-//   rows warp      TMA: up to 256 rows x 64 fp16 per stage
-//   8 widen warps  a channel per thread: 64 codes from shared memory to fp16
-//                  pairs in registers to the A operand in tensor memory (two
-//                  groups of 4 warps take alternate 64-wide steps)
+//   rows warp      TMA: up to 256 rows x 128 fp16 per stage
+//   8 widen warps  a channel per thread and half stage: 64 codes from shared
+//                  memory to fp16 pairs in registers to the A operand in
+//                  tensor memory
 //   MMA warp       tcgen05.mma, M = 128 channels (A in tensor memory),
 //                  N = rows (B in shared memory), fp32 sums in tensor memory
-//   4 finish warps the sums times both scales, the softcap, the store
+//   8 finish warps the sums times both scales, the softcap, the store
 // A in tensor memory keeps the widened codes out of shared memory, whose
-// bandwidth is what a 128 x 256 fp16 tile asks most of.
+// bandwidth is what a 128 x 256 fp16 tile asks most of.  The A tile then
+// costs each MMA (K = 16) about 120 cycles up to 128 rows and 156 at 256, so
+// 17 to 128 rows are bound by that (24 x 262144 x 2816: 186 us, 117 us with
+// the MMAs left out) and many rows by it and the rows' way into shared memory
+// (4096 x 4096 x 2816: 77 us, 1230 TFLOP/s; a library product of fp16 operands
+// takes 53 us on such integers, 60 us on random values).  Forms that were
+// slower: A widened into shared memory (24 rows: 203 us) and pairs of blocks
+// on one tile (91 us).
 // Few tiles: the blocks of a cluster share a tile, each takes a part of K, and
 // the parts are added through distributed shared memory in rank order.
 #include <cuda.h>
@@ -42,7 +56,7 @@ namespace {
 constexpr int kQdWarps = 8;
 constexpr int kQdThreads = kQdWarps * 32;
 constexpr int kQdRowsMax = 8;   // rows that the dp4a kernel takes
-constexpr int kQdFewMax = 32;   // rows that the mma.sync kernel takes, where they fit
+constexpr int kQdFewMax = 16;   // rows that the mma.sync kernel takes, where they fit
 
 __device__ __forceinline__ int4 qd_stream(const int8_t *p) {
   int4 v;
@@ -145,24 +159,18 @@ cudaError_t launch_rows(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl
                   pdl, a);
 }
 
-#ifndef QA1
-#define QA1 6
-#endif
-#ifndef QA4
-#define QA4 3
-#endif
 template <int kT>
 cudaError_t launch_rows_t(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
-  if (a.N >= 4 * kQdWarps * 4 * n_sm) return launch_rows<kT, 4, QA4>(a, n_sm, st, pdl);
-  return launch_rows<kT, 1, QA1>(a, n_sm, st, pdl);
+  if (a.N >= 4 * kQdWarps * 4 * n_sm) return launch_rows<kT, 4, 3>(a, n_sm, st, pdl);
+  return launch_rows<kT, 1, 6>(a, n_sm, st, pdl);
 }
 
 template <int kT>
 cudaError_t set_rows_attr() {
-  cudaError_t e = cudaFuncSetAttribute(qdense_rows_kernel<kT, 4, QA4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(qdense_rows_kernel<kT, 4, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kT * kQdenseMaxK);
   if (e) return e;
-  return cudaFuncSetAttribute(qdense_rows_kernel<kT, 1, QA1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(qdense_rows_kernel<kT, 1, 6>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kT * kQdenseMaxK);
 }
 
@@ -351,22 +359,13 @@ bool few_fits(int T, int K) {
 }
 
 cudaError_t launch_few(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
-  switch ((a.T + 7) / 8) {
-    case 1: return launch_few_n<1>(a, n_sm, st, pdl);
-    case 2: return launch_few_n<2>(a, n_sm, st, pdl);
-    case 3: return launch_few_n<3>(a, n_sm, st, pdl);
-    default: return launch_few_n<4>(a, n_sm, st, pdl);
-  }
+  return a.T <= 8 ? launch_few_n<1>(a, n_sm, st, pdl) : launch_few_n<2>(a, n_sm, st, pdl);
 }
 
 cudaError_t set_few_attr() {
   const cudaFuncAttribute f = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e;
-  if ((e = cudaFuncSetAttribute(qdense_few_kernel<1>, f, (int)kQfSmemMax)) ||
-      (e = cudaFuncSetAttribute(qdense_few_kernel<2>, f, (int)kQfSmemMax)) ||
-      (e = cudaFuncSetAttribute(qdense_few_kernel<3>, f, (int)kQfSmemMax)))
-    return e;
-  return cudaFuncSetAttribute(qdense_few_kernel<4>, f, (int)kQfSmemMax);
+  const cudaError_t e = cudaFuncSetAttribute(qdense_few_kernel<1>, f, (int)kQfSmemMax);
+  return e ? e : cudaFuncSetAttribute(qdense_few_kernel<2>, f, (int)kQfSmemMax);
 }
 
 // ------------------------------------------------------------------ rows to fp16
@@ -396,8 +395,9 @@ __global__ void __launch_bounds__(kWidenThreads) qdense_widen_kernel(const Qdens
 // ------------------------------------------------------------------ tensor cores
 constexpr int kMmM = 128;                  // channels per tile
 constexpr int kMmWiden = 8;                // widen warps
-constexpr int kMmFin0 = kMmWiden;          // 4 finish warps
-constexpr int kMmWts = kMmFin0 + 4;        // weights warp
+constexpr int kMmFin0 = kMmWiden;
+constexpr int kMmFin = 8;                  // finish warps
+constexpr int kMmWts = kMmFin0 + kMmFin;   // weights warp
 constexpr int kMmRows = kMmWts + 1;        // rows warp
 constexpr int kMmMma = kMmRows + 1;        // MMA warp
 constexpr int kMmThreads = (kMmMma + 1) * 32;
@@ -407,7 +407,7 @@ constexpr uint32_t kMmACol = 256;          // first column of the A tiles; the s
 constexpr int kMmWStage = kMmM * kMmK;     // bytes of a weight stage
 constexpr int kMmMaxN = 256;
 constexpr int kMmSplitN = 128;             // rows per tile, at most, where a cluster shares a tile
-constexpr int kMmMaxSplit = 8;
+constexpr int kMmMaxSplit = kQdenseMaxCluster;
 constexpr int kMmBarBytes = 512;
 constexpr int kMmXsBytes = kMmMaxN * 4;
 
@@ -417,15 +417,32 @@ struct MmPlan {
   int dbufs;        // sets of sums in tensor memory
   int split;        // blocks of a cluster that share a tile along K
   int ntile, ttile; // tiles of channels, of rows
+  int whole, units; // units of work: `whole` tiles, then halves of tiles (by rows)
   int smem;
 };
 
 struct MmParams {
-  CUtensorMap w;    // 8-bit codes {K, N}, box {128, 128}, 128-byte swizzle
-  CUtensorMap x;    // fp16 rows {K, T}, box {64, n}, 128-byte swizzle
+  CUtensorMap w;     // 8-bit codes {K, N}, box {128, 128}, 128-byte swizzle
+  CUtensorMap x[2];  // fp16 rows {K, T}, box {64, n} and {64, n / 2}, 128-byte swizzle
   QdenseArgs a;
   MmPlan p;
 };
+
+// A unit's place: first channel, first row, rows (the MMA N) and how many of
+// them there are.
+struct MmUnit {
+  int n0, t0, n, cnt, half;
+};
+__device__ __forceinline__ MmUnit mm_unit(const MmPlan &p, int T, int u) {
+  MmUnit q;
+  q.half = u >= p.whole ? 1 : 0;
+  const int tile = q.half ? p.whole + (u - p.whole) / 2 : u;
+  q.n = q.half ? p.n / 2 : p.n;
+  q.n0 = tile / p.ttile * kMmM;
+  q.t0 = tile % p.ttile * p.n + (q.half ? ((u - p.whole) & 1) * q.n : 0);
+  q.cnt = min(q.n, T - q.t0);  // none: a half past the last row, which every warp passes over
+  return q;
+}
 
 // Bounded wait that suspends in hardware; the timer is read only once a wait
 // is not over at its first look (reading it costs more than most waits).
@@ -491,7 +508,7 @@ __device__ __forceinline__ void cluster_st(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// Rows per block of a shared tile.
+// Rows of a shared tile that one block of the cluster adds up.
 __host__ __device__ inline int mm_quota(const MmPlan &p) { return (p.n + p.split - 1) / p.split; }
 
 __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_constant__ MmParams prm) {
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     const int nb = 2 * P.wst + 2 * P.rst + 2 * kMmABufs + 5;
     if (tid < nb) {
       uint64_t *b = bar + tid;
-      mbar_init(b, b >= wempty && b < rfull ? kMmWiden : b >= afull && b < aempty ? kMmWiden : b >= dempty && b < tready ? 4 : 1);
+      mbar_init(b, b >= wempty && b < rfull ? kMmWiden : b >= afull && b < aempty ? kMmWiden : b >= dempty && b < tready ? kMmFin : 1);
       fence_mbar_init();
     }
   }
@@ -528,9 +545,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   const int part = split > 1 ? (int)cluster_rank() : 0;
   if (split > 1) cluster_sync_all();  // every block of the cluster runs: its shared memory can be written
   const int first = blockIdx.x / split, stride = gridDim.x / split;  // units of this block
-  const int units = P.ntile * P.ttile;
+  const int units = P.units;
   const int nst = (a.K + kMmK - 1) / kMmK, st0 = nst * part / split, st1 = nst * (part + 1) / split;  // its part of K
-  const uint32_t idesc = dense::idesc_f16(kMmM, P.n);
   auto halves = [&](int s) { return a.K - s * kMmK > 64 ? 2 : 1; };  // 64-wide halves of stage s with codes
 
   if (warp == kMmWts) {
@@ -541,11 +557,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       bool ok = true;
       int st = 0, ph = 0, issued = 0;
       for (int u = first; u < units && ok; u += stride) {
-        const int n0 = u / P.ttile * kMmM;
+        const MmUnit q = mm_unit(P, a.T, u);
+        if (q.cnt <= 0) continue;
         for (int s = st0; s < st1; ++s, ++issued) {
           if (issued >= P.wst && !(ok = mm_wait(&wempty[st], ph ^ 1))) break;
           mbar_arrive_expect_tx(&wfull[st], kMmWStage);
-          dense::tma_load_2d(wbuf + st * kMmWStage, &prm.w, kMmK * s, n0, &wfull[st]);
+          dense::tma_load_2d(wbuf + st * kMmWStage, &prm.w, kMmK * s, q.n0, &wfull[st]);
           if (++st == P.wst) {
             st = 0;
             ph ^= 1;
@@ -565,13 +582,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       bool ok = true;
       int st = 0, ph = 0, issued = 0;
       for (int u = first; u < units && ok; u += stride) {
-        const int t0 = u % P.ttile * P.n;
+        const MmUnit q = mm_unit(P, a.T, u);
+        if (q.cnt <= 0) continue;
         for (int s = st0; s < st1; ++s, ++issued) {
           if (issued >= P.rst && !(ok = mm_wait(&rempty[st], ph ^ 1))) break;
           const int h = halves(s);
-          mbar_arrive_expect_tx(&rfull[st], (uint32_t)(h * rhalf));
+          mbar_arrive_expect_tx(&rfull[st], (uint32_t)(h * q.n * 128));
           for (int i = 0; i < h; ++i)
-            dense::tma_load_2d(rbuf + st * rstage + i * rhalf, &prm.x, kMmK * s + 64 * i, t0, &rfull[st]);
+            dense::tma_load_2d(rbuf + st * rstage + i * rhalf, &prm.x[q.half], kMmK * s + 64 * i, q.t0, &rfull[st]);
           if (++st == P.rst) {
             st = 0;
             ph ^= 1;
@@ -593,6 +611,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       bool ok = true;
       int gi = 0, du = 0, st = 0, ph = 0, ab = 0, aph = 0;
       for (int u = first; u < units && ok; u += stride) {
+        const MmUnit q = mm_unit(P, a.T, u);
+        if (q.cnt <= 0) continue;
+        const uint32_t idesc = dense::idesc_f16(kMmM, q.n);
         const int db = du % P.dbufs;
         if (du >= P.dbufs && !(ok = mm_wait(&dempty[db], ((du / P.dbufs) - 1) & 1))) break;
         ++du;
@@ -631,78 +652,82 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     dense::tc_dealloc(tmem, 512);
   } else if (warp >= kMmFin0) {
     // ============================================================ finish
-    // Warp w reads tensor-memory lanes 32 (w % 4) .. +31: channels n0 + rr.
-    // A register per lane and column: 32 neighbouring channels of one row are
-    // one store instruction.
+    // Warp w reads tensor-memory lanes 32 (w % 4) .. +31: channels n0 + rr; the
+    // two warps of a lane quarter take turns at pieces of 32 columns.  A
+    // register per lane and column: 32 neighbouring channels of one row are one
+    // store instruction.
     bool ok = mm_wait(tready, 0);
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
-    const int rr = 32 * (warp & 3) + lane, ft = tid - kMmFin0 * 32;
+    const int rr = 32 * (warp & 3) + lane, ft = tid - kMmFin0 * 32, side = (warp - kMmFin0) >> 2;
     int du = 0;
-    for (int u = first; u < units; u += stride, ++du) {
-      const int n = u / P.ttile * kMmM + rr, t0 = u % P.ttile * P.n, cnt = min(P.n, a.T - t0);
+    for (int u = first; u < units; u += stride) {
+      const MmUnit q = mm_unit(P, a.T, u);
+      if (q.cnt <= 0) continue;
+      const int n = q.n0 + rr, t0 = q.t0, cnt = q.cnt;
       const int db = du % P.dbufs;
       float ws = 0.f;
       if (split == 1) {  // the tile's row scales to shared memory while its sums are made
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // every finish warp is done with the tile before
-        for (int i = ft; i < P.n; i += 128) s_xs[i] = i < cnt ? __ldcg(a.xs + t0 + i) : 0.f;
+        asm volatile("bar.sync 1, %0;" ::"n"(kMmFin * 32) : "memory");  // every finish warp is done with the tile before
+        for (int i = ft; i < q.n; i += kMmFin * 32) s_xs[i] = i < cnt ? __ldcg(a.xs + t0 + i) : 0.f;
         ws = n < a.N ? __ldg(a.ws + n) : 0.f;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kMmFin * 32) : "memory");
       }
       ok = __all_sync(0xffffffffu, ok && mm_wait(&dfull[db], (du / P.dbufs) & 1));
-      if (ok) {
-        dense::tc_fence_after();
-        const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + db * 128;
-        if (split > 1) {
-          // rows o * quota .. of the tile are added up in block o of the cluster
-          const int quota = mm_quota(P);
-          for (int o = 0; o < split; ++o) {
-            const uint32_t to = cluster_map(smem_addr(s_part + (size_t)(part * quota) * kMmM + rr), o);
-            for (int c0 = 0; c0 < quota && o * quota + c0 < cnt; c0 += 16) {
-              float v[16];
-              dense::tc_ld16(ta + o * quota + c0, v);
+      dense::tc_fence_after();
+      const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + db * 128;
+      if (split > 1) {
+        // rows o * quota .. of the tile are added up in block o of the cluster
+        // (a lane per channel: 128 bytes a store; 16 bytes per lane in rows of a
+        // padded pitch took half as long again)
+        const int quota = mm_quota(P);
+        for (int o = side; ok && o * quota < cnt; o += kMmFin / 4) {
+          const uint32_t to = cluster_map(smem_addr(s_part + (size_t)(part * quota) * kMmM + rr), o);
+          for (int c0 = 0; c0 < quota; c0 += 16) {
+            float v[16];
+            dense::tc_ld16(ta + o * quota + c0, v);  // (columns past the tile's: not used)
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (c0 + j < quota) cluster_st(to + (uint32_t)((c0 + j) * kMmM) * 4u, v[j]);
-            }
+            for (int j = 0; j < 16; ++j)
+              if (c0 + j < quota) cluster_st(to + (uint32_t)((c0 + j) * kMmM) * 4u, v[j]);
           }
-        } else {
-          for (int c0 = 0; c0 < cnt; c0 += 32) {
-            float v[32];
-            dense::tc_ld32(ta + c0, v);  // (columns past the tile's: not used)
-            const int m = min(32, cnt - c0);
-            if (n < a.N) {
-              const size_t o = (size_t)(t0 + c0) * a.N + n;
+        }
+      } else {
+        for (int c0 = 32 * side; ok && c0 < cnt; c0 += 8 * kMmFin) {
+          float v[32];
+          dense::tc_ld32(ta + c0, v);  // (columns past the tile's: not used)
+          const int m = min(32, cnt - c0);
+          if (n < a.N) {
+            const size_t o = (size_t)(t0 + c0) * a.N + n;
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 xs = *reinterpret_cast<const float4 *>(s_xs + c0 + j);
-                v[j] = __fmul_rn(__fmul_rn(v[j], xs.x), ws);
-                v[j + 1] = __fmul_rn(__fmul_rn(v[j + 1], xs.y), ws);
-                v[j + 2] = __fmul_rn(__fmul_rn(v[j + 2], xs.z), ws);
-                v[j + 3] = __fmul_rn(__fmul_rn(v[j + 3], xs.w), ws);
-              }
-              if (a.softcap > 0.f) {
+            for (int j = 0; j < 32; j += 4) {
+              const float4 xs = *reinterpret_cast<const float4 *>(s_xs + c0 + j);
+              v[j] = __fmul_rn(__fmul_rn(v[j], xs.x), ws);
+              v[j + 1] = __fmul_rn(__fmul_rn(v[j + 1], xs.y), ws);
+              v[j + 2] = __fmul_rn(__fmul_rn(v[j + 2], xs.z), ws);
+              v[j + 3] = __fmul_rn(__fmul_rn(v[j + 3], xs.w), ws);
+            }
+            if (a.softcap > 0.f) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = a.softcap * tanhf(v[j] / a.softcap);
-              }
-              if (a.y32) {
-                float *p = a.y32 + o;
+              for (int j = 0; j < 32; ++j) v[j] = a.softcap * tanhf(v[j] / a.softcap);
+            }
+            if (a.y32) {
+              float *p = a.y32 + o;
 #pragma unroll
-                for (int j = 0; j < 32; ++j, p += a.N)
-                  if (j < m) *p = v[j];
-              }
-              if (a.y) {
-                uint16_t *p = a.y + o;
+              for (int j = 0; j < 32; ++j, p += a.N)
+                if (j < m) *p = v[j];
+            }
+            if (a.y) {
+              uint16_t *p = a.y + o;
 #pragma unroll
-                for (int j = 0; j < 32; ++j, p += a.N)
-                  if (j < m) *p = float_to_bf16_bits(v[j]);
-              }
+              for (int j = 0; j < 32; ++j, p += a.N)
+                if (j < m) *p = float_to_bf16_bits(v[j]);
             }
           }
         }
-        dense::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mm_arrive(&dempty[db]);
       }
+      dense::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mm_arrive(&dempty[db]);
+      ++du;
     }
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
   } else {
@@ -724,6 +749,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       ++told;
     };
     for (int u = first; u < units && ok; u += stride) {
+      if (mm_unit(P, a.T, u).cnt <= 0) continue;
       for (int s = st0; s < st1 && ok; ++s, ++gi) {
         ok = mm_wait(&wfull[st], ph);
         const uint8_t *row = wbuf + st * kMmWStage + rr * 128;
@@ -760,29 +786,55 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   }
 
   if (split > 1) {
-    // One tile per cluster; the parts of this block's rows are here.
+    // One tile per cluster; this block adds the parts of its rows, a warp to a
+    // row, four channels per lane.
     __syncwarp();
-    cluster_sync_all();
-    const int n0 = first / P.ttile * kMmM, t0 = first % P.ttile * P.n, cnt = min(P.n, a.T - t0), quota = mm_quota(P);
+    const MmUnit q = mm_unit(P, a.T, first);
+    const int n0 = q.n0, t0 = q.t0, cnt = q.cnt;
+    const int quota = mm_quota(P), r0 = part * quota, mine = min(quota, cnt - r0);
     float ws[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) ws[i] = n0 + lane + 32 * i < a.N ? __ldg(a.ws + n0 + lane + 32 * i) : 0.f;
-    for (int c = warp; c < quota && part * quota + c < cnt; c += kMmThreads / 32) {
-      const int t = t0 + part * quota + c;
-      const float xs = __ldcg(a.xs + t);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int r = 0; r < split; ++r)  // in rank order
+    const float xl = lane < mine ? __ldcg(a.xs + t0 + r0 + lane) : 0.f;  // scales of rows lane, lane + 32
+    const float xh = lane + 32 < mine ? __ldcg(a.xs + t0 + r0 + lane + 32) : 0.f;
+    __syncwarp();
+    cluster_sync_all();
+    for (int c = warp; c < mine; c += kMmThreads / 32) {
+      const float xs = __shfl_sync(0xffffffffu, c < 32 ? xl : xh, c & 31);
+      float v[kMmMaxSplit][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += s_part[(size_t)(r * quota + c) * kMmM + lane + 32 * i];
+      for (int r = 0; r < kMmMaxSplit; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n0 + lane + 32 * i < a.N) qd_put(a, t, n0 + lane + 32 * i, sum[i], xs, ws[i]);
+        for (int i = 0; i < 4; ++i)
+          v[r][i] = r < split ? s_part[(size_t)(r * quota + c) * kMmM + lane + 32 * i] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float sum = v[0][i];
+#pragma unroll
+        for (int r = 1; r < kMmMaxSplit; ++r) sum += v[r][i];  // in rank order
+        if (n0 + lane + 32 * i < a.N) qd_put(a, t0 + r0 + c, n0 + lane + 32 * i, sum, xs, ws[i]);
+      }
     }
   }
   if (tracer) trace_max(a.trace, kTrExit);
 }
 
-MmPlan mm_plan(int T, int N, int K, int n_sm) {
+// Tiles of up to 256 rows where they fill the device: an MMA with A in tensor
+// memory takes about as long for 128 rows as for fewer, and for 256 not twice
+// as long (a 128-wide K stage: 0.55 us up to 128 rows, 0.86 us at 256), so
+// more rows per tile are better while every SM has a tile.
+//
+// Fewer tiles than half the SMs: up to 128 rows per tile, and a cluster of
+// `split` blocks per tile if that pays: the stages go down by the factor, the
+// exchange of the parts costs 1.3 us + 13 ns per row of the tile, 0.8 us more
+// for clusters of over four blocks (128 x 2816 x 4096, clusters of 1, 2, 3, 4,
+// 6: 22.0, 16.4, 13.8, 11.8, 12.1 us; 333 x 1411 x 1072, 1 .. 4: 9.8, 10.0,
+// 9.1, 9.8).  clusters[s]: clusters of s blocks that the device holds at once
+// (more than those would run in a second wave: 16 tiles in clusters of 8 took
+// 15.7 us, in clusters of 4 10.4).
+//
+// The last round of tiles, if at most half the SMs have one: in halves.
+MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   MmPlan p;
   auto tiles = [&](int most) {
     p.ttile = (T + most - 1) / most;
@@ -794,36 +846,44 @@ MmPlan mm_plan(int T, int N, int K, int n_sm) {
   const int nst = (K + kMmK - 1) / kMmK;
   if (2 * p.ntile * p.ttile <= n_sm) {
     tiles(kMmSplitN);
-    const int units = p.ntile * p.ttile;
-    p.split = n_sm / units;
-    if (p.split > kMmMaxSplit) p.split = kMmMaxSplit;
-    if (p.split > nst) p.split = nst;
-    if (p.split < 1) p.split = 1;
+    double least = 0.55 * nst;
+    for (int s = 2; s <= kMmMaxSplit && s <= nst; ++s) {
+      const double t = 0.55 * ((nst + s - 1) / s) + 1.3 + 0.013 * p.n + (s > 4 ? 0.8 : 0.0);
+      if (p.ntile * p.ttile <= clusters[s] && t < least) {
+        least = t;
+        p.split = s;
+      }
+    }
+  }
+  p.whole = p.ntile * p.ttile;
+  p.units = p.whole;
+  const int rest = p.whole % n_sm;
+  if (p.whole > n_sm && rest > 0 && 2 * rest <= n_sm && p.n > 128) {
+    p.n = (p.n + 31) / 32 * 32;
+    p.whole -= rest;
+    p.units = p.whole + 2 * rest;
   }
   p.dbufs = p.n <= 128 ? 2 : 1;
-  p.wst = p.n <= 64 ? 8 : 5;
-  p.rst = p.n <= 64 ? 4 : p.n <= 128 ? 3 : 2;
-  if (p.split > 1) {
-    p.wst = 5;
-    p.rst = 2;
-  }
+  p.wst = 5;
+  p.rst = p.n > 128 || p.split > 1 ? 2 : 3;
   p.smem = p.wst * kMmWStage + p.rst * p.n * 256 + kMmBarBytes + kMmXsBytes + 1024 +
            (p.split > 1 ? p.split * mm_quota(p) * kMmM * 4 : 0);
   return p;
 }
 
-cudaError_t launch_mma(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
+cudaError_t launch_mma(const QdenseArgs &a, int n_sm, const int *clusters, cudaStream_t st, bool pdl) {
   const EncodeTiledFn f = encode_tiled();
   if (!f) return cudaErrorNotSupported;
   MmParams prm;
   memset(&prm, 0, sizeof(prm));
   prm.a = a;
-  const MmPlan &p = prm.p = mm_plan(a.T, a.N, a.K, n_sm);
+  const MmPlan &p = prm.p = mm_plan(a.T, a.N, a.K, n_sm, clusters);
   const cuuint64_t dw[2] = {(cuuint64_t)a.K, (cuuint64_t)a.N}, sw[1] = {(cuuint64_t)a.K};
   const cuuint64_t dx[2] = {(cuuint64_t)a.K, (cuuint64_t)a.T}, sx[1] = {(cuuint64_t)a.K * 2};
-  const cuuint32_t bw[2] = {128, kMmM}, bx[2] = {64, (cuuint32_t)p.n};
+  const cuuint32_t bw[2] = {128, kMmM}, bx[2] = {64, (cuuint32_t)p.n}, by[2] = {64, (cuuint32_t)p.n / 2};
   if (!encode_map(f, &prm.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.w, dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(f, &prm.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B))
+      !encode_map(f, &prm.x[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_map(f, &prm.x[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, by, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const size_t pieces = (size_t)a.T * (a.K / 16), blocks = (pieces + kWidenThreads - 1) / kWidenThreads;
   const size_t most = (size_t)n_sm * 8;
@@ -831,7 +891,7 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl)
                            st, pdl, a);
   if (e != cudaSuccess) return e;
   if (prm.a.trace) prm.a.trace += 4;
-  const int units = p.ntile * p.ttile;
+  const int units = p.units;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.split > 1 ? units * p.split : (units < n_sm ? units : n_sm));
   cfg.blockDim = dim3(kMmThreads);
@@ -855,12 +915,29 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl)
 }
 }  // namespace
 
-cudaError_t qdense_set_attributes() {
+cudaError_t qdense_set_attributes(int *clusters) {
   cudaError_t e;
   if ((e = set_rows_attr<1>()) || (e = set_rows_attr<2>()) || (e = set_rows_attr<4>()) || (e = set_rows_attr<8>()) ||
-      (e = set_few_attr()))
+      (e = set_few_attr()) ||
+      (e = cudaFuncSetAttribute(qdense_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)))
     return e;
-  return cudaFuncSetAttribute(qdense_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  for (int s = 0; s <= kQdenseMaxCluster; ++s) {
+    clusters[s] = 0;
+    if (s < 2) continue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s);
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = 227 * 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters[s], qdense_mma_kernel, &cfg))) return e;
+  }
+  return cudaSuccess;
 }
 
 // The widened rows of the tensor-core path.
@@ -868,16 +945,13 @@ size_t qdense_ws_bytes(int T, int K) {
   return T <= kQdRowsMax || few_fits(T, K) ? 0 : ((size_t)T * K * 2 + 255) / 256 * 256;
 }
 
-#ifndef QFMIN
-#define QFMIN 3
-#endif
-cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
-  if (a.T >= QFMIN && few_fits(a.T, a.K)) return launch_few(a, n_sm, st, pdl);
+cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, const int *clusters, cudaStream_t st, bool pdl) {
+  if (a.T > 2 && few_fits(a.T, a.K)) return launch_few(a, n_sm, st, pdl);
   if (a.T <= 1) return launch_rows_t<1>(a, n_sm, st, pdl);
   if (a.T <= 2) return launch_rows_t<2>(a, n_sm, st, pdl);
   if (a.T <= 4) return launch_rows_t<4>(a, n_sm, st, pdl);
   if (a.T <= kQdRowsMax) return launch_rows_t<8>(a, n_sm, st, pdl);
-  return launch_mma(a, n_sm, st, pdl);
+  return launch_mma(a, n_sm, clusters, st, pdl);
 }
 
 }  // namespace moe

@@ -23,7 +23,7 @@
 // qdense_widen_kernel; the matrix, the larger operand, is read as 8-bit codes
 // and widened on its way into the tensor cores:
 //   weights warp   TMA: 128 channels x 128 codes per stage
-//   rows warp      TMA: up to 256 rows x 128 fp16 per stage
+//   rows warp      TMA: up to 256 rows x 64 fp16 per stage
 //   8 widen warps  a channel per thread and half stage: 64 codes from shared
 //                  memory to fp16 pairs in registers to the A operand in
 //                  tensor memory
@@ -414,6 +414,7 @@ constexpr int kMmXsBytes = kMmMaxN * 4;
 struct MmPlan {
   int n;            // rows per tile (the MMA N): a multiple of 16
   int wst, rst;     // stages of weights and of rows
+  int rk;           // 64-wide steps of K per rows stage: 1 or 2
   int dbufs;        // sets of sums in tensor memory
   int split;        // blocks of a cluster that share a tile along K
   int ntile, ttile; // tiles of channels, of rows
@@ -462,6 +463,12 @@ __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity) {
     if (mm_try(bar, parity)) return true;
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void mm_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -517,7 +524,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   const MmPlan &P = prm.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *base = msm + ((1024u - (smem_addr(msm) & 1023u)) & 1023u);
-  const int rhalf = P.n * 128, rstage = 2 * rhalf;  // a rows stage: two halves of 64 of K
+  const int rstep = P.n * 128, rstage = P.rk * rstep;  // a rows stage: rk steps of 64 of K
   uint8_t *wbuf = base, *rbuf = base + P.wst * kMmWStage;
   uint64_t *bar = reinterpret_cast<uint64_t *>(rbuf + P.rst * rstage);
   uint64_t *wfull = bar, *wempty = wfull + P.wst, *rfull = wempty + P.wst, *rempty = rfull + P.rst;
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   const int first = blockIdx.x / split, stride = gridDim.x / split;  // units of this block
   const int units = P.units;
   const int nst = (a.K + kMmK - 1) / kMmK, st0 = nst * part / split, st1 = nst * (part + 1) / split;  // its part of K
-  auto halves = [&](int s) { return a.K - s * kMmK > 64 ? 2 : 1; };  // 64-wide halves of stage s with codes
+  const int g0 = 2 * st0, g1 = min(2 * st1, (a.K + 63) / 64);  // the same in steps of 64
 
   if (warp == kMmWts) {
     // ============================================================ weights
@@ -584,12 +591,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       for (int u = first; u < units && ok; u += stride) {
         const MmUnit q = mm_unit(P, a.T, u);
         if (q.cnt <= 0) continue;
-        for (int s = st0; s < st1; ++s, ++issued) {
+        for (int g = g0; g < g1; g += P.rk, ++issued) {
           if (issued >= P.rst && !(ok = mm_wait(&rempty[st], ph ^ 1))) break;
-          const int h = halves(s);
+          const int h = min(P.rk, g1 - g);
           mbar_arrive_expect_tx(&rfull[st], (uint32_t)(h * q.n * 128));
           for (int i = 0; i < h; ++i)
-            dense::tma_load_2d(rbuf + st * rstage + i * rhalf, &prm.x[q.half], kMmK * s + 64 * i, q.t0, &rfull[st]);
+            dense::tma_load_2d(rbuf + st * rstage + i * rstep, &prm.x[q.half], 64 * (g + i), q.t0, &rfull[st]);
           if (++st == P.rst) {
             st = 0;
             ph ^= 1;
@@ -605,49 +612,72 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     dense::tc_fence_before();
     __syncwarp();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
-    if (lane == 0) {
-      mm_arrive(tready);
-      const uint64_t bdesc0 = dense::sdesc(smem_addr(rbuf), 16, 1024, 2);
-      bool ok = true;
-      int gi = 0, du = 0, st = 0, ph = 0, ab = 0, aph = 0;
-      for (int u = first; u < units && ok; u += stride) {
-        const MmUnit q = mm_unit(P, a.T, u);
-        if (q.cnt <= 0) continue;
-        const uint32_t idesc = dense::idesc_f16(kMmM, q.n);
-        const int db = du % P.dbufs;
-        if (du >= P.dbufs && !(ok = mm_wait(&dempty[db], ((du / P.dbufs) - 1) & 1))) break;
-        ++du;
-        const uint32_t acc = tmem + db * 128;
-        for (int s = st0; s < st1; ++s, ++gi) {
-          if (!(ok = mm_wait(&rfull[st], ph) && mm_wait(&afull[ab], aph))) break;
-          dense::tc_fence_after();
-          const uint64_t bd = bdesc0 + (uint64_t)((st * rstage) >> 4);
-          const uint32_t ad = tmem + kMmACol + 64 * ab;
-          const int h = halves(s);
-          for (int i = 0; i < h; ++i)
+    // The whole warp runs the loop and one lane issues: with the loop in one
+    // lane's branch the descriptors have to be moved to uniform registers for
+    // every MMA, and an MMA of few rows takes three times as long (24 x 262144
+    // x 2816: 186 us against 129).
+    if (lane == 0) mm_arrive(tready);
+    const uint64_t bdesc0 = dense::sdesc(smem_addr(rbuf), 16, 1024, 2);
+    bool ok = true;
+    int gi = 0, du = 0, st = 0, ph = 0, ab = 0, aph = 0;
+    for (int u = first; u < units; u += stride) {
+      const MmUnit q = mm_unit(P, a.T, u);
+      if (q.cnt <= 0) continue;
+      const uint32_t idesc = dense::idesc_f16(kMmM, q.n);
+      const int db = du % P.dbufs;
+      if (du >= P.dbufs) ok = __all_sync(0xffffffffu, mm_wait(&dempty[db], ((du / P.dbufs) - 1) & 1));
+      if (!ok) break;
+      ++du;
+      const uint32_t acc = tmem + db * 128;
+      for (int s = st0; s < st1; ++s, ++gi) {
+        ok = __all_sync(0xffffffffu, mm_wait(&rfull[st], ph) && mm_wait(&afull[ab], aph));
+        if (!ok) break;
+        dense::tc_fence_after();
+        const uint32_t ad = tmem + kMmACol + 64 * ab;
+        uint64_t bd = bdesc0 + (uint64_t)((st * rstage) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)  // K = 16 per MMA: 8 columns of A, 32 bytes of B's rows
-              mm_mma(acc, ad + 32 * i + 8 * ks, bd + (uint64_t)((i * rhalf) >> 4) + 2 * ks, idesc,
-                     (s > st0 || i > 0 || ks > 0) ? 1u : 0u);
+        for (int ks = 0; ks < 4; ++ks)  // K = 16 per MMA: 8 columns of A, 32 bytes of B's rows
+          if (elect_one()) mm_mma(acc, ad + 8 * ks, bd + 2 * ks, idesc, (s > st0 || ks > 0) ? 1u : 0u);
+        if (2 * s + 1 < g1) {  // the stage's second half
+          if (P.rk == 1) {
+            if (elect_one()) dense::tc_commit(&rempty[st]);
+            if (++st == P.rst) {
+              st = 0;
+              ph ^= 1;
+            }
+            ok = __all_sync(0xffffffffu, mm_wait(&rfull[st], ph));
+            if (!ok) break;
+            dense::tc_fence_after();
+            bd = bdesc0 + (uint64_t)((st * rstage) >> 4);
+          } else {
+            bd += (uint64_t)(rstep >> 4);
+          }
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            if (elect_one()) mm_mma(acc, ad + 32 + 8 * ks, bd + 2 * ks, idesc, 1u);
+        }
+        if (elect_one()) {
           dense::tc_commit(&rempty[st]);
           dense::tc_commit(&aempty[ab]);
           if (s == st1 - 1) dense::tc_commit(&dfull[db]);
-          if (++st == P.rst) {
-            st = 0;
-            ph ^= 1;
-          }
-          if (++ab == kMmABufs) {
-            ab = 0;
-            aph ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++st == P.rst) {
+          st = 0;
+          ph ^= 1;
+        }
+        if (++ab == kMmABufs) {
+          ab = 0;
+          aph ^= 1;
         }
       }
-      if (!ok) set_error(a.err, kErrTimeout);
-      // the last MMAs are complete and the sums read before the memory goes back (bounded waits)
-      if (gi > 0) mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1);
-      if (du > 0) mm_wait(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
-      dense::tc_fence_after();
+      if (!ok) break;
     }
+    if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+    // the last MMAs are complete and the sums read before the memory goes back (bounded waits)
+    if (gi > 0) mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1);
+    if (du > 0) mm_wait(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
+    dense::tc_fence_after();
     __syncwarp();
     dense::tc_dealloc(tmem, 512);
   } else if (warp >= kMmFin0) {
@@ -864,9 +894,14 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
     p.units = p.whole + 2 * rest;
   }
   p.dbufs = p.n <= 128 ? 2 : 1;
-  p.wst = 5;
-  p.rst = p.n > 128 || p.split > 1 ? 2 : 3;
-  p.smem = p.wst * kMmWStage + p.rst * p.n * 256 + kMmBarBytes + kMmXsBytes + 1024 +
+  // Rows stages: many rows come in smaller pieces, more of which are on their
+  // way (256 x 19456 x 16384: 103 us against 117); few rows in larger ones, as
+  // every stage costs the MMA warp a wait and a commit (128 x 65536 x 2816: 44
+  // us against 50).
+  p.rk = p.n > 128 ? 1 : 2;
+  p.wst = p.n > 128 ? 4 : 5;
+  p.rst = p.n > 128 ? 4 : p.split > 1 ? 2 : 3;
+  p.smem = p.wst * kMmWStage + p.rst * p.rk * p.n * 128 + kMmBarBytes + kMmXsBytes + 1024 +
            (p.split > 1 ? p.split * mm_quota(p) * kMmM * 4 : 0);
   return p;
 }

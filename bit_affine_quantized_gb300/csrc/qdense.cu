@@ -10,11 +10,11 @@
 // integers (at most 128 * 128 * 16384 = 2^28 in magnitude).  HBM bound: 1 x
 // 262144 x 2816 in 107 us, 6.9 TB/s of codes; 1 x 4096 x 2816 in 3.3 us.
 //
-// qdense_few_kernel: 3 to 16 rows, mma.sync with the codes widened to fp16 in
+// qdense_few_kernel: 3 to 8 rows, mma.sync with the codes widened to fp16 in
 // registers on their way from global memory; the fp32 sums go to integers
-// every 1024 of K, so they stay exact.  Up to 8 rows HBM bound (8 x 262144 x
-// 2816: 117 us; dp4a took 186), from 9 to 16 by mma.sync's rate (155 us; 24
-// rows would take 186, no less than the next kernel).
+// every 1024 of K, so they stay exact.  HBM bound (8 x 262144 x 2816: 116 us;
+// dp4a took 186).  From 9 rows on mma.sync's rate bounds it (16 rows: 155 us
+// against 125 in the next kernel).
 //
 // qdense_mma_kernel: more rows, on the 5th-generation tensor cores.  sm_103a
 // has no 8-bit integer form of tcgen05.mma; 8-bit codes are exact in fp16, so
@@ -31,14 +31,14 @@
 //                  N = rows (B in shared memory), fp32 sums in tensor memory
 //   8 finish warps the sums times both scales, the softcap, the store
 // A in tensor memory keeps the widened codes out of shared memory, whose
-// bandwidth is what a 128 x 256 fp16 tile asks most of.  The A tile then
-// costs each MMA (K = 16) about 120 cycles up to 128 rows and 156 at 256, so
-// 17 to 128 rows are bound by that (24 x 262144 x 2816: 186 us, 117 us with
-// the MMAs left out) and many rows by it and the rows' way into shared memory
-// (4096 x 4096 x 2816: 77 us, 1230 TFLOP/s; a library product of fp16 operands
-// takes 53 us on such integers, 60 us on random values).  Forms that were
-// slower: A widened into shared memory (24 rows: 203 us) and pairs of blocks
-// on one tile (91 us).
+// bandwidth is what a 128 x 256 fp16 tile asks most of.  Up to 64 rows HBM
+// bounds it (24 x 262144 x 2816: 125 us with a bf16 output, 5.9 TB/s of
+// codes), many rows the tiles' way into shared memory: 80 KB per 128 of K at
+// 64 bytes a clock are 1280 of the 1520 clocks that a 256-row stage takes, its
+// MMAs 1024 (4096 x 4096 x 2816: 67 us, 1420 TFLOP/s; a library product of
+// fp16 operands takes 53 us on such integers, 60 us on random values).  Forms
+// that were slower: A widened into shared memory, and pairs of blocks on one
+// tile.
 // Few tiles: the blocks of a cluster share a tile, each takes a part of K, and
 // the parts are added through distributed shared memory in rank order.
 #include <cuda.h>
@@ -55,8 +55,7 @@ namespace moe {
 namespace {
 constexpr int kQdWarps = 8;
 constexpr int kQdThreads = kQdWarps * 32;
-constexpr int kQdRowsMax = 8;   // rows that the dp4a kernel takes
-constexpr int kQdFewMax = 16;   // rows that the mma.sync kernel takes, where they fit
+constexpr int kQdRowsMax = 8;  // rows that the dp4a and mma.sync kernels take
 
 __device__ __forceinline__ int4 qd_stream(const int8_t *p) {
   int4 v;
@@ -191,13 +190,12 @@ constexpr int kQfFlush = 1024 / 64;  // blocks after which the fp32 sums go to i
 constexpr size_t kQfSmemMax = 200 * 1024;
 __host__ __device__ constexpr int qf_pitch(int K) { return 2 * K + 16; }  // bytes of a row: consecutive rows 4 banks apart
 
-// kNt: groups of 8 rows.  A warp takes a tile of 16 channels (or, where tiles
+// Up to 8 rows (those past T: zero).  A warp takes a tile of 16 channels (or, where tiles
 // are few, a part of a tile's K: split parts by neighbouring warps).  K comes
 // in 64-wide blocks; lane (r, c) = (lane / 4, lane % 4) loads the codes 16 c
 // .. 16 c + 15 of channels r and r + 8, and multiplication j of a block takes
 // codes 4 j .. 4 j + 3 of those for the k positions that mma.m16n8k16 gives
 // the lane; the rows, widened to fp16 in shared memory, follow the same order.
-template <int kNt>
 __global__ void __launch_bounds__(kQfThreads, 1) qdense_few_kernel(const QdenseArgs a, const int split) {
   extern __shared__ __align__(16) uint8_t fsm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -227,7 +225,7 @@ __global__ void __launch_bounds__(kQfThreads, 1) qdense_few_kernel(const QdenseA
   if (tile < tiles) request(tile * 16, b0);
   // the rows, widened (those past T: zero)
   const int nck = K / 16;
-  for (int i = tid; i < 8 * kNt * nck; i += kQfThreads) {
+  for (int i = tid; i < 8 * nck; i += kQfThreads) {
     const int t = i / nck, k = i - t * nck;
     const uint4 v = t < a.T ? __ldcg(reinterpret_cast<const uint4 *>(a.x + (size_t)t * K) + k) : make_uint4(0u, 0u, 0u, 0u);
     uint4 o0, o1;
@@ -240,24 +238,16 @@ __global__ void __launch_bounds__(kQfThreads, 1) qdense_few_kernel(const QdenseA
     dst[1] = o1;
   }
   __syncthreads();
-  int *parts = reinterpret_cast<int *>(fsm + (size_t)8 * kNt * pitch);  // [warp][4 kNt][32], split > 1
+  int *parts = reinterpret_cast<int *>(fsm + (size_t)8 * pitch);  // [warp][4][32], split > 1
   // (every warp of a block makes the same number of rounds: barriers below)
   const int rounds = (tiles + gridDim.x * per_block - 1) / (gridDim.x * per_block);
   for (int round = 0; round < rounds; ++round, tile += gridDim.x * per_block) {
     const int n0 = tile * 16;
-    int sum[kNt][4];
-#pragma unroll
-    for (int n = 0; n < kNt; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum[n][i] = 0;
+    int sum[4] = {0, 0, 0, 0};
     if (tile < tiles) {
       if (round > 0) request(n0, b0);
       for (int f = b0; f < b1; f += kQfFlush) {  // exact in fp32
-        float acc[kNt][4];
-#pragma unroll
-        for (int n = 0; n < kNt; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
         const int fe = min(b1, f + kQfFlush);
         for (int b = f; b < fe; b += kQfAhead) {
           int4 x0[kQfAhead], x1[kQfAhead];
@@ -278,62 +268,48 @@ __global__ void __launch_bounds__(kQfThreads, 1) qdense_few_kernel(const QdenseA
               widen4(q0[i], A[i][0], A[i][2]);
               widen4(q1[i], A[i][1], A[i][3]);
             }
-#pragma unroll
-            for (int n = 0; n < kNt; ++n) {
-              const uint4 *bx = reinterpret_cast<const uint4 *>(fsm + (size_t)(8 * n + r) * pitch + 2 * k);
-              const uint4 v0 = bx[0], v1 = bx[1];
-              mma_f16(acc[n], A[0], v0.x, v0.y);
-              mma_f16(acc[n], A[1], v0.z, v0.w);
-              mma_f16(acc[n], A[2], v1.x, v1.y);
-              mma_f16(acc[n], A[3], v1.z, v1.w);
-            }
+            const uint4 *bx = reinterpret_cast<const uint4 *>(fsm + (size_t)r * pitch + 2 * k);
+            const uint4 v0 = bx[0], v1 = bx[1];
+            mma_f16(acc, A[0], v0.x, v0.y);
+            mma_f16(acc, A[1], v0.z, v0.w);
+            mma_f16(acc, A[2], v1.x, v1.y);
+            mma_f16(acc, A[3], v1.z, v1.w);
           }
         }
 #pragma unroll
-        for (int n = 0; n < kNt; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum[n][i] += __float2int_rn(acc[n][i]);
+        for (int i = 0; i < 4; ++i) sum[i] += __float2int_rn(acc[i]);
       }
     }
     if (split > 1) {
 #pragma unroll
-      for (int n = 0; n < kNt; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) parts[(warp * kNt * 4 + n * 4 + i) * 32 + lane] = sum[n][i];
+      for (int i = 0; i < 4; ++i) parts[(warp * 4 + i) * 32 + lane] = sum[i];
       __syncthreads();
       if (part == 0) {
         for (int p = 1; p < split; ++p)
 #pragma unroll
-          for (int n = 0; n < kNt; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[n][i] += parts[((warp + p) * kNt * 4 + n * 4 + i) * 32 + lane];
+          for (int i = 0; i < 4; ++i) sum[i] += parts[((warp + p) * 4 + i) * 32 + lane];
       }
       __syncthreads();
     }
     if (part == 0 && tile < tiles) {
-      // sum[n][i]: channel n0 + r + 8 (i / 2), row 8 n + 2 c + i % 2
+      // sum[i]: channel n0 + r + 8 (i / 2), row 2 c + i % 2
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int ch = n0 + r + 8 * (i >> 1);
-        const float ws = ch < a.N ? __ldg(a.ws + ch) : 0.f;
-#pragma unroll
-        for (int n = 0; n < kNt; ++n) {
-          const int t = 8 * n + 2 * c + (i & 1);
-          if (t < a.T && ch < a.N) qd_store(a, t, ch, sum[n][i], __ldcg(a.xs + t), ws);
-        }
+        const int t = 2 * c + (i & 1);
+        if (t < a.T && ch < a.N) qd_store(a, t, ch, sum[i], __ldcg(a.xs + t), __ldg(a.ws + ch));
       }
     }
   }
   if (tracer) trace_max(a.trace, kTrExit);
 }
 
-template <int kNt>
-size_t few_smem(int K) {
-  return (size_t)8 * kNt * qf_pitch(K) + (size_t)kQfWarps * kNt * 4 * 32 * 4;
-}
+size_t few_smem(int K) { return (size_t)8 * qf_pitch(K) + (size_t)kQfWarps * 4 * 32 * 4; }
 
-template <int kNt>
-cudaError_t launch_few_n(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
+// Whether the rows, widened, fit a block's shared memory.
+bool few_fits(int T, int K) { return T <= kQdRowsMax && few_smem(K) <= kQfSmemMax; }
+
+cudaError_t launch_few(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
   const int tiles = (a.N + 15) / 16, nb = (a.K + 63) / 64;
   // parts of K per tile while whole tiles would leave warps without work
   int split = 1;
@@ -342,30 +318,14 @@ cudaError_t launch_few_n(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pd
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks < n_sm ? blocks : n_sm);
   cfg.blockDim = dim3(kQfThreads);
-  cfg.dynamicSmemBytes = few_smem<kNt>(a.K);
+  cfg.dynamicSmemBytes = few_smem(a.K);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, qdense_few_kernel<kNt>, a, split);
-}
-
-// Whether the rows, widened, fit a block's shared memory.
-bool few_fits(int T, int K) {
-  const int nt = (T + 7) / 8;
-  return T <= kQdFewMax && (size_t)8 * nt * qf_pitch(K) + (size_t)kQfWarps * nt * 4 * 32 * 4 <= kQfSmemMax;
-}
-
-cudaError_t launch_few(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl) {
-  return a.T <= 8 ? launch_few_n<1>(a, n_sm, st, pdl) : launch_few_n<2>(a, n_sm, st, pdl);
-}
-
-cudaError_t set_few_attr() {
-  const cudaFuncAttribute f = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const cudaError_t e = cudaFuncSetAttribute(qdense_few_kernel<1>, f, (int)kQfSmemMax);
-  return e ? e : cudaFuncSetAttribute(qdense_few_kernel<2>, f, (int)kQfSmemMax);
+  return cudaLaunchKernelEx(&cfg, qdense_few_kernel, a, split);
 }
 
 // ------------------------------------------------------------------ rows to fp16
@@ -849,19 +809,18 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   if (tracer) trace_max(a.trace, kTrExit);
 }
 
-// Tiles of up to 256 rows where they fill the device: an MMA with A in tensor
-// memory takes about as long for 128 rows as for fewer, and for 256 not twice
-// as long (a 128-wide K stage: 0.55 us up to 128 rows, 0.86 us at 256), so
-// more rows per tile are better while every SM has a tile.
+// Tiles of up to 256 rows where they fill the device: a 128-wide K stage takes
+// 0.45 us at 128 rows, 0.75 us at 256.
 //
 // Fewer tiles than half the SMs: up to 128 rows per tile, and a cluster of
-// `split` blocks per tile if that pays: the stages go down by the factor, the
-// exchange of the parts costs 1.3 us + 13 ns per row of the tile, 0.8 us more
-// for clusters of over four blocks (128 x 2816 x 4096, clusters of 1, 2, 3, 4,
-// 6: 22.0, 16.4, 13.8, 11.8, 12.1 us; 333 x 1411 x 1072, 1 .. 4: 9.8, 10.0,
-// 9.1, 9.8).  clusters[s]: clusters of s blocks that the device holds at once
-// (more than those would run in a second wave: 16 tiles in clusters of 8 took
-// 15.7 us, in clusters of 4 10.4).
+// `split` blocks per tile if that pays: the stages (0.36 us there) go down by
+// the factor, the exchange of the parts costs 1 us + 28 ns per row of the
+// tile, 0.8 us more for clusters of over four blocks (128 x 2816 x 4096,
+// clusters of 1, 2, 3, 4, 6: 16.4, 15.4, 13.3, 11.3, 12.0 us; 32 x 704 x 2816,
+// 1, 2, 4, 8: 11.4, 9.8, 8.0, 7.2; 128 x 1408 x 704, 1, 2, 4: 6.8, 9.1, 8.4).
+// clusters[s]: clusters of s blocks that the device holds at once (more than
+// those would run in a second wave: 16 tiles in clusters of 8 took 15.7 us, in
+// clusters of 4 10.4).
 //
 // The last round of tiles, if at most half the SMs have one: in halves.
 MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
@@ -876,9 +835,9 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   const int nst = (K + kMmK - 1) / kMmK;
   if (2 * p.ntile * p.ttile <= n_sm) {
     tiles(kMmSplitN);
-    double least = 0.55 * nst;
+    double least = 0.36 * nst;
     for (int s = 2; s <= kMmMaxSplit && s <= nst; ++s) {
-      const double t = 0.55 * ((nst + s - 1) / s) + 1.3 + 0.013 * p.n + (s > 4 ? 0.8 : 0.0);
+      const double t = 0.36 * ((nst + s - 1) / s) + 1.0 + 0.028 * p.n + (s > 4 ? 0.8 : 0.0);
       if (p.ntile * p.ttile <= clusters[s] && t < least) {
         least = t;
         p.split = s;
@@ -953,7 +912,7 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, const int *clusters, cudaS
 cudaError_t qdense_set_attributes(int *clusters) {
   cudaError_t e;
   if ((e = set_rows_attr<1>()) || (e = set_rows_attr<2>()) || (e = set_rows_attr<4>()) || (e = set_rows_attr<8>()) ||
-      (e = set_few_attr()) ||
+      (e = cudaFuncSetAttribute(qdense_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQfSmemMax)) ||
       (e = cudaFuncSetAttribute(qdense_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)))
     return e;
   for (int s = 0; s <= kQdenseMaxCluster; ++s) {
@@ -977,7 +936,7 @@ cudaError_t qdense_set_attributes(int *clusters) {
 
 // The widened rows of the tensor-core path.
 size_t qdense_ws_bytes(int T, int K) {
-  return T <= kQdRowsMax || few_fits(T, K) ? 0 : ((size_t)T * K * 2 + 255) / 256 * 256;
+  return T <= kQdRowsMax ? 0 : ((size_t)T * K * 2 + 255) / 256 * 256;
 }
 
 cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, const int *clusters, cudaStream_t st, bool pdl) {

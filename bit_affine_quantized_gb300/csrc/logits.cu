@@ -16,7 +16,7 @@
 // history stays in registers over the block's segments.  A table word holds
 // the count after the prompt in its low 31 bits and "occurs in the prompt" in
 // bit 31.  A second table holds, per token of the segment, the number of its
-// last bias entry.  A segment is up to four slices of four tokens per thread:
+// last bias entry.  A segment is up to two slices of eight tokens per thread:
 // every token of the history is looked at once per segment, which at
 // 4096-token segments and as many history tokens was a third of the time.
 // The logits are copied slices ahead into a ring in shared memory (cp.async)
@@ -27,16 +27,20 @@
 // the row's state.
 #include <math.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 
 namespace moe {
 
 namespace {
 constexpr int kLgThreads = 1024;
-constexpr int kLgSlice = 4 * kLgThreads;
-constexpr int kLgRing = 4;       // slices of logits in shared memory
-constexpr int kMaskSlice = kLgSlice / 32;  // mask words of a slice
-constexpr int kLgSegMax = 4;     // slices per segment, at most
+constexpr int kLgGroups = 2;     // groups of four tokens per thread and slice
+constexpr int kLgGroup = 4 * kLgThreads;        // tokens that the block's groups of one kind cover
+constexpr int kLgSlice = kLgGroups * kLgGroup;
+constexpr int kLgRing = 2;       // slices of logits in shared memory
+constexpr int kMaskSlice = kLgSlice / 32;       // mask words of a slice
+constexpr int kLgSegMax = 2;     // slices per segment, at most
 constexpr int kHistRegs = 4;     // history entries per thread that stay in registers
 constexpr unsigned kInPrompt = 0x80000000u;
 
@@ -83,6 +87,13 @@ __device__ __forceinline__ void lg_touched(float (&x)[4], uint4 c, uint4 b, cons
   }
 }
 
+// The larger of two, NaN if one of them is.
+__device__ __forceinline__ float lg_max(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ void lg_copy16(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
@@ -96,19 +107,20 @@ __device__ __forceinline__ void lg_wait() {
 }
 
 // kQuad: rows start on 16-byte boundaries, and a thread's tokens of a slice are
-// four neighbours, 4 tid + k; else tid + k threads.
+// four neighbours per group, 4 tid + k + 4096 g; else tid + k threads + 4096 g.
 template <bool kHist, bool kBias, bool kMask, bool kQuad>
 __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs a) {
   extern __shared__ __align__(16) unsigned lsm[];
   __shared__ unsigned long long s_best[kLgThreads / 32];
   const int tid = threadIdx.x, V = a.V;
   constexpr int kStep = kQuad ? 1 : kLgThreads;  // distance of a thread's tokens
-  const int own = kQuad ? 4 * tid : tid;         // its first token of a slice
+  const int own = kQuad ? 4 * tid : tid;         // its first token of a group
   const int seg = a.seg * kLgSlice;
-  float *const ring = reinterpret_cast<float *>(lsm) + own, *const ring_end = ring + kLgRing * kLgSlice;
+  float *const ring = reinterpret_cast<float *>(lsm) + own;
   unsigned *const cnt = lsm + kLgRing * kLgSlice, *const bix = cnt + (kHist ? seg : 0);
-  // mask words of the slices in the ring, four for the 128 tokens of a warp
-  uint32_t *const mring = bix + (kBias ? seg : 0) + (tid >> 5) * 4, *const mend = mring + kLgRing * kMaskSlice;
+  // mask words of the slices in the ring, per group four for the 128 tokens of a warp
+  uint32_t *const mring = bix + (kBias ? seg : 0) + (tid >> 5) * 4;
+  constexpr int kMaskGroup = kLgGroup / 32;
   const bool tracer = blockIdx.x == 0 && tid == 0;
   if (tracer) trace_min(a.trace, kTrEntry);
   const int ns = (V + seg - 1) / seg;  // segments per row
@@ -126,30 +138,31 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
   // copy; cleft: tokens from the slice's start to the row's end; the block's
   // part ends cend tokens before the end of row et.
   const float *cin = a.logits + (size_t)t * a.ld + (size_t)sg * seg + own;
-  float *cto = ring;
-  const int mown = kQuad ? (tid & ~31) * 4 + (tid & 3) * 32 : (tid & ~31) + (tid & 3) * kStep;  // first token of the lane's word
+  // lanes 4 g + j < 8 of a warp copy word j of its group g, whose first token is mown
+  const int mg = (tid >> 2) & (kLgGroups - 1);
+  const int mown = mg * kLgGroup + (kQuad ? (tid & ~31) * 4 + (tid & 3) * 32 : (tid & ~31) + (tid & 3) * kStep);
   const uint32_t *cmask = kMask ? a.mask + (size_t)t * a.mask_stride + ((sg * seg + mown) >> 5) : nullptr;
-  uint32_t *mto = mring;
   int ct = t, cleft = V - sg * seg;
   const int et = (int)((u1 - 1) / ns), cend = max(0, V - ((int)((u1 - 1) % ns) + 1) * seg);
-  auto copy_next = [&]() {
+  auto copy_next = [&](int place) {  // the next slice into a place of the ring
     if (ct < et || (ct == et && cleft > cend)) {
-      if (kQuad && own + 4 <= cleft) {
-        lg_copy16(cto, cin);
-      } else {
+      float *to = ring + place * kLgSlice;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (own + k * kStep < cleft) lg_copy4(cto + k * kStep, cin + k * kStep);
+      for (int g = 0; g < kLgGroups; ++g) {
+        if (kQuad && (cleft >= kLgSlice || own + g * kLgGroup + 4 <= cleft)) {
+          lg_copy16(to + g * kLgGroup, cin + g * kLgGroup);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (own + g * kLgGroup + k * kStep < cleft) lg_copy4(to + g * kLgGroup + k * kStep, cin + g * kLgGroup + k * kStep);
+        }
       }
+      cin += kLgSlice;
       if (kMask) {
-        if ((tid & 31) < 4 && mown < cleft) lg_copy4(mto + (tid & 3), cmask);
-        mto += kMaskSlice;
-        if (mto == mend) mto = mring;
+        if ((tid & 31) < 4 * kLgGroups && mown < cleft)
+          lg_copy4(mring + place * kMaskSlice + mg * kMaskGroup + (tid & 3), cmask);
         cmask += kLgSlice / 32;
       }
-      cto += kLgSlice;
-      if (cto == ring_end) cto = ring;
-      cin += kLgSlice;
       cleft -= kLgSlice;
       if (cleft <= 0) {  // the next row
         ++ct;
@@ -161,15 +174,14 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
     lg_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kLgRing - 1; ++i) copy_next();
+  for (int i = 0; i < kLgRing - 1; ++i) copy_next(i);  // one slice ahead of the reads
 
   bool fresh = true, bad_id = false, bad = false;
   RowRules rr = {1.f, 0.f, 0.f, nullptr};
   int hlen = 0, plen = 0, blen = 0, hv[kHistRegs], bv = 0, done = 0;
   float best = -INFINITY;  // the thread's best of the row so far
   int best_id = 0;
-  const float *in = ring;
-  const uint32_t *mslice = mring;
+  int place = 0;  // of the slice to read, in the ring
   for (long long u = u0; u < u1; ++u) {
     const int v0 = sg * seg, n = min(seg, V - v0);
     // this thread's places of the segment's first slice
@@ -241,92 +253,102 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
     }
     unsigned *ci = cnt + own, *bi = bix + own;
     int v = v0 + own;
-    for (int left = n; left > 0; left -= kLgSlice) {  // the segment's slices
-      lg_wait<kLgRing - 2>();  // the thread's part of the slice has landed
-      uint32_t m = 15u;
-      if (kMask) {
-        __syncwarp();  // and its warp's mask words
-        if (kQuad) {
-          m = mslice[(tid & 31) >> 3] >> (4 * (tid & 7));
-        } else {
-          const uint4 w = *reinterpret_cast<const uint4 *>(mslice);
-          const int i = tid & 31;
-          m = ((w.x >> i) & 1u) | (((w.y >> i) & 1u) << 1) | (((w.z >> i) & 1u) << 2) | (((w.w >> i) & 1u) << 3);
-        }
-        __syncwarp();  // every lane has its bits before the place is filled again
-        mslice += kMaskSlice;
-        if (mslice == mend) mslice = mring;
-      }
+    // one slice; `whole`: all its tokens are there, else `left` of them
+    auto slice = [&](auto whole, int left) {
+      constexpr bool kWhole = decltype(whole)::value;
+      copy_next((place + kLgRing - 1) % kLgRing);  // into the place that the thread read last
+      lg_wait<kLgRing - 1>();                      // the thread's part of this slice has landed
+      if (kMask) __syncwarp();                     // and its warp's mask words
+      const uint32_t *words = mring + place * kMaskSlice;
+      const float *from = ring + place * kLgSlice;
       const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-      uint4 c = none, b = none;
-      float l[4];
-      if (kQuad) {
-        const float4 f = *reinterpret_cast<const float4 *>(in);
-        l[0] = f.x;
-        l[1] = f.y;
-        l[2] = f.z;
-        l[3] = f.w;
-        if (kHist) c = *reinterpret_cast<const uint4 *>(ci);
-        if (kBias) b = *reinterpret_cast<const uint4 *>(bi);
-      } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) l[k] = in[k * kStep];
-        if (kHist) c = make_uint4(ci[0], ci[kStep], ci[2 * kStep], ci[3 * kStep]);
-        if (kBias) b = make_uint4(bi[0], bi[kStep], bi[2 * kStep], bi[3 * kStep]);
-      }
-      copy_next();  // into the place before this one, which the thread has read
-      in += kLgSlice;
-      if (in == ring_end) in = ring;
-      if ((kHist || kBias) && (c.x | c.y | c.z | c.w | b.x | b.y | b.z | b.w) != 0u) {
-        lg_touched(l, c, b, rr);
+      for (int g = 0; g < kLgGroups; ++g) {
+        uint32_t m = 15u;
+        if (kMask) {
+          if (kQuad) {
+            m = words[g * kMaskGroup + ((tid & 31) >> 3)] >> (4 * (tid & 7));
+          } else {
+            const uint4 w = *reinterpret_cast<const uint4 *>(words + g * kMaskGroup);
+            const int i = tid & 31;
+            m = ((w.x >> i) & 1u) | (((w.y >> i) & 1u) << 1) | (((w.z >> i) & 1u) << 2) | (((w.w >> i) & 1u) << 3);
+          }
+        }
+        uint4 c = none, b = none;
+        float l[4];
+        const float *in = from + g * kLgGroup;
+        unsigned *cg = ci + g * kLgGroup, *bg = bi + g * kLgGroup;
         if (kQuad) {
-          if (kHist) *reinterpret_cast<uint4 *>(ci) = none;
-          if (kBias) *reinterpret_cast<uint4 *>(bi) = none;
+          const float4 f = *reinterpret_cast<const float4 *>(in);
+          l[0] = f.x;
+          l[1] = f.y;
+          l[2] = f.z;
+          l[3] = f.w;
+          if (kHist) c = *reinterpret_cast<const uint4 *>(cg);
+          if (kBias) b = *reinterpret_cast<const uint4 *>(bg);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) l[k] = in[k * kStep];
+          if (kHist) c = make_uint4(cg[0], cg[kStep], cg[2 * kStep], cg[3 * kStep]);
+          if (kBias) b = make_uint4(bg[0], bg[kStep], bg[2 * kStep], bg[3 * kStep]);
+        }
+        if ((kHist || kBias) && (c.x | c.y | c.z | c.w | b.x | b.y | b.z | b.w) != 0u) {
+          lg_touched(l, c, b, rr);
+          if (kQuad) {
+            if (kHist) *reinterpret_cast<uint4 *>(cg) = none;
+            if (kBias) *reinterpret_cast<uint4 *>(bg) = none;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (kHist) cg[k * kStep] = 0u;
+              if (kBias) bg[k * kStep] = 0u;
+            }
+          }
+        }
+        if (kMask) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) l[k] = m & (1u << k) ? l[k] : -INFINITY;
+        }
+        float *o = out + g * kLgGroup;
+        if (kWhole) {
+          if (out) {
+            if (kQuad) {
+              __stcs(reinterpret_cast<float4 *>(o), make_float4(l[0], l[1], l[2], l[3]));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) __stcs(o + k * kStep, l[k]);
+            }
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if (kHist) ci[k * kStep] = 0u;
-            if (kBias) bi[k * kStep] = 0u;
+            const bool there = own + g * kLgGroup + k * kStep < left;
+            l[k] = there ? l[k] : -INFINITY;
+            if (out && there) __stcs(o + k * kStep, l[k]);
           }
         }
-      }
-      if (kMask) {
+        float top = lg_max(lg_max(l[0], l[1]), lg_max(l[2], l[3]));
+        if (!(top < INFINITY)) {  // NaN and +inf are not for the token
+          bad = true;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) l[k] = m & (1u << k) ? l[k] : -INFINITY;
-      }
-      if (left >= kLgSlice) {
-        if (out) {
-          if (kQuad) {
-            __stcs(reinterpret_cast<float4 *>(out), make_float4(l[0], l[1], l[2], l[3]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) __stcs(out + k * kStep, l[k]);
-          }
+          for (int k = 0; k < 4; ++k) l[k] = l[k] < INFINITY ? l[k] : -INFINITY;
+          top = lg_max(lg_max(l[0], l[1]), lg_max(l[2], l[3]));
         }
-      } else {  // the row's end
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool there = own + k * kStep < left;
-          l[k] = there ? l[k] : -INFINITY;
-          if (out && there) __stcs(out + k * kStep, l[k]);
+        if (top > best) {
+          best = top;
+          best_id = v + g * kLgGroup + kStep * (l[0] == top ? 0 : l[1] == top ? 1 : l[2] == top ? 2 : 3);  // the first of them
         }
       }
-      if (!(l[0] < INFINITY && l[1] < INFINITY && l[2] < INFINITY && l[3] < INFINITY)) {
-        bad = true;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (!(l[k] < INFINITY)) l[k] = -INFINITY;  // NaN and +inf are not for the token
-      }
-      const float top = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
-      if (top > best) {
-        best = top;
-        best_id = v + kStep * (l[0] == top ? 0 : l[1] == top ? 1 : l[2] == top ? 2 : 3);  // the first of them
-      }
+      if (kMask) __syncwarp();  // every lane has its bits before the place is filled again
+      place = (place + 1) % kLgRing;
       if (out) out += kLgSlice;
       v += kLgSlice;
       ci += kLgSlice;
       bi += kLgSlice;
-    }
+    };
+    int left = n;
+    for (; left >= kLgSlice; left -= kLgSlice) slice(std::true_type{}, left);
+    if (left > 0) slice(std::false_type{}, left);
     ++done;
     if (++sg == ns || u + 1 == u1) {  // the row ends, or the block's part of it
       if (a.tokens) {
@@ -400,9 +422,9 @@ cudaError_t launch_logits(const LogitsArgs &a0, int n_sm, cudaStream_t st, bool 
   const bool h = a.history != nullptr, b = a.bias_ids != nullptr;
   const bool quad = (((uintptr_t)a.logits | (uintptr_t)a.out) & 15u) == 0 && a.ld % 4 == 0 && (!a.out || a.ld_out % 4 == 0);
   // Slices per segment: the fewest slices for the block that has most of them,
-  // a segment's own work counted as half a slice and one per 6000 tokens of
-  // history.
-  const double own = 0.5 + (h ? a.history_stride / 6000.0 : 0.0);
+  // a segment's own work counted as a quarter of a slice and one per 12000
+  // tokens of history.
+  const double own = 0.25 + (h ? a.history_stride / 12000.0 : 0.0);
   double least = 0.0;
   long long blocks = 0;
   for (int s = 1; s <= kLgSegMax; s *= 2) {

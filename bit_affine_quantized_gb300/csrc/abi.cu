@@ -877,12 +877,12 @@ int moe_qdense_forward(moe_handle *h, const int8_t *x, const float *x_scales, in
   if (!aligned(x, 16) || !aligned(x_scales, 4) || (y && !aligned(y, 2)) || (y32 && !aligned(y32, 4)))
     return MOE_ERR_INVALID_ARG;
   if (!(softcap == softcap)) return MOE_ERR_INVALID_ARG;
-  if (!on_device(h)) return MOE_ERR_INVALID_ARG;
   const size_t need = moe::qdense_ws_bytes(n_rows, w->width);
   if (need) {
     if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   }
+  if (!on_device(h)) return MOE_ERR_INVALID_ARG;
   if (!h->qdense_ready) {
     if (moe::qdense_set_attributes(h->qdense_clusters) != cudaSuccess) return MOE_ERR_CUDA;
     h->qdense_ready = true;

@@ -521,6 +521,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     // Nothing that an earlier launch still writes is read here: the launch
     // before this one (the widening of the rows) waited for those.
     if (lane == 0) {
+      fused::fence_proxy_async_global();
       bool ok = true;
       int st = 0, ph = 0, issued = 0;
       for (int u = first; u < units && ok; u += stride) {

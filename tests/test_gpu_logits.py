@@ -114,7 +114,9 @@ def logits_of(seed, T, V):
 @pytest.mark.parametrize("T,V,L,B,mask", [
     (1, 1, 3, 2, 0.5), (1, 31, 5, 0, None), (3, 33, 40, 7, 0.5), (2, 4096, 300, 0, None), (5, 4097, 0, 9, None),
     (4, 5003, 0, 0, 0.3), (7, 1000, 2000, 1, 0.9), (1, 70001, 500, 300, None), (17, 8192, 100, 40, 0.1),
-    (2, 262144, 3000, 300, 0.25), (3, 20000, 0, 0, None), (300, 129, 20, 5, 0.5)])
+    (2, 262144, 3000, 300, 0.25), (3, 20000, 0, 0, None), (300, 129, 20, 5, 0.5),
+    # blocks that take parts of several rows; lists longer than what stays in registers, at odd strides
+    (40, 20000, 60, 12, 0.5), (200, 9001, 33, 0, None), (3, 30000, 5001, 2500, 0.5), (2, 40960, 9000, 1100, None)])
 def test_matches_oracle(moe, T, V, L, B, mask, out):
     lg = logits_of(T * V, T, V)
     a, rows, m = make(V + L, T, V, L, B, mask)

@@ -69,7 +69,7 @@ def check(got, want):
         assert np.all(np.abs(x - w) <= (2.0 ** -8 + REL) * np.abs(w) + 2.0 ** -133)
 
 
-@pytest.mark.parametrize("T,H", [(1, 16), (3, 48), (1, 2816), (130, 2816), (5, 1360), (2, 8192), (3, 8208), (2, 16384),
+@pytest.mark.parametrize("T,H", [(600, 16384), (460, 8208), (500, 48), (1, 16), (3, 48), (1, 2816), (130, 2816), (5, 1360), (2, 8192), (3, 8208), (2, 16384),
                                  (700, 64)])
 @pytest.mark.parametrize("add,weight", [(True, True), (True, False), (False, True), (False, False)])
 def test_matches_oracle(moe, T, H, add, weight):
@@ -174,6 +174,26 @@ def test_captured_and_on_another_stream(moe):
     torch.cuda.synchronize()
     assert moe.get_error() == bq.MOE_OK
     assert np.array_equal(q.cpu().numpy(), want["q"]) and np.array_equal(host16(out), want["s"])
+
+
+def test_rows_beyond_32_bits(moe):
+    """A matrix with more than 2^31 values."""
+    T, H = 270000, 8192
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    h = torch.zeros((T, H), dtype=torch.int16, device="cuda")
+    some = rows(50, 3, H)
+    at = [0, 140000, T - 1]
+    for i, t in enumerate(at):
+        h[t] = torch.from_numpy(some[i].view(np.int16)).cuda()
+    q, s = torch.empty((T, H), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    moe.norm_quant(h, T, q, s)
+    torch.cuda.synchronize()
+    assert moe.get_error() == bq.MOE_OK
+    want = BO.norm_quant(some)
+    assert np.array_equal(q[at].cpu().numpy(), want["q"])
+    assert np.all(np.abs(s[at].cpu().numpy() - want["scales"]) <= REL * want["scales"])
+    assert int((s != 0).sum()) == 3 and int(q.count_nonzero()) == int(np.count_nonzero(want["q"]))
 
 
 def test_binding_refuses(moe):

@@ -72,7 +72,11 @@ def scales(seed, T, N):
 SHAPES = [(1, 1, 16), (1, 2816, 2816), (1, 4097, 208), (2, 33, 64), (3, 130, 1072), (5, 700, 16384), (8, 515, 704),
           (9, 1, 16), (9, 128, 64), (16, 129, 80), (17, 2816, 704), (24, 1411, 2816), (64, 300, 4096), (100, 127, 1072),
           (128, 2816, 4096), (129, 257, 128), (255, 64, 2816), (257, 512, 704), (333, 1411, 1072), (1000, 384, 256),
-          (2049, 130, 48), (40, 40000, 64)]
+          (2049, 130, 48), (40, 40000, 64),
+          # more tiles than SMs: the last round in halves of tiles (one of them past the last row)
+          (512, 10240, 144), (520, 7000, 64), (4112, 1280, 64), (4097, 1290, 80),
+          # tiles shared by clusters of every size; K that ends inside a stage and inside its first half
+          (40, 128, 2816), (150, 128, 1040), (100, 1408, 2832), (64, 2816, 1120), (200, 704, 4112), (33, 5632, 528)]
 
 
 @pytest.mark.parametrize("T,N,K", SHAPES)
@@ -169,6 +173,72 @@ def test_captured_and_replayed(moe, T):
     for x, both in got:
         for o in both:
             assert np.all(np.abs(o.cpu().numpy() - BO.qdense(x, xs, w, ws)) <= bound(x, w, xs, ws))
+
+
+@pytest.mark.parametrize("T", [1, 5, 12])
+def test_weights_beyond_32_bits(moe, T):
+    """A matrix whose last rows start more than 2^31 bytes into it."""
+    N, K = 140000, 16384
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    w = torch.randint(-40, 41, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    x = codes(30, T, K)
+    xs, _ = scales(31, T, 1)
+    ws = torch.full((N,), 0.001, device="cuda")
+    wd = bq.make_qdense_weights(N, K, w, ws)
+    work = torch.empty(moe.qdense_workspace_bytes(wd, T), dtype=torch.uint8, device="cuda")
+    y = torch.empty((T, N), device="cuda")
+    moe.qdense_forward(torch.from_numpy(x).cuda(), torch.from_numpy(xs).cuda(), T, wd, work, y32=y)
+    torch.cuda.synchronize()
+    assert moe.get_error() == bq.MOE_OK
+    for a in (0, 70000, N - 300):
+        part = w[a:a + 300].cpu().numpy()
+        s = np.full(300, np.float32(0.001))
+        assert np.all(np.abs(y[:, a:a + 300].cpu().numpy() - BO.qdense(x, xs, part, s)) <= bound(x, part, xs, s))
+
+
+def test_outputs_beyond_32_bits(moe):
+    """An output with more than 2^31 values."""
+    T, N, K = 2100, 1050000, 16
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    x, w = codes(32, T, K), codes(33, N, K)
+    xs, ws = scales(34, T, N)
+    wd = bq.make_qdense_weights(N, K, torch.from_numpy(w).cuda(), torch.from_numpy(ws).cuda())
+    work = torch.empty(moe.qdense_workspace_bytes(wd, T), dtype=torch.uint8, device="cuda")
+    y = torch.empty((T, N), device="cuda")
+    moe.qdense_forward(torch.from_numpy(x).cuda(), torch.from_numpy(xs).cuda(), T, wd, work, y32=y)
+    torch.cuda.synchronize()
+    assert moe.get_error() == bq.MOE_OK
+    for t in (0, 1024, T - 1):
+        got = y[t].cpu().numpy()[None]
+        assert np.all(np.abs(got - BO.qdense(x[t:t + 1], xs[t:t + 1], w, ws)) <= bound(x[t:t + 1], w, xs[t:t + 1], ws))
+
+
+def test_two_handles_at_once(moe):
+    """Calls of two handles on two streams, each with its own workspace."""
+    N, K = 3000, 704
+    w = codes(40, N, K)
+    other = bq.Moe()
+    jobs = []
+    for i, (m, T) in enumerate(((moe, 40), (other, 300))):
+        x = codes(41 + i, T, K)
+        xs, ws = scales(43 + i, T, N)
+        wd = bq.make_qdense_weights(N, K, torch.from_numpy(w).cuda(), torch.from_numpy(ws).cuda())
+        work = torch.empty(m.qdense_workspace_bytes(wd, T), dtype=torch.uint8, device="cuda")
+        jobs.append((m, torch.from_numpy(x).cuda(), torch.from_numpy(xs).cuda(), T, wd, work,
+                     torch.empty((T, N), device="cuda"), torch.cuda.Stream(), x, xs, ws))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for m, xd, xsd, T, wd, work, y, st, *_ in jobs:
+            m.qdense_forward(xd, xsd, T, wd, work, y32=y, stream=st)
+    torch.cuda.synchronize()
+    for m, _, _, T, _, _, y, _, x, xs, ws in jobs:
+        assert m.get_error() == bq.MOE_OK
+        assert np.all(np.abs(y.cpu().numpy() - BO.qdense(x, xs, w, ws)) <= bound(x, w, xs, ws))
+    other.close()
 
 
 def test_binding_refuses(moe):

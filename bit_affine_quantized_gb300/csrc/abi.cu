@@ -1,5 +1,6 @@
 // C ABI of the MoE block: argument checks, workspace carving, launches.
 // Declarations and the contract of every call: include/moe.h.
+#include <float.h>
 #include <stdlib.h>
 #include <string.h>
 
@@ -876,7 +877,7 @@ int moe_qdense_forward(moe_handle *h, const int8_t *x, const float *x_scales, in
   if (n_rows < 1 || n_rows > moe::kQdenseMaxRows) return MOE_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(x_scales, 4) || (y && !aligned(y, 2)) || (y32 && !aligned(y32, 4)))
     return MOE_ERR_INVALID_ARG;
-  if (!(softcap == softcap)) return MOE_ERR_INVALID_ARG;
+  if (!(softcap <= FLT_MAX)) return MOE_ERR_INVALID_ARG;
   const size_t need = moe::qdense_ws_bytes(n_rows, w->width);
   if (need) {
     if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
       __syncthreads();  // every thread is done with the segment before: the tables are clear
       if (kHist) {
         auto count = [&](int id, int i) {
-          const unsigned d = (unsigned)(id - v0);
+          const unsigned d = (unsigned)id - (unsigned)v0;
           if (d < (unsigned)n) {
             if (i < plen)
               atomicOr(cnt + d, kInPrompt);
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
       }
       if (kBias) {
         auto enter = [&](int id, int i) {
-          const unsigned d = (unsigned)(id - v0);
+          const unsigned d = (unsigned)id - (unsigned)v0;
           if (d < (unsigned)n) atomicMax(bix + d, (unsigned)(i + 1));
           bad_id = bad_id || (unsigned)id >= (unsigned)V;
         };

@@ -15,7 +15,8 @@
 // m and 2^j <= |127 u / m| < 2^(j+1), a quotient that is no half integer is
 // at least 2^(j-6) / (2 B) > 2^(j-23) away from one, and the rounding moves
 // it by at most 2^(j-24).  The codes are therefore those of exact arithmetic,
-// ties to even, whatever the order of the sums.
+// ties to even, whatever the order of the sums.  (Products below fp32's normal
+// range, 2^-126, round when they are formed.)
 //
 // The kernel multiplies by k = 127 / m and divides only the vectors that have a
 // product within 2^-14 of a half integer: k is within 2 roundings of its value
@@ -108,9 +109,10 @@ __global__ void __launch_bounds__(kVec <= 2 ? 1024 : 512) norm_quant_kernel(cons
     m = __reduce_max_sync(0xffffffffu, m);
   }
 
-  const bool bad = m >= kInfBits || !(tot < INFINITY);
   const float mf = __uint_as_float(m);
-  const float r = 1.0f / sqrtf(tot / (float)H + a.eps);
+  // (a row of zeros: 0, where eps = 0 would make it infinite)
+  const float r = m == 0u ? 0.0f : 1.0f / sqrtf(tot / (float)H + a.eps);
+  const bool bad = m >= kInfBits || !(tot < INFINITY) || !(r < INFINITY);
   if (tid == 0) {
     if (bad) set_error(a.err, kErrNonFinite);
     a.scales[row] = bad ? NAN : mf * r / 127.0f;
@@ -126,7 +128,7 @@ __global__ void __launch_bounds__(kVec <= 2 ? 1024 : 512) norm_quant_kernel(cons
     if (v >= nvec) continue;
     uint32_t qw[2] = {0u, 0u};
     if (!zeros) {
-      float far = 0.f, z[8];
+      float far = mf < 0x1p-80f ? 1.f : 0.f, z[8];  // (k may be out of range there)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float c = u[i][j] * k;

@@ -414,18 +414,21 @@ int moe_embed(moe_handle *h, const int32_t *ids, int n, const moe_head_weights *
  *   r = 1 / sqrt(mean(s^2) + eps),  m = max |u|
  *   q = rint(127 u / m)  (ties to even; zero for m = 0),  scale = m r / 127
  * so q * scale stands for the normalised row u r.  The codes are those of
- * exact arithmetic on the stored bf16 values.
+ * exact arithmetic on the stored bf16 values (products below 2^-126 round to
+ * fp32).
  *   hidden      bf16 [n_rows, width];  y nullable bf16 [n_rows, width]
  *   norm        nullable bf16 [width]
- *   eps         0 .. 1 (the layers use 1e-6)
+ *   eps         0 .. 1 (the layers use 1e-6; below 1e-30, rows whose values all
+ *               lie below 2^-50 lose accuracy to the range of fp32)
  *   hidden_out  nullable bf16 [n_rows, width]: s; may be hidden itself;
  *               only with y
  *   q           int8 [n_rows, width], -127 .. 127;  scales fp32 [n_rows]
  *   x_out       nullable bf16 [n_rows, width]: bf16(u r)
  * width: a multiple of 16, 16 .. 16384; n_rows 1 .. MOE_NORM_MAX_ROWS;
  * matrices and norm 16-byte aligned.  Other outputs must not overlap an
- * input.  A row with a NaN or an infinity in s or u, or whose sum of squares
- * passes the range of fp32, gets codes 0, scale NaN and x_out NaN (s is
+ * input.  A row of zeros has codes and scale 0.  A row with a NaN or an
+ * infinity in s or u, or whose sum of squares passes the range of fp32 (also
+ * below, with eps = 0), gets codes 0, scale NaN and x_out NaN (s is
  * written all the same) and records MOE_ERR_NONFINITE. */
 #define MOE_NORM_MAX_ROWS (1 << 20)
 int moe_norm_quant(moe_handle *h, const void *hidden, const void *y, int n_rows, int width, const void *norm,
@@ -445,14 +448,17 @@ size_t moe_qdense_workspace_bytes(const moe_qdense_weights *w, int n_rows);
 
 /* Dense projection of 8-bit rows:
  *   y[t, n] = cap(x_scales[t] * scales[n] * sum_k x[t, k] q[n, k])
- *   cap(z) = softcap * tanh(z / softcap), or z for softcap <= 0
+ *   cap(z) = softcap * tanh(z / softcap), or z for softcap <= 0 (finite)
  *   x         int8 [n_rows, K], 16-byte aligned;  x_scales fp32 [n_rows]
  *   n_rows    1 .. MOE_QDENSE_MAX_ROWS
  *   y         nullable bf16 [n_rows, N];  y32 nullable fp32 [n_rows, N];
  *             not both null
  *   ws        moe_qdense_workspace_bytes(w, n_rows) bytes, 256-byte aligned
  *             (null where that is 0)
- * Up to 8 rows the sums are exact 32-bit integers. */
+ * Outputs must not overlap an input or each other.  Up to 8 rows the sums are
+ * exact 32-bit integers; more rows are summed in fp32, exact while the partial
+ * sums stay below 2^24 (always, for K up to 1024).  Calls that may run at the
+ * same time need a workspace each. */
 #define MOE_QDENSE_MAX_ROWS 65536
 int moe_qdense_forward(moe_handle *h, const int8_t *x, const float *x_scales, int n_rows, const moe_qdense_weights *w,
                        float softcap, void *y, float *y32, void *ws, size_t ws_bytes, moe_stream_t stream);
@@ -490,7 +496,7 @@ typedef struct {
  *   logits   fp32 [n_rows, logits_stride], the first vocab (1 .. 2^28) of a
  *            row; n_rows 1 .. MOE_LOGITS_MAX_ROWS; logits_stride >= vocab
  *   out      nullable fp32 [n_rows, out_stride]; may be logits itself (with
- *            the same stride); columns from vocab on are left as they are
+ *            the same stride), else must not overlap it; columns from vocab on are left as they are
  *   tokens   nullable int32 [n_rows]: argmax, ties to the lower id; -1 where
  *            no logit is above -inf;  out and tokens not both null
  * A NaN or +inf that the mask does not remove is passed on, skipped by the

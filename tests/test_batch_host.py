@@ -71,7 +71,7 @@ def _qdense(lib, h, **kw):
     (dict(wq=A + 8), bq.MOE_ERR_INVALID_ARG), (dict(wsc=A + 2), bq.MOE_ERR_INVALID_ARG),
     (dict(x=A + 4), bq.MOE_ERR_INVALID_ARG), (dict(xs=A + 2), bq.MOE_ERR_INVALID_ARG),
     (dict(y=A + 1), bq.MOE_ERR_INVALID_ARG), (dict(y32=A + 2), bq.MOE_ERR_INVALID_ARG),
-    (dict(cap=math.nan), bq.MOE_ERR_INVALID_ARG)])
+    (dict(cap=math.nan), bq.MOE_ERR_INVALID_ARG), (dict(cap=math.inf), bq.MOE_ERR_INVALID_ARG)])
 def test_qdense_refuses(lib, handle, change, status):
     assert _qdense(lib, handle[0], **change) == status
     assert _qdense(lib, None, **change) in (status, bq.MOE_ERR_INVALID_ARG)

@@ -114,6 +114,32 @@ def test_far_ranges(moe, scale):
     check(got, BO.norm_quant(small, eps=float(np.float32(1e-6))))
 
 
+@pytest.mark.parametrize("top", [-100, -120, -125, -130])
+def test_smallest_rows(moe, top):
+    """Largest values of 2^top, down to bf16's subnormal numbers (steps of 2^-133)."""
+    rng = np.random.default_rng(-top)
+    step = max(2.0 ** (top - 7), 2.0 ** -133)
+    v = rng.integers(-round(2.0 ** top / step), round(2.0 ** top / step) + 1, (3, 320)) * step
+    v[:, 0] = 2.0 ** top
+    bits = to_bf16(v)
+    got, want = run(moe, bits, x_out=False), BO.norm_quant(bits, eps=float(np.float32(1e-6)))
+    assert np.array_equal(got["q"], want["q"])
+    # m r / 127 in fp32, a step of 2^-149 where it is subnormal
+    assert np.all(np.abs(got["scales"] - want["scales"]) <= REL * want["scales"] + 2.0 ** -149)
+
+
+def test_eps_zero(moe):
+    """Rows of zeros stay zeros; rows whose squares leave fp32's range are told."""
+    h = rows(8, 3, 320)
+    h[1] = 0
+    got, want = run(moe, h, eps=0.0, x_out=True), BO.norm_quant(h[[0, 2]], eps=0.0)
+    assert got["scales"][1] == 0.0 and not got["q"][1].any() and not got["x"][1].any()
+    check({k: (v[[0, 2]] if v is not None else None) for k, v in got.items()}, want)
+    small = to_bf16(np.full((1, 64), 2.0 ** -90))
+    got = run(moe, small, eps=0.0, x_out=False, status=bq.MOE_ERR_NONFINITE)
+    assert np.isnan(got["scales"]).all() and not got["q"].any()
+
+
 def test_zero_rows(moe):
     h = rows(4, 5, 320)
     h[2] = 0

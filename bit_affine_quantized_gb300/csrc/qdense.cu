@@ -33,12 +33,17 @@
 // A in tensor memory keeps the widened codes out of shared memory, whose
 // bandwidth is what a 128 x 256 fp16 tile asks most of.  Up to 64 rows HBM
 // bounds it (24 x 262144 x 2816: 125 us with a bf16 output, 5.9 TB/s of
-// codes), many rows the tiles' way into shared memory: 80 KB per 128 of K at
-// 64 bytes a clock are 1280 of the 1520 clocks that a 256-row stage takes, its
-// MMAs 1024 (4096 x 4096 x 2816: 67 us, 1420 TFLOP/s; a library product of
-// fp16 operands takes 53 us on such integers, 60 us on random values).  Forms
-// that were slower: A widened into shared memory, and pairs of blocks on one
-// tile.
+// codes).
+// More than 128 rows: a pair of blocks on a tile of 256 channels, each with 128
+// of them in its tensor memory and half of the rows in its shared memory, which
+// both read (cta_group::2).  A 256-row stage brings 48 KB into an SM's shared
+// memory, 768 clocks at 64 bytes each; single blocks would bring 80 KB, 1280
+// clocks, more than the stage's MMAs (1024), and took 4 to 9 % longer.  Of 4096
+// x 4096 x 2816's 63 us (1500 TFLOP/s; a library product of fp16 operands takes
+// 53 us on such integers, 60 us on random values) the widening of the rows is
+// 7, the stores of the outputs 6, and the rest runs at the rate that a library
+// product reaches.  Up to 128 rows pairs were 3 to 7 % slower than single
+// blocks.
 // Few tiles: the blocks of a cluster share a tile, each takes a part of K, and
 // the parts are added through distributed shared memory in rank order.
 #include <cuda.h>
@@ -330,6 +335,7 @@ cudaError_t launch_few(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl)
 
 // ------------------------------------------------------------------ rows to fp16
 constexpr int kWidenThreads = 256;
+constexpr int kWidenAhead = 4;  // loads of a thread in flight
 
 __global__ void __launch_bounds__(kWidenThreads) qdense_widen_kernel(const QdenseArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0) trace_min(a.trace, kTrEntry);
@@ -339,15 +345,23 @@ __global__ void __launch_bounds__(kWidenThreads) qdense_widen_kernel(const Qdens
   const size_t n = (size_t)a.T * (a.K / 16);
   const uint4 *src = reinterpret_cast<const uint4 *>(a.x);
   uint4 *dst = reinterpret_cast<uint4 *>(a.work);
-  for (size_t i = (size_t)blockIdx.x * kWidenThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kWidenThreads) {
-    const uint4 v = __ldcs(src + i);
-    uint4 o0, o1;
-    widen4(v.x, o0.x, o0.y);
-    widen4(v.y, o0.z, o0.w);
-    widen4(v.z, o1.x, o1.y);
-    widen4(v.w, o1.z, o1.w);
-    dst[2 * i] = o0;
-    dst[2 * i + 1] = o1;
+  const size_t step = (size_t)gridDim.x * kWidenThreads;
+  for (size_t i = (size_t)blockIdx.x * kWidenThreads + threadIdx.x; i < n; i += kWidenAhead * step) {
+    uint4 v[kWidenAhead];
+#pragma unroll
+    for (int j = 0; j < kWidenAhead; ++j)
+      if (i + j * step < n) v[j] = __ldcs(src + i + j * step);
+#pragma unroll
+    for (int j = 0; j < kWidenAhead; ++j) {
+      if (i + j * step >= n) break;
+      uint4 o0, o1;
+      widen4(v[j].x, o0.x, o0.y);
+      widen4(v[j].y, o0.z, o0.w);
+      widen4(v[j].z, o1.x, o1.y);
+      widen4(v[j].w, o1.z, o1.w);
+      dst[2 * (i + j * step)] = o0;
+      dst[2 * (i + j * step) + 1] = o1;
+    }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) trace_max(a.trace, kTrExit);
 }
@@ -373,18 +387,19 @@ constexpr int kMmXsBytes = kMmMaxN * 4;
 
 struct MmPlan {
   int n;            // rows per tile (the MMA N): a multiple of 16
-  int wst, rst;     // stages of weights and of rows
-  int rk;           // 64-wide steps of K per rows stage: 1 or 2
+  int wst, rst;     // stages of weights and of rows, 128 of K each
   int dbufs;        // sets of sums in tensor memory
   int split;        // blocks of a cluster that share a tile along K
   int ntile, ttile; // tiles of channels, of rows
   int whole, units; // units of work: `whole` tiles, then halves of tiles (by rows)
+  int pair;         // 1: pairs of blocks, tiles of 256 channels
+  int nload;        // rows that a block loads of a tile: n, or n / 2 in pairs
   int smem;
 };
 
 struct MmParams {
   CUtensorMap w;     // 8-bit codes {K, N}, box {128, 128}, 128-byte swizzle
-  CUtensorMap x[2];  // fp16 rows {K, T}, box {64, n} and {64, n / 2}, 128-byte swizzle
+  CUtensorMap x[2];  // fp16 rows {K, T}, box {64, nload} and {64, nload / 2}, 128-byte swizzle
   QdenseArgs a;
   MmPlan p;
 };
@@ -394,12 +409,13 @@ struct MmParams {
 struct MmUnit {
   int n0, t0, n, cnt, half;
 };
-__device__ __forceinline__ MmUnit mm_unit(const MmPlan &p, int T, int u) {
+template <bool kPair>
+__device__ __forceinline__ MmUnit mm_unit(const MmPlan &p, int T, int u, int rank) {
   MmUnit q;
   q.half = u >= p.whole ? 1 : 0;
   const int tile = q.half ? p.whole + (u - p.whole) / 2 : u;
   q.n = q.half ? p.n / 2 : p.n;
-  q.n0 = tile / p.ttile * kMmM;
+  q.n0 = (kPair ? tile / p.ttile * 2 + rank : tile / p.ttile) * kMmM;
   q.t0 = tile % p.ttile * p.n + (q.half ? ((u - p.whole) & 1) * q.n : 0);
   q.cnt = min(q.n, T - q.t0);  // none: a half past the last row, which every warp passes over
   return q;
@@ -407,20 +423,31 @@ __device__ __forceinline__ MmUnit mm_unit(const MmPlan &p, int T, int u) {
 
 // Bounded wait that suspends in hardware; the timer is read only once a wait
 // is not over at its first look (reading it costs more than most waits).
+// kCluster: blocks of the cluster arrive on the barrier, not this one alone.
+template <bool kCluster>
 __device__ __forceinline__ bool mm_try(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
+  if (kCluster)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, "
+        "p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
   return ok != 0;
 }
+template <bool kCluster = false>
 __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity) {
-  if (mm_try(bar, parity)) return true;
+  if (mm_try<kCluster>(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
   for (;;) {
-    if (mm_try(bar, parity)) return true;
+    if (mm_try<kCluster>(bar, parity)) return true;
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
 }
@@ -434,13 +461,51 @@ __device__ __forceinline__ void mm_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// D (tensor memory) += A (tensor memory, 128 x 16) * B (shared memory, n x 16)^T
+// D (tensor memory) += A (tensor memory, 128 x 16) * B (shared memory, n x 16)^T;
+// kPair: A is 256 x 16 and B n x 16, a half of each in either block's memory.
+template <bool kPair>
 __device__ __forceinline__ void mm_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-          d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+  if (kPair)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+            d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+            d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Arrives on `bar` (kPair: in both blocks) once the MMAs issued before are complete.
+template <bool kPair>
+__device__ __forceinline__ void mm_commit(uint64_t *bar) {
+  if (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    dense::tc_commit(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void mm_alloc(uint32_t *dst) {
+  if (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    dense::tc_alloc(dst, 512);
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void mm_dealloc(uint32_t tmem) {
+  if (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  else
+    dense::tc_dealloc(tmem, 512);
 }
 
 // 32 registers of each lane to 32 tensor-memory columns of the warp's lanes
@@ -471,6 +536,9 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
   return at;
 }
+__device__ __forceinline__ void cluster_arrive(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
 __device__ __forceinline__ void cluster_st(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -478,13 +546,14 @@ __device__ __forceinline__ void cluster_st(uint32_t addr, float v) {
 // Rows of a shared tile that one block of the cluster adds up.
 __host__ __device__ inline int mm_quota(const MmPlan &p) { return (p.n + p.split - 1) / p.split; }
 
+template <bool kPair>
 __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_constant__ MmParams prm) {
   extern __shared__ __align__(1024) uint8_t msm[];
   const QdenseArgs &a = prm.a;
   const MmPlan &P = prm.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *base = msm + ((1024u - (smem_addr(msm) & 1023u)) & 1023u);
-  const int rstep = P.n * 128, rstage = P.rk * rstep;  // a rows stage: rk steps of 64 of K
+  const int rstep = P.nload * 128, rstage = 2 * rstep;  // a rows stage: two steps of 64 of K
   uint8_t *wbuf = base, *rbuf = base + P.wst * kMmWStage;
   uint64_t *bar = reinterpret_cast<uint64_t *>(rbuf + P.rst * rstage);
   uint64_t *wfull = bar, *wempty = wfull + P.wst, *rfull = wempty + P.wst, *rempty = rfull + P.rst;
@@ -494,24 +563,30 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   float *s_xs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bar) + kMmBarBytes);  // [n] row scales
   float *s_part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(s_xs) + kMmXsBytes);  // [split][quota][128]
   const bool tracer = blockIdx.x == 0 && tid == 0;
+  const int split = kPair ? 1 : P.split;
+  const int rank = kPair || split > 1 ? (int)cluster_rank() : 0;
+  const int part = kPair ? 0 : rank;  // this block's part of K
+  const bool leader = !kPair || rank == 0;
 
-  {
-    // arrivals per phase, in the order of the barriers
-    const int nb = 2 * P.wst + 2 * P.rst + 2 * kMmABufs + 5;
-    if (tid < nb) {
-      uint64_t *b = bar + tid;
-      mbar_init(b, b >= wempty && b < rfull ? kMmWiden : b >= afull && b < aempty ? kMmWiden : b >= dempty && b < tready ? kMmFin : 1);
-      fence_mbar_init();
-    }
+  if (tid < 2 * P.wst + 2 * P.rst + 2 * kMmABufs + 5) {
+    // arrivals per phase.  The leader of a pair hears of both blocks' A tiles,
+    // rows (its own copies, and a word from the other block) and finish warps.
+    uint64_t *b = bar + tid;
+    int n = 1;
+    if ((b >= wempty && b < rfull) || (b >= afull && b < aempty)) n = kMmWiden;
+    if (b >= dempty && b < tready) n = kMmFin;
+    if (kPair && leader && ((b >= rfull && b < rempty) || (b >= afull && b < aempty) || (b >= dempty && b < tready)))
+      n *= 2;
+    mbar_init(b, n);
+    fence_mbar_init();
   }
   __syncthreads();
   if (tracer) trace_min(a.trace, kTrEntry);
   pdl_launch_dependents();
 
-  const int split = P.split;
-  const int part = split > 1 ? (int)cluster_rank() : 0;
-  if (split > 1) cluster_sync_all();  // every block of the cluster runs: its shared memory can be written
-  const int first = blockIdx.x / split, stride = gridDim.x / split;  // units of this block
+  if (kPair || split > 1) cluster_sync_all();  // every block of the cluster runs, its barriers are set
+  const int csize = kPair ? 2 : split;
+  const int first = blockIdx.x / csize, stride = gridDim.x / csize;  // units of this block
   const int units = P.units;
   const int nst = (a.K + kMmK - 1) / kMmK, st0 = nst * part / split, st1 = nst * (part + 1) / split;  // its part of K
   const int g0 = 2 * st0, g1 = min(2 * st1, (a.K + 63) / 64);  // the same in steps of 64
@@ -525,7 +600,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       bool ok = true;
       int st = 0, ph = 0, issued = 0;
       for (int u = first; u < units && ok; u += stride) {
-        const MmUnit q = mm_unit(P, a.T, u);
+        const MmUnit q = mm_unit<kPair>(P, a.T, u, rank);
         if (q.cnt <= 0) continue;
         for (int s = st0; s < st1; ++s, ++issued) {
           if (issued >= P.wst && !(ok = mm_wait(&wempty[st], ph ^ 1))) break;
@@ -550,14 +625,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       bool ok = true;
       int st = 0, ph = 0, issued = 0;
       for (int u = first; u < units && ok; u += stride) {
-        const MmUnit q = mm_unit(P, a.T, u);
+        const MmUnit q = mm_unit<kPair>(P, a.T, u, rank);
         if (q.cnt <= 0) continue;
-        for (int g = g0; g < g1; g += P.rk, ++issued) {
+        const int rows = kPair ? q.n / 2 : q.n, t0 = q.t0 + (kPair ? rank * rows : 0);
+        for (int g = g0; g < g1; g += 2, ++issued) {
           if (issued >= P.rst && !(ok = mm_wait(&rempty[st], ph ^ 1))) break;
-          const int h = min(P.rk, g1 - g);
-          mbar_arrive_expect_tx(&rfull[st], (uint32_t)(h * q.n * 128));
+          const int h = min(2, g1 - g);
+          mbar_arrive_expect_tx(&rfull[st], (uint32_t)(h * rows * 128));
           for (int i = 0; i < h; ++i)
-            dense::tma_load_2d(rbuf + st * rstage + i * rstep, &prm.x[q.half], 64 * (g + i), q.t0, &rfull[st]);
+            dense::tma_load_2d(rbuf + st * rstage + i * rstep, &prm.x[q.half], 64 * (g + i), t0, &rfull[st]);
           if (++st == P.rst) {
             st = 0;
             ph ^= 1;
@@ -565,11 +641,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
         }
       }
       if (!ok) set_error(a.err, kErrTimeout);
-      for (int j = max(0, issued - P.rst); j < issued; ++j) mm_wait(&rfull[j % P.rst], (j / P.rst) & 1);
+      for (int j = max(0, issued - P.rst); j < issued; ++j) mm_wait<kPair>(&rfull[j % P.rst], (j / P.rst) & 1);
     }
   } else if (warp == kMmMma) {
     // ============================================================ MMA
-    dense::tc_alloc(s_tmem, 512);
+    mm_alloc<kPair>(s_tmem);
     dense::tc_fence_before();
     __syncwarp();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
@@ -581,46 +657,48 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     const uint64_t bdesc0 = dense::sdesc(smem_addr(rbuf), 16, 1024, 2);
     bool ok = true;
     int gi = 0, du = 0, st = 0, ph = 0, ab = 0, aph = 0;
-    for (int u = first; u < units; u += stride) {
-      const MmUnit q = mm_unit(P, a.T, u);
+    if (!leader) {
+      // the other block of a pair: passes on that its rows have landed
+      for (int u = first; u < units && ok; u += stride) {
+        if (mm_unit<kPair>(P, a.T, u, rank).cnt <= 0) continue;
+        for (int s = st0; s < st1; ++s) {
+          if (!(ok = __all_sync(0xffffffffu, mm_wait(&rfull[st], ph)))) break;
+          if (lane == 0) cluster_arrive(cluster_map(smem_addr(&rfull[st]), 0));
+          if (++st == P.rst) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    }
+    for (int u = first; leader && u < units; u += stride) {
+      const MmUnit q = mm_unit<kPair>(P, a.T, u, rank);
       if (q.cnt <= 0) continue;
-      const uint32_t idesc = dense::idesc_f16(kMmM, q.n);
+      const uint32_t idesc = dense::idesc_f16(kPair ? 2 * kMmM : kMmM, q.n);
       const int db = du % P.dbufs;
-      if (du >= P.dbufs) ok = __all_sync(0xffffffffu, mm_wait(&dempty[db], ((du / P.dbufs) - 1) & 1));
+      if (du >= P.dbufs) ok = __all_sync(0xffffffffu, mm_wait<kPair>(&dempty[db], ((du / P.dbufs) - 1) & 1));
       if (!ok) break;
       ++du;
       const uint32_t acc = tmem + db * 128;
       for (int s = st0; s < st1; ++s, ++gi) {
-        ok = __all_sync(0xffffffffu, mm_wait(&rfull[st], ph) && mm_wait(&afull[ab], aph));
+        ok = __all_sync(0xffffffffu, mm_wait<kPair>(&rfull[st], ph) && mm_wait<kPair>(&afull[ab], aph));
         if (!ok) break;
         dense::tc_fence_after();
         const uint32_t ad = tmem + kMmACol + 64 * ab;
         uint64_t bd = bdesc0 + (uint64_t)((st * rstage) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)  // K = 16 per MMA: 8 columns of A, 32 bytes of B's rows
-          if (elect_one()) mm_mma(acc, ad + 8 * ks, bd + 2 * ks, idesc, (s > st0 || ks > 0) ? 1u : 0u);
+          if (elect_one()) mm_mma<kPair>(acc, ad + 8 * ks, bd + 2 * ks, idesc, (s > st0 || ks > 0) ? 1u : 0u);
         if (2 * s + 1 < g1) {  // the stage's second half
-          if (P.rk == 1) {
-            if (elect_one()) dense::tc_commit(&rempty[st]);
-            if (++st == P.rst) {
-              st = 0;
-              ph ^= 1;
-            }
-            ok = __all_sync(0xffffffffu, mm_wait(&rfull[st], ph));
-            if (!ok) break;
-            dense::tc_fence_after();
-            bd = bdesc0 + (uint64_t)((st * rstage) >> 4);
-          } else {
-            bd += (uint64_t)(rstep >> 4);
-          }
+          bd += (uint64_t)(rstep >> 4);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            if (elect_one()) mm_mma(acc, ad + 32 + 8 * ks, bd + 2 * ks, idesc, 1u);
+            if (elect_one()) mm_mma<kPair>(acc, ad + 32 + 8 * ks, bd + 2 * ks, idesc, 1u);
         }
         if (elect_one()) {
-          dense::tc_commit(&rempty[st]);
-          dense::tc_commit(&aempty[ab]);
-          if (s == st1 - 1) dense::tc_commit(&dfull[db]);
+          mm_commit<kPair>(&rempty[st]);
+          mm_commit<kPair>(&aempty[ab]);
+          if (s == st1 - 1) mm_commit<kPair>(&dfull[db]);
         }
         __syncwarp();
         if (++st == P.rst) {
@@ -637,10 +715,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
     // the last MMAs are complete and the sums read before the memory goes back (bounded waits)
     if (gi > 0) mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1);
-    if (du > 0) mm_wait(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
+    if (du > 0) mm_wait<kPair>(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
     dense::tc_fence_after();
     __syncwarp();
-    dense::tc_dealloc(tmem, 512);
+    if (!kPair) mm_dealloc<kPair>(tmem);
   } else if (warp >= kMmFin0) {
     // ============================================================ finish
     // Warp w reads tensor-memory lanes 32 (w % 4) .. +31: channels n0 + rr; the
@@ -652,7 +730,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     const int rr = 32 * (warp & 3) + lane, ft = tid - kMmFin0 * 32, side = (warp - kMmFin0) >> 2;
     int du = 0;
     for (int u = first; u < units; u += stride) {
-      const MmUnit q = mm_unit(P, a.T, u);
+      const MmUnit q = mm_unit<kPair>(P, a.T, u, rank);
       if (q.cnt <= 0) continue;
       const int n = q.n0 + rr, t0 = q.t0, cnt = q.cnt;
       const int db = du % P.dbufs;
@@ -686,38 +764,42 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
           float v[32];
           dense::tc_ld32(ta + c0, v);  // (columns past the tile's: not used)
           const int m = min(32, cnt - c0);
-          if (n < a.N) {
-            const size_t o = (size_t)(t0 + c0) * a.N + n;
+          if (n >= a.N) continue;
+          const size_t o = (size_t)(t0 + c0) * a.N + n;
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 xs = *reinterpret_cast<const float4 *>(s_xs + c0 + j);
-              v[j] = __fmul_rn(__fmul_rn(v[j], xs.x), ws);
-              v[j + 1] = __fmul_rn(__fmul_rn(v[j + 1], xs.y), ws);
-              v[j + 2] = __fmul_rn(__fmul_rn(v[j + 2], xs.z), ws);
-              v[j + 3] = __fmul_rn(__fmul_rn(v[j + 3], xs.w), ws);
-            }
-            if (a.softcap > 0.f) {
+          for (int j = 0; j < 32; j += 4) {
+            const float4 xs = *reinterpret_cast<const float4 *>(s_xs + c0 + j);
+            v[j] = __fmul_rn(__fmul_rn(v[j], xs.x), ws);
+            v[j + 1] = __fmul_rn(__fmul_rn(v[j + 1], xs.y), ws);
+            v[j + 2] = __fmul_rn(__fmul_rn(v[j + 2], xs.z), ws);
+            v[j + 3] = __fmul_rn(__fmul_rn(v[j + 3], xs.w), ws);
+          }
+          if (a.softcap > 0.f) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = a.softcap * tanhf(v[j] / a.softcap);
-            }
-            if (a.y32) {
-              float *p = a.y32 + o;
+            for (int j = 0; j < 32; ++j) v[j] = a.softcap * tanhf(v[j] / a.softcap);
+          }
+          if (a.y32) {
+            float *p = a.y32 + o;
 #pragma unroll
-              for (int j = 0; j < 32; ++j, p += a.N)
-                if (j < m) *p = v[j];
-            }
-            if (a.y) {
-              uint16_t *p = a.y + o;
+            for (int j = 0; j < 32; ++j, p += a.N)
+              if (j < m) *p = v[j];
+          }
+          if (a.y) {
+            uint16_t *p = a.y + o;
 #pragma unroll
-              for (int j = 0; j < 32; ++j, p += a.N)
-                if (j < m) *p = float_to_bf16_bits(v[j]);
-            }
+            for (int j = 0; j < 32; ++j, p += a.N)
+              if (j < m) *p = float_to_bf16_bits(v[j]);
           }
         }
       }
       dense::tc_fence_before();
       __syncwarp();
-      if (lane == 0) mm_arrive(&dempty[db]);
+      if (lane == 0) {
+        if (leader)
+          mm_arrive(&dempty[db]);
+        else
+          cluster_arrive(cluster_map(smem_addr(&dempty[db]), 0));
+      }
       ++du;
     }
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
@@ -736,11 +818,16 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       mm_st_wait();
       dense::tc_fence_before();
       __syncwarp();
-      if (lane == 0) mm_arrive(&afull[told % kMmABufs]);
+      if (lane == 0) {
+        if (leader)
+          mm_arrive(&afull[told % kMmABufs]);
+        else
+          cluster_arrive(cluster_map(smem_addr(&afull[told % kMmABufs]), 0));
+      }
       ++told;
     };
     for (int u = first; u < units && ok; u += stride) {
-      if (mm_unit(P, a.T, u).cnt <= 0) continue;
+      if (mm_unit<kPair>(P, a.T, u, rank).cnt <= 0) continue;
       for (int s = st0; s < st1 && ok; ++s, ++gi) {
         ok = mm_wait(&wfull[st], ph);
         const uint8_t *row = wbuf + st * kMmWStage + rr * 128;
@@ -776,11 +863,20 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
   }
 
-  if (split > 1) {
+  if (kPair) {
+    // neither block leaves, or frees its tensor memory, while the other may
+    // still arrive on its barriers or the leader's MMAs use it
+    __syncwarp();
+    dense::tc_fence_before();
+    cluster_sync_all();
+    dense::tc_fence_after();
+    if (warp == kMmMma) mm_dealloc<kPair>(*reinterpret_cast<volatile uint32_t *>(s_tmem));
+  }
+  if (!kPair && split > 1) {
     // One tile per cluster; this block adds the parts of its rows, a warp to a
     // row, four channels per lane.
     __syncwarp();
-    const MmUnit q = mm_unit(P, a.T, first);
+    const MmUnit q = mm_unit<kPair>(P, a.T, first, rank);
     const int n0 = q.n0, t0 = q.t0, cnt = q.cnt;
     const int quota = mm_quota(P), r0 = part * quota, mine = min(quota, cnt - r0);
     float ws[4];
@@ -810,8 +906,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   if (tracer) trace_max(a.trace, kTrExit);
 }
 
-// Tiles of up to 256 rows where they fill the device: a 128-wide K stage takes
-// 0.45 us at 128 rows, 0.75 us at 256.
+// Tiles of up to 256 rows where they fill the device, by pairs of blocks above
+// 128: a 128-wide K stage takes 0.45 us at 128 rows, 0.65 us at 256.
 //
 // Fewer tiles than half the SMs: up to 128 rows per tile, and a cluster of
 // `split` blocks per tile if that pays: the stages (0.36 us there) go down by
@@ -823,7 +919,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
 // those would run in a second wave: 16 tiles in clusters of 8 took 15.7 us, in
 // clusters of 4 10.4).
 //
-// The last round of tiles, if at most half the SMs have one: in halves.
+// The last round of tiles of pairs, if at most half the pairs have one: in
+// halves.
 MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   MmPlan p;
   auto tiles = [&](int most) {
@@ -845,23 +942,26 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
       }
     }
   }
+  p.pair = p.n > 128;  // (split tiles are narrower)
+  int room = n_sm;  // units at once
+  if (p.pair) {
+    p.ntile = (p.ntile + 1) / 2;
+    p.n = (p.n + 31) / 32 * 32;
+    room = clusters[2];
+  }
   p.whole = p.ntile * p.ttile;
   p.units = p.whole;
-  const int rest = p.whole % n_sm;
-  if (p.whole > n_sm && rest > 0 && 2 * rest <= n_sm && p.n > 128) {
-    p.n = (p.n + 31) / 32 * 32;
+  const int rest = p.whole % room;
+  if (p.pair && p.whole > room && rest > 0 && 2 * rest <= room) {
+    p.n = (p.n + 63) / 64 * 64;
     p.whole -= rest;
     p.units = p.whole + 2 * rest;
   }
+  p.nload = p.pair ? p.n / 2 : p.n;
   p.dbufs = p.n <= 128 ? 2 : 1;
-  // Rows stages: many rows come in smaller pieces, more of which are on their
-  // way (256 x 19456 x 16384: 103 us against 117); few rows in larger ones, as
-  // every stage costs the MMA warp a wait and a commit (128 x 65536 x 2816: 44
-  // us against 50).
-  p.rk = p.n > 128 ? 1 : 2;
-  p.wst = p.n > 128 ? 4 : 5;
-  p.rst = p.n > 128 ? 4 : p.split > 1 ? 2 : 3;
-  p.smem = p.wst * kMmWStage + p.rst * p.rk * p.n * 128 + kMmBarBytes + kMmXsBytes + 1024 +
+  p.wst = 5;
+  p.rst = p.pair ? 4 : p.split > 1 ? 2 : 3;
+  p.smem = p.wst * kMmWStage + p.rst * 2 * p.nload * 128 + kMmBarBytes + kMmXsBytes + 1024 +
            (p.split > 1 ? p.split * mm_quota(p) * kMmM * 4 : 0);
   return p;
 }
@@ -875,7 +975,7 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, const int *clusters, cudaS
   const MmPlan &p = prm.p = mm_plan(a.T, a.N, a.K, n_sm, clusters);
   const cuuint64_t dw[2] = {(cuuint64_t)a.K, (cuuint64_t)a.N}, sw[1] = {(cuuint64_t)a.K};
   const cuuint64_t dx[2] = {(cuuint64_t)a.K, (cuuint64_t)a.T}, sx[1] = {(cuuint64_t)a.K * 2};
-  const cuuint32_t bw[2] = {128, kMmM}, bx[2] = {64, (cuuint32_t)p.n}, by[2] = {64, (cuuint32_t)p.n / 2};
+  const cuuint32_t bw[2] = {128, kMmM}, bx[2] = {64, (cuuint32_t)p.nload}, by[2] = {64, (cuuint32_t)p.nload / 2};
   if (!encode_map(f, &prm.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.w, dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map(f, &prm.x[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map(f, &prm.x[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, by, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -888,7 +988,9 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, const int *clusters, cudaS
   if (prm.a.trace) prm.a.trace += 4;
   const int units = p.units;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.split > 1 ? units * p.split : (units < n_sm ? units : n_sm));
+  const int room = p.pair ? clusters[2] : n_sm;
+  const int csize = p.pair ? 2 : p.split;
+  cfg.gridDim = dim3(p.split > 1 ? units * p.split : (units < room ? units : room) * csize);
   cfg.blockDim = dim3(kMmThreads);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
@@ -898,15 +1000,15 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, const int *clusters, cudaS
     attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[n++].val.programmaticStreamSerializationAllowed = 1;
   }
-  if (p.split > 1) {
+  if (csize > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = p.split;
+    attr[n].val.clusterDim.x = csize;
     attr[n].val.clusterDim.y = 1;
     attr[n++].val.clusterDim.z = 1;
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, qdense_mma_kernel, prm);
+  return cudaLaunchKernelEx(&cfg, p.pair ? qdense_mma_kernel<true> : qdense_mma_kernel<false>, prm);
 }
 }  // namespace
 
@@ -914,7 +1016,8 @@ cudaError_t qdense_set_attributes(int *clusters) {
   cudaError_t e;
   if ((e = set_rows_attr<1>()) || (e = set_rows_attr<2>()) || (e = set_rows_attr<4>()) || (e = set_rows_attr<8>()) ||
       (e = cudaFuncSetAttribute(qdense_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQfSmemMax)) ||
-      (e = cudaFuncSetAttribute(qdense_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)))
+      (e = cudaFuncSetAttribute(qdense_mma_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)) ||
+      (e = cudaFuncSetAttribute(qdense_mma_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)))
     return e;
   for (int s = 0; s <= kQdenseMaxCluster; ++s) {
     clusters[s] = 0;
@@ -930,8 +1033,10 @@ cudaError_t qdense_set_attributes(int *clusters) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaOccupancyMaxActiveClusters(&clusters[s], qdense_mma_kernel, &cfg))) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters[s], s == 2 ? qdense_mma_kernel<true> : qdense_mma_kernel<false>, &cfg)))
+      return e;
   }
+  if (clusters[2] < 1) return cudaErrorInvalidConfiguration;
   return cudaSuccess;
 }
 

@@ -68,25 +68,6 @@ __device__ __forceinline__ float lg_apply(float l, unsigned c, unsigned b, const
   return l;
 }
 
-// The rules on the few of four neighbouring logits that one of them names:
-// most groups have none, and a loop over those that are keeps the division
-// and the branches off the others.
-__device__ __forceinline__ void lg_touched(float (&x)[4], uint4 c, uint4 b, const RowRules &r) {
-  unsigned todo = ((c.x | b.x) ? 1u : 0u) | ((c.y | b.y) ? 2u : 0u) | ((c.z | b.z) ? 4u : 0u) | ((c.w | b.w) ? 8u : 0u);
-  while (todo) {
-    const int k = __ffs(todo) - 1;
-    todo &= todo - 1;
-    const float l = k == 0 ? x[0] : k == 1 ? x[1] : k == 2 ? x[2] : x[3];
-    const unsigned ck = k == 0 ? c.x : k == 1 ? c.y : k == 2 ? c.z : c.w;
-    const unsigned bk = k == 0 ? b.x : k == 1 ? b.y : k == 2 ? b.z : b.w;
-    const float v = lg_apply(l, ck, bk, r);
-    x[0] = k == 0 ? v : x[0];
-    x[1] = k == 1 ? v : x[1];
-    x[2] = k == 2 ? v : x[2];
-    x[3] = k == 3 ? v : x[3];
-  }
-}
-
 // The larger of two, NaN if one of them is.
 __device__ __forceinline__ float lg_max(float a, float b) {
   float r;
@@ -118,8 +99,9 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
   const int seg = a.seg * kLgSlice;
   float *const ring = reinterpret_cast<float *>(lsm) + own;
   unsigned *const cnt = lsm + kLgRing * kLgSlice, *const bix = cnt + (kHist ? seg : 0);
+  unsigned *const bits = bix + (kBias ? seg : 0);  // one per token: a rule names it
   // mask words of the slices in the ring, per group four for the 128 tokens of a warp
-  uint32_t *const mring = bix + (kBias ? seg : 0) + (tid >> 5) * 4;
+  uint32_t *const mring = bits + (kHist || kBias ? seg / 32 : 0) + (tid >> 5) * 4;
   constexpr int kMaskGroup = kLgGroup / 32;
   const bool tracer = blockIdx.x == 0 && tid == 0;
   if (tracer) trace_min(a.trace, kTrEntry);
@@ -127,7 +109,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
   const long long units = (long long)ns * a.T;
   const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
   if (kHist || kBias)
-    for (int i = tid; i < ((kHist ? 1 : 0) + (kBias ? 1 : 0)) * seg / 4; i += kLgThreads)
+    for (int i = tid; i < (((kHist ? 1 : 0) + (kBias ? 1 : 0)) * seg + seg / 32) / 4; i += kLgThreads)
       reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
   pdl_wait();
   pdl_launch_dependents();
@@ -182,6 +164,11 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
   float best = -INFINITY;  // the thread's best of the row so far
   int best_id = 0;
   int place = 0;  // of the slice to read, in the ring
+  // Of the warp's tokens of a slice, eight whose rules this lane applies (they
+  // are copied and read by the warp's lanes alone).
+  const int pg = (tid >> 4) & 1, pk = (tid >> 2) & 3, pb = 8 * (tid & 3);
+  const int patch = pg * kLgGroup + (kQuad ? (tid & ~31) * 4 + pk * 32 : pk * kLgThreads + (tid & ~31)) + pb;
+  static_assert(kLgGroups == 2, "a warp's 256 tokens of a slice: eight per lane");
   for (long long u = u0; u < u1; ++u) {
     const int v0 = sg * seg, n = min(seg, V - v0);
     // this thread's places of the segment's first slice
@@ -217,6 +204,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
               atomicOr(cnt + d, kInPrompt);
             else
               atomicAdd(cnt + d, 1u);
+            atomicOr(bits + (d >> 5), 1u << (d & 31u));
           }
           bad_id = bad_id || (unsigned)id >= (unsigned)V;
         };
@@ -242,7 +230,10 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
       if (kBias) {
         auto enter = [&](int id, int i) {
           const unsigned d = (unsigned)id - (unsigned)v0;
-          if (d < (unsigned)n) atomicMax(bix + d, (unsigned)(i + 1));
+          if (d < (unsigned)n) {
+            atomicMax(bix + d, (unsigned)(i + 1));
+            atomicOr(bits + (d >> 5), 1u << (d & 31u));
+          }
           bad_id = bad_id || (unsigned)id >= (unsigned)V;
         };
         if (tid < blen) enter(bv, tid);
@@ -251,17 +242,33 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
       }
       __syncthreads();  // the tables are complete
     }
-    unsigned *ci = cnt + own, *bi = bix + own;
     int v = v0 + own;
+    int at = patch;  // this lane's eight, in the segment
     // one slice; `whole`: all its tokens are there, else `left` of them
     auto slice = [&](auto whole, int left) {
       constexpr bool kWhole = decltype(whole)::value;
       copy_next((place + kLgRing - 1) % kLgRing);  // into the place that the thread read last
       lg_wait<kLgRing - 1>();                      // the thread's part of this slice has landed
-      if (kMask) __syncwarp();                     // and its warp's mask words
+      if (kMask || kHist || kBias) __syncwarp();   // and its warp's
+      if (kHist || kBias) {
+        uint8_t *const byte = reinterpret_cast<uint8_t *>(bits) + (at >> 3);
+        unsigned todo = *byte;
+        if (todo != 0u) {
+          *byte = 0;
+          float *const lg = reinterpret_cast<float *>(lsm) + place * kLgSlice + patch;
+          do {
+            const int k = __ffs(todo) - 1;
+            todo &= todo - 1u;
+            lg[k] = lg_apply(lg[k], kHist ? cnt[at + k] : 0u, kBias ? bix[at + k] : 0u, rr);
+            if (kHist) cnt[at + k] = 0u;
+            if (kBias) bix[at + k] = 0u;
+          } while (todo != 0u);
+        }
+        at += kLgSlice;
+        __syncwarp();
+      }
       const uint32_t *words = mring + place * kMaskSlice;
       const float *from = ring + place * kLgSlice;
-      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
       for (int g = 0; g < kLgGroups; ++g) {
         uint32_t m = 15u;
@@ -274,36 +281,17 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
             m = ((w.x >> i) & 1u) | (((w.y >> i) & 1u) << 1) | (((w.z >> i) & 1u) << 2) | (((w.w >> i) & 1u) << 3);
           }
         }
-        uint4 c = none, b = none;
         float l[4];
         const float *in = from + g * kLgGroup;
-        unsigned *cg = ci + g * kLgGroup, *bg = bi + g * kLgGroup;
         if (kQuad) {
           const float4 f = *reinterpret_cast<const float4 *>(in);
           l[0] = f.x;
           l[1] = f.y;
           l[2] = f.z;
           l[3] = f.w;
-          if (kHist) c = *reinterpret_cast<const uint4 *>(cg);
-          if (kBias) b = *reinterpret_cast<const uint4 *>(bg);
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) l[k] = in[k * kStep];
-          if (kHist) c = make_uint4(cg[0], cg[kStep], cg[2 * kStep], cg[3 * kStep]);
-          if (kBias) b = make_uint4(bg[0], bg[kStep], bg[2 * kStep], bg[3 * kStep]);
-        }
-        if ((kHist || kBias) && (c.x | c.y | c.z | c.w | b.x | b.y | b.z | b.w) != 0u) {
-          lg_touched(l, c, b, rr);
-          if (kQuad) {
-            if (kHist) *reinterpret_cast<uint4 *>(cg) = none;
-            if (kBias) *reinterpret_cast<uint4 *>(bg) = none;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (kHist) cg[k * kStep] = 0u;
-              if (kBias) bg[k * kStep] = 0u;
-            }
-          }
         }
         if (kMask) {
 #pragma unroll
@@ -343,8 +331,6 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
       place = (place + 1) % kLgRing;
       if (out) out += kLgSlice;
       v += kLgSlice;
-      ci += kLgSlice;
-      bi += kLgSlice;
     };
     int left = n;
     for (; left >= kLgSlice; left -= kLgSlice) slice(std::true_type{}, left);
@@ -392,7 +378,8 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
 }
 
 size_t lg_smem(bool h, bool b, int seg) {
-  return (size_t)kLgSlice * 4 * (kLgRing + seg * ((h ? 1 : 0) + (b ? 1 : 0))) + (size_t)kLgRing * kMaskSlice * 4;
+  return (size_t)kLgSlice * 4 * (kLgRing + seg * ((h ? 1 : 0) + (b ? 1 : 0))) + (h || b ? (size_t)kLgSlice / 8 * seg : 0) +
+         (size_t)kLgRing * kMaskSlice * 4;
 }
 
 using LgKernel = void (*)(const LogitsArgs);

@@ -39,9 +39,9 @@
 // both read (cta_group::2).  A 256-row stage brings 48 KB into an SM's shared
 // memory, 768 clocks at 64 bytes each; single blocks would bring 80 KB, 1280
 // clocks, more than the stage's MMAs (1024), and took 4 to 9 % longer.  Of 4096
-// x 4096 x 2816's 63 us (1500 TFLOP/s; a library product of fp16 operands takes
+// x 4096 x 2816's 62 us (1530 TFLOP/s; a library product of fp16 operands takes
 // 53 us on such integers, 60 us on random values) the widening of the rows is
-// 7, the stores of the outputs 6, and the rest runs at the rate that a library
+// 6, the stores of the outputs 6, and the rest runs at the rate that a library
 // product reaches.  Up to 128 rows pairs were 3 to 7 % slower than single
 // blocks.
 // Few tiles: the blocks of a cluster share a tile, each takes a part of K, and
@@ -335,32 +335,31 @@ cudaError_t launch_few(const QdenseArgs &a, int n_sm, cudaStream_t st, bool pdl)
 
 // ------------------------------------------------------------------ rows to fp16
 constexpr int kWidenThreads = 256;
-constexpr int kWidenAhead = 4;  // loads of a thread in flight
+constexpr int kWidenAhead = 2;  // loads of a thread in flight
 
+// (16 bytes per thread and store, whole lines per warp: from 16 codes per
+// thread, in two stores, 4096 x 2816 took 1.5 us longer)
 __global__ void __launch_bounds__(kWidenThreads) qdense_widen_kernel(const QdenseArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0) trace_min(a.trace, kTrEntry);
   pdl_wait();
   pdl_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) trace_min(a.trace, kTrWaited);
-  const size_t n = (size_t)a.T * (a.K / 16);
-  const uint4 *src = reinterpret_cast<const uint4 *>(a.x);
+  const size_t n = (size_t)a.T * (a.K / 8);
+  const uint2 *src = reinterpret_cast<const uint2 *>(a.x);
   uint4 *dst = reinterpret_cast<uint4 *>(a.work);
   const size_t step = (size_t)gridDim.x * kWidenThreads;
   for (size_t i = (size_t)blockIdx.x * kWidenThreads + threadIdx.x; i < n; i += kWidenAhead * step) {
-    uint4 v[kWidenAhead];
+    uint2 v[kWidenAhead];
 #pragma unroll
     for (int j = 0; j < kWidenAhead; ++j)
       if (i + j * step < n) v[j] = __ldcs(src + i + j * step);
 #pragma unroll
     for (int j = 0; j < kWidenAhead; ++j) {
       if (i + j * step >= n) break;
-      uint4 o0, o1;
-      widen4(v[j].x, o0.x, o0.y);
-      widen4(v[j].y, o0.z, o0.w);
-      widen4(v[j].z, o1.x, o1.y);
-      widen4(v[j].w, o1.z, o1.w);
-      dst[2 * (i + j * step)] = o0;
-      dst[2 * (i + j * step) + 1] = o1;
+      uint4 o;
+      widen4(v[j].x, o.x, o.y);
+      widen4(v[j].y, o.z, o.w);
+      dst[i + j * step] = o;
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) trace_max(a.trace, kTrExit);
@@ -980,7 +979,7 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, const int *clusters, cudaS
       !encode_map(f, &prm.x[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode_map(f, &prm.x[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, by, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const size_t pieces = (size_t)a.T * (a.K / 16), blocks = (pieces + kWidenThreads - 1) / kWidenThreads;
+  const size_t pieces = (size_t)a.T * (a.K / 8), blocks = (pieces + kWidenThreads - 1) / kWidenThreads;
   const size_t most = (size_t)n_sm * 8;
   cudaError_t e = launch_k(qdense_widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kWidenThreads), 0,
                            st, pdl, a);

@@ -14,7 +14,7 @@
 // registers on their way from global memory; the fp32 sums go to integers
 // every 1024 of K, so they stay exact.  HBM bound (8 x 262144 x 2816: 116 us;
 // dp4a took 186).  From 9 rows on mma.sync's rate bounds it (16 rows: 155 us
-// against 125 in the next kernel).
+// against 123 in the next kernel).
 //
 // qdense_mma_kernel: more rows, on the 5th-generation tensor cores.  sm_103a
 // has no 8-bit integer form of tcgen05.mma; 8-bit codes are exact in fp16, so
@@ -23,7 +23,7 @@
 // qdense_widen_kernel; the matrix, the larger operand, is read as 8-bit codes
 // and widened on its way into the tensor cores:
 //   weights warp   TMA: 128 channels x 128 codes per stage
-//   rows warp      TMA: up to 256 rows x 64 fp16 per stage
+//   rows warp      TMA: up to 128 rows x 128 fp16 per stage and block
 //   8 widen warps  a channel per thread and half stage: 64 codes from shared
 //                  memory to fp16 pairs in registers to the A operand in
 //                  tensor memory
@@ -32,8 +32,9 @@
 //   8 finish warps the sums times both scales, the softcap, the store
 // A in tensor memory keeps the widened codes out of shared memory, whose
 // bandwidth is what a 128 x 256 fp16 tile asks most of.  Up to 64 rows HBM
-// bounds it (24 x 262144 x 2816: 125 us with a bf16 output, 5.9 TB/s of
-// codes).
+// bounds it (24 x 262144 x 2816: 123 us with a bf16 output, 6.0 TB/s of
+// codes; 14 rounds of tiles for 13.5 rounds of work are 4 of it, the stores of
+// the outputs 5).
 // More than 128 rows: a pair of blocks on a tile of 256 channels, each with 128
 // of them in its tensor memory and half of the rows in its shared memory, which
 // both read (cta_group::2).  A 256-row stage brings 48 KB into an SM's shared
@@ -958,7 +959,9 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   }
   p.nload = p.pair ? p.n / 2 : p.n;
   p.dbufs = p.n <= 128 ? 2 : 1;
-  p.wst = 5;
+  // Weight stages: whole tiles stream them from HBM (24 x 262144 x 2816 with 5,
+  // 7, 9, 12: 128, 123, 124, 125 us); the others need the room otherwise.
+  p.wst = p.pair || p.split > 1 ? 5 : 7;
   p.rst = p.pair ? 4 : p.split > 1 ? 2 : 3;
   p.smem = p.wst * kMmWStage + p.rst * 2 * p.nload * 128 + kMmBarBytes + kMmXsBytes + 1024 +
            (p.split > 1 ? p.split * mm_quota(p) * kMmM * 4 : 0);

@@ -60,11 +60,13 @@ class HeadWeights(ctypes.Structure):
 
 
 class QdenseWeights(ctypes.Structure):
+    device = None  # of the tensors, where make_qdense_weights knows them
     _fields_ = [("channels", ctypes.c_int), ("width", ctypes.c_int), ("q", ctypes.c_void_p),
                 ("scales", ctypes.c_void_p)]
 
 
 class LogitRules(ctypes.Structure):
+    device = rows = words = None  # of the tensors, where make_logit_rules knows them
     _fields_ = [("history", ctypes.c_void_p), ("history_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p),
                 ("history_stride", ctypes.c_int), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
                 ("frequency", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
@@ -203,14 +205,31 @@ def make_head_weights(vocab: int, hidden: int, q: int, scales: int, biases: int)
     return HeadWeights(vocab, hidden, QMat(_ptr(q), _ptr(scales), _ptr(biases)))
 
 
-def _data(t, what: str, kind: str, numel: int):
-    """Device address of a tensor that a call of the batched path takes (None
-    stays None), after a check of its type, size and layout.  kind: "b16"
-    (bf16, or its bits as 16-bit integers), "f32", "i32" or "i8"."""
+_current_device = None
+
+
+def _device() -> int:
+    """The current device, on which the calls of the batched path launch and
+    their tensors have to be."""
+    return (_current_device or _find_current_device())()
+
+
+def _find_current_device():
+    global _current_device
+    import torch
+    torch.cuda.current_device()  # torch's device state is set up
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _current_device
+
+
+def _data(t, what: str, kind: str, numel: int, dev: int):
+    """Device address of a tensor on device dev that a call of the batched path
+    takes (None stays None), after a check of its type, size and layout.  kind:
+    "b16" (bf16, or its bits as 16-bit integers), "f32", "i32", "i8" or "u8"."""
     if t is None:
         return None
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous CUDA tensor is wanted")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous CUDA tensor on device {max(dev, 0)} is wanted, one on {t.device} given")
     if t.dtype not in (_DTYPES or _fill_dtypes())[kind]:
         raise ValueError(f"{what}: {t.dtype} given, {_DTYPES[kind][0]} wanted")
     if t.numel() < numel:
@@ -228,20 +247,23 @@ def _fill_dtypes():
     return _DTYPES
 
 
-def _rows(t, what: str, n_rows: int, width: int):
-    """Device address and row stride of an fp32 matrix of at least n_rows rows
-    and `width` columns."""
-    if not t.is_cuda or t.dtype not in (_DTYPES or _fill_dtypes())["f32"] or t.dim() != 2 or t.shape[0] < n_rows or t.shape[1] < width \
-            or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a float32 CUDA matrix of at least {n_rows} x {width} with adjacent columns is wanted")
+def _rows(t, what: str, n_rows: int, width: int, dev: int):
+    """Device address and row stride of an fp32 matrix on device dev of at least
+    n_rows rows and `width` columns."""
+    if t.get_device() != dev or t.dtype not in (_DTYPES or _fill_dtypes())["f32"] or t.dim() != 2 \
+            or t.shape[0] < n_rows or t.shape[1] < width or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a float32 matrix on CUDA device {dev} of at least {n_rows} x {width} with adjacent "
+                         f"columns is wanted")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(width, t.stride(0))
 
 
 def make_qdense_weights(channels: int, width: int, q, scales) -> QdenseWeights:
     """QdenseWeights from CUDA tensors: q int8 [channels, width], scales fp32
     [channels].  The result keeps the tensors alive."""
-    w = QdenseWeights(channels, width, _data(q, "q", "i8", channels * width), _data(scales, "scales", "f32", channels))
-    w.keep = (q, scales)
+    dev = max(q.get_device(), 0)
+    w = QdenseWeights(channels, width, _data(q, "q", "i8", channels * width, dev),
+                      _data(scales, "scales", "f32", channels, dev))
+    w.keep, w.device = (q, scales), dev
     return w
 
 
@@ -267,14 +289,18 @@ def make_logit_rules(history=None, history_len=None, prompt_len=None, repetition
     n = T or 0
     L = history.shape[1] if history is not None else 0
     B = bias_ids.shape[1] if bias_ids is not None else 0
-    r = LogitRules(_data(history, "history", "i32", n * L), _data(history_len, "history_len", "i32", n),
-                   _data(prompt_len, "prompt_len", "i32", n), L, _data(repetition, "repetition", "f32", n),
-                   _data(presence, "presence", "f32", n), _data(frequency, "frequency", "f32", n),
-                   _data(bias_ids, "bias_ids", "i32", n * B), _data(bias_values, "bias_values", "f32", n * B),
-                   _data(bias_len, "bias_len", "i32", n), B, _data(mask, "mask", "i32", 0),
+    every = (history, history_len, prompt_len, repetition, presence, frequency, bias_ids, bias_values, bias_len, mask)
+    dev = max((t.get_device() for t in every if t is not None), default=-1)
+    dev = max(dev, 0)
+    r = LogitRules(_data(history, "history", "i32", n * L, dev), _data(history_len, "history_len", "i32", n, dev),
+                   _data(prompt_len, "prompt_len", "i32", n, dev), L, _data(repetition, "repetition", "f32", n, dev),
+                   _data(presence, "presence", "f32", n, dev), _data(frequency, "frequency", "f32", n, dev),
+                   _data(bias_ids, "bias_ids", "i32", n * B, dev), _data(bias_values, "bias_values", "f32", n * B, dev),
+                   _data(bias_len, "bias_len", "i32", n, dev), B, _data(mask, "mask", "i32", 0, dev),
                    mask.shape[1] if mask is not None and mask.dim() == 2 else 0)
+    r.device = dev if any(t is not None for t in every) else None
     r.rows, r.words = T, mask.shape[-1] if mask is not None else None
-    r.keep = (history, history_len, prompt_len, repetition, presence, frequency, bias_ids, bias_values, bias_len, mask)
+    r.keep = every
     return r
 
 
@@ -458,11 +484,12 @@ class Moe:
         whose bf16 rows go to x_out where these are given.  H is q's last
         dimension."""
         H = q.shape[-1]
-        n = n_rows * H
-        self._check(self.lib.moe_norm_quant(self.h, _data(hidden, "hidden", "b16", n), _data(y, "y", "b16", n), n_rows,
-                                            H, _data(norm, "norm", "b16", H), eps,
-                                            _data(hidden_out, "hidden_out", "b16", n), _data(q, "q", "i8", n),
-                                            _data(scales, "scales", "f32", n_rows), _data(x_out, "x_out", "b16", n),
+        n, dev = n_rows * H, _device()
+        self._check(self.lib.moe_norm_quant(self.h, _data(hidden, "hidden", "b16", n, dev),
+                                            _data(y, "y", "b16", n, dev), n_rows, H, _data(norm, "norm", "b16", H, dev),
+                                            eps, _data(hidden_out, "hidden_out", "b16", n, dev),
+                                            _data(q, "q", "i8", n, dev), _data(scales, "scales", "f32", n_rows, dev),
+                                            _data(x_out, "x_out", "b16", n, dev),
                                             _stream(stream)), "moe_norm_quant")
 
     def qdense_workspace_bytes(self, w: QdenseWeights, n_rows: int) -> int:
@@ -474,11 +501,14 @@ class Moe:
         x int8 [T, K] with x_scales fp32 [T]; outputs y bf16 and/or y32 fp32
         [T, N], through a softcap if one is given; ws of
         qdense_workspace_bytes(w, n_rows) bytes."""
-        n = n_rows * w.channels
-        self._check(self.lib.moe_qdense_forward(self.h, _data(x, "x", "i8", n_rows * w.width),
-                                                _data(x_scales, "x_scales", "f32", n_rows), n_rows, ctypes.byref(w),
-                                                softcap, _data(y, "y", "b16", n), _data(y32, "y32", "f32", n),
-                                                _data(ws, "ws", "u8", 0), 0 if ws is None else ws.numel(),
+        n, dev = n_rows * w.channels, _device()
+        if w.device is not None and w.device != dev:
+            raise ValueError(f"weights on CUDA device {w.device} given, the current device is {dev}")
+        self._check(self.lib.moe_qdense_forward(self.h, _data(x, "x", "i8", n_rows * w.width, dev),
+                                                _data(x_scales, "x_scales", "f32", n_rows, dev), n_rows,
+                                                ctypes.byref(w), softcap, _data(y, "y", "b16", n, dev),
+                                                _data(y32, "y32", "f32", n, dev), _data(ws, "ws", "u8", 0, dev),
+                                                0 if ws is None else ws.numel(),
                                                 _stream(stream)), "moe_qdense_forward")
 
     def logits_process(self, logits, n_rows, vocab, rules: LogitRules, out=None, tokens=None, stream=None):
@@ -489,10 +519,13 @@ class Moe:
             raise ValueError(f"rules for {rules.rows} rows given, {n_rows} wanted")
         if rules.words is not None and rules.words < (vocab + 31) // 32:
             raise ValueError(f"mask: {rules.words} words given, {(vocab + 31) // 32} wanted")
-        at, ld = _rows(logits, "logits", n_rows, vocab)
-        to, ld_out = _rows(out, "out", n_rows, vocab) if out is not None else (None, 0)
+        dev = _device()
+        if rules.device is not None and rules.device != dev:
+            raise ValueError(f"rules on CUDA device {rules.device} given, the current device is {dev}")
+        at, ld = _rows(logits, "logits", n_rows, vocab, dev)
+        to, ld_out = _rows(out, "out", n_rows, vocab, dev) if out is not None else (None, 0)
         self._check(self.lib.moe_logits_process(self.h, at, ld, n_rows, vocab, ctypes.byref(rules), to, ld_out,
-                                                _data(tokens, "tokens", "i32", n_rows), _stream(stream)),
+                                                _data(tokens, "tokens", "i32", n_rows, dev), _stream(stream)),
                     "moe_logits_process")
 
     def embed(self, ids, n, hw: HeadWeights, out, stream=None):

@@ -135,6 +135,52 @@ def test_binding_checks():
     assert bq.make_logit_rules().rows is None
 
 
+class OnDevice:
+    """What the binding asks of a tensor, on a device of its own."""
+
+    def __init__(self, t, device):
+        self.t, self.device = t, f"cuda:{device}"
+        self.get_device, self.data_ptr = (lambda: device), (lambda: A)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_binding_refuses_other_devices(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(bq, "_current_device", lambda: 0)
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: bq.MOE_OK
+
+    moe = object.__new__(bq.Moe)
+    moe.lib, moe.h = Lib(), None
+
+    def on(dev, shape, dtype):
+        return OnDevice(torch.zeros(shape, dtype=dtype), dev)
+
+    i8, f32, i32, b16 = torch.int8, torch.float32, torch.int32, torch.bfloat16
+    # (T = 2, K = N = 16; a stream is given: there is no device here to ask for its own)
+    calls = {
+        "norm_quant": lambda d: moe.norm_quant(on(d[0], (2, 16), b16), 2, on(d[1], (2, 16), i8), on(d[2], 2, f32),
+                                               stream=1),
+        "qdense": lambda d: moe.qdense_forward(on(d[0], (2, 16), i8), on(d[1], 2, f32), 2, bq.make_qdense_weights(
+            16, 16, on(d[2], (16, 16), i8), on(d[2], 16, f32)), y32=on(0, (2, 16), f32), stream=1),
+        "logits": lambda d: moe.logits_process(on(d[0], (2, 16), f32), 2, 16, bq.make_logit_rules(mask=on(d[1], 1, i32)),
+                                               tokens=on(d[2], 2, i32), stream=1),
+    }
+    for call in calls.values():
+        call((0, 0, 0))
+        for bad in ((1, 0, 0), (0, 1, 0), (0, 0, 1)):
+            with pytest.raises(ValueError):
+                call(bad)
+    with pytest.raises(ValueError):  # one of the tensors elsewhere
+        bq.make_qdense_weights(16, 16, on(0, (16, 16), i8), on(1, 16, f32))
+    with pytest.raises(ValueError):
+        bq.make_logit_rules(history=on(0, (2, 4), i32), history_len=on(1, 2, i32))
+
+
 # ------------------------------------------------------------------ the oracle
 def test_oracle_norm_quant_by_hand():
     # rms of (3, 4, 0, 0) is 2.5; weight 2 on the second: u = (3, 8, 0, 0)

@@ -20,7 +20,8 @@
 // has no 8-bit integer form of tcgen05.mma; 8-bit codes are exact in fp16, so
 // the products run as fp16 with fp32 sums (exact while the partial sums stay
 // below 2^24).  The rows are widened to fp16 once per call by
-// qdense_widen_kernel; the matrix, the larger operand, is read as 8-bit codes
+// qdense_widen_kernel, or, where every block has one tile or less, by each
+// block; the matrix, the larger operand, is read as 8-bit codes
 // and widened on its way into the tensor cores:
 //   weights warp   TMA: 128 channels x 128 codes per stage
 //   rows warp      TMA: up to 128 rows x 128 fp16 per stage and block
@@ -380,26 +381,34 @@ constexpr int kMmABufs = 4;                // A tiles in tensor memory (64 colum
 constexpr uint32_t kMmACol = 256;          // first column of the A tiles; the sums lie below
 constexpr int kMmWStage = kMmM * kMmK;     // bytes of a weight stage
 constexpr int kMmMaxN = 256;
-constexpr int kMmSplitN = 128;             // rows per tile, at most, where a cluster shares a tile
+constexpr int kMmSplitN = 128;             // rows per tile, at most, where blocks have one tile or a part of one
 constexpr int kMmMaxSplit = kQdenseMaxCluster;
 constexpr int kMmBarBytes = 512;
+constexpr int kMmSmemMax = 227 * 1024;
 constexpr int kMmXsBytes = kMmMaxN * 4;
+
+// kOne: tiles of up to 128 rows or parts of them; the rows widened by a launch
+// before.  kPair: wider tiles, a pair of blocks on each.  kFew: as kOne, one
+// tile or part of a tile per block; the rows come as 8-bit codes, and the finish
+// warps, idle until the sums are there, widen them.
+enum { kOne, kPair, kFew };
 
 struct MmPlan {
   int n;            // rows per tile (the MMA N): a multiple of 16
   int wst, rst;     // stages of weights and of rows, 128 of K each
+  int xst;          // kFew: stages of the rows' codes
   int dbufs;        // sets of sums in tensor memory
   int split;        // blocks of a cluster that share a tile along K
   int ntile, ttile; // tiles of channels, of rows
   int whole, units; // units of work: `whole` tiles, then halves of tiles (by rows)
-  int pair;         // 1: pairs of blocks, tiles of 256 channels
+  int form;
   int nload;        // rows that a block loads of a tile: n, or n / 2 in pairs
   int smem;
 };
 
 struct MmParams {
   CUtensorMap w;     // 8-bit codes {K, N}, box {128, 128}, 128-byte swizzle
-  CUtensorMap x[2];  // fp16 rows {K, T}, box {64, nload} and {64, nload / 2}, 128-byte swizzle
+  CUtensorMap x[2];  // fp16 rows {K, T}, box {64, nload} and {64, nload / 2}, 128-byte swizzle; kFew: codes, box {128, n}
   QdenseArgs a;
   MmPlan p;
 };
@@ -409,13 +418,13 @@ struct MmParams {
 struct MmUnit {
   int n0, t0, n, cnt, half;
 };
-template <bool kPair>
+template <int kForm>
 __device__ __forceinline__ MmUnit mm_unit(const MmPlan &p, int T, int u, int rank) {
   MmUnit q;
   q.half = u >= p.whole ? 1 : 0;
   const int tile = q.half ? p.whole + (u - p.whole) / 2 : u;
   q.n = q.half ? p.n / 2 : p.n;
-  q.n0 = (kPair ? tile / p.ttile * 2 + rank : tile / p.ttile) * kMmM;
+  q.n0 = (kForm == kPair ? tile / p.ttile * 2 + rank : tile / p.ttile) * kMmM;
   q.t0 = tile % p.ttile * p.n + (q.half ? ((u - p.whole) & 1) * q.n : 0);
   q.cnt = min(q.n, T - q.t0);  // none: a half past the last row, which every warp passes over
   return q;
@@ -463,9 +472,9 @@ __device__ __forceinline__ void mm_arrive(uint64_t *bar) {
 
 // D (tensor memory) += A (tensor memory, 128 x 16) * B (shared memory, n x 16)^T;
 // kPair: A is 256 x 16 and B n x 16, a half of each in either block's memory.
-template <bool kPair>
+template <int kForm>
 __device__ __forceinline__ void mm_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  if (kPair)
+  if (kForm == kPair)
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
             d),
@@ -479,9 +488,9 @@ __device__ __forceinline__ void mm_mma(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 // Arrives on `bar` (kPair: in both blocks) once the MMAs issued before are complete.
-template <bool kPair>
+template <int kForm>
 __device__ __forceinline__ void mm_commit(uint64_t *bar) {
-  if (kPair)
+  if (kForm == kPair)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_addr(bar)),
@@ -490,9 +499,9 @@ __device__ __forceinline__ void mm_commit(uint64_t *bar) {
   else
     dense::tc_commit(bar);
 }
-template <bool kPair>
+template <int kForm>
 __device__ __forceinline__ void mm_alloc(uint32_t *dst) {
-  if (kPair) {
+  if (kForm == kPair) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -500,9 +509,9 @@ __device__ __forceinline__ void mm_alloc(uint32_t *dst) {
     dense::tc_alloc(dst, 512);
   }
 }
-template <bool kPair>
+template <int kForm>
 __device__ __forceinline__ void mm_dealloc(uint32_t tmem) {
-  if (kPair)
+  if (kForm == kPair)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   else
     dense::tc_dealloc(tmem, 512);
@@ -546,7 +555,7 @@ __device__ __forceinline__ void cluster_st(uint32_t addr, float v) {
 // Rows of a shared tile that one block of the cluster adds up.
 __host__ __device__ inline int mm_quota(const MmPlan &p) { return (p.n + p.split - 1) / p.split; }
 
-template <bool kPair>
+template <int kForm>
 __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_constant__ MmParams prm) {
   extern __shared__ __align__(1024) uint8_t msm[];
   const QdenseArgs &a = prm.a;
@@ -554,28 +563,31 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *base = msm + ((1024u - (smem_addr(msm) & 1023u)) & 1023u);
   const int rstep = P.nload * 128, rstage = 2 * rstep;  // a rows stage: two steps of 64 of K
-  uint8_t *wbuf = base, *rbuf = base + P.wst * kMmWStage;
-  uint64_t *bar = reinterpret_cast<uint64_t *>(rbuf + P.rst * rstage);
+  uint8_t *wbuf = base, *rbuf = base + P.wst * kMmWStage, *xbuf = rbuf + P.rst * rstage;
+  const int xstage = P.n * 128;  // kFew
+  uint64_t *bar = reinterpret_cast<uint64_t *>(xbuf + P.xst * xstage);
   uint64_t *wfull = bar, *wempty = wfull + P.wst, *rfull = wempty + P.wst, *rempty = rfull + P.rst;
   uint64_t *afull = rempty + P.rst, *aempty = afull + kMmABufs, *dfull = aempty + kMmABufs, *dempty = dfull + 2;
-  uint64_t *tready = dempty + 2;
-  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(tready + 1);
+  uint64_t *tready = dempty + 2, *xfull = tready + 1, *xempty = xfull + P.xst;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(xempty + P.xst);
   float *s_xs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bar) + kMmBarBytes);  // [n] row scales
   float *s_part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(s_xs) + kMmXsBytes);  // [split][quota][128]
+  constexpr bool kPairs = kForm == kPair, kOwn = kForm == kFew;
   const bool tracer = blockIdx.x == 0 && tid == 0;
-  const int split = kPair ? 1 : P.split;
-  const int rank = kPair || split > 1 ? (int)cluster_rank() : 0;
-  const int part = kPair ? 0 : rank;  // this block's part of K
-  const bool leader = !kPair || rank == 0;
+  const int split = kPairs ? 1 : P.split;
+  const int rank = kPairs || split > 1 ? (int)cluster_rank() : 0;
+  const int part = kPairs ? 0 : rank;  // this block's part of K
+  const bool leader = !kPairs || rank == 0;
 
-  if (tid < 2 * P.wst + 2 * P.rst + 2 * kMmABufs + 5) {
+  if (tid < 2 * P.wst + 2 * P.rst + 2 * P.xst + 2 * kMmABufs + 5) {
     // arrivals per phase.  The leader of a pair hears of both blocks' A tiles,
     // rows (its own copies, and a word from the other block) and finish warps.
     uint64_t *b = bar + tid;
     int n = 1;
     if ((b >= wempty && b < rfull) || (b >= afull && b < aempty)) n = kMmWiden;
     if (b >= dempty && b < tready) n = kMmFin;
-    if (kPair && leader && ((b >= rfull && b < rempty) || (b >= afull && b < aempty) || (b >= dempty && b < tready)))
+    if (b >= xempty || (kOwn && b >= rfull && b < rempty)) n = kMmFin / 2;
+    if (kPairs && leader && ((b >= rfull && b < rempty) || (b >= afull && b < aempty) || (b >= dempty && b < tready)))
       n *= 2;
     mbar_init(b, n);
     fence_mbar_init();
@@ -584,8 +596,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   if (tracer) trace_min(a.trace, kTrEntry);
   pdl_launch_dependents();
 
-  if (kPair || split > 1) cluster_sync_all();  // every block of the cluster runs, its barriers are set
-  const int csize = kPair ? 2 : split;
+  if (kPairs || split > 1) cluster_sync_all();  // every block of the cluster runs, its barriers are set
+  const int csize = kPairs ? 2 : split;
   const int first = blockIdx.x / csize, stride = gridDim.x / csize;  // units of this block
   const int units = P.units;
   const int nst = (a.K + kMmK - 1) / kMmK, st0 = nst * part / split, st1 = nst * (part + 1) / split;  // its part of K
@@ -595,12 +607,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     // ============================================================ weights
     // Nothing that an earlier launch still writes is read here: the launch
     // before this one (the widening of the rows) waited for those.
+    if (kOwn) pdl_wait();
     if (lane == 0) {
       fused::fence_proxy_async_global();
       bool ok = true;
       int st = 0, ph = 0, issued = 0;
       for (int u = first; u < units && ok; u += stride) {
-        const MmUnit q = mm_unit<kPair>(P, a.T, u, rank);
+        const MmUnit q = mm_unit<kForm>(P, a.T, u, rank);
         if (q.cnt <= 0) continue;
         for (int s = st0; s < st1; ++s, ++issued) {
           if (issued >= P.wst && !(ok = mm_wait(&wempty[st], ph ^ 1))) break;
@@ -624,10 +637,23 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       fused::fence_proxy_async_global();
       bool ok = true;
       int st = 0, ph = 0, issued = 0;
-      for (int u = first; u < units && ok; u += stride) {
-        const MmUnit q = mm_unit<kPair>(P, a.T, u, rank);
+      if (kOwn) {
+        const MmUnit q = mm_unit<kForm>(P, a.T, first, rank);
+        for (int s = st0; s < st1; ++s, ++issued) {
+          if (issued >= P.xst && !(ok = mm_wait(&xempty[st], ph ^ 1))) break;
+          mbar_arrive_expect_tx(&xfull[st], (uint32_t)xstage);
+          dense::tma_load_2d(xbuf + st * xstage, &prm.x[0], kMmK * s, q.t0, &xfull[st]);
+          if (++st == P.xst) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        for (int j = max(0, issued - P.xst); j < issued; ++j) mm_wait(&xfull[j % P.xst], (j / P.xst) & 1);
+      }
+      for (int u = first; !kOwn && u < units && ok; u += stride) {
+        const MmUnit q = mm_unit<kForm>(P, a.T, u, rank);
         if (q.cnt <= 0) continue;
-        const int rows = kPair ? q.n / 2 : q.n, t0 = q.t0 + (kPair ? rank * rows : 0);
+        const int rows = kPairs ? q.n / 2 : q.n, t0 = q.t0 + (kPairs ? rank * rows : 0);
         for (int g = g0; g < g1; g += 2, ++issued) {
           if (issued >= P.rst && !(ok = mm_wait(&rempty[st], ph ^ 1))) break;
           const int h = min(2, g1 - g);
@@ -641,11 +667,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
         }
       }
       if (!ok) set_error(a.err, kErrTimeout);
-      for (int j = max(0, issued - P.rst); j < issued; ++j) mm_wait<kPair>(&rfull[j % P.rst], (j / P.rst) & 1);
+      for (int j = max(0, issued - P.rst); !kOwn && j < issued; ++j) mm_wait<kPairs>(&rfull[j % P.rst], (j / P.rst) & 1);
     }
   } else if (warp == kMmMma) {
     // ============================================================ MMA
-    mm_alloc<kPair>(s_tmem);
+    mm_alloc<kForm>(s_tmem);
     dense::tc_fence_before();
     __syncwarp();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
@@ -660,7 +686,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     if (!leader) {
       // the other block of a pair: passes on that its rows have landed
       for (int u = first; u < units && ok; u += stride) {
-        if (mm_unit<kPair>(P, a.T, u, rank).cnt <= 0) continue;
+        if (mm_unit<kForm>(P, a.T, u, rank).cnt <= 0) continue;
         for (int s = st0; s < st1; ++s) {
           if (!(ok = __all_sync(0xffffffffu, mm_wait(&rfull[st], ph)))) break;
           if (lane == 0) cluster_arrive(cluster_map(smem_addr(&rfull[st]), 0));
@@ -672,33 +698,33 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       }
     }
     for (int u = first; leader && u < units; u += stride) {
-      const MmUnit q = mm_unit<kPair>(P, a.T, u, rank);
+      const MmUnit q = mm_unit<kForm>(P, a.T, u, rank);
       if (q.cnt <= 0) continue;
-      const uint32_t idesc = dense::idesc_f16(kPair ? 2 * kMmM : kMmM, q.n);
+      const uint32_t idesc = dense::idesc_f16(kPairs ? 2 * kMmM : kMmM, q.n);
       const int db = du % P.dbufs;
-      if (du >= P.dbufs) ok = __all_sync(0xffffffffu, mm_wait<kPair>(&dempty[db], ((du / P.dbufs) - 1) & 1));
+      if (du >= P.dbufs) ok = __all_sync(0xffffffffu, mm_wait<kPairs>(&dempty[db], ((du / P.dbufs) - 1) & 1));
       if (!ok) break;
       ++du;
       const uint32_t acc = tmem + db * 128;
       for (int s = st0; s < st1; ++s, ++gi) {
-        ok = __all_sync(0xffffffffu, mm_wait<kPair>(&rfull[st], ph) && mm_wait<kPair>(&afull[ab], aph));
+        ok = __all_sync(0xffffffffu, mm_wait<kPairs>(&rfull[st], ph) && mm_wait<kPairs>(&afull[ab], aph));
         if (!ok) break;
         dense::tc_fence_after();
         const uint32_t ad = tmem + kMmACol + 64 * ab;
         uint64_t bd = bdesc0 + (uint64_t)((st * rstage) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)  // K = 16 per MMA: 8 columns of A, 32 bytes of B's rows
-          if (elect_one()) mm_mma<kPair>(acc, ad + 8 * ks, bd + 2 * ks, idesc, (s > st0 || ks > 0) ? 1u : 0u);
+          if (elect_one()) mm_mma<kForm>(acc, ad + 8 * ks, bd + 2 * ks, idesc, (s > st0 || ks > 0) ? 1u : 0u);
         if (2 * s + 1 < g1) {  // the stage's second half
           bd += (uint64_t)(rstep >> 4);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            if (elect_one()) mm_mma<kPair>(acc, ad + 32 + 8 * ks, bd + 2 * ks, idesc, 1u);
+            if (elect_one()) mm_mma<kForm>(acc, ad + 32 + 8 * ks, bd + 2 * ks, idesc, 1u);
         }
         if (elect_one()) {
-          mm_commit<kPair>(&rempty[st]);
-          mm_commit<kPair>(&aempty[ab]);
-          if (s == st1 - 1) mm_commit<kPair>(&dfull[db]);
+          mm_commit<kForm>(&rempty[st]);
+          mm_commit<kForm>(&aempty[ab]);
+          if (s == st1 - 1) mm_commit<kForm>(&dfull[db]);
         }
         __syncwarp();
         if (++st == P.rst) {
@@ -715,10 +741,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
     // the last MMAs are complete and the sums read before the memory goes back (bounded waits)
     if (gi > 0) mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1);
-    if (du > 0) mm_wait<kPair>(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
+    if (du > 0) mm_wait<kPairs>(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
     dense::tc_fence_after();
     __syncwarp();
-    if (!kPair) mm_dealloc<kPair>(tmem);
+    if (!kPairs) mm_dealloc<kForm>(tmem);
   } else if (warp >= kMmFin0) {
     // ============================================================ finish
     // Warp w reads tensor-memory lanes 32 (w % 4) .. +31: channels n0 + rr; the
@@ -728,9 +754,53 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     bool ok = mm_wait(tready, 0);
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
     const int rr = 32 * (warp & 3) + lane, ft = tid - kMmFin0 * 32, side = (warp - kMmFin0) >> 2;
+    if (kOwn) {
+      // First the rows of this block's stages, taken in turn by the two halves
+      // of the warps.  (The rings' lengths are even, so each barrier belongs to
+      // one half: a waiter that meets a barrier at every second phase only would
+      // take the phase before last for the last.)  Eight lanes to a row, 16 codes each: 16-byte chunk j of a
+      // row of codes (swizzled as the copy left it) becomes chunks 2 j, 2 j + 1
+      // of the row's 256 bytes in two steps of 64; lanes 4 to 7 of the eight
+      // store theirs in the other order, for 32 different banks.
+      pdl_wait();
+      const int j = lane & 7, r0 = 4 * (warp & 3) + (lane >> 3), c = 2 * (j & 3), odd = j >> 2;
+      for (int i = side; i < st1 - st0 && ok; i += kMmFin / 4) {
+        const int st = i % P.rst, xs = i % P.xst;
+        ok = mm_wait(&xfull[xs], (i / P.xst) & 1);
+        if (i >= P.rst) ok = ok && mm_wait(&rempty[st], ((i / P.rst) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t *const from = xbuf + xs * xstage;
+        uint8_t *const to = rbuf + st * rstage + odd * rstep;
+        uint4 v[kMmSplitN / 16];
+#pragma unroll
+        for (int k = 0; k < kMmSplitN / 16; ++k) {
+          const int r = r0 + 16 * k;
+          if (16 * k < P.n) v[k] = *reinterpret_cast<const uint4 *>(from + r * 128 + ((j ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int k = 0; k < kMmSplitN / 16; ++k) {
+          if (16 * k >= P.n) break;
+          const int r = r0 + 16 * k;
+          uint4 o[2];
+          widen4(v[k].x, o[0].x, o[0].y);
+          widen4(v[k].y, o[0].z, o[0].w);
+          widen4(v[k].z, o[1].x, o[1].y);
+          widen4(v[k].w, o[1].z, o[1].w);
+          *reinterpret_cast<uint4 *>(to + r * 128 + (((c + odd) ^ (r & 7)) << 4)) = odd ? o[1] : o[0];
+          *reinterpret_cast<uint4 *>(to + r * 128 + (((c + 1 - odd) ^ (r & 7)) << 4)) = odd ? o[0] : o[1];
+        }
+        dense::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mm_arrive(&xempty[xs]);
+          mm_arrive(&rfull[st]);
+        }
+      }
+    }
     int du = 0;
     for (int u = first; u < units; u += stride) {
-      const MmUnit q = mm_unit<kPair>(P, a.T, u, rank);
+      const MmUnit q = mm_unit<kForm>(P, a.T, u, rank);
       if (q.cnt <= 0) continue;
       const int n = q.n0 + rr, t0 = q.t0, cnt = q.cnt;
       const int db = du % P.dbufs;
@@ -827,7 +897,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       ++told;
     };
     for (int u = first; u < units && ok; u += stride) {
-      if (mm_unit<kPair>(P, a.T, u, rank).cnt <= 0) continue;
+      if (mm_unit<kForm>(P, a.T, u, rank).cnt <= 0) continue;
       for (int s = st0; s < st1 && ok; ++s, ++gi) {
         ok = mm_wait(&wfull[st], ph);
         const uint8_t *row = wbuf + st * kMmWStage + rr * 128;
@@ -863,20 +933,21 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
   }
 
-  if (kPair) {
+  if (kPairs) {
     // neither block leaves, or frees its tensor memory, while the other may
     // still arrive on its barriers or the leader's MMAs use it
     __syncwarp();
     dense::tc_fence_before();
     cluster_sync_all();
     dense::tc_fence_after();
-    if (warp == kMmMma) mm_dealloc<kPair>(*reinterpret_cast<volatile uint32_t *>(s_tmem));
+    if (warp == kMmMma) mm_dealloc<kForm>(*reinterpret_cast<volatile uint32_t *>(s_tmem));
   }
-  if (!kPair && split > 1) {
+  if (!kPairs && split > 1) {
     // One tile per cluster; this block adds the parts of its rows, a warp to a
     // row, four channels per lane.
     __syncwarp();
-    const MmUnit q = mm_unit<kPair>(P, a.T, first, rank);
+    if (kOwn) pdl_wait();
+    const MmUnit q = mm_unit<kForm>(P, a.T, first, rank);
     const int n0 = q.n0, t0 = q.t0, cnt = q.cnt;
     const int quota = mm_quota(P), r0 = part * quota, mine = min(quota, cnt - r0);
     float ws[4];
@@ -919,6 +990,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
 // those would run in a second wave: 16 tiles in clusters of 8 took 15.7 us, in
 // clusters of 4 10.4).
 //
+// One tile or part per block: the finish warps widen the rows, which saves the
+// launch for it (about 1 us) and costs each stage 0.04 us at 16 rows, 0.09 at
+// 64, 0.19 at 128.  16 x 4096 x 2816 (6 stages): 6.8 us against 7.9 with the
+// launch; 64 x 1408 x 2816 (3 stages) 6.2 against 7.3; 48 x 16384 x 2816 (22)
+// 14.1 both; 64 x 16384 x 8192 (64) 36.1 against 31.4; 128 x 2816 x 8192 (11)
+// 14.7 against 13.8; 128 x 4096 x 704 (6, whole tiles) 7.5 against 6.9.
+//
 // The last round of tiles of pairs, if at most half the pairs have one: in
 // halves.
 MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
@@ -942,9 +1020,13 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
       }
     }
   }
-  p.pair = p.n > 128;  // (split tiles are narrower)
+  p.form = p.n > 128 ? kPair : kOne;  // (split tiles are narrower)
+  const int stages = (nst + p.split - 1) / p.split;
+  if (p.form == kOne && p.ntile * p.ttile * p.split <= n_sm &&
+      (p.n <= 96 ? stages * (p.n + 16) < 1550 : p.split > 1 && stages * (p.n + 16) < 900))
+    p.form = kFew;
   int room = n_sm;  // units at once
-  if (p.pair) {
+  if (p.form == kPair) {
     p.ntile = (p.ntile + 1) / 2;
     p.n = (p.n + 31) / 32 * 32;
     room = clusters[2];
@@ -952,19 +1034,26 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   p.whole = p.ntile * p.ttile;
   p.units = p.whole;
   const int rest = p.whole % room;
-  if (p.pair && p.whole > room && rest > 0 && 2 * rest <= room) {
+  if (p.form == kPair && p.whole > room && rest > 0 && 2 * rest <= room) {
     p.n = (p.n + 63) / 64 * 64;
     p.whole -= rest;
     p.units = p.whole + 2 * rest;
   }
-  p.nload = p.pair ? p.n / 2 : p.n;
+  p.nload = p.form == kPair ? p.n / 2 : p.n;
   p.dbufs = p.n <= 128 ? 2 : 1;
   // Weight stages: whole tiles stream them from HBM (24 x 262144 x 2816 with 5,
   // 7, 9, 12: 128, 123, 124, 125 us); the others need the room otherwise.
-  p.wst = p.pair || p.split > 1 ? 5 : 7;
-  p.rst = p.pair ? 4 : p.split > 1 ? 2 : 3;
-  p.smem = p.wst * kMmWStage + p.rst * 2 * p.nload * 128 + kMmBarBytes + kMmXsBytes + 1024 +
-           (p.split > 1 ? p.split * mm_quota(p) * kMmM * 4 : 0);
+  p.wst = p.form == kOne && p.split == 1 ? 7 : 5;
+  p.rst = p.form == kOne ? (p.split > 1 ? 2 : 3) : 4;
+  p.xst = p.form == kFew ? 4 : 0;
+  const int parts = p.split > 1 ? p.split * mm_quota(p) * kMmM * 4 : 0;
+  auto bytes = [&] {
+    return p.wst * kMmWStage + p.rst * 2 * p.nload * 128 + p.xst * p.n * 128 + kMmBarBytes + kMmXsBytes + 1024 + parts;
+  };
+  if (p.form == kFew && bytes() > kMmSmemMax) p.rst = 2;
+  if (p.form == kFew && bytes() > kMmSmemMax) p.xst = 2;
+  while (bytes() > kMmSmemMax) --p.wst;
+  p.smem = bytes();
   return p;
 }
 
@@ -978,20 +1067,28 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, const int *clusters, cudaS
   const cuuint64_t dw[2] = {(cuuint64_t)a.K, (cuuint64_t)a.N}, sw[1] = {(cuuint64_t)a.K};
   const cuuint64_t dx[2] = {(cuuint64_t)a.K, (cuuint64_t)a.T}, sx[1] = {(cuuint64_t)a.K * 2};
   const cuuint32_t bw[2] = {128, kMmM}, bx[2] = {64, (cuuint32_t)p.nload}, by[2] = {64, (cuuint32_t)p.nload / 2};
-  if (!encode_map(f, &prm.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.w, dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(f, &prm.x[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_map(f, &prm.x[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.work, dx, sx, by, CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  const size_t pieces = (size_t)a.T * (a.K / 8), blocks = (pieces + kWidenThreads - 1) / kWidenThreads;
-  const size_t most = (size_t)n_sm * 8;
-  cudaError_t e = launch_k(qdense_widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kWidenThreads), 0,
-                           st, pdl, a);
-  if (e != cudaSuccess) return e;
-  if (prm.a.trace) prm.a.trace += 4;
+  const cuuint32_t bc[2] = {128, (cuuint32_t)p.n};
+  constexpr CUtensorMapDataType k8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, k16 = CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B;
+  bool ok = encode_map(f, &prm.w, k8, 2, a.w, dw, sw, bw, k128);
+  if (p.form == kFew)
+    ok = ok && encode_map(f, &prm.x[0], k8, 2, a.x, dx, sw, bc, k128);
+  else
+    ok = ok && encode_map(f, &prm.x[0], k16, 2, a.work, dx, sx, bx, k128);
+  if (p.units > p.whole) ok = ok && encode_map(f, &prm.x[1], k16, 2, a.work, dx, sx, by, k128);
+  if (!ok) return cudaErrorInvalidValue;
+  if (p.form != kFew) {
+    const size_t pieces = (size_t)a.T * (a.K / 8), blocks = (pieces + kWidenThreads - 1) / kWidenThreads;
+    const size_t most = (size_t)n_sm * 8;
+    const cudaError_t e = launch_k(qdense_widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)),
+                                   dim3(kWidenThreads), 0, st, pdl, a);
+    if (e != cudaSuccess) return e;
+    if (prm.a.trace) prm.a.trace += 4;
+  }
   const int units = p.units;
   cudaLaunchConfig_t cfg = {};
-  const int room = p.pair ? clusters[2] : n_sm;
-  const int csize = p.pair ? 2 : p.split;
+  const int room = p.form == kPair ? clusters[2] : n_sm;
+  const int csize = p.form == kPair ? 2 : p.split;
   cfg.gridDim = dim3(p.split > 1 ? units * p.split : (units < room ? units : room) * csize);
   cfg.blockDim = dim3(kMmThreads);
   cfg.dynamicSmemBytes = p.smem;
@@ -1010,7 +1107,8 @@ cudaError_t launch_mma(const QdenseArgs &a, int n_sm, const int *clusters, cudaS
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, p.pair ? qdense_mma_kernel<true> : qdense_mma_kernel<false>, prm);
+  return cudaLaunchKernelEx(&cfg, p.form == kPair ? qdense_mma_kernel<kPair> : p.form == kFew ? qdense_mma_kernel<kFew> : qdense_mma_kernel<kOne>,
+                            prm);
 }
 }  // namespace
 
@@ -1018,8 +1116,9 @@ cudaError_t qdense_set_attributes(int *clusters) {
   cudaError_t e;
   if ((e = set_rows_attr<1>()) || (e = set_rows_attr<2>()) || (e = set_rows_attr<4>()) || (e = set_rows_attr<8>()) ||
       (e = cudaFuncSetAttribute(qdense_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQfSmemMax)) ||
-      (e = cudaFuncSetAttribute(qdense_mma_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)) ||
-      (e = cudaFuncSetAttribute(qdense_mma_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)))
+      (e = cudaFuncSetAttribute(qdense_mma_kernel<kOne>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmemMax)) ||
+      (e = cudaFuncSetAttribute(qdense_mma_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmemMax)) ||
+      (e = cudaFuncSetAttribute(qdense_mma_kernel<kFew>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmemMax)))
     return e;
   for (int s = 0; s <= kQdenseMaxCluster; ++s) {
     clusters[s] = 0;
@@ -1027,7 +1126,7 @@ cudaError_t qdense_set_attributes(int *clusters) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(s);
     cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = 227 * 1024;
+    cfg.dynamicSmemBytes = kMmSmemMax;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = s;
@@ -1035,7 +1134,7 @@ cudaError_t qdense_set_attributes(int *clusters) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaOccupancyMaxActiveClusters(&clusters[s], s == 2 ? qdense_mma_kernel<true> : qdense_mma_kernel<false>, &cfg)))
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters[s], qdense_mma_kernel<kFew>, &cfg)))
       return e;
   }
   if (clusters[2] < 1) return cudaErrorInvalidConfiguration;

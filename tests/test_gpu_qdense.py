@@ -75,6 +75,8 @@ SHAPES = [(1, 1, 16), (1, 2816, 2816), (1, 4097, 208), (2, 33, 64), (3, 130, 107
           (2049, 130, 48), (40, 40000, 64),
           # more tiles than SMs: the last round in halves of tiles (one of them past the last row)
           (512, 10240, 144), (520, 7000, 64), (4112, 1280, 64), (4097, 1290, 80),
+          # one tile or part per block, with more stages of K than a block holds at once
+          (16, 8200, 4096), (24, 12800, 2832), (9, 5000, 80), (96, 1300, 1936), (64, 19400, 2176),
           # tiles shared by clusters of every size; K that ends inside a stage and inside its first half
           (40, 128, 2816), (150, 128, 1040), (100, 1408, 2832), (64, 2816, 1120), (200, 704, 4112), (33, 5632, 528)]
 
@@ -173,6 +175,30 @@ def test_captured_and_replayed(moe, T):
     for x, both in got:
         for o in both:
             assert np.all(np.abs(o.cpu().numpy() - BO.qdense(x, xs, w, ws)) <= bound(x, w, xs, ws))
+
+
+@pytest.mark.parametrize("T,N,K", [(2, 3000, 2816), (7, 3000, 2816), (16, 8200, 4096), (24, 12800, 2832),
+                                   (90, 2816, 2816), (333, 700, 2816), (30, 20000, 704), (300, 5000, 704)])
+def test_the_same_on_every_call(moe, T, N, K):
+    """Sums are added in a fixed order: every call gives the same bits."""
+    x, w = codes(50, T, K), codes(51, N, K)
+    xs, ws = scales(52, T, N)
+    wd = bq.make_qdense_weights(N, K, torch.from_numpy(w).cuda(), torch.from_numpy(ws).cuda())
+    work = torch.empty(moe.qdense_workspace_bytes(wd, T), dtype=torch.uint8, device="cuda")
+    xd, xsd = torch.from_numpy(x).cuda(), torch.from_numpy(xs).cuda()
+    y = torch.empty((T, N), device="cuda")
+    moe.qdense_forward(xd, xsd, T, wd, work, y32=y)
+    first, same = y.clone(), torch.ones((), dtype=torch.bool, device="cuda")
+    for _ in range(100):
+        y.zero_()
+        for _ in range(3):
+            moe.qdense_forward(xd, xsd, T, wd, work, y32=y)
+        same &= (y == first).all()
+    torch.cuda.synchronize()
+    assert moe.get_error() == bq.MOE_OK and bool(same)
+    some = np.unique(np.linspace(0, N - 1, 400).astype(int))
+    assert np.all(np.abs(first.cpu().numpy()[:, some] - BO.qdense(x, xs, w[some], ws[some]))
+                  <= bound(x, w[some], xs, ws[some]))
 
 
 @pytest.mark.parametrize("T", [1, 5, 12])

@@ -72,9 +72,12 @@ __device__ __forceinline__ int4 qd_stream(const int8_t *p) {
   return v;
 }
 
+__device__ __forceinline__ float qd_value(const QdenseArgs &a, float acc, float xs, float ws) {
+  const float v = __fmul_rn(__fmul_rn(acc, xs), ws);
+  return a.softcap > 0.f ? a.softcap * tanhf(v / a.softcap) : v;
+}
 __device__ __forceinline__ void qd_put(const QdenseArgs &a, int t, int n, float acc, float xs, float ws) {
-  float v = __fmul_rn(__fmul_rn(acc, xs), ws);
-  if (a.softcap > 0.f) v = a.softcap * tanhf(v / a.softcap);
+  const float v = qd_value(a, acc, xs, ws);
   const size_t o = (size_t)t * a.N + n;
   if (a.y32) a.y32[o] = v;
   if (a.y) a.y[o] = float_to_bf16_bits(v);
@@ -383,6 +386,8 @@ constexpr int kMmWStage = kMmM * kMmK;     // bytes of a weight stage
 constexpr int kMmMaxN = 256;
 constexpr int kMmSplitN = 128;             // rows per tile, at most, where blocks have one tile or a part of one
 constexpr int kMmMaxSplit = kQdenseMaxCluster;
+constexpr int kMmWst = 5;                  // weight stages, at least
+static_assert(kMmWst * kMmWStage >= kMmSplitN * kMmM * 4, "a block's part of the sums lies over them");
 constexpr int kMmBarBytes = 512;
 constexpr int kMmSmemMax = 227 * 1024;
 constexpr int kMmXsBytes = kMmMaxN * 4;
@@ -548,8 +553,10 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_arrive(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ void cluster_st(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
 // Rows of a shared tile that one block of the cluster adds up.
@@ -571,7 +578,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   uint64_t *tready = dempty + 2, *xfull = tready + 1, *xempty = xfull + P.xst;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(xempty + P.xst);
   float *s_xs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bar) + kMmBarBytes);  // [n] row scales
-  float *s_part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(s_xs) + kMmXsBytes);  // [split][quota][128]
+  float *s_part = reinterpret_cast<float *>(base);  // [n][128] this block's part of the sums, over the stages
   constexpr bool kPairs = kForm == kPair, kOwn = kForm == kFew;
   const bool tracer = blockIdx.x == 0 && tid == 0;
   const int split = kPairs ? 1 : P.split;
@@ -596,7 +603,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   if (tracer) trace_min(a.trace, kTrEntry);
   pdl_launch_dependents();
 
-  if (kPairs || split > 1) cluster_sync_all();  // every block of the cluster runs, its barriers are set
+  if (kPairs) cluster_sync_all();  // the other block runs, its barriers are set
   const int csize = kPairs ? 2 : split;
   const int first = blockIdx.x / csize, stride = gridDim.x / csize;  // units of this block
   const int units = P.units;
@@ -815,19 +822,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       dense::tc_fence_after();
       const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + db * 128;
       if (split > 1) {
-        // rows o * quota .. of the tile are added up in block o of the cluster
-        // (a lane per channel: 128 bytes a store; 16 bytes per lane in rows of a
-        // padded pitch took half as long again)
-        const int quota = mm_quota(P);
-        for (int o = side; ok && o * quota < cnt; o += kMmFin / 4) {
-          const uint32_t to = cluster_map(smem_addr(s_part + (size_t)(part * quota) * kMmM + rr), o);
-          for (int c0 = 0; c0 < quota; c0 += 16) {
-            float v[16];
-            dense::tc_ld16(ta + o * quota + c0, v);  // (columns past the tile's: not used)
+        // its part to shared memory, over the stages: their last MMA is complete
+        for (int c0 = 32 * side; ok && c0 < cnt; c0 += 8 * kMmFin) {
+          float v[32];
+          dense::tc_ld32(ta + c0, v);
+          const int m = min(32, cnt - c0);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c0 + j < quota) cluster_st(to + (uint32_t)((c0 + j) * kMmM) * 4u, v[j]);
-          }
+          for (int j = 0; j < 32; ++j)
+            if (j < m) s_part[(c0 + j) * kMmM + rr] = v[j];
         }
       } else {
         for (int c0 = 32 * side; ok && c0 < cnt; c0 += 8 * kMmFin) {
@@ -944,35 +946,61 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   }
   if (!kPairs && split > 1) {
     // One tile per cluster; this block adds the parts of its rows, a warp to a
-    // row, four channels per lane.
+    // row, four channels per lane, read from the other blocks' shared memory, 16
+    // bytes a lane.  (Single floats pushed by the blocks that have them: 128 x
+    // 2816 x 4096 11.4 us against 10.4, 128 x 704 x 2816 7.6 against 8.1.)
     __syncwarp();
     if (kOwn) pdl_wait();
     const MmUnit q = mm_unit<kForm>(P, a.T, first, rank);
-    const int n0 = q.n0, t0 = q.t0, cnt = q.cnt;
+    const int n0 = q.n0 + 4 * lane, t0 = q.t0, cnt = q.cnt;
     const int quota = mm_quota(P), r0 = part * quota, mine = min(quota, cnt - r0);
     float ws[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ws[i] = n0 + lane + 32 * i < a.N ? __ldg(a.ws + n0 + lane + 32 * i) : 0.f;
+    for (int i = 0; i < 4; ++i) ws[i] = n0 + i < a.N ? __ldg(a.ws + n0 + i) : 0.f;
     const float xl = lane < mine ? __ldcg(a.xs + t0 + r0 + lane) : 0.f;  // scales of rows lane, lane + 32
     const float xh = lane + 32 < mine ? __ldcg(a.xs + t0 + r0 + lane + 32) : 0.f;
+    const bool quad = a.N % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.y32) & 15) | (reinterpret_cast<uintptr_t>(a.y) & 7)) == 0;
     __syncwarp();
     cluster_sync_all();
+    uint32_t from[kMmMaxSplit];
+#pragma unroll
+    for (int r = 0; r < kMmMaxSplit; ++r)
+      from[r] = r < split ? cluster_map(smem_addr(s_part + (size_t)r0 * kMmM + 4 * lane), r) : 0u;
     for (int c = warp; c < mine; c += kMmThreads / 32) {
       const float xs = __shfl_sync(0xffffffffu, c < 32 ? xl : xh, c & 31);
-      float v[kMmMaxSplit][4];
+      float4 v[kMmMaxSplit];
 #pragma unroll
       for (int r = 0; r < kMmMaxSplit; ++r)
+        if (r < split) v[r] = cluster_ld4(from[r] + (uint32_t)(c * kMmM) * 4u);
+      float z[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int r = 1; r < kMmMaxSplit; ++r) {  // in rank order
+        if (r >= split) break;
+        z[0] += v[r].x;
+        z[1] += v[r].y;
+        z[2] += v[r].z;
+        z[3] += v[r].w;
+      }
+      const int t = t0 + r0 + c;
+      if (quad) {
+        if (n0 < a.N) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = qd_value(a, z[i], xs, ws[i]);
+          const size_t o = (size_t)t * a.N + n0;
+          if (a.y32) *reinterpret_cast<float4 *>(a.y32 + o) = make_float4(z[0], z[1], z[2], z[3]);
+          if (a.y) {
+            const uint32_t lo = float_to_bf16_bits(z[0]) | (uint32_t)float_to_bf16_bits(z[1]) << 16;
+            const uint32_t hi = float_to_bf16_bits(z[2]) | (uint32_t)float_to_bf16_bits(z[3]) << 16;
+            *reinterpret_cast<uint2 *>(a.y + o) = make_uint2(lo, hi);
+          }
+        }
+      } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          v[r][i] = r < split ? s_part[(size_t)(r * quota + c) * kMmM + lane + 32 * i] : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float sum = v[0][i];
-#pragma unroll
-        for (int r = 1; r < kMmMaxSplit; ++r) sum += v[r][i];  // in rank order
-        if (n0 + lane + 32 * i < a.N) qd_put(a, t0 + r0 + c, n0 + lane + 32 * i, sum, xs, ws[i]);
+          if (n0 + i < a.N) qd_put(a, t, n0 + i, z[i], xs, ws[i]);
       }
     }
+    cluster_sync_all();  // no block leaves while another reads its part
   }
   if (tracer) trace_max(a.trace, kTrExit);
 }
@@ -980,22 +1008,23 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
 // Tiles of up to 256 rows where they fill the device, by pairs of blocks above
 // 128: a 128-wide K stage takes 0.45 us at 128 rows, 0.65 us at 256.
 //
-// Fewer tiles than half the SMs: up to 128 rows per tile, and a cluster of
-// `split` blocks per tile if that pays: the stages (0.36 us there) go down by
-// the factor, the exchange of the parts costs 1 us + 28 ns per row of the
-// tile, 0.8 us more for clusters of over four blocks (128 x 2816 x 4096,
-// clusters of 1, 2, 3, 4, 6: 16.4, 15.4, 13.3, 11.3, 12.0 us; 32 x 704 x 2816,
-// 1, 2, 4, 8: 11.4, 9.8, 8.0, 7.2; 128 x 1408 x 704, 1, 2, 4: 6.8, 9.1, 8.4).
+// Fewer of those than half the SMs: up to 128 rows per tile.  Where every block
+// then has one tile or less, two choices by what they were measured to cost:
+//   a cluster of s blocks per tile, each with a part of its stages, the parts
+//   added up at 1.2 us + 7 ns per row of the tile + 6 ns per block (4 ns more per
+//   row for clusters of over four; 0.6 us where there are several tiles of rows:
+//   their norm's blocks leave a cluster's SMs late);
+//   the rows widened by a launch before (1.45 us, then 0.35 us per stage) or by
+//   the finish warps (0.37 us + 2 ns per row and stage).
+// Measured, us, clusters of 1, 2, 3, 4, 6 (16 x 704 also 8):
+//   16 x 704 x 2816    launch 11.2 8.8 7.8 7.3 6.6 6.3, finish warps 11.4 8.1 6.9 6.2 5.3 5.1
+//   48 x 2816 x 2816   launch 11.5 9.5 8.4 7.8 7.4, finish warps 12.7 9.4 7.8 7.2 6.8
+//   80 x 704 x 704     launch 6.3 7.2 7.0 7.1 6.7, finish warps 6.0 6.2 5.8 6.0 5.6
+//   128 x 2816 x 4096  launch 16.1 12.7 11.3 10.4 10.4, finish warps 24.3 15.7 12.8 11.0 10.6
+//   128 x 8192 x 1408  launch 8.8 9.3, finish warps 10.7 9.8
 // clusters[s]: clusters of s blocks that the device holds at once (more than
 // those would run in a second wave: 16 tiles in clusters of 8 took 15.7 us, in
 // clusters of 4 10.4).
-//
-// One tile or part per block: the finish warps widen the rows, which saves the
-// launch for it (about 1 us) and costs each stage 0.04 us at 16 rows, 0.09 at
-// 64, 0.19 at 128.  16 x 4096 x 2816 (6 stages): 6.8 us against 7.9 with the
-// launch; 64 x 1408 x 2816 (3 stages) 6.2 against 7.3; 48 x 16384 x 2816 (22)
-// 14.1 both; 64 x 16384 x 8192 (64) 36.1 against 31.4; 128 x 2816 x 8192 (11)
-// 14.7 against 13.8; 128 x 4096 x 704 (6, whole tiles) 7.5 against 6.9.
 //
 // The last round of tiles of pairs, if at most half the pairs have one: in
 // halves.
@@ -1009,22 +1038,25 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   p.split = 1;
   tiles(kMmMaxN);
   const int nst = (K + kMmK - 1) / kMmK;
-  if (2 * p.ntile * p.ttile <= n_sm) {
-    tiles(kMmSplitN);
-    double least = 0.36 * nst;
-    for (int s = 2; s <= kMmMaxSplit && s <= nst; ++s) {
-      const double t = 0.36 * ((nst + s - 1) / s) + 1.0 + 0.028 * p.n + (s > 4 ? 0.8 : 0.0);
-      if (p.ntile * p.ttile <= clusters[s] && t < least) {
+  if (2 * p.ntile * p.ttile <= n_sm) tiles(kMmSplitN);
+  p.form = p.n > kMmSplitN ? kPair : kOne;
+  if (p.form == kOne && p.ntile * p.ttile <= n_sm) {
+    const int count = p.ntile * p.ttile;
+    double least = 0.0;
+    for (int s = 1; s <= kMmMaxSplit && s <= nst; ++s) {
+      if (s > 1 && count > clusters[s]) continue;
+      const int stages = (nst + s - 1) / s;
+      const double sum =
+          s == 1 ? 0.0 : 1.2 + 0.007 * p.n + 0.006 * count * s + (s > 4 ? 0.004 * p.n : 0.0) + (p.ttile > 1 ? 0.6 : 0.0);
+      const double one = 1.45 + 0.35 * stages, few = (0.37 + 0.002 * p.n) * stages;
+      const double t = sum + (one < few ? one : few);
+      if (s == 1 || t < least) {
         least = t;
         p.split = s;
+        p.form = one < few ? kOne : kFew;
       }
     }
   }
-  p.form = p.n > 128 ? kPair : kOne;  // (split tiles are narrower)
-  const int stages = (nst + p.split - 1) / p.split;
-  if (p.form == kOne && p.ntile * p.ttile * p.split <= n_sm &&
-      (p.n <= 96 ? stages * (p.n + 16) < 1550 : p.split > 1 && stages * (p.n + 16) < 900))
-    p.form = kFew;
   int room = n_sm;  // units at once
   if (p.form == kPair) {
     p.ntile = (p.ntile + 1) / 2;
@@ -1043,16 +1075,13 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   p.dbufs = p.n <= 128 ? 2 : 1;
   // Weight stages: whole tiles stream them from HBM (24 x 262144 x 2816 with 5,
   // 7, 9, 12: 128, 123, 124, 125 us); the others need the room otherwise.
-  p.wst = p.form == kOne && p.split == 1 ? 7 : 5;
-  p.rst = p.form == kOne ? (p.split > 1 ? 2 : 3) : 4;
+  p.wst = p.form == kOne && p.split == 1 ? 7 : kMmWst;
+  p.rst = p.form == kOne ? 3 : 4;
   p.xst = p.form == kFew ? 4 : 0;
-  const int parts = p.split > 1 ? p.split * mm_quota(p) * kMmM * 4 : 0;
   auto bytes = [&] {
-    return p.wst * kMmWStage + p.rst * 2 * p.nload * 128 + p.xst * p.n * 128 + kMmBarBytes + kMmXsBytes + 1024 + parts;
+    return p.wst * kMmWStage + p.rst * 2 * p.nload * 128 + p.xst * p.n * 128 + kMmBarBytes + kMmXsBytes + 1024;
   };
-  if (p.form == kFew && bytes() > kMmSmemMax) p.rst = 2;
-  if (p.form == kFew && bytes() > kMmSmemMax) p.xst = 2;
-  while (bytes() > kMmSmemMax) --p.wst;
+  if (bytes() > kMmSmemMax) p.rst = 2;  // (kFew, over 80 rows)
   p.smem = bytes();
   return p;
 }

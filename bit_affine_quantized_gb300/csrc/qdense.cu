@@ -25,7 +25,7 @@
 // and widened on its way into the tensor cores:
 //   weights warp   TMA: 128 channels x 128 codes per stage
 //   rows warp      TMA: up to 128 rows x 128 fp16 per stage and block
-//   8 widen warps  a channel per thread and half stage: 64 codes from shared
+//   8 widen warps  four to a stage, a channel per thread: 128 codes from shared
 //                  memory to fp16 pairs in registers to the A operand in
 //                  tensor memory
 //   MMA warp       tcgen05.mma, M = 128 channels (A in tensor memory),
@@ -41,7 +41,7 @@
 // both read (cta_group::2).  A 256-row stage brings 48 KB into an SM's shared
 // memory, 768 clocks at 64 bytes each; single blocks would bring 80 KB, 1280
 // clocks, more than the stage's MMAs (1024), and took 4 to 9 % longer.  Of 4096
-// x 4096 x 2816's 62 us (1530 TFLOP/s; a library product of fp16 operands takes
+// x 4096 x 2816's 60 us (1570 TFLOP/s; a library product of fp16 operands takes
 // 53 us on such integers, 60 us on random values) the widening of the rows is
 // 6, the stores of the outputs 6, and the rest runs at the rate that a library
 // product reaches.  Up to 128 rows pairs were 3 to 7 % slower than single
@@ -386,7 +386,7 @@ constexpr int kMmWStage = kMmM * kMmK;     // bytes of a weight stage
 constexpr int kMmMaxN = 256;
 constexpr int kMmSplitN = 128;             // rows per tile, at most, where blocks have one tile or a part of one
 constexpr int kMmMaxSplit = kQdenseMaxCluster;
-constexpr int kMmWst = 5;                  // weight stages, at least
+constexpr int kMmWst = 6;                  // weight stages, at least
 static_assert(kMmWst * kMmWStage >= kMmSplitN * kMmM * 4, "a block's part of the sums lies over them");
 constexpr int kMmBarBytes = 512;
 constexpr int kMmSmemMax = 227 * 1024;
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     // rows (its own copies, and a word from the other block) and finish warps.
     uint64_t *b = bar + tid;
     int n = 1;
-    if ((b >= wempty && b < rfull) || (b >= afull && b < aempty)) n = kMmWiden;
+    if ((b >= wempty && b < rfull) || (b >= afull && b < aempty)) n = kMmWiden / 2;
     if (b >= dempty && b < tready) n = kMmFin;
     if (b >= xempty || (kOwn && b >= rfull && b < rempty)) n = kMmFin / 2;
     if (kPairs && leader && ((b >= rfull && b < rempty) || (b >= afull && b < aempty) || (b >= dempty && b < tready)))
@@ -877,60 +877,62 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
   } else {
     // ============================================================ widen
-    // Thread: channel rr of the tile, 64 of a stage's 128 codes.  Its 16-byte
-    // chunk j lies at j ^ (rr % 8) of the row (128-byte swizzle).  A stage's
-    // tile is announced one stage later, when its store into tensor memory is
-    // long complete.
-    const int half = warp >> 2, rr = 32 * (warp & 3) + lane, sw = rr & 7;
+    // Two halves of the warps take turns at the stages, so that one's waits and
+    // loads pass while the other converts.  (The rings of weights and A tiles have
+    // even lengths: each barrier belongs to one half.)  Thread: channel rr of the
+    // tile, a stage's 128 codes in two pieces of 64.  Its 16-byte chunk j lies at
+    // j ^ (rr % 8) of the row (128-byte swizzle).
+    const int grp = warp >> 2, rr = 32 * (warp & 3) + lane, sw = rr & 7;
     bool ok = mm_wait(tready, 0);
-    const uint32_t tmem =
-        *reinterpret_cast<volatile uint32_t *>(s_tmem) + ((uint32_t)(32 * (warp & 3)) << 16) + kMmACol + 32 * half;
-    int st = 0, ph = 0, gi = 0, told = 0;
-    auto tell = [&]() {  // stage `told` is in tensor memory
-      mm_st_wait();
-      dense::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (leader)
-          mm_arrive(&afull[told % kMmABufs]);
-        else
-          cluster_arrive(cluster_map(smem_addr(&afull[told % kMmABufs]), 0));
-      }
-      ++told;
-    };
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem) + ((uint32_t)(32 * (warp & 3)) << 16) + kMmACol;
+    int st = grp, ph = 0, gi = 0;
     for (int u = first; u < units && ok; u += stride) {
       if (mm_unit<kForm>(P, a.T, u, rank).cnt <= 0) continue;
       for (int s = st0; s < st1 && ok; ++s, ++gi) {
+        if ((gi & 1) != grp) continue;
+        const int ab = gi % kMmABufs;
         ok = mm_wait(&wfull[st], ph);
         const uint8_t *row = wbuf + st * kMmWStage + rr * 128;
-        uint4 c[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4 *>(row + (((4 * half + j) ^ sw) << 4));
-        uint32_t o[32];
+        for (int h = 0; h < 2; ++h) {
+          uint4 c[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          widen4(c[j].x, o[8 * j], o[8 * j + 1]);
-          widen4(c[j].y, o[8 * j + 2], o[8 * j + 3]);
-          widen4(c[j].z, o[8 * j + 4], o[8 * j + 5]);
-          widen4(c[j].w, o[8 * j + 6], o[8 * j + 7]);
+          for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4 *>(row + (((4 * h + j) ^ sw) << 4));
+          uint32_t o[32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            widen4(c[j].x, o[8 * j], o[8 * j + 1]);
+            widen4(c[j].y, o[8 * j + 2], o[8 * j + 3]);
+            widen4(c[j].z, o[8 * j + 4], o[8 * j + 5]);
+            widen4(c[j].w, o[8 * j + 6], o[8 * j + 7]);
+          }
+          if (h == 0) {
+            if (gi >= kMmABufs) ok = ok && mm_wait(&aempty[ab], ((gi / kMmABufs) - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            dense::tc_fence_after();
+          } else {
+            __syncwarp();
+            if (lane == 0) mm_arrive(&wempty[st]);
+          }
+          mm_st32(tmem + 64 * ab + 32 * h, o);
         }
+        if (!ok) break;
+        mm_st_wait();
+        dense::tc_fence_before();
         __syncwarp();
-        if (lane == 0) mm_arrive(&wempty[st]);
-        if (++st == P.wst) {
-          st = 0;
+        if (lane == 0) {
+          if (leader)
+            mm_arrive(&afull[ab]);
+          else
+            cluster_arrive(cluster_map(smem_addr(&afull[ab]), 0));
+        }
+        st += 2;
+        if (st >= P.wst) {
+          st -= P.wst;
           ph ^= 1;
         }
-        if (told < gi) tell();
-        const int ab = gi % kMmABufs;
-        if (gi >= kMmABufs) ok = ok && mm_wait(&aempty[ab], ((gi / kMmABufs) - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          dense::tc_fence_after();
-          mm_st32(tmem + 64 * ab, o);
-        }
       }
-      // a unit's last stage is not kept waiting for the next unit's weights
-      if (ok && told < gi) tell();
     }
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
   }
@@ -1073,9 +1075,10 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   }
   p.nload = p.form == kPair ? p.n / 2 : p.n;
   p.dbufs = p.n <= 128 ? 2 : 1;
-  // Weight stages: whole tiles stream them from HBM (24 x 262144 x 2816 with 5,
-  // 7, 9, 12: 128, 123, 124, 125 us); the others need the room otherwise.
-  p.wst = p.form == kOne && p.split == 1 ? 7 : kMmWst;
+  // Weight stages, an even number: whole tiles stream them from HBM (24 x 262144 x
+  // 2816 with 5, 7, 9, 12: 128, 123, 124, 125 us); the others need the room
+  // otherwise.
+  p.wst = p.form == kOne && p.split == 1 ? 8 : kMmWst;
   p.rst = p.form == kOne ? 3 : 4;
   p.xst = p.form == kFew ? 4 : 0;
   auto bytes = [&] {

@@ -54,7 +54,8 @@ __device__ __forceinline__ unsigned long long lg_key(float f, unsigned id) {
 
 struct RowRules {
   float rep, pres, freq;
-  const float *bias;  // the row's bias values
+  const float *bias;   // the row's bias values
+  const float *first;  // the first of them, one per thread of the block, in shared memory
 };
 
 // One logit through the rules; c, b: its words of the two tables.
@@ -64,7 +65,7 @@ __device__ __forceinline__ float lg_apply(float l, unsigned c, unsigned b, const
     const unsigned n = c & ~kInPrompt;
     if (n != 0u) l = __fsub_rn(__fsub_rn(l, __fmul_rn(r.freq, (float)n)), r.pres);
   }
-  if (b != 0u) l = __fadd_rn(l, __ldg(r.bias + b - 1));
+  if (b != 0u) l = __fadd_rn(l, b <= (unsigned)kLgThreads ? r.first[b - 1] : __ldg(r.bias + b - 1));
   return l;
 }
 
@@ -93,6 +94,7 @@ template <bool kHist, bool kBias, bool kMask, bool kQuad>
 __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs a) {
   extern __shared__ __align__(16) unsigned lsm[];
   __shared__ unsigned long long s_best[kLgThreads / 32];
+  __shared__ float s_first[kBias ? kLgThreads : 1];  // the row's first bias values: from memory each would stall its warp
   const int tid = threadIdx.x, V = a.V;
   constexpr int kStep = kQuad ? 1 : kLgThreads;  // distance of a thread's tokens
   const int own = kQuad ? 4 * tid : tid;         // its first token of a group
@@ -159,7 +161,8 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
   for (int i = 0; i < kLgRing - 1; ++i) copy_next(i);  // one slice ahead of the reads
 
   bool fresh = true, bad_id = false, bad = false;
-  RowRules rr = {1.f, 0.f, 0.f, nullptr};
+  RowRules rr = {1.f, 0.f, 0.f, nullptr, s_first};
+  float bw = 0.f;
   int hlen = 0, plen = 0, blen = 0, hv[kHistRegs], bv = 0, done = 0;
   float best = -INFINITY;  // the thread's best of the row so far
   int best_id = 0;
@@ -174,6 +177,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
     // this thread's places of the segment's first slice
     float *out = a.out ? a.out + (size_t)t * a.ld_out + v0 + own : nullptr;
     if (kHist || kBias) {
+      const bool begun = fresh;
       const int32_t *hist = a.history + (size_t)t * a.history_stride, *bids = a.bias_ids + (size_t)t * a.bias_stride;
       if (fresh) {  // a row begins: its rules and its lists' first entries (a list's buffer is a stride long whatever its length)
         fresh = false;
@@ -191,11 +195,13 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
           blen = __ldcg(a.bias_len + t);
           rr.bias = a.bias_values + (size_t)t * a.bias_stride;
           bv = tid < a.bias_stride ? __ldcg(bids + tid) : 0;
+          bw = tid < a.bias_stride ? __ldcg(rr.bias + tid) : 0.f;
         }
         hlen = max(0, min(hlen, a.history_stride));
         blen = max(0, min(blen, a.bias_stride));
       }
       __syncthreads();  // every thread is done with the segment before: the tables are clear
+      if (kBias && begun) s_first[tid] = bw;
       if (kHist) {
         auto count = [&](int id, int i) {
           const unsigned d = (unsigned)id - (unsigned)v0;

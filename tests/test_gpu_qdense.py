@@ -76,7 +76,7 @@ SHAPES = [(1, 1, 16), (1, 2816, 2816), (1, 4097, 208), (2, 33, 64), (3, 130, 107
           # more tiles than SMs: the last round in halves of tiles (one of them past the last row)
           (512, 10240, 144), (520, 7000, 64), (4112, 1280, 64), (4097, 1290, 80),
           # one tile or part per block, with more stages of K than a block holds at once
-          (16, 8200, 4096), (24, 12800, 2832), (9, 5000, 80), (96, 1300, 1936), (64, 19400, 2176),
+          (20, 300, 16), (128, 1, 48), (16, 8200, 4096), (24, 12800, 2832), (9, 5000, 80), (96, 1300, 1936), (64, 19400, 2176),
           # tiles shared by clusters of every size; K that ends inside a stage and inside its first half
           (40, 128, 2816), (150, 128, 1040), (100, 1408, 2832), (64, 2816, 1120), (200, 704, 4112), (33, 5632, 528)]
 
@@ -175,6 +175,31 @@ def test_captured_and_replayed(moe, T):
     for x, both in got:
         for o in both:
             assert np.all(np.abs(o.cpu().numpy() - BO.qdense(x, xs, w, ws)) <= bound(x, w, xs, ws))
+
+
+@pytest.mark.parametrize("T", [1, 5, 16, 40, 128, 150, 300, 700])
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_outputs_off_a_boundary(moe, T, off):
+    """Outputs and scales that start off a 16-byte boundary, the values around them left alone."""
+    N, K = 1412, 1040
+    x, w = codes(60, T, K), codes(61, N, K)
+    xs, ws = scales(62, T, N)
+    shift = lambda v: torch.cat([torch.zeros(off, device="cuda"), torch.from_numpy(v).cuda()])[off:]
+    wd = bq.make_qdense_weights(N, K, torch.from_numpy(w).cuda(), shift(ws))
+    work = torch.empty(moe.qdense_workspace_bytes(wd, T), dtype=torch.uint8, device="cuda")
+    a = torch.full((T * N + 8,), 1234, dtype=torch.int16, device="cuda")
+    b = torch.full((T * N + 8,), 1234.0, device="cuda")
+    moe.qdense_forward(torch.from_numpy(x).cuda(), shift(xs), T, wd, work, y=a[off:off + T * N], y32=b[off:off + T * N])
+    torch.cuda.synchronize()
+    assert moe.get_error() == bq.MOE_OK
+    z, lim = BO.qdense(x, xs, w, ws), bound(x, w, xs, ws)
+    got = b.cpu().numpy()
+    assert np.all(np.abs(got[off:off + T * N].reshape(T, N) - z) <= lim)
+    bits = a.cpu().numpy().view(np.uint16)
+    y16 = (bits[off:off + T * N].astype(np.uint32) << 16).view(np.float32).reshape(T, N)
+    assert np.all(np.abs(y16 - z) <= lim + 2.0 ** -8 * (np.abs(z) + lim))
+    for v in (got, a.cpu().numpy()):
+        assert np.all(v[:off] == 1234) and np.all(v[off + T * N:] == 1234)
 
 
 @pytest.mark.parametrize("T,N,K", [(2, 3000, 2816), (7, 3000, 2816), (16, 8200, 4096), (24, 12800, 2832),

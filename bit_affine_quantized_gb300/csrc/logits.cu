@@ -14,14 +14,23 @@
 // memory (integer atomics: the result does not depend on their order), so no
 // table in global memory has to be kept or cleared; the start of a row's
 // history stays in registers over the block's segments.  A table word holds
-// the count after the prompt in its low 31 bits and "occurs in the prompt" in
-// bit 31.  A second table holds, per token of the segment, the number of its
-// last bias entry.  A segment is up to two slices of eight tokens per thread:
-// every token of the history is looked at once per segment, which at
-// 4096-token segments and as many history tokens was a third of the time.
-// The logits are copied slices ahead into a ring in shared memory (cp.async)
-// in which every thread has places of its own, so that tables are built while
-// logits are on their way and only a segment's ends need barriers.
+// the count after the prompt, a bitmap which tokens occur at all.  A second
+// table holds, per token of the segment, the number of its last bias entry, a
+// second bitmap which tokens have one.  A segment is up to two slices of eight
+// tokens per thread: every token of the history is looked at once per segment,
+// which at 4096-token segments and as many history tokens was a third of the
+// time.  The logits are copied slices ahead into a ring in shared memory
+// (cp.async) in which every thread has places of its own, so that tables are
+// built while logits are on their way and only a segment's ends need barriers.
+// A slice's rules are applied in the ring, to the tokens whose bits are set, by
+// the warp that the tokens belong to; the pass over all tokens is free of them.
+//
+// 64 x 262144 with a history of 4096, 300 biases and a mask: 32 us; the logits
+// alone, read and written, 27.6 (134 MB, 20 at the copy rate): the rest are the
+// two barriers and the counting per segment.  A ring of three or four slices was
+// slower (28.7, 29.1), two blocks of 512 threads per SM gained 0.7 on the logits
+// alone and lost 1.3 with the histories, tables read for every token took 36.
+// 17 x 100003 with a history of 20000, biases and a mask: 13.7 us.
 // The blocks of a row merge their best (logit, id) with one 64-bit atomicMax
 // each; the one that adds the row's last segments writes the token and clears
 // the row's state.
@@ -42,7 +51,6 @@ constexpr int kLgRing = 2;       // slices of logits in shared memory
 constexpr int kMaskSlice = kLgSlice / 32;       // mask words of a slice
 constexpr int kLgSegMax = 2;     // slices per segment, at most
 constexpr int kHistRegs = 4;     // history entries per thread that stay in registers
-constexpr unsigned kInPrompt = 0x80000000u;
 
 // Orders finite floats as unsigned integers (larger float, larger key; both
 // zeros the same); with the id's complement the lower id of equals wins.
@@ -58,13 +66,11 @@ struct RowRules {
   const float *first;  // the first of them, one per thread of the block, in shared memory
 };
 
-// One logit through the rules; c, b: its words of the two tables.
-__device__ __forceinline__ float lg_apply(float l, unsigned c, unsigned b, const RowRules &r) {
-  if (c != 0u) {
-    l = l > 0.f ? __fdiv_rn(l, r.rep) : __fmul_rn(l, r.rep);
-    const unsigned n = c & ~kInPrompt;
-    if (n != 0u) l = __fsub_rn(__fsub_rn(l, __fmul_rn(r.freq, (float)n)), r.pres);
-  }
+// One logit through the rules; in: it occurs in the history, n times of those
+// after the prompt; b: 1 + its bias entry, 0 for none.
+__device__ __forceinline__ float lg_apply(float l, bool in, unsigned n, unsigned b, const RowRules &r) {
+  if (in) l = l > 0.f ? __fdiv_rn(l, r.rep) : __fmul_rn(l, r.rep);
+  if (n != 0u) l = __fsub_rn(__fsub_rn(l, __fmul_rn(r.freq, (float)n)), r.pres);
   if (b != 0u) l = __fadd_rn(l, b <= (unsigned)kLgThreads ? r.first[b - 1] : __ldg(r.bias + b - 1));
   return l;
 }
@@ -101,9 +107,10 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
   const int seg = a.seg * kLgSlice;
   float *const ring = reinterpret_cast<float *>(lsm) + own;
   unsigned *const cnt = lsm + kLgRing * kLgSlice, *const bix = cnt + (kHist ? seg : 0);
-  unsigned *const bits = bix + (kBias ? seg : 0);  // one per token: a rule names it
+  // a bit per token: it is in the history, it has a bias
+  unsigned *const hbits = bix + (kBias ? seg : 0), *const bbits = hbits + (kHist ? seg / 32 : 0);
   // mask words of the slices in the ring, per group four for the 128 tokens of a warp
-  uint32_t *const mring = bits + (kHist || kBias ? seg / 32 : 0) + (tid >> 5) * 4;
+  uint32_t *const mring = bbits + (kBias ? seg / 32 : 0) + (tid >> 5) * 4;
   constexpr int kMaskGroup = kLgGroup / 32;
   const bool tracer = blockIdx.x == 0 && tid == 0;
   if (tracer) trace_min(a.trace, kTrEntry);
@@ -111,7 +118,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
   const long long units = (long long)ns * a.T;
   const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
   if (kHist || kBias)
-    for (int i = tid; i < (((kHist ? 1 : 0) + (kBias ? 1 : 0)) * seg + seg / 32) / 4; i += kLgThreads)
+    for (int i = tid; i < ((kHist ? 1 : 0) + (kBias ? 1 : 0)) * (seg + seg / 32) / 4; i += kLgThreads)
       reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0u, 0u, 0u, 0u);
   pdl_wait();
   pdl_launch_dependents();
@@ -160,6 +167,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
 #pragma unroll
   for (int i = 0; i < kLgRing - 1; ++i) copy_next(i);  // one slice ahead of the reads
 
+  __shared__ unsigned s_queue[kHist ? kLgThreads / 32 : 1][64];
   bool fresh = true, bad_id = false, bad = false;
   RowRules rr = {1.f, 0.f, 0.f, nullptr, s_first};
   float bw = 0.f;
@@ -203,34 +211,65 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
       __syncthreads();  // every thread is done with the segment before: the tables are clear
       if (kBias && begun) s_first[tid] = bw;
       if (kHist) {
-        auto count = [&](int id, int i) {
-          const unsigned d = (unsigned)id - (unsigned)v0;
-          if (d < (unsigned)n) {
-            if (i < plen)
-              atomicOr(cnt + d, kInPrompt);
-            else
-              atomicAdd(cnt + d, 1u);
-            atomicOr(bits + (d >> 5), 1u << (d & 31u));
-          }
-          bad_id = bad_id || (unsigned)id >= (unsigned)V;
+        auto count = [&](unsigned e) {  // a token of the segment, "in the prompt" in bit 31
+          const unsigned d = e & 0x7FFFFFFFu;
+          if (d == e) atomicAdd(cnt + d, 1u);
+          atomicOr(hbits + (d >> 5), 1u << (d & 31u));
         };
 #pragma unroll
-        for (int k = 0; k < kHistRegs; ++k)
-          if (tid + k * kLgThreads < hlen) count(hv[k], tid + k * kLgThreads);
-        int i = kHistRegs * kLgThreads;
-        if ((reinterpret_cast<uintptr_t>(hist) & 15u) == 0) {
+        for (int k = 0; k < kHistRegs; ++k) {
+          const int i = tid + k * kLgThreads;
+          const unsigned d = (unsigned)hv[k] - (unsigned)v0;
+          if (i < hlen && d < (unsigned)n) count(i < plen ? d | 0x80000000u : d);
+          bad_id = bad_id || (i < hlen && (unsigned)hv[k] >= (unsigned)V);
+        }
+        if (hlen > kHistRegs * kLgThreads) {
+          // Few of a longer history's tokens are the segment's.  A warp collects
+          // those and counts them 32 at a time: an atomic takes as long for one lane
+          // as for all (17 x 100003, history 20000: 13.3 us without, 11.9 so; for the tokens
+          // above, which cost no loads, collecting takes longer than it saves).
+          const int lane = tid & 31;
+          unsigned *const queue = s_queue[tid >> 5];
+          int held = 0;
+          auto look = [&](int id, int i) {  // (every lane of the warp; past the history: not there)
+            const unsigned d = (unsigned)id - (unsigned)v0;
+            const bool there = i < hlen, here = there && d < (unsigned)n;
+            bad_id = bad_id || (there && (unsigned)id >= (unsigned)V);
+            const unsigned m = __ballot_sync(0xffffffffu, here);
+            if (here) queue[held + __popc(m & ((1u << lane) - 1u))] = i < plen ? d | 0x80000000u : d;
+            held += __popc(m);
+            if (held >= 32) {
+              __syncwarp();
+              count(queue[lane]);
+              held -= 32;
+              const unsigned e = queue[32 + lane];
+              __syncwarp();
+              if (lane < held) queue[lane] = e;
+            }
+          };
+          if ((reinterpret_cast<uintptr_t>(hist) & 15u) == 0) {
+#pragma unroll 2
+            for (int i = kHistRegs * kLgThreads + 4 * tid; i - 4 * lane < hlen; i += 4 * kLgThreads) {
+              int4 q = make_int4(0, 0, 0, 0);
+              if (i + 3 < a.history_stride) {
+                q = __ldcg(reinterpret_cast<const int4 *>(hist + i));
+              } else {  // the buffer's last one to three
+                if (i < hlen) q.x = __ldcg(hist + i);
+                if (i + 1 < hlen) q.y = __ldcg(hist + i + 1);
+                if (i + 2 < hlen) q.z = __ldcg(hist + i + 2);
+              }
+              look(q.x, i);
+              look(q.y, i + 1);
+              look(q.z, i + 2);
+              look(q.w, i + 3);
+            }
+          } else {
 #pragma unroll 4
-          for (i += 4 * tid; i + 3 < hlen; i += 4 * kLgThreads) {
-            const int4 q = __ldcg(reinterpret_cast<const int4 *>(hist + i));
-            count(q.x, i);
-            count(q.y, i + 1);
-            count(q.z, i + 2);
-            count(q.w, i + 3);
+            for (int i = kHistRegs * kLgThreads + tid; i - lane < hlen; i += kLgThreads)
+              look(i < hlen ? __ldcg(hist + i) : 0, i);
           }
-          for (; i < hlen; ++i) count(__ldcg(hist + i), i);  // the last one to three (their thread's loop ended there)
-        } else {
-#pragma unroll 8
-          for (i += tid; i < hlen; i += kLgThreads) count(__ldcg(hist + i), i);
+          __syncwarp();
+          if (lane < held) count(queue[lane]);
         }
       }
       if (kBias) {
@@ -238,7 +277,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
           const unsigned d = (unsigned)id - (unsigned)v0;
           if (d < (unsigned)n) {
             atomicMax(bix + d, (unsigned)(i + 1));
-            atomicOr(bits + (d >> 5), 1u << (d & 31u));
+            atomicOr(bbits + (d >> 5), 1u << (d & 31u));
           }
           bad_id = bad_id || (unsigned)id >= (unsigned)V;
         };
@@ -257,15 +296,17 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
       lg_wait<kLgRing - 1>();                      // the thread's part of this slice has landed
       if (kMask || kHist || kBias) __syncwarp();   // and its warp's
       if (kHist || kBias) {
-        uint8_t *const byte = reinterpret_cast<uint8_t *>(bits) + (at >> 3);
-        unsigned todo = *byte;
+        uint8_t *const hb = reinterpret_cast<uint8_t *>(hbits) + (at >> 3), *const bb = reinterpret_cast<uint8_t *>(bbits) + (at >> 3);
+        const unsigned in = kHist ? *hb : 0u;
+        unsigned todo = in | (kBias ? *bb : 0u);
         if (todo != 0u) {
-          *byte = 0;
+          if (kHist) *hb = 0;
+          if (kBias) *bb = 0;
           float *const lg = reinterpret_cast<float *>(lsm) + place * kLgSlice + patch;
           do {
             const int k = __ffs(todo) - 1;
             todo &= todo - 1u;
-            lg[k] = lg_apply(lg[k], kHist ? cnt[at + k] : 0u, kBias ? bix[at + k] : 0u, rr);
+            lg[k] = lg_apply(lg[k], in >> k & 1u, kHist ? cnt[at + k] : 0u, kBias ? bix[at + k] : 0u, rr);
             if (kHist) cnt[at + k] = 0u;
             if (kBias) bix[at + k] = 0u;
           } while (todo != 0u);
@@ -384,7 +425,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
 }
 
 size_t lg_smem(bool h, bool b, int seg) {
-  return (size_t)kLgSlice * 4 * (kLgRing + seg * ((h ? 1 : 0) + (b ? 1 : 0))) + (h || b ? (size_t)kLgSlice / 8 * seg : 0) +
+  return (size_t)kLgSlice * 4 * kLgRing + (size_t)(kLgSlice * 4 + kLgSlice / 8) * seg * ((h ? 1 : 0) + (b ? 1 : 0)) +
          (size_t)kLgRing * kMaskSlice * 4;
 }
 

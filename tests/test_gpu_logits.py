@@ -155,6 +155,27 @@ def test_counts_are_exact_over_a_long_history(moe):
     assert np.all(np.delete(got, 7, 1) == 1.0)
 
 
+@pytest.mark.parametrize("L", [4096, 4097, 4099, 4127, 5000, 8195, 12289, 20003])
+@pytest.mark.parametrize("stride", [0, 1])
+def test_every_token_of_a_long_history_counts(moe, L, stride):
+    """Histories at and past what stays in registers; a vocabulary of one
+    segment, so that every token is the segment's, and rows off a boundary."""
+    V, T = 777, 3
+    rng = np.random.default_rng(L)
+    h = rng.integers(0, V, (T, L + stride)).astype(np.int32)
+    n = np.array([L, L - 1, max(L - 40, 0)], dtype=np.int32)
+    p = np.array([0, 4100, L // 2], dtype=np.int32)
+    r = bq.make_logit_rules(history=cuda(h), history_len=cuda(n), prompt_len=cuda(p),
+                            frequency=torch.full((T,), 1.0, device="cuda"))
+    lg = torch.zeros((T, V), device="cuda")
+    out = torch.empty_like(lg)
+    moe.logits_process(lg, T, V, r, out=out)
+    torch.cuda.synchronize()
+    assert moe.get_error() == bq.MOE_OK
+    want = np.stack([-np.bincount(h[t, p[t]:n[t]], minlength=V) for t in range(T)])
+    assert np.array_equal(out.cpu().numpy(), want.astype(np.float32))
+
+
 def test_rows_with_nothing_left(moe):
     lg = logits_of(5, 4, 6000)
     lg[3] = -np.inf

@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   }
   __syncthreads();
   if (tracer) trace_min(a.trace, kTrEntry);
-  pdl_launch_dependents();
+  if (!kOwn) pdl_launch_dependents();  // (the launch before has waited for those before it)
 
   if (kPairs) cluster_sync_all();  // the other block runs, its barriers are set
   const int csize = kPairs ? 2 : split;
@@ -613,8 +613,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   if (warp == kMmWts) {
     // ============================================================ weights
     // Nothing that an earlier launch still writes is read here: the launch
-    // before this one (the widening of the rows) waited for those.
-    if (kOwn) pdl_wait();
+    // before this one (the widening of the rows) waited for those, or this does.
+    if (kOwn) {
+      pdl_wait();
+      pdl_launch_dependents();
+    }
     if (lane == 0) {
       fused::fence_proxy_async_global();
       bool ok = true;

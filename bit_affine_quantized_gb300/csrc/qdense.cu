@@ -36,16 +36,15 @@
 // bounds it (24 x 262144 x 2816: 123 us with a bf16 output, 6.0 TB/s of
 // codes; 14 rounds of tiles for 13.5 rounds of work are 4 of it, the stores of
 // the outputs 5).
-// More than 128 rows: a pair of blocks on a tile of 256 channels, each with 128
-// of them in its tensor memory and half of the rows in its shared memory, which
-// both read (cta_group::2).  A 256-row stage brings 48 KB into an SM's shared
-// memory, 768 clocks at 64 bytes each; single blocks would bring 80 KB, 1280
-// clocks, more than the stage's MMAs (1024), and took 4 to 9 % longer.  Of 4096
-// x 4096 x 2816's 60 us (1570 TFLOP/s; a library product of fp16 operands takes
-// 53 us on such integers, 60 us on random values) the widening of the rows is
-// 6, the stores of the outputs 6, and the rest runs at the rate that a library
-// product reaches.  Up to 128 rows pairs were 3 to 7 % slower than single
-// blocks.
+// More rows: a pair of blocks on a tile of 256 channels, each with 128 of them in
+// its tensor memory and half of the rows in its shared memory, which both read
+// (cta_group::2).  A 256-row stage brings 48 KB into an SM's shared memory, 768
+// clocks at 64 bytes each; single blocks would bring 80 KB, 1280 clocks, more
+// than the stage's MMAs (1024), and took 4 to 9 % longer.  Of 4096 x 4096 x
+// 2816's 60 us (1570 TFLOP/s; a library product of fp16 operands takes 53 us on
+// such integers, 60 us on random values) the widening of the rows is 6, the
+// stores of the outputs 6, and the rest runs at the rate that a library product
+// reaches.
 // Few tiles: the blocks of a cluster share a tile, each takes a part of K, and
 // the parts are added through distributed shared memory in rank order.
 #include <cuda.h>
@@ -393,7 +392,7 @@ constexpr int kMmSmemMax = 227 * 1024;
 constexpr int kMmXsBytes = kMmMaxN * 4;
 
 // kOne: tiles of up to 128 rows or parts of them; the rows widened by a launch
-// before.  kPair: wider tiles, a pair of blocks on each.  kFew: as kOne, one
+// before.  kPair: wider tiles, whole, a pair of blocks on each.  kFew: as kOne, one
 // tile or part of a tile per block; the rows come as 8-bit codes, and the finish
 // warps, idle until the sums are there, widen them.
 enum { kOne, kPair, kFew };
@@ -1010,8 +1009,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   if (tracer) trace_max(a.trace, kTrExit);
 }
 
-// Tiles of up to 256 rows where they fill the device, by pairs of blocks above
-// 128: a 128-wide K stage takes 0.45 us at 128 rows, 0.65 us at 256.
+// Tiles of up to 256 rows where they fill the device, by pairs of blocks: a
+// 128-wide K stage takes 0.45 us at 128 rows, 0.65 us at 256.
 //
 // Fewer of those than half the SMs: up to 128 rows per tile.  Where every block
 // then has one tile or less, two choices by what they were measured to cost:
@@ -1031,8 +1030,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
 // those would run in a second wave: 16 tiles in clusters of 8 took 15.7 us, in
 // clusters of 4 10.4).
 //
-// The last round of tiles of pairs, if at most half the pairs have one: in
-// halves.
+// Whole tiles of 48 rows and more go to pairs of blocks too, which halves what
+// each takes of the rows (64 x 131072 x 2816 67.4 us by single blocks, 66.5 by
+// pairs; 128 x 65536 x 2816 44.5, 41.6; 128 x 16384 x 16384 67.1, 60.4; 24 x
+// 65536 x 2816 38.2, 38.5), unless they are soon done (48 x 65536 x 704, 6
+// stages, 16.1, 16.4); of several tiles of rows from 112 (160 x 8192 x 2816,
+// 80 each, 12.0, 12.7; 512 x 4096 x 8192 29.7, 27.2).
+//
+// The last round of tiles of more than 128 rows, if at most half the pairs have
+// one: in halves.
 MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   MmPlan p;
   auto tiles = [&](int most) {
@@ -1062,6 +1068,8 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
       }
     }
   }
+  if (p.form == kOne && p.split == 1 && p.ntile > 1 && p.n >= (p.ttile == 1 ? 48 : 112) && nst * p.n >= 560)
+    p.form = kPair;
   int room = n_sm;  // units at once
   if (p.form == kPair) {
     p.ntile = (p.ntile + 1) / 2;
@@ -1071,7 +1079,7 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   p.whole = p.ntile * p.ttile;
   p.units = p.whole;
   const int rest = p.whole % room;
-  if (p.form == kPair && p.whole > room && rest > 0 && 2 * rest <= room) {
+  if (p.n > 128 && p.whole > room && rest > 0 && 2 * rest <= room) {
     p.n = (p.n + 63) / 64 * 64;
     p.whole -= rest;
     p.units = p.whole + 2 * rest;
@@ -1081,7 +1089,7 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   // Weight stages, an even number: whole tiles stream them from HBM (24 x 262144 x
   // 2816 with 5, 7, 9, 12: 128, 123, 124, 125 us); the others need the room
   // otherwise.
-  p.wst = p.form == kOne && p.split == 1 ? 8 : kMmWst;
+  p.wst = p.form != kFew && p.split == 1 && p.n <= 128 ? 8 : kMmWst;
   p.rst = p.form == kOne ? 3 : 4;
   p.xst = p.form == kFew ? 4 : 0;
   auto bytes = [&] {

@@ -76,6 +76,8 @@ SHAPES = [(1, 1, 16), (1, 2816, 2816), (1, 4097, 208), (2, 33, 64), (3, 130, 107
           # more tiles than SMs: the last round in halves of tiles (one of them past the last row)
           (512, 10240, 144), (520, 7000, 64), (4112, 1280, 64), (4097, 1290, 80),
           # one tile or part per block, with more stages of K than a block holds at once
+          # pairs of blocks on tiles of up to 128 rows, the second block's channels not there in the last
+          (48, 20000, 1600), (70, 19600, 1168), (128, 9900, 704), (333, 3900, 784), (1000, 1300, 1040),
           (20, 300, 16), (128, 1, 48), (16, 8200, 4096), (24, 12800, 2832), (9, 5000, 80), (96, 1300, 1936), (64, 19400, 2176),
           # tiles shared by clusters of every size; K that ends inside a stage and inside its first half
           (40, 128, 2816), (150, 128, 1040), (100, 1408, 2832), (64, 2816, 1120), (200, 704, 4112), (33, 5632, 528)]

@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(kQfThreads, 1) qdense_few_kernel(const QdenseA
             x1[j] = w1[j];
           }
           request(n0, b + kQfAhead);
+          __syncwarp();  // (mma.sync wants the warp together, and the loads depend on the lane)
 #pragma unroll
           for (int j = 0; j < kQfAhead; ++j) {
             if (b + j >= fe) break;  // (warp-uniform)
@@ -503,8 +504,13 @@ __device__ __forceinline__ void mm_commit(uint64_t *bar) {
   else
     dense::tc_commit(bar);
 }
+// The instructions below with .aligned (and bar.sync) have to be executed by a
+// warp's lanes together.  Lanes come apart wherever a branch depends on the lane
+// (one lane's arrival, channels past the last), and what brings them together for
+// certain is a warp barrier alone: each of these functions begins with one.
 template <int kForm>
 __device__ __forceinline__ void mm_alloc(uint32_t *dst) {
+  __syncwarp();
   if (kForm == kPair) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(dst)), "r"(512)
                  : "memory");
@@ -515,6 +521,7 @@ __device__ __forceinline__ void mm_alloc(uint32_t *dst) {
 }
 template <int kForm>
 __device__ __forceinline__ void mm_dealloc(uint32_t tmem) {
+  __syncwarp();
   if (kForm == kPair)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   else
@@ -524,6 +531,7 @@ __device__ __forceinline__ void mm_dealloc(uint32_t tmem) {
 // 32 registers of each lane to 32 tensor-memory columns of the warp's lanes
 // (complete after mm_st_wait).
 __device__ __forceinline__ void mm_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  __syncwarp();
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
@@ -533,7 +541,20 @@ __device__ __forceinline__ void mm_st32(uint32_t taddr, const uint32_t (&r)[32])
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void mm_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void mm_st_wait() {
+  __syncwarp();
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// 32 tensor-memory columns of the warp's lanes.
+__device__ __forceinline__ void mm_ld32(uint32_t taddr, float (&v)[32]) {
+  __syncwarp();
+  dense::tc_ld32(taddr, v);
+}
+// Barrier of the finish warps.
+__device__ __forceinline__ void mm_fin_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kMmFin * 32) : "memory");
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -541,6 +562,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The address of this block's shared memory `addr` in block `rank` of the cluster.
@@ -815,10 +837,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       const int db = du % P.dbufs;
       float ws = 0.f;
       if (split == 1) {  // the tile's row scales to shared memory while its sums are made
-        asm volatile("bar.sync 1, %0;" ::"n"(kMmFin * 32) : "memory");  // every finish warp is done with the tile before
+        mm_fin_sync();  // every finish warp is done with the tile before
         for (int i = ft; i < q.n; i += kMmFin * 32) s_xs[i] = i < cnt ? __ldcg(a.xs + t0 + i) : 0.f;
         ws = n < a.N ? __ldg(a.ws + n) : 0.f;
-        asm volatile("bar.sync 1, %0;" ::"n"(kMmFin * 32) : "memory");
+        mm_fin_sync();
       }
       ok = __all_sync(0xffffffffu, ok && mm_wait(&dfull[db], (du / P.dbufs) & 1));
       dense::tc_fence_after();
@@ -827,7 +849,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
         // its part to shared memory, over the stages: their last MMA is complete
         for (int c0 = 32 * side; ok && c0 < cnt; c0 += 8 * kMmFin) {
           float v[32];
-          dense::tc_ld32(ta + c0, v);
+          mm_ld32(ta + c0, v);
           const int m = min(32, cnt - c0);
 #pragma unroll
           for (int j = 0; j < 32; ++j)
@@ -836,33 +858,34 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       } else {
         for (int c0 = 32 * side; ok && c0 < cnt; c0 += 8 * kMmFin) {
           float v[32];
-          dense::tc_ld32(ta + c0, v);  // (columns past the tile's: not used)
+          mm_ld32(ta + c0, v);  // (columns past the tile's: not used)
           const int m = min(32, cnt - c0);
-          if (n >= a.N) continue;
-          const size_t o = (size_t)(t0 + c0) * a.N + n;
+          if (n < a.N) {
+            const size_t o = (size_t)(t0 + c0) * a.N + n;
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 xs = *reinterpret_cast<const float4 *>(s_xs + c0 + j);
-            v[j] = __fmul_rn(__fmul_rn(v[j], xs.x), ws);
-            v[j + 1] = __fmul_rn(__fmul_rn(v[j + 1], xs.y), ws);
-            v[j + 2] = __fmul_rn(__fmul_rn(v[j + 2], xs.z), ws);
-            v[j + 3] = __fmul_rn(__fmul_rn(v[j + 3], xs.w), ws);
-          }
-          if (a.softcap > 0.f) {
+            for (int j = 0; j < 32; j += 4) {
+              const float4 xs = *reinterpret_cast<const float4 *>(s_xs + c0 + j);
+              v[j] = __fmul_rn(__fmul_rn(v[j], xs.x), ws);
+              v[j + 1] = __fmul_rn(__fmul_rn(v[j + 1], xs.y), ws);
+              v[j + 2] = __fmul_rn(__fmul_rn(v[j + 2], xs.z), ws);
+              v[j + 3] = __fmul_rn(__fmul_rn(v[j + 3], xs.w), ws);
+            }
+            if (a.softcap > 0.f) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = a.softcap * tanhf(v[j] / a.softcap);
-          }
-          if (a.y32) {
-            float *p = a.y32 + o;
+              for (int j = 0; j < 32; ++j) v[j] = a.softcap * tanhf(v[j] / a.softcap);
+            }
+            if (a.y32) {
+              float *p = a.y32 + o;
 #pragma unroll
-            for (int j = 0; j < 32; ++j, p += a.N)
-              if (j < m) *p = v[j];
-          }
-          if (a.y) {
-            uint16_t *p = a.y + o;
+              for (int j = 0; j < 32; ++j, p += a.N)
+                if (j < m) *p = v[j];
+            }
+            if (a.y) {
+              uint16_t *p = a.y + o;
 #pragma unroll
-            for (int j = 0; j < 32; ++j, p += a.N)
-              if (j < m) *p = float_to_bf16_bits(v[j]);
+              for (int j = 0; j < 32; ++j, p += a.N)
+                if (j < m) *p = float_to_bf16_bits(v[j]);
+            }
           }
         }
       }

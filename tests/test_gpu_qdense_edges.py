@@ -1,0 +1,28 @@
+"""The dense 8-bit projection where its tiles end: channels that end inside a
+warp's 32, in every form of the tensor-core kernel; bounds as in
+test_gpu_qdense.py."""
+import numpy as np
+import pytest
+
+from oracle import batch_oracle as BO
+from synth import gen
+from test_gpu_qdense import F32, bound, codes, moe, run, scales  # noqa: F401  (moe: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,N,K", [
+    (70, 19585, 1168), (128, 9889, 704), (100, 39009, 80),       # whole tiles of up to 128 rows, several per warp
+    (300, 5007, 704), (512, 10223, 144), (1000, 1281, 1040), (250, 31, 80),  # pairs of blocks, halves of tiles
+    (128, 2785, 4096), (333, 1411, 1072), (16, 705, 2816), (24, 33, 80)])    # parts of tiles
+def test_channels_that_end_inside_a_warp(moe, T, N, K):  # noqa: F811
+    """With a softcap and both outputs; every call gives the same bits."""
+    x, w = codes(T, T, K), codes(N, N, K)
+    xs, ws = scales(K, T, N)
+    xs = xs * np.float32(20.0)
+    want = BO.qdense(x, xs, w, ws, 30.0)
+    y16, y32 = run(moe, x, xs, w, ws, softcap=30.0)
+    assert np.all(np.abs(y32 - want) <= bound(x, w, xs, ws) + 12 * F32 * np.abs(want))
+    assert np.array_equal(y16, gen.to_bf16_bits(y32.astype(np.float64)))
+    for _ in range(3):
+        assert np.array_equal(run(moe, x, xs, w, ws, softcap=30.0, y=False)[1], y32)

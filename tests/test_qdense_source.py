@@ -1,0 +1,52 @@
+"""Rules of csrc/qdense.cu that no run can show: a fault against them may pass
+on one compiler and hang the next.  They are read from the source."""
+import os
+import re
+
+import pytest
+
+import bit_affine_quantized_gb300.build as build
+
+CSRC = os.path.join(build.HERE, "csrc")
+
+
+def _code(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*|__launch_bounds__\([^)]*\)", "", f.read())
+
+
+def _functions(code):
+    """name -> body of every function at namespace level (the file's braces balance there)."""
+    out = {}
+    for m in re.finditer(r"^(?:__device__ __forceinline__|__global__)[^;{]*?(\w+)\([^{;]*\)\s*\{", code, re.M):
+        depth, i = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(code[i], 0)
+            i += 1
+        out[m.group(1)] = code[m.end():i - 1]
+    return out
+
+
+# instructions that every lane of a warp has to execute together, as qdense.cu writes or calls them
+ALIGNED = re.compile(r"\.aligned|bar\.sync|dense::tc_(?:ld32|ld16|alloc|dealloc)\b")
+
+
+def test_aligned_instructions_follow_a_warp_barrier():
+    """Lanes may come apart at any branch that depends on the lane, and only a
+    warp barrier brings them together for certain: each wrapper of an aligned
+    instruction begins with one, and the kernels use the wrappers alone."""
+    functions = _functions(_code("qdense.cu"))
+    assert {"qdense_mma_kernel", "qdense_few_kernel", "mm_st32", "cluster_sync_all"} <= set(functions)
+    for name, body in functions.items():
+        first = ALIGNED.search(body)
+        if name.endswith("_kernel"):
+            assert not first, f"{name}: {first.group(0)} outside a wrapper"
+        elif first:
+            assert "__syncwarp();" in body[:first.start()], f"{name}: {first.group(0)} without a warp barrier before it"
+
+
+def test_few_rows_mma_follows_a_warp_barrier():
+    """mma.sync after loads that depend on the lane."""
+    body = _functions(_code("qdense.cu"))["qdense_few_kernel"]
+    loads, mma = body.index("request(n0, b + kQfAhead);"), body.index("mma_f16(")
+    assert "__syncwarp();" in body[loads:mma]

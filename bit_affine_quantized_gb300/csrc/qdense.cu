@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     // two warps of a lane quarter take turns at pieces of 32 columns.  A
     // register per lane and column: 32 neighbouring channels of one row are one
     // store instruction.
-    bool ok = mm_wait(tready, 0);
+    bool ok = __all_sync(0xffffffffu, mm_wait(tready, 0));
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem);
     const int rr = 32 * (warp & 3) + lane, ft = tid - kMmFin0 * 32, side = (warp - kMmFin0) >> 2;
     if (kOwn) {
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     // tile, a stage's 128 codes in two pieces of 64.  Its 16-byte chunk j lies at
     // j ^ (rr % 8) of the row (128-byte swizzle).
     const int grp = warp >> 2, rr = 32 * (warp & 3) + lane, sw = rr & 7;
-    bool ok = mm_wait(tready, 0);
+    bool ok = __all_sync(0xffffffffu, mm_wait(tready, 0));
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(s_tmem) + ((uint32_t)(32 * (warp & 3)) << 16) + kMmACol;
     int st = grp, ph = 0, gi = 0;
     for (int u = first; u < units && ok; u += stride) {

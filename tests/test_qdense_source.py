@@ -50,3 +50,35 @@ def test_few_rows_mma_follows_a_warp_barrier():
     body = _functions(_code("qdense.cu"))["qdense_few_kernel"]
     loads, mma = body.index("request(n0, b + kQfAhead);"), body.index("mma_f16(")
     assert "__syncwarp();" in body[loads:mma]
+
+
+def _branches(body):
+    """The bodies of the branches that one lane of a warp takes."""
+    for m in re.finditer(r"if \(lane == 0\) \{", body):
+        depth, i = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(body[i], 0)
+            i += 1
+        yield m.start(), i
+
+
+def test_waits_of_whole_warps_have_one_result():
+    """A bounded wait that runs out in some lanes only would part the warp
+    before its next full-mask vote, which then never ends.  A warp's waits are
+    voted on where they stand, or by a vote before the first branch that looks
+    at the result; those of one lane are in that lane's branch; waits whose
+    result nobody looks at follow the loops."""
+    body = _functions(_code("qdense.cu"))["qdense_mma_kernel"]
+    alone = list(_branches(body))
+    for m in re.finditer(r"mm_wait(?:<\w+>)?\(", body):
+        if any(a <= m.start() < b for a, b in alone):
+            continue
+        start = max(body.rfind(c, 0, m.start()) for c in ";{}") + 1
+        statement = body[start:body.index(";", m.start())]
+        if "ok" not in statement:
+            continue
+        vote = body.find("__all_sync(", m.start())
+        between = body[m.start():vote if vote >= 0 else None]
+        parts = r"\b(?:break|continue|return)\b|(?:for|while|if) \((?:[^()]|\([^()]*\))*\bok\b"  # that a lane's own result could part
+        voted = "__all_sync(" in statement or (vote >= 0 and not re.search(parts, between))
+        assert voted, f"a warp goes on from a lane's own wait: {statement.strip()}"

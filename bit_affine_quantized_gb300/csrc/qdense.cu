@@ -389,6 +389,9 @@ constexpr int kMmMaxSplit = kQdenseMaxCluster;
 constexpr int kMmWst = 6;                  // weight stages, at least
 static_assert(kMmWst * kMmWStage >= kMmSplitN * kMmM * 4, "a block's part of the sums lies over them");
 constexpr int kMmBarBytes = 512;
+// Waits for the other warps' last words, at most, where a wait ran out (a warp
+// leaves its loop once one of its own, of a stage's two or three, has run out).
+constexpr int kMmLastWaits = 4;
 constexpr int kMmSmemMax = 227 * 1024;
 constexpr int kMmXsBytes = kMmMaxN * 4;
 
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   uint64_t *bar = reinterpret_cast<uint64_t *>(xbuf + P.xst * xstage);
   uint64_t *wfull = bar, *wempty = wfull + P.wst, *rfull = wempty + P.wst, *rempty = rfull + P.rst;
   uint64_t *afull = rempty + P.rst, *aempty = afull + kMmABufs, *dfull = aempty + kMmABufs, *dempty = dfull + 2;
-  uint64_t *tready = dempty + 2, *xfull = tready + 1, *xempty = xfull + P.xst;
+  uint64_t *tready = dempty + 2, *tdone = tready + 1, *xfull = tdone + 1, *xempty = xfull + P.xst;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(xempty + P.xst);
   float *s_xs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bar) + kMmBarBytes);  // [n] row scales
   float *s_part = reinterpret_cast<float *>(base);  // [n][128] this block's part of the sums, over the stages
@@ -607,13 +610,14 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   const int part = kPairs ? 0 : rank;  // this block's part of K
   const bool leader = !kPairs || rank == 0;
 
-  if (tid < 2 * P.wst + 2 * P.rst + 2 * P.xst + 2 * kMmABufs + 5) {
+  if (tid < 2 * P.wst + 2 * P.rst + 2 * P.xst + 2 * kMmABufs + 6) {
     // arrivals per phase.  The leader of a pair hears of both blocks' A tiles,
     // rows (its own copies, and a word from the other block) and finish warps.
     uint64_t *b = bar + tid;
     int n = 1;
     if ((b >= wempty && b < rfull) || (b >= afull && b < aempty)) n = kMmWiden / 2;
     if (b >= dempty && b < tready) n = kMmFin;
+    if (b == tdone) n = kMmWiden + kMmFin;
     if (b >= xempty || (kOwn && b >= rfull && b < rempty)) n = kMmFin / 2;
     if (kPairs && leader && ((b >= rfull && b < rempty) || (b >= afull && b < aempty) || (b >= dempty && b < tready)))
       n *= 2;
@@ -770,12 +774,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       if (!ok) break;
     }
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
-    // the last MMAs are complete and the sums read before the memory goes back (bounded waits)
-    if (gi > 0) mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1);
-    if (du > 0) mm_wait<kPairs>(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1);
-    dense::tc_fence_after();
-    __syncwarp();
-    if (!kPairs) mm_dealloc<kForm>(tmem);
+    // The last MMAs are complete and the sums read before the tensor memory goes
+    // back (bounded waits): every A tile was used and every set of sums handed back,
+    // so no warp uses it any more.  Where one of the waits ran out the other warps
+    // may still do so, and their last words are waited for.
+    if (gi > 0) ok = mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1) && ok;
+    if (leader && du > 0) ok = mm_wait<kPairs>(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1) && ok;
+    if (!kPairs) {
+      if (!__all_sync(0xffffffffu, ok))
+        for (int i = 0; i < kMmLastWaits && !__all_sync(0xffffffffu, mm_wait(tdone, 0)); ++i) {
+        }
+      dense::tc_fence_after();
+      mm_dealloc<kForm>(tmem);
+    }
   } else if (warp >= kMmFin0) {
     // ============================================================ finish
     // Warp w reads tensor-memory lanes 32 (w % 4) .. +31: channels n0 + rr; the
@@ -900,6 +911,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       ++du;
     }
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+    if (!kPairs && lane == 0) mm_arrive(tdone);
   } else {
     // ============================================================ widen
     // Two halves of the warps take turns at the stages, so that one's waits and
@@ -960,6 +972,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
       }
     }
     if (!ok && lane == 0) set_error(a.err, kErrTimeout);
+    if (!kPairs && lane == 0) mm_arrive(tdone);
   }
 
   if (kPairs) {

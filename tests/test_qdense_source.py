@@ -82,3 +82,22 @@ def test_waits_of_whole_warps_have_one_result():
         parts = r"\b(?:break|continue|return)\b|(?:for|while|if) \((?:[^()]|\([^()]*\))*\bok\b"  # that a lane's own result could part
         voted = "__all_sync(" in statement or (vote >= 0 and not re.search(parts, between))
         assert voted, f"a warp goes on from a lane's own wait: {statement.strip()}"
+
+
+def test_tensor_memory_is_freed_when_no_warp_uses_it():
+    """A wait that ran out lets the warps of a block leave their loops at
+    different times, and none may free the tensor memory that another still loads
+    or stores: the MMA warp frees it once its own last waits are over, and where
+    one of them ran out after the last word of every other warp that uses it; a
+    pair behind a barrier of both blocks."""
+    body = _functions(_code("qdense.cu"))["qdense_mma_kernel"]
+    alone, pair = (m.start() for m in re.finditer("mm_dealloc", body))
+    before = body[body.rindex("if (gi > 0)", 0, alone):alone]
+    assert before.count("ok = mm_wait") == 2 and before.count("&& ok;") == 2
+    assert before.index("__all_sync(0xffffffffu, ok)") < before.index("mm_wait(tdone, 0)")
+    words = [m.start() for m in re.finditer(re.escape("if (!kPairs && lane == 0) mm_arrive(tdone);"), body)]
+    assert len(words) == 2
+    for at, last_use in zip(words, ("cluster_arrive(cluster_map(smem_addr(&dempty[db]), 0));", "mm_st_wait();")):
+        assert body.rindex(last_use) < at  # the finish warps, the widen warps
+    assert "n = kMmWiden + kMmFin;" in body
+    assert "cluster_sync_all();" in body[body.rindex("if (kPairs) {", 0, pair):pair]

@@ -440,14 +440,25 @@ __device__ __forceinline__ MmUnit mm_unit(const MmPlan &p, int T, int u, int ran
 
 // Bounded wait that suspends in hardware; the timer is read only once a wait
 // is not over at its first look (reading it costs more than most waits).
-// kCluster: blocks of the cluster arrive on the barrier, not this one alone.
-template <bool kCluster>
+// What it orders, by who arrives: kBlock threads and copies of this block;
+// kClusterAcquire copies of the pair's other block too; kClusterRelaxed the
+// tensor cores or threads of the other block, for accesses of tensor memory (the
+// tcgen05 fences on either side order those) and for places that are free again.
+enum { kBlock, kClusterAcquire, kClusterRelaxed };
+template <int kOrder>
 __device__ __forceinline__ bool mm_try(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
-  if (kCluster)
+  if (kOrder == kClusterAcquire)
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, "
-        "p;\n}\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, "
+        "0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+  else if (kOrder == kClusterRelaxed)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, "
+        "0, p;\n}\n"
         : "=r"(ok)
         : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
         : "memory");
@@ -459,12 +470,12 @@ __device__ __forceinline__ bool mm_try(uint64_t *bar, uint32_t parity) {
         : "memory");
   return ok != 0;
 }
-template <bool kCluster = false>
+template <int kOrder = kBlock>
 __device__ __forceinline__ bool mm_wait(uint64_t *bar, uint32_t parity) {
-  if (mm_try<kCluster>(bar, parity)) return true;
+  if (mm_try<kOrder>(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
   for (;;) {
-    if (mm_try<kCluster>(bar, parity)) return true;
+    if (mm_try<kOrder>(bar, parity)) return true;
     if (global_ns() - t0 > kWaitLimitNs) return false;
   }
 }
@@ -574,8 +585,23 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
   return at;
 }
+// An arrival on a barrier of another block of the cluster.  No thread of a pair
+// reads memory that a thread of the other block writes: what the arrivals pass on
+// are A tiles and sums in tensor memory, ordered by the tcgen05 fences before the
+// arrival and after the wait, so the arrival itself need not order anything (a
+// release at cluster scope, which waits for the warp's own stores too, nearly
+// doubles the time: 128 x 65536 x 2816 78 us against 42).
 __device__ __forceinline__ void cluster_arrive(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// A block's rows of a pair's tile; their bytes count on the barrier at `bar`, which
+// may be the other block's.  A copy's completion is a release at cluster scope.
+__device__ __forceinline__ void mm_load_pair(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
   float4 v;
@@ -604,6 +630,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   float *s_xs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(bar) + kMmBarBytes);  // [n] row scales
   float *s_part = reinterpret_cast<float *>(base);  // [n][128] this block's part of the sums, over the stages
   constexpr bool kPairs = kForm == kPair, kOwn = kForm == kFew;
+  constexpr int kTc = kPairs ? kClusterRelaxed : kBlock;  // waits on barriers that pass on tensor memory, or the MMAs' words
   const bool tracer = blockIdx.x == 0 && tid == 0;
   const int split = kPairs ? 1 : P.split;
   const int rank = kPairs || split > 1 ? (int)cluster_rank() : 0;
@@ -611,15 +638,15 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   const bool leader = !kPairs || rank == 0;
 
   if (tid < 2 * P.wst + 2 * P.rst + 2 * P.xst + 2 * kMmABufs + 6) {
-    // arrivals per phase.  The leader of a pair hears of both blocks' A tiles,
-    // rows (its own copies, and a word from the other block) and finish warps.
+    // arrivals per phase.  The leader of a pair hears of both blocks' A tiles, rows
+    // (one arrival, for the bytes of both) and finish warps.
     uint64_t *b = bar + tid;
     int n = 1;
     if ((b >= wempty && b < rfull) || (b >= afull && b < aempty)) n = kMmWiden / 2;
     if (b >= dempty && b < tready) n = kMmFin;
     if (b == tdone) n = kMmWiden + kMmFin;
     if (b >= xempty || (kOwn && b >= rfull && b < rempty)) n = kMmFin / 2;
-    if (kPairs && leader && ((b >= rfull && b < rempty) || (b >= afull && b < aempty) || (b >= dempty && b < tready)))
+    if (kPairs && leader && ((b >= afull && b < aempty) || (b >= dempty && b < tready)))
       n *= 2;
     mbar_init(b, n);
     fence_mbar_init();
@@ -690,11 +717,16 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
         if (q.cnt <= 0) continue;
         const int rows = kPairs ? q.n / 2 : q.n, t0 = q.t0 + (kPairs ? rank * rows : 0);
         for (int g = g0; g < g1; g += 2, ++issued) {
-          if (issued >= P.rst && !(ok = mm_wait(&rempty[st], ph ^ 1))) break;
+          if (issued >= P.rst && !(ok = mm_wait<kTc>(&rempty[st], ph ^ 1))) break;
           const int h = min(2, g1 - g);
-          mbar_arrive_expect_tx(&rfull[st], (uint32_t)(h * rows * 128));
-          for (int i = 0; i < h; ++i)
-            dense::tma_load_2d(rbuf + st * rstage + i * rstep, &prm.x[q.half], 64 * (g + i), t0, &rfull[st]);
+          if (leader) mbar_arrive_expect_tx(&rfull[st], (uint32_t)((kPairs ? 2 : 1) * h * rows * 128));
+          for (int i = 0; i < h; ++i) {
+            if (kPairs)  // (rempty is passed, so the MMAs have used the place's last rows and the leader's rfull is in this phase)
+              mm_load_pair(rbuf + st * rstage + i * rstep, &prm.x[q.half], 64 * (g + i), t0,
+                           cluster_map(smem_addr(&rfull[st]), 0));
+            else
+              dense::tma_load_2d(rbuf + st * rstage + i * rstep, &prm.x[q.half], 64 * (g + i), t0, &rfull[st]);
+          }
           if (++st == P.rst) {
             st = 0;
             ph ^= 1;
@@ -702,7 +734,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
         }
       }
       if (!ok) set_error(a.err, kErrTimeout);
-      for (int j = max(0, issued - P.rst); !kOwn && j < issued; ++j) mm_wait<kPairs>(&rfull[j % P.rst], (j / P.rst) & 1);
+      for (int j = max(0, issued - P.rst); !kOwn && j < issued; ++j) {
+        if (leader)
+          mm_wait<kPairs ? kClusterAcquire : kBlock>(&rfull[j % P.rst], (j / P.rst) & 1);
+        else  // its copies count on the leader's barrier: they have landed once the MMAs have read them
+          mm_wait<kTc>(&rempty[j % P.rst], (j / P.rst) & 1);
+      }
     }
   } else if (warp == kMmMma) {
     // ============================================================ MMA
@@ -718,31 +755,17 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     const uint64_t bdesc0 = dense::sdesc(smem_addr(rbuf), 16, 1024, 2);
     bool ok = true;
     int gi = 0, du = 0, st = 0, ph = 0, ab = 0, aph = 0;
-    if (!leader) {
-      // the other block of a pair: passes on that its rows have landed
-      for (int u = first; u < units && ok; u += stride) {
-        if (mm_unit<kForm>(P, a.T, u, rank).cnt <= 0) continue;
-        for (int s = st0; s < st1; ++s) {
-          if (!(ok = __all_sync(0xffffffffu, mm_wait(&rfull[st], ph)))) break;
-          if (lane == 0) cluster_arrive(cluster_map(smem_addr(&rfull[st]), 0));
-          if (++st == P.rst) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
-      }
-    }
     for (int u = first; leader && u < units; u += stride) {
       const MmUnit q = mm_unit<kForm>(P, a.T, u, rank);
       if (q.cnt <= 0) continue;
       const uint32_t idesc = dense::idesc_f16(kPairs ? 2 * kMmM : kMmM, q.n);
       const int db = du % P.dbufs;
-      if (du >= P.dbufs) ok = __all_sync(0xffffffffu, mm_wait<kPairs>(&dempty[db], ((du / P.dbufs) - 1) & 1));
+      if (du >= P.dbufs) ok = __all_sync(0xffffffffu, mm_wait<kTc>(&dempty[db], ((du / P.dbufs) - 1) & 1));
       if (!ok) break;
       ++du;
       const uint32_t acc = tmem + db * 128;
       for (int s = st0; s < st1; ++s, ++gi) {
-        ok = __all_sync(0xffffffffu, mm_wait<kPairs>(&rfull[st], ph) && mm_wait<kPairs>(&afull[ab], aph));
+        ok = __all_sync(0xffffffffu, mm_wait<kPairs ? kClusterAcquire : kBlock>(&rfull[st], ph) && mm_wait<kTc>(&afull[ab], aph));
         if (!ok) break;
         dense::tc_fence_after();
         const uint32_t ad = tmem + kMmACol + 64 * ab;
@@ -778,8 +801,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     // back (bounded waits): every A tile was used and every set of sums handed back,
     // so no warp uses it any more.  Where one of the waits ran out the other warps
     // may still do so, and their last words are waited for.
-    if (gi > 0) ok = mm_wait(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1) && ok;
-    if (leader && du > 0) ok = mm_wait<kPairs>(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1) && ok;
+    if (gi > 0) ok = mm_wait<kTc>(&aempty[(gi - 1) % kMmABufs], ((gi - 1) / kMmABufs) & 1) && ok;
+    if (leader && du > 0) ok = mm_wait<kTc>(&dempty[(du - 1) % P.dbufs], ((du - 1) / P.dbufs) & 1) && ok;
     if (!kPairs) {
       if (!__all_sync(0xffffffffu, ok))
         for (int i = 0; i < kMmLastWaits && !__all_sync(0xffffffffu, mm_wait(tdone, 0)); ++i) {
@@ -853,7 +876,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
         ws = n < a.N ? __ldg(a.ws + n) : 0.f;
         mm_fin_sync();
       }
-      ok = __all_sync(0xffffffffu, ok && mm_wait(&dfull[db], (du / P.dbufs) & 1));
+      ok = __all_sync(0xffffffffu, ok && mm_wait<kTc>(&dfull[db], (du / P.dbufs) & 1));
       dense::tc_fence_after();
       const uint32_t ta = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + db * 128;
       if (split > 1) {
@@ -944,7 +967,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
             widen4(c[j].w, o[8 * j + 6], o[8 * j + 7]);
           }
           if (h == 0) {
-            if (gi >= kMmABufs) ok = ok && mm_wait(&aempty[ab], ((gi / kMmABufs) - 1) & 1);
+            if (gi >= kMmABufs) ok = ok && mm_wait<kTc>(&aempty[ab], ((gi / kMmABufs) - 1) & 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             dense::tc_fence_after();

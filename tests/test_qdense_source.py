@@ -70,7 +70,7 @@ def test_waits_of_whole_warps_have_one_result():
     result nobody looks at follow the loops."""
     body = _functions(_code("qdense.cu"))["qdense_mma_kernel"]
     alone = list(_branches(body))
-    for m in re.finditer(r"mm_wait(?:<\w+>)?\(", body):
+    for m in re.finditer(r"mm_wait(?:<[^>]*>)?\(", body):
         if any(a <= m.start() < b for a, b in alone):
             continue
         start = max(body.rfind(c, 0, m.start()) for c in ";{}") + 1
@@ -101,3 +101,18 @@ def test_tensor_memory_is_freed_when_no_warp_uses_it():
         assert body.rindex(last_use) < at  # the finish warps, the widen warps
     assert "n = kMmWiden + kMmFin;" in body
     assert "cluster_sync_all();" in body[body.rindex("if (kPairs) {", 0, pair):pair]
+
+
+def test_arrivals_of_another_block_name_their_scope():
+    """An arrival on a barrier of another block is of cluster scope, not of the
+    default, the block's own; the forms of the wait differ from one another, and
+    the leader's wait for rows, which two blocks' copies write, acquires at that
+    scope."""
+    code = _code("qdense.cu")
+    remote = re.findall(r"mbarrier\.arrive[\w.:]*shared::cluster[\w.:]*", code)
+    assert remote and all(".cluster.shared::cluster" in r for r in remote)
+    waits = re.findall(r"mbarrier\.try_wait[\w.:]*", code)
+    assert len(waits) == len(set(waits)) and any(".acquire.cluster" in w for w in waits)
+    body = _functions(code)["qdense_mma_kernel"]
+    mma = body[body.index("mm_alloc"):body.index("mm_dealloc")]
+    assert re.search(r"mm_wait<kPairs \? kClusterAcquire : kBlock>\(&rfull", mma)

@@ -694,8 +694,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
   } else if (warp == kMmRows) {
     // ============================================================ rows
     pdl_wait();  // the widened rows
-    if (tracer) trace_min(a.trace, kTrWaited);
     if (lane == 0) {
+      if (blockIdx.x == 0) trace_min(a.trace, kTrWaited);
       fused::fence_proxy_async_global();
       bool ok = true;
       int st = 0, ph = 0, issued = 0;

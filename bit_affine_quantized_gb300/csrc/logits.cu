@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kLgThreads, 1) logits_kernel(const LogitsArgs 
   lg_wait<0>();
   if (bad_id) set_error(a.err, kErrBadId);
   if (bad) set_error(a.err, kErrNonFinite);
-  if (tracer) trace_max(a.trace, kTrExit);
+  if (tid == 0) trace_max(a.trace, kTrExit);
 }
 
 size_t lg_smem(bool h, bool b, int seg) {

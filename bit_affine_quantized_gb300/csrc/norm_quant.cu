@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kVec <= 2 ? 1024 : 512) norm_quant_kernel(cons
       __stcs(reinterpret_cast<uint4 *>(a.x_out + at) + v, make_uint4(xw[0], xw[1], xw[2], xw[3]));
     }
   }
-  if (tracer) trace_max(a.trace, kTrExit);
+  if (tid == 0) trace_max(a.trace, kTrExit);
 }
 
 template <int kVec>

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kQdThreads) qdense_rows_kernel(const QdenseArg
     const int r = lane / kT, t = lane % kT;
     if (r < kR && t < nt && n0 + r < a.N) qd_store(a, t, n0 + r, mine, __ldcg(a.xs + t), __ldg(a.ws + n0 + r));
   }
-  if (tracer) trace_max(a.trace, kTrExit);
+  if (tid == 0) trace_max(a.trace, kTrExit);
 }
 
 template <int kT, int kR, int kAhead>
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kQfThreads, 1) qdense_few_kernel(const QdenseA
       }
     }
   }
-  if (tracer) trace_max(a.trace, kTrExit);
+  if (tid == 0) trace_max(a.trace, kTrExit);
 }
 
 size_t few_smem(int K) { return (size_t)8 * qf_pitch(K) + (size_t)kQfWarps * 4 * 32 * 4; }
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kWidenThreads) qdense_widen_kernel(const Qdens
       dst[i + j * step] = o;
     }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) trace_max(a.trace, kTrExit);
+  if (threadIdx.x == 0) trace_max(a.trace, kTrExit);
 }
 
 // ------------------------------------------------------------------ tensor cores
@@ -1065,7 +1065,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) qdense_mma_kernel(const __grid_
     }
     cluster_sync_all();  // no block leaves while another reads its part
   }
-  if (tracer) trace_max(a.trace, kTrExit);
+  if (warp >= kMmFin0 && warp < kMmWts && lane == 0) trace_max(a.trace, kTrExit);  // the last warps at work
 }
 
 // Tiles of up to 256 rows where they fill the device, by pairs of blocks: a

@@ -58,3 +58,44 @@ def test_every_launch_is_stamped(moe, T, N, K):
     got = stamps(moe, projection(T, N, K)(moe))
     used = [g for g in got if any(g)]
     assert 1 <= len(used) <= 2 and all(in_order(g) for g in used), got
+
+
+def test_exit_is_the_last_blocks(moe):
+    """A launch of many short blocks: its exit is the last one's, not the first's."""
+    T, H = 300000, 1024
+    if torch.cuda.mem_get_info()[0] < 4 << 30:
+        pytest.skip("needs 4 GB")
+    h = torch.ones((T, H), dtype=torch.bfloat16, device="cuda")
+    q, s = torch.empty((T, H), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    moe.norm_quant(h, T, q, s)
+    torch.cuda.synchronize()
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+
+    def call():
+        begin.record()
+        moe.norm_quant(h, T, q, s)
+        end.record()
+
+    group = stamps(moe, call)[0]
+    assert in_order(group)
+    assert group[3] - (2 ** 64 - 1 - group[0]) > 0.5e6 * begin.elapsed_time(end)  # ns against ms
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 300000, 704), (5, 300000, 704), (24, 300000, 704), (4000, 5000, 704)])
+def test_exit_of_a_projection(moe, T, N, K):
+    """Its last launch leaves no later than a launch behind it passes its dependency wait."""
+    call = projection(T, N, K)(moe)
+    h = torch.ones((1, 64), dtype=torch.bfloat16, device="cuda")
+    q, s = torch.empty((1, 64), dtype=torch.int8, device="cuda"), torch.empty(1, device="cuda")
+    call()
+
+    def both():
+        call()
+        moe.norm_quant(h, 1, q, s)
+
+    used = [g for g in stamps(moe, both) if any(g)]
+    assert all(in_order(g) for g in used)
+    first, last, behind = used[0], used[-2], used[-1]
+    lived, waited = last[3] - (2 ** 64 - 1 - first[0]), 2 ** 64 - 1 - behind[1]
+    # (the blocks end together: what is left are the last stores and the next launch's start)
+    assert last[3] <= waited and waited - last[3] < max(4000, lived // 4)

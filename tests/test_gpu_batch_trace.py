@@ -88,12 +88,20 @@ def test_exit_of_a_projection(moe, T, N, K):
     h = torch.ones((1, 64), dtype=torch.bfloat16, device="cuda")
     q, s = torch.empty((1, 64), dtype=torch.int8, device="cuda"), torch.empty(1, device="cuda")
     call()
-
-    def both():
+    moe.norm_quant(h, 1, q, s)
+    trace = torch.zeros((GROUPS, 4), dtype=torch.int64, device="cuda")
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    moe.set_trace(trace, GROUPS)
+    with torch.cuda.graph(graph, stream=stream):  # the launches follow each other whatever the host does
         call()
         moe.norm_quant(h, 1, q, s)
-
-    used = [g for g in stamps(moe, both) if any(g)]
+    moe.set_trace(None, 0)
+    graph.replay()
+    trace.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert moe.get_error() == bq.MOE_OK
+    used = [g for g in ([v & (2 ** 64 - 1) for v in row] for row in trace.tolist()) if any(g)]
     assert all(in_order(g) for g in used)
     first, last, behind = used[0], used[-2], used[-1]
     lived, waited = last[3] - (2 ** 64 - 1 - first[0]), 2 ** 64 - 1 - behind[1]

@@ -901,7 +901,9 @@ int moe_qdense_forward(moe_handle *h, const int8_t *x, const float *x_scales, in
   a.N = w->channels;
   a.K = w->width;
   a.err = h->dwords;
-  a.trace = take_trace(h, need ? 2 : 1);
+  a.trace = nullptr;
+  if (h->trace)
+    a.trace = take_trace(h, moe::qdense_launches(n_rows, w->channels, w->width, h->n_sm, h->qdense_clusters));
   return cuda_status(moe::launch_qdense(a, h->n_sm, h->qdense_clusters, (cudaStream_t)stream, h->pdl));
 }
 

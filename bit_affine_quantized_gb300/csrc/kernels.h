@@ -258,6 +258,8 @@ constexpr int kQdenseMaxCluster = 8;
 // clusters[s], s <= kQdenseMaxCluster: clusters of s blocks of the tensor-core
 // kernel that the device holds at once
 cudaError_t qdense_set_attributes(int *clusters);
+// launches of a call: two where another launch widens the rows
+int qdense_launches(int T, int N, int K, int n_sm, const int *clusters);
 cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, const int *clusters, cudaStream_t st, bool pdl);
 
 // smem budgets (bytes) for a given shape; 0 = shape not supported by that kernel

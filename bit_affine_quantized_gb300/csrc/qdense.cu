@@ -1248,6 +1248,10 @@ size_t qdense_ws_bytes(int T, int K) {
   return T <= kQdRowsMax ? 0 : ((size_t)T * K * 2 + 255) / 256 * 256;
 }
 
+int qdense_launches(int T, int N, int K, int n_sm, const int *clusters) {
+  return T > kQdRowsMax && mm_plan(T, N, K, n_sm, clusters).form != kFew ? 2 : 1;
+}
+
 cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, const int *clusters, cudaStream_t st, bool pdl) {
   if (a.T > 2 && few_fits(a.T, a.K)) return launch_few(a, n_sm, st, pdl);
   if (a.T <= 1) return launch_rows_t<1>(a, n_sm, st, pdl);

@@ -518,8 +518,10 @@ int moe_logits_process(moe_handle *h, const float *logits, size_t logits_stride,
  *   [2] latest time a block had its weights in shared memory (0: n/a)
  *   [3] latest block exit time (the router: its last block's exit).
  * A call launches 3 (T == 1) or 4 kernels; slot groups are reserved as
- * router 1, gate/up 1, down (+ combine) 2, sort 1.  Buffer owned by the
- * caller; NULL turns tracing off.  Tracing adds a few atomics per block. */
+ * router 1, gate/up 1, down (+ combine) 2, sort 1; moe_norm_quant and
+ * moe_logits_process 1, moe_qdense_forward 1, or 2 where a launch of its own
+ * widens the rows.  Buffer owned by the caller; NULL turns tracing off.
+ * Tracing adds a few atomics per block. */
 int moe_set_trace(moe_handle *h, unsigned long long *buffer, int n_launches);
 
 /* Self-test of the device-side bounded waits (failure detection without a

@@ -107,3 +107,36 @@ def test_exit_of_a_projection(moe, T, N, K):
     lived, waited = last[3] - (2 ** 64 - 1 - first[0]), 2 ** 64 - 1 - behind[1]
     # (the blocks end together: what is left are the last stores and the next launch's start)
     assert last[3] <= waited and waited - last[3] < max(4000, lived // 4)
+
+
+@pytest.mark.parametrize("T,N,K,launches", [(1, 300, 704, 1), (8, 300, 704, 1), (16, 704, 2816, 1), (24, 40000, 704, 2),
+                                            (300, 5000, 704, 2)])
+def test_groups_in_a_row(moe, T, N, K, launches):
+    """Launches take groups one after another: a projection between two norms
+    leaves none between them, whether it widens its rows in a launch before or in
+    the same one."""
+    call = projection(T, N, K)(moe)
+    h = torch.ones((1, 64), dtype=torch.bfloat16, device="cuda")
+    q, s = torch.empty((1, 64), dtype=torch.int8, device="cuda"), torch.empty(1, device="cuda")
+
+    def chain():
+        moe.norm_quant(h, 1, q, s)
+        call()
+        moe.norm_quant(h, 1, q, s)
+
+    got = stamps(moe, chain)
+    assert [any(g) for g in got] == [i < launches + 2 for i in range(GROUPS)], got
+    assert all(in_order(g) for g in got[:launches + 2])
+    for a, b in zip(got, got[1:launches + 2]):
+        assert a[3] <= b[3]  # in the stream's order
+
+
+def test_one_group_is_enough_for_one_launch(moe):
+    """A call that makes one launch is stamped in a buffer of one group."""
+    call = projection(16, 704, 2816)(moe)
+    trace = torch.zeros((1, 4), dtype=torch.int64, device="cuda")
+    moe.set_trace(trace, 1)
+    call()
+    torch.cuda.synchronize()
+    moe.set_trace(None, 0)
+    assert moe.get_error() == bq.MOE_OK and bool((trace[0, :2] != 0).all())

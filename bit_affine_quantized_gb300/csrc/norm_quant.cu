@@ -73,7 +73,13 @@ __global__ void __launch_bounds__(kVec <= 2 ? 1024 : 512) norm_quant_kernel(cons
     gv[i] = a.g && v < nvec ? __ldg(reinterpret_cast<const uint4 *>(a.g) + v) : zero;
   }
   float u[kVec][8];
-  float ss = 0.f, mx = 0.f;
+  // The squares of two vectors each: no chain of additions is longer than 16, so a
+  // scale is within 20 * 2^-24 of its value (16 + 1 + 10 roundings of the sum, halved
+  // by the square root, and 6 more operations).
+  constexpr int kParts = (kVec + 1) / 2;
+  float part[kParts], mx = 0.f;
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) part[p] = 0.f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int v = tid + i * blockDim.x;
@@ -83,13 +89,16 @@ __global__ void __launch_bounds__(kVec <= 2 ? 1024 : 512) norm_quant_kernel(cons
     for (int j = 0; j < 4; ++j) {
       if (a.y) h4[j] = nq_pack(nq_lo(h4[j]) + nq_lo(y4[j]), nq_hi(h4[j]) + nq_hi(y4[j]));
       const float s0 = nq_lo(h4[j]), s1 = nq_hi(h4[j]);
-      ss = fmaf(s0, s0, fmaf(s1, s1, ss));
+      part[i / 2] = fmaf(s0, s0, fmaf(s1, s1, part[i / 2]));
       u[i][2 * j] = a.g ? s0 * nq_lo(g4[j]) : s0;
       u[i][2 * j + 1] = a.g ? s1 * nq_hi(g4[j]) : s1;
       mx = nq_max(nq_max(mx, fabsf(u[i][2 * j])), fabsf(u[i][2 * j + 1]));
     }
     if (a.h_out && v < nvec) __stcs(reinterpret_cast<uint4 *>(a.h_out + at) + v, make_uint4(h4[0], h4[1], h4[2], h4[3]));
   }
+  float ss = part[0];
+#pragma unroll
+  for (int p = 1; p < kParts; ++p) ss += part[p];
   // as bit patterns infinity and NaN compare above every finite value
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);

@@ -121,10 +121,13 @@ __global__ void __launch_bounds__(kVec <= 2 ? 1024 : 512) norm_quant_kernel(cons
   const float mf = __uint_as_float(m);
   // (a row of zeros: 0, where eps = 0 would make it infinite)
   const float r = m == 0u ? 0.0f : 1.0f / sqrtf(tot / (float)H + a.eps);
-  const bool bad = m >= kInfBits || !(tot < INFINITY) || !(r < INFINITY);
+  // the largest normalised value: past fp32's range the scale, from 2^128 - 2^119 on
+  // its bf16 rounding would be infinite
+  const float mr = mf * r;
+  const bool bad = m >= kInfBits || !(tot < INFINITY) || !(r < INFINITY) || !(mr < (a.x_out ? 0x1.FFp127f : INFINITY));
   if (tid == 0) {
     if (bad) set_error(a.err, kErrNonFinite);
-    a.scales[row] = bad ? NAN : mf * r / 127.0f;
+    a.scales[row] = bad ? NAN : mr / 127.0f;
   }
   // a power of two that keeps 127 u and the divisor in range (exact)
   const float pre = mf > 0x1p100f ? 0x1p-24f : mf < 0x1p-80f ? 0x1p40f : 1.0f;

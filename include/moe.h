@@ -428,7 +428,8 @@ int moe_embed(moe_handle *h, const int32_t *ids, int n, const moe_head_weights *
  * matrices and norm 16-byte aligned.  Other outputs must not overlap an
  * input.  A row of zeros has codes and scale 0.  A row with a NaN or an
  * infinity in s or u, or whose sum of squares passes the range of fp32 (also
- * below, with eps = 0), gets codes 0, scale NaN and x_out NaN (s is
+ * below, with eps = 0), or whose largest normalised value m r passes it (where
+ * x_out is given that of bf16), gets codes 0, scale NaN and x_out NaN (s is
  * written all the same) and records MOE_ERR_NONFINITE. */
 #define MOE_NORM_MAX_ROWS (1 << 20)
 int moe_norm_quant(moe_handle *h, const void *hidden, const void *y, int n_rows, int width, const void *norm,

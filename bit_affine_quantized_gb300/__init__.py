@@ -7,6 +7,7 @@ fails loudly when the compiled library is missing: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -162,23 +163,27 @@ def _ptr(t):
 _raw_stream = None
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
+    """Handle of a stream; without one, of device dev's current stream (the current device's)."""
     if stream is None:
-        return (_raw_stream or _find_raw_stream())()
+        return (_raw_stream or _find_raw_stream())(dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _find_raw_stream():
-    """Sets _raw_stream, the handle of the current device's current stream:
-    torch's own getter where there is one (a Stream object costs several times
-    as much as a small call), else through torch.cuda."""
+    """Sets _raw_stream, the handle of a device's current stream: torch's own
+    getter where there is one (a Stream object costs several times as much as a
+    small call), else through torch.cuda."""
     global _raw_stream
     import torch
     torch.cuda.current_stream()  # torch's device state is set up
-    get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
-    _raw_stream = (lambda: get(dev())) if get and dev else lambda: torch.cuda.current_stream().cuda_stream
+    get, now = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if get and now:
+        _raw_stream = lambda dev: get(now() if dev is None else dev)
+    else:
+        _raw_stream = lambda dev: torch.cuda.current_stream(dev).cuda_stream
     return _raw_stream
 
 
@@ -222,19 +227,37 @@ def _find_current_device():
     return _current_device
 
 
-def _data(t, what: str, kind: str, numel: int, dev: int):
+def _data(t, what: str, types, n: int, dev: int, width: int = 1):
     """Device address of a tensor on device dev that a call of the batched path
-    takes (None stays None), after a check of its type, size and layout.  kind:
-    "b16" (bf16, or its bits as 16-bit integers), "f32", "i32", "i8" or "u8"."""
+    takes (None stays None), after a check of its type (one of `types`), layout
+    and size: n values, or more in rows of `width` (1: a vector)."""
     if t is None:
         return None
     if t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous CUDA tensor on device {max(dev, 0)} is wanted, one on {t.device} given")
-    if t.dtype not in (_DTYPES or _fill_dtypes())[kind]:
-        raise ValueError(f"{what}: {t.dtype} given, {_DTYPES[kind][0]} wanted")
-    if t.numel() < numel:
-        raise ValueError(f"{what}: {t.numel()} elements given, {numel} wanted")
+    if t.dtype not in types:
+        raise ValueError(f"{what}: {t.dtype} given, {types[0]} wanted")
+    if t.numel() != n:  # (exactly n values lie in memory as the call reads them; t.shape costs more than t.numel())
+        _check_rows(t.shape, what, n, width)
     return t.data_ptr()
+
+
+def _check_rows(shape, what: str, n: int, width: int):
+    """Refuses a shape of fewer than n values, or whose last dimensions do not
+    make up rows of `width` (flat tensors have no rows; width 1: a vector, the one
+    row or column of a matrix too; 0: any)."""
+    if math.prod(shape) < n:
+        raise ValueError(f"{what}: {math.prod(shape)} elements given, {n} wanted")
+    if width == 1:
+        fits = max(shape, default=1) == math.prod(shape)
+    else:
+        size, at = 1, len(shape)
+        while at > 0 and size < width:
+            at -= 1
+            size *= shape[at]
+        fits = size == width or len(shape) == 1
+    if width and not fits:
+        raise ValueError(f"{what}: {tuple(shape)} given, {'a vector' if width == 1 else f'rows of {width}'} wanted")
 
 
 _DTYPES = {}
@@ -260,9 +283,10 @@ def _rows(t, what: str, n_rows: int, width: int, dev: int):
 def make_qdense_weights(channels: int, width: int, q, scales) -> QdenseWeights:
     """QdenseWeights from CUDA tensors: q int8 [channels, width], scales fp32
     [channels].  The result keeps the tensors alive."""
-    dev = max(q.get_device(), 0)
-    w = QdenseWeights(channels, width, _data(q, "q", "i8", channels * width, dev),
-                      _data(scales, "scales", "f32", channels, dev))
+    dev, k = max(q.get_device(), 0), _DTYPES or _fill_dtypes()
+    w = QdenseWeights(channels, width, _data(q, "q", k["i8"], channels * width, dev, width),
+                      _data(scales, "scales", k["f32"], channels, dev))
+    _check_rows(q.shape, "q", channels * width, width)
     w.keep, w.device = (q, scales), dev
     return w
 
@@ -292,12 +316,17 @@ def make_logit_rules(history=None, history_len=None, prompt_len=None, repetition
     every = (history, history_len, prompt_len, repetition, presence, frequency, bias_ids, bias_values, bias_len, mask)
     dev = max((t.get_device() for t in every if t is not None), default=-1)
     dev = max(dev, 0)
-    r = LogitRules(_data(history, "history", "i32", n * L, dev), _data(history_len, "history_len", "i32", n, dev),
-                   _data(prompt_len, "prompt_len", "i32", n, dev), L, _data(repetition, "repetition", "f32", n, dev),
-                   _data(presence, "presence", "f32", n, dev), _data(frequency, "frequency", "f32", n, dev),
-                   _data(bias_ids, "bias_ids", "i32", n * B, dev), _data(bias_values, "bias_values", "f32", n * B, dev),
-                   _data(bias_len, "bias_len", "i32", n, dev), B, _data(mask, "mask", "i32", 0, dev),
+    k = _DTYPES or _fill_dtypes()
+    i32, f32 = k["i32"], k["f32"]
+    r = LogitRules(_data(history, "history", i32, n * L, dev, L), _data(history_len, "history_len", i32, n, dev),
+                   _data(prompt_len, "prompt_len", i32, n, dev), L, _data(repetition, "repetition", f32, n, dev),
+                   _data(presence, "presence", f32, n, dev), _data(frequency, "frequency", f32, n, dev),
+                   _data(bias_ids, "bias_ids", i32, n * B, dev, B),
+                   _data(bias_values, "bias_values", f32, n * B, dev, B), _data(bias_len, "bias_len", i32, n, dev), B,
+                   _data(mask, "mask", i32, 0, dev, 0),
                    mask.shape[1] if mask is not None and mask.dim() == 2 else 0)
+    if bias_values is not None:
+        _check_rows(bias_values.shape, "bias_values", n * B, B)
     r.device = dev if any(t is not None for t in every) else None
     r.rows, r.words = T, mask.shape[-1] if mask is not None else None
     r.keep = every
@@ -483,14 +512,15 @@ class Moe:
         normalised hidden (+ y) bf16 [T, H], whose sum goes to hidden_out and
         whose bf16 rows go to x_out where these are given.  H is q's last
         dimension."""
-        H = q.shape[-1]
-        n, dev = n_rows * H, _device()
-        self._check(self.lib.moe_norm_quant(self.h, _data(hidden, "hidden", "b16", n, dev),
-                                            _data(y, "y", "b16", n, dev), n_rows, H, _data(norm, "norm", "b16", H, dev),
-                                            eps, _data(hidden_out, "hidden_out", "b16", n, dev),
-                                            _data(q, "q", "i8", n, dev), _data(scales, "scales", "f32", n_rows, dev),
-                                            _data(x_out, "x_out", "b16", n, dev),
-                                            _stream(stream)), "moe_norm_quant")
+        H, dev, k = q.shape[-1], _device(), _DTYPES or _fill_dtypes()
+        n, b16 = n_rows * H, k["b16"]
+        st = self.lib.moe_norm_quant(self.h, _data(hidden, "hidden", b16, n, dev, H), _data(y, "y", b16, n, dev, H),
+                                     n_rows, H, _data(norm, "norm", b16, H, dev), eps,
+                                     _data(hidden_out, "hidden_out", b16, n, dev, H), _data(q, "q", k["i8"], n, dev, H),
+                                     _data(scales, "scales", k["f32"], n_rows, dev),
+                                     _data(x_out, "x_out", b16, n, dev, H), _stream(stream, dev))
+        if st:
+            self._check(st, "moe_norm_quant")
 
     def qdense_workspace_bytes(self, w: QdenseWeights, n_rows: int) -> int:
         return int(self.lib.moe_qdense_workspace_bytes(ctypes.byref(w), n_rows))
@@ -501,15 +531,18 @@ class Moe:
         x int8 [T, K] with x_scales fp32 [T]; outputs y bf16 and/or y32 fp32
         [T, N], through a softcap if one is given; ws of
         qdense_workspace_bytes(w, n_rows) bytes."""
-        n, dev = n_rows * w.channels, _device()
+        dev, k = _device(), _DTYPES or _fill_dtypes()
         if w.device is not None and w.device != dev:
             raise ValueError(f"weights on CUDA device {w.device} given, the current device is {dev}")
-        self._check(self.lib.moe_qdense_forward(self.h, _data(x, "x", "i8", n_rows * w.width, dev),
-                                                _data(x_scales, "x_scales", "f32", n_rows, dev), n_rows,
-                                                ctypes.byref(w), softcap, _data(y, "y", "b16", n, dev),
-                                                _data(y32, "y32", "f32", n, dev), _data(ws, "ws", "u8", 0, dev),
-                                                0 if ws is None else ws.numel(),
-                                                _stream(stream)), "moe_qdense_forward")
+        f32, N, K = k["f32"], w.channels, w.width
+        n = n_rows * N
+        st = self.lib.moe_qdense_forward(self.h, _data(x, "x", k["i8"], n_rows * K, dev, K),
+                                         _data(x_scales, "x_scales", f32, n_rows, dev), n_rows, ctypes.byref(w),
+                                         softcap, _data(y, "y", k["b16"], n, dev, N), _data(y32, "y32", f32, n, dev, N),
+                                         _data(ws, "ws", k["u8"], 0, dev, 0), 0 if ws is None else ws.numel(),
+                                         _stream(stream, dev))
+        if st:
+            self._check(st, "moe_qdense_forward")
 
     def logits_process(self, logits, n_rows, vocab, rules: LogitRules, out=None, tokens=None, stream=None):
         """Penalties, biases, a mask (rules: make_logit_rules) and the greedy
@@ -524,9 +557,10 @@ class Moe:
             raise ValueError(f"rules on CUDA device {rules.device} given, the current device is {dev}")
         at, ld = _rows(logits, "logits", n_rows, vocab, dev)
         to, ld_out = _rows(out, "out", n_rows, vocab, dev) if out is not None else (None, 0)
-        self._check(self.lib.moe_logits_process(self.h, at, ld, n_rows, vocab, ctypes.byref(rules), to, ld_out,
-                                                _data(tokens, "tokens", "i32", n_rows, dev), _stream(stream)),
-                    "moe_logits_process")
+        st = self.lib.moe_logits_process(self.h, at, ld, n_rows, vocab, ctypes.byref(rules), to, ld_out,
+                                         _data(tokens, "tokens", _DTYPES["i32"], n_rows, dev), _stream(stream, dev))
+        if st:
+            self._check(st, "moe_logits_process")
 
     def embed(self, ids, n, hw: HeadWeights, out, stream=None):
         """Tied embedding rows (bf16 [n, H]) of int32 token ids on the device."""

@@ -203,6 +203,7 @@ struct NormQuantArgs {
   uint16_t *x_out;            // nullable bf16 [T, H]: the normalised rows
   int T, H;
   float eps;
+  float most;                 // largest normalised values from here on are out of range (set by the launcher)
   unsigned *err;
   unsigned long long *trace;
 };

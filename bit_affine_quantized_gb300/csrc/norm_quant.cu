@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kVec <= 2 ? 1024 : 512) norm_quant_kernel(cons
   const int H = a.H, nvec = H / 8, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nw = blockDim.x >> 5;
   const size_t row = blockIdx.x, at = row * H;
-  const bool tracer = blockIdx.x == 0 && tid == 0;
+  const bool leaver = a.trace && tid == 0, tracer = blockIdx.x == 0 && leaver;
   if (tracer) trace_min(a.trace, kTrEntry);
   pdl_wait();
   pdl_launch_dependents();
@@ -121,10 +121,8 @@ __global__ void __launch_bounds__(kVec <= 2 ? 1024 : 512) norm_quant_kernel(cons
   const float mf = __uint_as_float(m);
   // (a row of zeros: 0, where eps = 0 would make it infinite)
   const float r = m == 0u ? 0.0f : 1.0f / sqrtf(tot / (float)H + a.eps);
-  // the largest normalised value: past fp32's range the scale, from 2^128 - 2^119 on
-  // its bf16 rounding would be infinite
-  const float mr = mf * r;
-  const bool bad = m >= kInfBits || !(tot < INFINITY) || !(r < INFINITY) || !(mr < (a.x_out ? 0x1.FFp127f : INFINITY));
+  const float mr = mf * r;  // the largest normalised value (infinite if r is)
+  const bool bad = m >= kInfBits || !(tot < INFINITY) || !(mr < a.most);
   if (tid == 0) {
     if (bad) set_error(a.err, kErrNonFinite);
     a.scales[row] = bad ? NAN : mr / 127.0f;
@@ -164,7 +162,7 @@ __global__ void __launch_bounds__(kVec <= 2 ? 1024 : 512) norm_quant_kernel(cons
       __stcs(reinterpret_cast<uint4 *>(a.x_out + at) + v, make_uint4(xw[0], xw[1], xw[2], xw[3]));
     }
   }
-  if (tid == 0) trace_max(a.trace, kTrExit);
+  if (leaver) trace_max(a.trace, kTrExit);
 }
 
 template <int kVec>
@@ -178,7 +176,10 @@ cudaError_t launch_rows(const NormQuantArgs &a, cudaStream_t st, bool pdl) {
 // in flight (4096 x 2816 at kVec 1, 2, 4: 17.0, 15.8, 14.5 us, 81 MB at 5.6
 // TB/s; 600 rows: 3.6, 3.8, 3.5); few rows finish sooner with more threads
 // (128 rows: 2.06, 2.20, 2.74 us; one row 1.9, 2.0, 2.3).
-cudaError_t launch_norm_quant(const NormQuantArgs &a, int n_sm, cudaStream_t st, bool pdl) {
+cudaError_t launch_norm_quant(const NormQuantArgs &a0, int n_sm, cudaStream_t st, bool pdl) {
+  NormQuantArgs a = a0;
+  // past fp32's range the scale would be infinite, from 2^128 - 2^119 on its bf16 rounding
+  a.most = a.x_out ? 0x1.FFp127f : INFINITY;
   if (a.T < 1 || a.H < 16 || a.H % 16 || a.H > kNormMaxWidth) return cudaErrorInvalidValue;
   if (a.T > 3 * n_sm) return launch_rows<4>(a, st, pdl);
   return a.H <= 8 * 1024 ? launch_rows<1>(a, st, pdl) : launch_rows<2>(a, st, pdl);

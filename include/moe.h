@@ -444,7 +444,10 @@ typedef struct {
 } moe_qdense_weights;
 
 /* Workspace of moe_qdense_forward for n_rows rows (0: none needed, and for
- * arguments that the call refuses). */
+ * arguments that the call refuses): room for the rows in 2 bytes a value, from
+ * 9 rows on.  It depends on n_rows and the width alone.  A call that widens its
+ * rows without a launch of their own, which depends on the device too, takes
+ * the workspace all the same and leaves it as it was. */
 size_t moe_qdense_workspace_bytes(const moe_qdense_weights *w, int n_rows);
 
 /* Dense projection of 8-bit rows:

@@ -3,18 +3,20 @@
 //
 //   y[t, n] = cap(xs[t] * ws[n] * sum_k x[t, k] w[n, k]),  cap(z) = c tanh(z / c) or z
 //
-// qdense_rows_kernel: one or two rows (and up to 8 that the next kernel has no
-// room for).  A warp takes kR channels; each lane loads 16 bytes of every
+// qdense_rows_kernel: one or two rows, and 3 to 8 rows wider than 12272, for whose
+// widened codes the next kernel has no room.  A warp takes kR channels; each lane loads 16 bytes of every
 // channel's row (one 512-byte run per warp and channel) and multiplies them
 // with the rows' codes in shared memory by dp4a, so the sums are exact 32-bit
 // integers (at most 128 * 128 * 16384 = 2^28 in magnitude).  HBM bound: 1 x
-// 262144 x 2816 in 107 us, 6.9 TB/s of codes; 1 x 4096 x 2816 in 3.3 us.
+// 262144 x 2816 in 107 us, 6.9 TB/s of codes; 1 x 4096 x 2816 in 3.3 us; 3 and 8 x
+// 65536 x 12288 in 119 and 133 us, 6.8 and 6.1 TB/s.
 //
 // qdense_few_kernel: 3 to 8 rows, mma.sync with the codes widened to fp16 in
 // registers on their way from global memory; the fp32 sums go to integers
-// every 1024 of K, so they stay exact.  HBM bound (8 x 262144 x 2816: 116 us;
-// dp4a took 186).  From 9 rows on mma.sync's rate bounds it (16 rows: 155 us
-// against 123 in the next kernel).
+// every 1024 of K, so they stay exact.  HBM bound (8 x 262144 x 2816: 119 us;
+// dp4a took 186).  Rows wider than 8192 leave it less and less of that rate (8 x
+// 65536 x 8192 91 us, 5.9 TB/s; x 10240 146; x 12272 379, 2.1 TB/s).  From 9 rows
+// on mma.sync's rate bounds it (16 rows: 155 us against 122 in the next kernel).
 //
 // qdense_mma_kernel: more rows, on the 5th-generation tensor cores.  sm_103a
 // has no 8-bit integer form of tcgen05.mma; 8-bit codes are exact in fp16, so

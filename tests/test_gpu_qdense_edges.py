@@ -30,6 +30,19 @@ def test_channels_that_end_inside_a_warp(moe, T, N, K):  # noqa: F811
         assert np.array_equal(run(moe, x, xs, w, ws, softcap=30.0, y=False)[1], y32)
 
 
+@pytest.mark.parametrize("T,N,K", [(3, 700, 12272), (3, 700, 12288), (4, 131, 12288), (3, 33, 16384), (4, 1027, 16384),
+                                   (5, 131, 12288), (8, 515, 16384), (8, 515, 12272), (2, 515, 16384)])
+@pytest.mark.parametrize("kind", ["bell", "full"])
+def test_few_wide_rows(moe, T, N, K, kind):  # noqa: F811
+    """3 to 8 rows on both sides of the width up to which their widened codes fit
+    a block's shared memory; the sums are integers on both."""
+    x, w = codes(T, T, K, kind), codes(N, N, K, kind)
+    xs, ws = scales(K, T, N)
+    y16, y32 = run(moe, x, xs, w, ws)
+    assert np.all(np.abs(y32 - BO.qdense(x, xs, w, ws)) <= bound(x, w, xs, ws))
+    assert np.array_equal(y16, gen.to_bf16_bits(y32.astype(np.float64)))
+
+
 @pytest.mark.parametrize("T,N,K", [(16, 704, 2816), (128, 2816, 4096), (300, 5000, 704)])
 def test_workspace_edges(moe, T, N, K):  # noqa: F811
     """A workspace of exactly the size asked for, what lies around it left alone;

@@ -173,9 +173,9 @@ cudaError_t launch_rows(const NormQuantArgs &a, cudaStream_t st, bool pdl) {
 }  // namespace
 
 // Vectors per thread: many rows go with few threads each, whose loads are all
-// in flight (4096 x 2816 at kVec 1, 2, 4: 17.0, 15.8, 14.5 us, 81 MB at 5.6
-// TB/s; 600 rows: 3.6, 3.8, 3.5); few rows finish sooner with more threads
-// (128 rows: 2.06, 2.20, 2.74 us; one row 1.9, 2.0, 2.3).
+// in flight (4096 x 2816 at kVec 1, 2, 4: 17.5, 16.2, 14.7 us, 81 MB at 5.5
+// TB/s; 600 rows: 3.8, 3.8, 3.6); few rows finish sooner with more threads
+// (128 rows: 2.12, 2.33, 2.80 us; one row 2.0, 2.05, 2.4).
 cudaError_t launch_norm_quant(const NormQuantArgs &a0, int n_sm, cudaStream_t st, bool pdl) {
   NormQuantArgs a = a0;
   // past fp32's range the scale would be infinite, from 2^128 - 2^119 on its bf16 rounding

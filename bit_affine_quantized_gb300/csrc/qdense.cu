@@ -1147,9 +1147,9 @@ MmPlan mm_plan(int T, int N, int K, int n_sm, const int *clusters) {
   }
   p.nload = p.form == kPair ? p.n / 2 : p.n;
   p.dbufs = p.n <= 128 ? 2 : 1;
-  // Weight stages, an even number: whole tiles stream them from HBM (24 x 262144 x
-  // 2816 with 5, 7, 9, 12: 128, 123, 124, 125 us); the others need the room
-  // otherwise.
+  // Weight stages, an even number: whole tiles stream them from HBM (24 x 65536 x
+  // 2816 with 6, 8, 10, 12: 39.0, 38.8, 39.5, 40.2 us; 24 x 262144 x 2816 124.3,
+  // 124.3, 125.1, 125.0); the others need the room otherwise.
   p.wst = p.form != kFew && p.split == 1 && p.n <= 128 ? 8 : kMmWst;
   p.rst = p.form == kOne ? 3 : 4;
   p.xst = p.form == kFew ? 4 : 0;

@@ -535,12 +535,11 @@ class Moe:
         if w.device is not None and w.device != dev:
             raise ValueError(f"weights on CUDA device {w.device} given, the current device is {dev}")
         f32, N, K = k["f32"], w.channels, w.width
-        n = n_rows * N
+        n, ws_bytes = n_rows * N, 0 if ws is None else ws.numel()
         st = self.lib.moe_qdense_forward(self.h, _data(x, "x", k["i8"], n_rows * K, dev, K),
                                          _data(x_scales, "x_scales", f32, n_rows, dev), n_rows, ctypes.byref(w),
                                          softcap, _data(y, "y", k["b16"], n, dev, N), _data(y32, "y32", f32, n, dev, N),
-                                         _data(ws, "ws", k["u8"], 0, dev, 0), 0 if ws is None else ws.numel(),
-                                         _stream(stream, dev))
+                                         _data(ws, "ws", k["u8"], ws_bytes, dev), ws_bytes, _stream(stream, dev))
         if st:
             self._check(st, "moe_qdense_forward")
 

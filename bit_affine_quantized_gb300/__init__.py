@@ -18,6 +18,7 @@ __all__ = [
     "MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED", "MOE_ERR_CUDA", "MOE_ERR_BAD_EXPERT_ID",
     "MOE_ERR_TIMEOUT", "MOE_ERR_NONFINITE", "MOE_ERR_WORKSPACE", "build_library", "static_get_error",
     "layer_forward_static", "ExpertCache", "QdenseWeights", "LogitRules", "make_qdense_weights", "make_logit_rules",
+    "KvCache", "SampleRules", "make_kv_cache", "make_sample_rules",
 ]
 
 MOE_OK = 0
@@ -75,6 +76,20 @@ class LogitRules(ctypes.Structure):
                 ("mask_stride", ctypes.c_int)]
 
 
+class KvCache(ctypes.Structure):
+    device = None  # of the tensors, where make_kv_cache knows them
+    _fields_ = [("n_pages", ctypes.c_int), ("kv_heads", ctypes.c_int), ("page_rows", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int), ("table_stride", ctypes.c_int)]
+
+
+class SampleRules(ctypes.Structure):
+    device = rows = None  # of the tensors, where make_sample_rules knows them
+    _fields_ = [("uniform", ctypes.c_void_p), ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -125,6 +140,11 @@ def load_library(path: str = LIB_PATH):
         "moe_qdense_workspace_bytes": (Z, [P(QdenseWeights), I]),
         "moe_qdense_forward": (I, [V, V, V, I, P(QdenseWeights), ctypes.c_float, V, V, V, Z, V]),
         "moe_logits_process": (I, [V, V, Z, I, I, P(LogitRules), V, Z, V, V]),
+        "moe_kv_append": (I, [V, V, Z, I, V, Z, V, Z, I, V, V, P(KvCache), V, I, V, Z, V]),
+        "moe_kv_read": (I, [V, P(KvCache), V, V, I, V, Z, V, Z, V]),
+        "moe_kv_attend_workspace_bytes": (Z, [P(KvCache), I]),
+        "moe_kv_attend": (I, [V, V, Z, P(KvCache), V, I, ctypes.c_float, ctypes.c_float, I, V, Z, V, V, Z, V]),
+        "moe_sample": (I, [V, V, Z, I, I, P(SampleRules), V, V, V]),
         "moe_prompt_workspace_bytes": (Z, [P(Dims), I]),
         "moe_layer_forward_prompt": (I, [V, V, I, P(LayerWeights), V, V, V, V, V, Z, V]),
     }
@@ -330,6 +350,60 @@ def make_logit_rules(history=None, history_len=None, prompt_len=None, repetition
     r.device = dev if any(t is not None for t in every) else None
     r.rows, r.words = T, mask.shape[-1] if mask is not None else None
     r.keep = every
+    return r
+
+
+def _heads(t, what: str, n_rows: int, heads: int, dim: int, dev: int):
+    """Device address and row stride of bf16 rows on device dev: a tensor of at
+    least n_rows x heads x dim, or x (heads * dim), whose rows may lie apart."""
+    if t is None:
+        return None, 0
+    shape, stride, width = t.shape, t.stride(), heads * dim
+    if t.get_device() != dev or t.dtype not in (_DTYPES or _fill_dtypes())["b16"]:
+        raise ValueError(f"{what}: bf16 values on CUDA device {dev} are wanted, {t.dtype} on {t.device} given")
+    if len(shape) == 3:
+        fits = shape[1] == heads and shape[2] == dim and stride[2] == 1 and (heads == 1 or stride[1] == dim)
+    else:
+        fits = len(shape) == 2 and shape[1] == width and stride[1] == 1
+    if not fits or shape[0] < n_rows:
+        raise ValueError(f"{what}: {tuple(shape)} with strides {stride} given, at least {n_rows} rows of {heads} x {dim} "
+                         f"adjacent values are wanted")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else width
+
+
+def make_kv_cache(k, v, table, k_scales=None, v_scales=None) -> KvCache:
+    """KvCache from CUDA tensors: k and v [n_pages, kv_heads, page_rows,
+    head_dim], bf16, or int8 with k_scales and v_scales fp32 [n_pages,
+    kv_heads, page_rows]; table int32 [n_seqs, pages].  The result keeps the
+    tensors alive."""
+    if k.dim() != 4:
+        raise ValueError(f"k: [n_pages, kv_heads, page_rows, head_dim] is wanted, {tuple(k.shape)} given")
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales, v_scales: both or neither are wanted")
+    types, dev = _DTYPES or _fill_dtypes(), max(k.get_device(), 0)
+    kind = types["b16"] if k_scales is None else types["i8"]
+    for name, t, like in (("v", v, k.shape), ("k_scales", k_scales, k.shape[:3]), ("v_scales", v_scales, k.shape[:3])):
+        if t is not None and t.shape != like:
+            raise ValueError(f"{name}: {tuple(t.shape)} given, {tuple(like)} wanted")
+    if table.dim() != 2:
+        raise ValueError(f"table: a matrix is wanted, {tuple(table.shape)} given")
+    rows = math.prod(k.shape[:3])
+    c = KvCache(*k.shape, _data(k, "k", kind, k.numel(), dev, 0), _data(v, "v", kind, k.numel(), dev, 0),
+                _data(k_scales, "k_scales", types["f32"], rows, dev, 0),
+                _data(v_scales, "v_scales", types["f32"], rows, dev, 0),
+                _data(table, "table", types["i32"], table.numel(), dev, 0), *table.shape)
+    c.keep, c.device = (k, v, k_scales, v_scales, table), dev
+    return c
+
+
+def make_sample_rules(uniform, temperature=None, top_k=None, top_p=None, min_p=None) -> SampleRules:
+    """SampleRules from CUDA tensors of a value per row: uniform, temperature,
+    top_p and min_p fp32, top_k int32.  The result keeps the tensors alive."""
+    k, dev, n = _DTYPES or _fill_dtypes(), max(uniform.get_device(), 0), uniform.numel()
+    every = (uniform, temperature, top_k, top_p, min_p)
+    r = SampleRules(*[_data(t, name, k["i32"] if name == "top_k" else k["f32"], n, dev) for t, name in
+                      zip(every, ("uniform", "temperature", "top_k", "top_p", "min_p"))])
+    r.keep, r.device, r.rows = every, dev, n
     return r
 
 
@@ -560,6 +634,80 @@ class Moe:
                                          _data(tokens, "tokens", _DTYPES["i32"], n_rows, dev), _stream(stream, dev))
         if st:
             self._check(st, "moe_logits_process")
+
+    def _on_device(self, what, dev):
+        now = _device()
+        if dev is not None and dev != now:
+            raise ValueError(f"{what} on CUDA device {dev} given, the current device is {now}")
+        return now
+
+    def kv_append(self, k, v, positions, cache: KvCache, seqs=None, q=None, q_out=None, inv_freq=None, stream=None):
+        """Rotary positions on q and k (inv_freq fp32 [r / 2]: the first r
+        dimensions of a head; None: none), q_out <- q, and k and v into the
+        cache (moe_kv_append).  A row per entry of positions (int32, as seqs;
+        None: row t is of sequence t): q bf16 [T, q_heads, head_dim], k and v
+        [T, kv_heads, head_dim], or with the last two dimensions as one; rows may
+        lie apart, as the parts of one projection's output do."""
+        dev, types = self._on_device("cache", cache.device), _DTYPES or _fill_dtypes()
+        T, H, D = positions.numel(), cache.kv_heads, cache.head_dim
+        q_heads = 0 if q is None else q.shape[1] if q.dim() == 3 else q.shape[-1] // D
+        (qp, lq), (kp, lk) = _heads(q, "q", T, q_heads, D, dev), _heads(k, "k", T, H, D, dev)
+        (vp, lv), (op, lo) = _heads(v, "v", T, H, D, dev), _heads(q_out, "q_out", T, q_heads, D, dev)
+        rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+        st = self.lib.moe_kv_append(self.h, qp, lq, q_heads, kp, lk, vp, lv, T,
+                                    _data(seqs, "seqs", types["i32"], T, dev),
+                                    _data(positions, "positions", types["i32"], T, dev), ctypes.byref(cache),
+                                    _data(inv_freq, "inv_freq", types["f32"], rot // 2, dev), rot, op, lo,
+                                    _stream(stream, dev))
+        if st:
+            self._check(st, "moe_kv_append")
+
+    def kv_read(self, cache: KvCache, positions, k_out=None, v_out=None, seqs=None, stream=None):
+        """Rows of the cache as bf16 [T, kv_heads, head_dim], one per entry of
+        positions (moe_kv_read; seqs None: row t is of sequence t)."""
+        dev, types = self._on_device("cache", cache.device), _DTYPES or _fill_dtypes()
+        T, H, D = positions.numel(), cache.kv_heads, cache.head_dim
+        (kp, lk), (vp, lv) = _heads(k_out, "k_out", T, H, D, dev), _heads(v_out, "v_out", T, H, D, dev)
+        st = self.lib.moe_kv_read(self.h, ctypes.byref(cache), _data(seqs, "seqs", types["i32"], T, dev),
+                                  _data(positions, "positions", types["i32"], T, dev), T, kp, lk, vp, lv,
+                                  _stream(stream, dev))
+        if st:
+            self._check(st, "moe_kv_read")
+
+    def kv_attend_workspace_bytes(self, cache: KvCache, q_heads: int) -> int:
+        return int(self.lib.moe_kv_attend_workspace_bytes(ctypes.byref(cache), q_heads))
+
+    def kv_attend(self, q, lengths, cache: KvCache, out, ws, scale: float, softcap: float = 0.0, window: int = 0,
+                  lse=None, stream=None):
+        """Attention of one new token per sequence of the cache's table
+        (moe_kv_attend): q and out bf16 [n_seqs, q_heads, head_dim], or with the
+        last two dimensions as one, lengths int32 and lse fp32 [n_seqs,
+        q_heads]; ws of kv_attend_workspace_bytes(cache, q_heads) bytes."""
+        dev, types = self._on_device("cache", cache.device), _DTYPES or _fill_dtypes()
+        n, D = cache.n_seqs, cache.head_dim
+        q_heads = q.shape[1] if q.dim() == 3 else q.shape[-1] // D
+        (qp, lq), (op, lo) = _heads(q, "q", n, q_heads, D, dev), _heads(out, "out", n, q_heads, D, dev)
+        ws_bytes = ws.numel()
+        st = self.lib.moe_kv_attend(self.h, qp, lq, ctypes.byref(cache),
+                                    _data(lengths, "lengths", types["i32"], n, dev), q_heads, scale, softcap, window,
+                                    op, lo, _data(lse, "lse", types["f32"], n * q_heads, dev, q_heads),
+                                    _data(ws, "ws", types["u8"], ws_bytes, dev), ws_bytes, _stream(stream, dev))
+        if st:
+            self._check(st, "moe_kv_attend")
+
+    def sample(self, logits, n_rows, vocab, rules: SampleRules, tokens, logprobs=None, stream=None):
+        """A token per row of logits (an fp32 matrix whose rows may lie apart)
+        through the filters of rules (make_sample_rules), and the log of its
+        share of what remained (moe_sample): tokens int32, logprobs fp32."""
+        if rules.rows is not None and rules.rows < n_rows:
+            raise ValueError(f"rules for {rules.rows} rows given, {n_rows} wanted")
+        dev, types = self._on_device("rules", rules.device), _DTYPES or _fill_dtypes()
+        at, ld = _rows(logits, "logits", n_rows, vocab, dev)
+        st = self.lib.moe_sample(self.h, at, ld, n_rows, vocab, ctypes.byref(rules),
+                                 _data(tokens, "tokens", types["i32"], n_rows, dev),
+                                 _data(logprobs, "logprobs", types["f32"], n_rows, dev), _stream(stream, dev))
+        if st:
+            self._check(st, "moe_sample")
 
     def embed(self, ids, n, hw: HeadWeights, out, stream=None):
         """Tied embedding rows (bf16 [n, H]) of int32 token ids on the device."""

@@ -17,7 +17,7 @@ BUILD_DIR = os.path.join(ROOT, "_build", "moe")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe_gb300.so")
 SOURCES = ["abi.cu", "router.cu", "ffn.cu", "decode.cu", "prefill.cu", "noalloc.cu", "tail.cu", "head.cu", "offload.cu", "prompt.cu",
-           "norm_quant.cu", "qdense.cu", "logits.cu"]
+           "norm_quant.cu", "qdense.cu", "logits.cu", "kv_cache.cu", "kv_attend.cu", "sample.cu"]
 HEADERS = ["common.cuh", "fused.cuh", "kernels.h", "abi_internal.h", "dense.cuh", "tma_maps.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -1,6 +1,7 @@
 // C ABI of the MoE block: argument checks, workspace carving, launches.
 // Declarations and the contract of every call: include/moe.h.
 #include <float.h>
+#include <math.h>
 #include <stdlib.h>
 #include <string.h>
 
@@ -260,6 +261,37 @@ int check_head(const moe_head_weights *w) {
 bool on_device(const moe_handle *h) {
   int dev = -1;
   return cudaGetDevice(&dev) == cudaSuccess && dev == h->device;
+}
+
+constexpr int kKvMaxQueryHeads = 1024;
+
+int check_kv(const moe_kv_cache *c) {
+  if (!c || !c->k || !c->v || !c->table || !c->k_scales != !c->v_scales) return MOE_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->kv_heads < 1 || c->n_seqs < 1 || c->table_stride < 1) return MOE_ERR_INVALID_ARG;
+  if (c->page_rows < 16 || c->page_rows > 256 || (c->page_rows & (c->page_rows - 1))) return MOE_ERR_UNSUPPORTED;
+  if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16) return MOE_ERR_UNSUPPORTED;
+  if (c->kv_heads > 128 || c->n_seqs > moe::kKvMaxSeqs) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)c->n_pages * c->kv_heads * c->page_rows > ((int64_t)1 << 31) - 256) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)c->table_stride * c->page_rows > ((int64_t)1 << 30)) return MOE_ERR_UNSUPPORTED;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_scales, 16) ||
+      !aligned(c->table, 4))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+int check_kv_heads(const moe_kv_cache *c, int q_heads) {
+  if (q_heads < 1) return MOE_ERR_INVALID_ARG;
+  return q_heads % c->kv_heads || q_heads / c->kv_heads > 64 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// bf16 rows of `width` values that lie `stride` apart
+bool kv_rows(const void *p, size_t stride, size_t width) {
+  return aligned(p, 16) && stride % 8 == 0 && stride >= width && stride <= ((size_t)1 << 32);
+}
+
+moe::KvCache kv_cache(const moe_kv_cache *c) {
+  return moe::KvCache{(uint8_t *)c->k, (uint8_t *)c->v, c->k_scales,  c->v_scales, c->table,       c->n_pages,
+                      c->kv_heads,     c->page_rows,    c->head_dim, c->n_seqs,   c->table_stride};
 }
 
 int check_qdense(const moe_qdense_weights *w) {
@@ -966,6 +998,134 @@ int moe_logits_process(moe_handle *h, const float *logits, size_t logits_stride,
   a.err = h->dwords;
   a.trace = take_trace(h, 1);
   return cuda_status(moe::launch_logits(a, h->n_sm, (cudaStream_t)stream, h->pdl));
+}
+
+int moe_kv_append(moe_handle *h, const void *q, size_t q_stride, int q_heads, const void *k, size_t k_stride,
+                  const void *v, size_t v_stride, int n_rows, const int32_t *row_seq, const int32_t *row_pos,
+                  const moe_kv_cache *cache, const float *inv_freq, int rot_dims, void *q_out, size_t q_out_stride,
+                  moe_stream_t stream) {
+  if (!h || !k || !v || !row_pos || (q && !q_out) || (!q && q_out)) return MOE_ERR_INVALID_ARG;
+  const int st = check_kv(cache);
+  if (st) return st;
+  if (n_rows < 1 || n_rows > moe::kKvMaxRows) return MOE_ERR_INVALID_ARG;
+  if (q && q_heads < 1) return MOE_ERR_INVALID_ARG;
+  if (q && q_heads > kKvMaxQueryHeads) return MOE_ERR_UNSUPPORTED;
+  const size_t D = cache->head_dim, kv_width = (size_t)cache->kv_heads * D, q_width = (size_t)q_heads * D;
+  if (!kv_rows(k, k_stride, kv_width) || !kv_rows(v, v_stride, kv_width)) return MOE_ERR_INVALID_ARG;
+  if (q && (!kv_rows(q, q_stride, q_width) || !kv_rows(q_out, q_out_stride, q_width))) return MOE_ERR_INVALID_ARG;
+  if (q && q == q_out && q_stride != q_out_stride) return MOE_ERR_INVALID_ARG;
+  if (!aligned(row_pos, 4) || !aligned(row_seq, 4) || !aligned(inv_freq, 4)) return MOE_ERR_INVALID_ARG;
+  if (rot_dims < 0 || (rot_dims > 0) != (inv_freq != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (rot_dims % 16 || rot_dims > cache->head_dim) return MOE_ERR_UNSUPPORTED;
+  if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  moe::KvAppendArgs a;
+  a.c = kv_cache(cache);
+  a.q = (const uint16_t *)q;
+  a.k = (const uint16_t *)k;
+  a.v = (const uint16_t *)v;
+  a.q_out = (uint16_t *)q_out;
+  a.ldq = q_stride;
+  a.ldk = k_stride;
+  a.ldv = v_stride;
+  a.ldo = q_out_stride;
+  a.seq = row_seq;
+  a.pos = row_pos;
+  a.freq = inv_freq;
+  a.T = n_rows;
+  a.Hq = q ? q_heads : 0;
+  a.rot = rot_dims;
+  a.err = h->dwords;
+  a.trace = take_trace(h, 1);
+  return cuda_status(moe::launch_kv_append(a, h->n_sm, (cudaStream_t)stream, h->pdl));
+}
+
+int moe_kv_read(moe_handle *h, const moe_kv_cache *cache, const int32_t *row_seq, const int32_t *row_pos, int n_rows,
+                void *k_out, size_t k_stride, void *v_out, size_t v_stride, moe_stream_t stream) {
+  if (!h || !row_pos || (!k_out && !v_out)) return MOE_ERR_INVALID_ARG;
+  const int st = check_kv(cache);
+  if (st) return st;
+  if (n_rows < 1 || n_rows > moe::kKvMaxRows) return MOE_ERR_INVALID_ARG;
+  const size_t width = (size_t)cache->kv_heads * cache->head_dim;
+  if ((k_out && !kv_rows(k_out, k_stride, width)) || (v_out && !kv_rows(v_out, v_stride, width)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(row_pos, 4) || !aligned(row_seq, 4)) return MOE_ERR_INVALID_ARG;
+  if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  moe::KvReadArgs a;
+  a.c = kv_cache(cache);
+  a.seq = row_seq;
+  a.pos = row_pos;
+  a.k = (uint16_t *)k_out;
+  a.v = (uint16_t *)v_out;
+  a.ldk = k_stride;
+  a.ldv = v_stride;
+  a.T = n_rows;
+  a.err = h->dwords;
+  a.trace = take_trace(h, 1);
+  return cuda_status(moe::launch_kv_read(a, h->n_sm, (cudaStream_t)stream, h->pdl));
+}
+
+size_t moe_kv_attend_workspace_bytes(const moe_kv_cache *cache, int q_heads) {
+  if (check_kv(cache) != MOE_OK || check_kv_heads(cache, q_heads) != MOE_OK) return 0;
+  return align256(moe::kv_attend_ws_bytes(kv_cache(cache), q_heads));
+}
+
+int moe_kv_attend(moe_handle *h, const void *q, size_t q_stride, const moe_kv_cache *cache, const int32_t *lengths,
+                  int q_heads, float scale, float softcap, int window, void *out, size_t out_stride, float *lse,
+                  void *ws, size_t ws_bytes, moe_stream_t stream) {
+  if (!h || !q || !lengths || !out || !ws) return MOE_ERR_INVALID_ARG;
+  int st = check_kv(cache);
+  if (!st) st = check_kv_heads(cache, q_heads);
+  if (st) return st;
+  const size_t width = (size_t)q_heads * cache->head_dim;
+  if (!kv_rows(q, q_stride, width) || !kv_rows(out, out_stride, width)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(lengths, 4) || !aligned(lse, 4) || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+  if (!(fabsf(scale) <= FLT_MAX) || !(softcap >= 0.0f && softcap <= FLT_MAX) || window < 0) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_kv_attend_workspace_bytes(cache, q_heads)) return MOE_ERR_WORKSPACE;
+  if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  moe::KvAttendArgs a;
+  a.c = kv_cache(cache);
+  a.q = (const uint16_t *)q;
+  a.out = (uint16_t *)out;
+  a.lse = lse;
+  a.lengths = lengths;
+  a.ldq = q_stride;
+  a.ldo = out_stride;
+  a.work = (uint8_t *)ws;
+  a.Hq = q_heads;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.window = window;
+  a.err = h->dwords;
+  a.trace = take_trace(h, 1);
+  return cuda_status(moe::launch_kv_attend(a, h->n_sm, (cudaStream_t)stream, h->pdl));
+}
+
+int moe_sample(moe_handle *h, const float *logits, size_t logits_stride, int n_rows, int vocab,
+               const moe_sample_rules *r, int32_t *tokens, float *logprobs, moe_stream_t stream) {
+  if (!h || !logits || !r || !r->uniform || !tokens) return MOE_ERR_INVALID_ARG;
+  if (n_rows < 1 || n_rows > moe::kLogitsMaxRows) return MOE_ERR_INVALID_ARG;
+  if (vocab < 1 || vocab > (1 << 28)) return MOE_ERR_UNSUPPORTED;
+  if (logits_stride < (size_t)vocab) return MOE_ERR_INVALID_ARG;
+  if (logits_stride > ((size_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+  const void *p4[8] = {logits, r->uniform, r->temperature, r->top_k, r->top_p, r->min_p, tokens, logprobs};
+  for (const void *p : p4)
+    if (!aligned(p, 4)) return MOE_ERR_INVALID_ARG;
+  if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  moe::SampleArgs a;
+  a.logits = logits;
+  a.ld = logits_stride;
+  a.uniform = r->uniform;
+  a.temperature = r->temperature;
+  a.top_k = r->top_k;
+  a.top_p = r->top_p;
+  a.min_p = r->min_p;
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  a.T = n_rows;
+  a.V = vocab;
+  a.err = h->dwords;
+  a.trace = take_trace(h, 1);
+  return cuda_status(moe::launch_sample(a, h->n_sm, (cudaStream_t)stream, h->pdl));
 }
 
 int moe_embed(moe_handle *h, const int32_t *ids, int n, const moe_head_weights *w, void *out, moe_stream_t stream) {

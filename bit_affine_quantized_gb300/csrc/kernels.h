@@ -263,6 +263,79 @@ cudaError_t qdense_set_attributes(int *clusters);
 int qdense_launches(int T, int N, int K, int n_sm, const int *clusters);
 cudaError_t launch_qdense(const QdenseArgs &a, int n_sm, const int *clusters, cudaStream_t st, bool pdl);
 
+// The paged cache of keys and values (kv_cache.cu, kv_attend.cu).
+constexpr int kKvMaxSeqs = 4096;
+constexpr int kKvMaxRows = 1 << 20;
+struct KvCache {
+  uint8_t *k, *v;             // [n_pages, heads, rows, D], bf16 or 8-bit codes
+  float *ks, *vs;             // [n_pages, heads, rows]; null: bf16
+  const int32_t *table;       // [n_seqs, stride]
+  int n_pages, heads, rows, D, n_seqs, stride;
+};
+// Row of the pages, over all pages, of head 0 of a position (the heads' rows lie
+// `rows` apart); -1 for a sequence, a position or a page that is not there.
+__device__ __forceinline__ long long kv_row(const KvCache &c, int seq, int pos) {
+  if ((unsigned)seq >= (unsigned)c.n_seqs || pos < 0 || pos / c.rows >= c.stride) return -1;
+  const int page = __ldg(c.table + (size_t)seq * c.stride + pos / c.rows);
+  return (unsigned)page < (unsigned)c.n_pages ? (long long)page * c.heads * c.rows + pos % c.rows : -1;
+}
+struct KvAppendArgs {
+  KvCache c;
+  const uint16_t *q, *k, *v;  // bf16 rows; q nullable
+  uint16_t *q_out;
+  size_t ldq, ldk, ldv, ldo;  // values from row to row
+  const int32_t *seq, *pos;   // [T]; seq nullable
+  const float *freq;          // [rot / 2]
+  int T, Hq, rot;
+  int parts;                  // blocks per row (set by the launcher)
+  unsigned *err;
+  unsigned long long *trace;
+};
+cudaError_t launch_kv_append(const KvAppendArgs &a, int n_sm, cudaStream_t st, bool pdl);
+struct KvReadArgs {
+  KvCache c;
+  const int32_t *seq, *pos;   // [T]; seq nullable
+  uint16_t *k, *v;            // nullable bf16 rows
+  size_t ldk, ldv;
+  int T;
+  int per;                    // rows per block (set by the launcher)
+  unsigned *err;
+  unsigned long long *trace;
+};
+cudaError_t launch_kv_read(const KvReadArgs &a, int n_sm, cudaStream_t st, bool pdl);
+struct KvAttendArgs {
+  KvCache c;
+  const uint16_t *q;          // bf16 [n_seqs, Hq, D], rows ldq apart
+  uint16_t *out;
+  float *lse;                 // nullable [n_seqs, Hq]
+  const int32_t *lengths;     // [n_seqs]
+  size_t ldq, ldo;
+  uint8_t *work;
+  int Hq;
+  float scale, softcap;       // softcap 0: none
+  int window;                 // 0: none
+  unsigned *err;
+  unsigned long long *trace;
+};
+size_t kv_attend_ws_bytes(const KvCache &c, int Hq);
+cudaError_t launch_kv_attend(const KvAttendArgs &a, int n_sm, cudaStream_t st, bool pdl);
+
+// A token drawn from filtered logits (sample.cu).
+struct SampleArgs {
+  const float *logits;        // fp32 [T, ld]
+  size_t ld;
+  const float *uniform;       // [T]
+  const float *temperature;   // nullable [T], like the filters below
+  const int32_t *top_k;
+  const float *top_p, *min_p;
+  int32_t *tokens;            // [T]
+  float *logprobs;            // nullable [T]
+  int T, V;
+  unsigned *err;
+  unsigned long long *trace;
+};
+cudaError_t launch_sample(const SampleArgs &a, int n_sm, cudaStream_t st, bool pdl);
+
 // smem budgets (bytes) for a given shape; 0 = shape not supported by that kernel
 size_t router_smem(const Dims &d, int tb);
 size_t gateup_smem(const Dims &d, int tt);

@@ -513,6 +513,135 @@ int moe_logits_process(moe_handle *h, const float *logits, size_t logits_stride,
                        const moe_logit_rules *rules, float *out, size_t out_stride, int32_t *tokens,
                        moe_stream_t stream);
 
+/* ---- Attention of a decode loop, over a paged cache of keys and values, and
+ * the choice of the next token.  As above: a launch each, nothing allocated,
+ * capturable in a CUDA graph, the handle's device the current one. */
+
+/* A cache of keys and values.  The rows of a sequence's positions lie in pages
+ * of page_rows positions: position p of sequence s is row p % page_rows of page
+ * table[s * table_stride + p / page_rows].  Sequences may share pages, and
+ * a table may name a page again (the oldest page of a sliding window taken up
+ * anew), as long as no call reads a position whose row holds another's values.
+ * A page holds, per head, page_rows rows of head_dim values: bf16, or where
+ * k_scales and v_scales are given 8-bit codes with a scale per row (value =
+ * code * scale). */
+typedef struct {
+  int n_pages;           /* 1 ..; n_pages * kv_heads * page_rows up to 2^31 - 256    */
+  int kv_heads;          /* 1 .. 128                                                 */
+  int page_rows;         /* 16, 32, 64, 128 or 256                                   */
+  int head_dim;          /* a multiple of 16, 16 .. 256                              */
+  void *k, *v;           /* [n_pages, kv_heads, page_rows, head_dim], 16-byte aligned */
+  float *k_scales, *v_scales; /* both null (bf16), or [n_pages, kv_heads, page_rows], 16-byte aligned */
+  const int32_t *table;  /* [n_seqs, table_stride]                                   */
+  int n_seqs;            /* 1 .. MOE_KV_MAX_SEQS                                     */
+  int table_stride;      /* 1 ..; table_stride * page_rows up to 2^30                */
+} moe_kv_cache;
+#define MOE_KV_MAX_SEQS 4096
+#define MOE_KV_MAX_ROWS (1 << 20)
+
+/* Rotary positions, and new rows into the cache.  Row t is position row_pos[t]
+ * of sequence row_seq[t] (row_seq null: of sequence t).  With rot_dims = r > 0
+ * the first r dimensions of every head of q and k turn by the position's
+ * angles, a pair j, j + r/2 by a = row_pos[t] * inv_freq[j]:
+ *   x_j cos a - x_{j+r/2} sin a,  x_{j+r/2} cos a + x_j sin a     (j < r/2)
+ * (the angle is reduced in 64 bits: positions may be far).  Then
+ *   q_out[t]  bf16 of q's turned row
+ *   cache     bf16 of k's turned and v's row; in 8 bits, with m the largest
+ *             magnitude of a head's row: rint(127 x / m) (zero for m = 0) and
+ *             the scale m / 127, of k's turned row before any rounding to bf16
+ *   q         nullable bf16 [n_rows, q_heads, head_dim]; q_out only with q, may
+ *             be q itself (with the same stride)
+ *   k, v      bf16 [n_rows, kv_heads, head_dim]
+ *   strides   of q, k, v, q_out: values from row to row, multiples of 8 (the
+ *             parts of one projection's output can be given as they lie)
+ *   row_pos   int32 [n_rows]; row_seq nullable int32 [n_rows]
+ *   inv_freq  fp32 [rot_dims / 2] (null: rot_dims 0)
+ *   rot_dims  0, or a multiple of 16 up to head_dim
+ * n_rows 1 .. MOE_KV_MAX_ROWS, q_heads 1 .. 1024; all bf16 data 16-byte
+ * aligned.  A row of a negative position is left out: nothing is written for
+ * it.  A row of a sequence, a position or a page that is not there is not
+ * written to the cache (its q_out is) and records MOE_ERR_BAD_EXPERT_ID.  In 8
+ * bits a head's row with a NaN or an infinity gets codes 0 and the scale NaN
+ * and records MOE_ERR_NONFINITE.  No two rows of a call may go to one place of
+ * the cache (its row would hold values of both).  Outputs must not overlap
+ * inputs otherwise. */
+int moe_kv_append(moe_handle *h, const void *q, size_t q_stride, int q_heads, const void *k, size_t k_stride,
+                  const void *v, size_t v_stride, int n_rows, const int32_t *row_seq, const int32_t *row_pos,
+                  const moe_kv_cache *cache, const float *inv_freq, int rot_dims, void *q_out, size_t q_out_stride,
+                  moe_stream_t stream);
+
+/* Rows of the cache as bf16 (8-bit rows: the fp32 product code * scale,
+ * rounded): row t is position row_pos[t] of sequence row_seq[t] (null: of sequence
+ * t), as above; positions may be named again.
+ *   k_out, v_out  nullable bf16 [n_rows, kv_heads, head_dim] with strides of
+ *                 multiples of 8 values from row to row, 16-byte aligned; not
+ *                 both null
+ * A row of a negative position is left as it was; one that is not there is all
+ * zeros and records MOE_ERR_BAD_EXPERT_ID. */
+int moe_kv_read(moe_handle *h, const moe_kv_cache *cache, const int32_t *row_seq, const int32_t *row_pos, int n_rows,
+                void *k_out, size_t k_stride, void *v_out, size_t v_stride, moe_stream_t stream);
+
+/* Workspace of moe_kv_attend: the same for any lengths (0 for arguments that
+ * the call refuses). */
+size_t moe_kv_attend_workspace_bytes(const moe_kv_cache *cache, int q_heads);
+
+/* Attention of one new token per sequence (whose own key and value are in the
+ * cache already).  Query head i of sequence s looks at the keys of head
+ * i / (q_heads / kv_heads) at the positions p with
+ *   max(0, lengths[s] - window) <= p < lengths[s]       (window 0: from 0 on)
+ *   z_p = cap(scale * sum_d q[d] k_p[d]),  cap(z) = softcap * tanh(z / softcap),
+ *         or z for softcap 0
+ *   out = sum_p e^(z_p - L) v_p,  L = log sum_p e^(z_p)
+ * and lengths outside 0 .. table_stride * page_rows count as the nearer end.
+ *   q        bf16 [n_seqs, q_heads, head_dim], rows q_stride values apart;
+ *   out      the same with out_stride (strides multiples of 8, 16-byte aligned)
+ *   lse      nullable fp32 [n_seqs, q_heads]: L
+ *   lengths  int32 [n_seqs]
+ *   q_heads  a multiple of kv_heads, up to 64 times as many
+ *   scale    finite;  softcap 0 or above, finite;  window 0 or above
+ *   ws       moe_kv_attend_workspace_bytes(cache, q_heads) bytes, 256-byte aligned
+ * A sequence without a position to look at gets zeros and L = -inf.  Positions
+ * of a page that is not there are left out, and one among those looked at
+ * records MOE_ERR_BAD_EXPERT_ID; what the cache holds from the length on, or
+ * ahead of the window, does not matter.  Sums and statistics are fp32; a weight
+ * e^(z - max) is rounded once, to bf16 with a bf16 cache and to fp16 (with its
+ * value row's scale) with an 8-bit one.  Finished-block counters live in the
+ * handle, so calls on one handle must not overlap on the GPU; calls that may
+ * run at the same time need a handle and a workspace each. */
+int moe_kv_attend(moe_handle *h, const void *q, size_t q_stride, const moe_kv_cache *cache, const int32_t *lengths,
+                  int q_heads, float scale, float softcap, int window, void *out, size_t out_stride, float *lse,
+                  void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The filters of moe_sample, a value per row (device pointers; null: the value
+ * in brackets for every row). */
+typedef struct {
+  const float *uniform;      /* the random numbers, 0 <= u < 1 (never null)              */
+  const float *temperature;  /* [1]; not above 0: the greedy token                       */
+  const int32_t *top_k;      /* [0]; not above 0: off                                    */
+  const float *top_p;        /* [1]; from 1 on: off                                      */
+  const float *min_p;        /* [0]; not above 0: off; 1 at most                         */
+} moe_sample_rules;
+
+/* A token drawn from each row's logits.  With M the largest logit and the
+ * tokens in the order of their logits, the lower id first of equal ones, those
+ * that remain are
+ *   of all tokens with a logit above -inf those with (l - M) / temperature >= ln(min_p),
+ *   of these the first top_k,
+ *   of these the fewest first ones whose weights w = e^((l - M) / temperature)
+ *   sum to top_p of the sum or more, one at least.
+ * The token is the first by id whose running sum of the remaining weights is
+ * above u times their whole sum.
+ *   logits    fp32 [n_rows, logits_stride], the first vocab (1 .. 2^28) of a
+ *             row; n_rows 1 .. MOE_LOGITS_MAX_ROWS; logits_stride >= vocab
+ *   tokens    int32 [n_rows]: the token; -1 where no logit is above -inf
+ *   logprobs  nullable fp32 [n_rows]: the log of the token's share of the
+ *             remaining weights (0 for a greedy row; -inf with token -1)
+ * u counts as 0 below 0 or NaN, and as the last remaining token from 1 on.  A
+ * NaN filter is off, a NaN temperature is greedy.  A NaN or +inf among the
+ * logits counts as -inf and records MOE_ERR_NONFINITE. */
+int moe_sample(moe_handle *h, const float *logits, size_t logits_stride, int n_rows, int vocab,
+               const moe_sample_rules *rules, int32_t *tokens, float *logprobs, moe_stream_t stream);
+
 /* Launch tracing (diagnostics).  With a non-null device buffer of
  * 4 * n_launches u64, each subsequent kernel launch by this handle takes the
  * next 4 slots (wrapping) and records %globaltimer values, combined with
@@ -522,8 +651,9 @@ int moe_logits_process(moe_handle *h, const float *logits, size_t logits_stride,
  *   [2] latest time a block had its weights in shared memory (0: n/a)
  *   [3] latest block exit time (the router: its last block's exit).
  * A call launches 3 (T == 1) or 4 kernels; slot groups are reserved as
- * router 1, gate/up 1, down (+ combine) 2, sort 1; moe_norm_quant and
- * moe_logits_process 1, moe_qdense_forward 1, or 2 where a launch of its own
+ * router 1, gate/up 1, down (+ combine) 2, sort 1; moe_norm_quant,
+ * moe_logits_process, moe_kv_append, moe_kv_read, moe_kv_attend and moe_sample
+ * 1, moe_qdense_forward 1, or 2 where a launch of its own
  * widens the rows.  Buffer owned by the caller; NULL turns tracing off.
  * Tracing adds a few atomics per block. */
 int moe_set_trace(moe_handle *h, unsigned long long *buffer, int n_launches);

@@ -28,6 +28,7 @@ struct moe_handle {
   bool qdense_ready;          // the same for the 8-bit projection's kernels
   int qdense_clusters[moe::kQdenseMaxCluster + 1];  // clusters that fit the device, by their blocks
   bool logits_ready;          // and for the logits kernel
+  bool attend_ready;          // and for the attention's
   bool prefill_dense;         // multi-token calls may run dense slots on the tensor cores (tcgen05)
   // failure-detection hook, consumed by the next fused single-token launch
   int skip_block_next;                  // -1: none
@@ -72,7 +73,9 @@ static_assert(kDeviceWords <= kMboxOffset, "mailboxes overlap the device words")
 // after the mailboxes: the processed logits' greedy state, a 64-bit maximum
 // per row, then a finished-block ticket per row (zero between launches)
 size_t logits_state_offset(int n_sm) { return kMboxOffset + (size_t)n_sm * moe::kMaxExperts * 2; }
-size_t device_words(int n_sm) { return logits_state_offset(n_sm) + 3 * (size_t)moe::kLogitsMaxRows; }
+// then the attention's finished-part tickets, one per block (zero between launches)
+size_t attend_state_offset(int n_sm) { return logits_state_offset(n_sm) + 3 * (size_t)moe::kLogitsMaxRows; }
+size_t device_words(int n_sm) { return attend_state_offset(n_sm) + (size_t)n_sm; }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
@@ -1082,6 +1085,10 @@ int moe_kv_attend(moe_handle *h, const void *q, size_t q_stride, const moe_kv_ca
   if (!(fabsf(scale) <= FLT_MAX) || !(softcap >= 0.0f && softcap <= FLT_MAX) || window < 0) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_kv_attend_workspace_bytes(cache, q_heads)) return MOE_ERR_WORKSPACE;
   if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  if (!h->attend_ready) {
+    if (moe::kv_attend_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    h->attend_ready = true;
+  }
   moe::KvAttendArgs a;
   a.c = kv_cache(cache);
   a.q = (const uint16_t *)q;
@@ -1095,6 +1102,7 @@ int moe_kv_attend(moe_handle *h, const void *q, size_t q_stride, const moe_kv_ca
   a.scale = scale;
   a.softcap = softcap;
   a.window = window;
+  a.tickets = h->dwords + attend_state_offset(h->n_sm);
   a.err = h->dwords;
   a.trace = take_trace(h, 1);
   return cuda_status(moe::launch_kv_attend(a, h->n_sm, (cudaStream_t)stream, h->pdl));

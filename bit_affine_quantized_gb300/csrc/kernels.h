@@ -314,10 +314,12 @@ struct KvAttendArgs {
   int Hq;
   float scale, softcap;       // softcap 0: none
   int window;                 // 0: none
+  unsigned *tickets;          // [n_sm] finished parts of an item, by its first block: zero between launches
   unsigned *err;
   unsigned long long *trace;
 };
 size_t kv_attend_ws_bytes(const KvCache &c, int Hq);
+cudaError_t kv_attend_set_attributes();
 cudaError_t launch_kv_attend(const KvAttendArgs &a, int n_sm, cudaStream_t st, bool pdl);
 
 // A token drawn from filtered logits (sample.cu).

@@ -284,7 +284,10 @@ int check_kv(const moe_kv_cache *c) {
 
 int check_kv_heads(const moe_kv_cache *c, int q_heads) {
   if (q_heads < 1) return MOE_ERR_INVALID_ARG;
-  return q_heads % c->kv_heads || q_heads / c->kv_heads > 64 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  if (q_heads % c->kv_heads || q_heads / c->kv_heads > 64) return MOE_ERR_UNSUPPORTED;
+  // the kernel counts tiles of 16 positions or more in 32 bits
+  const int64_t most = (int64_t)c->n_seqs * c->table_stride * (c->page_rows / 16) * c->kv_heads;
+  return most * ((q_heads / c->kv_heads + 15) / 16) < ((int64_t)1 << 31) ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 // bf16 rows of `width` values that lie `stride` apart

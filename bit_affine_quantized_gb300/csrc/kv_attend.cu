@@ -50,14 +50,18 @@ template <bool kBits8, int kD, int kN>
 struct AtShape {
   static constexpr int kRow = kD * (kBits8 ? 1 : 2);   // bytes of a row in shared memory
   static constexpr int kBox = kRow < 128 ? kRow : 128; // bytes of a row in one copy
-  static constexpr int kTile = kRow >= 512 ? 16 : 32;  // positions
+  static constexpr int kTile = kRow <= 128 ? 32 : 16;  // positions
   static constexpr int kHalf = kTile * kRow;           // bytes of a tile's keys, and of its values
-  static constexpr int kWarps = kHalf >= 8192 ? 6 : 8;
-  static constexpr int kStages = kHalf >= 8192 ? 2 : kHalf >= 4096 ? 3 : 4;
+  // Warps: as many as the registers of a lane's share of the outputs allow, for a
+  // warp waits out its own products and shuffles.
+  static constexpr int kWarps = kN == 1 ? 12 : 8;
+  static constexpr int kFit = (int)(200 * 1024 / ((size_t)kWarps * 2 * kHalf));
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
   static constexpr int kPart = 16 * kN + kD / 16 * kN * 128;  // floats of a part: maxima, sums, the output's sum
+  static constexpr size_t kTiles = (size_t)kWarps * kStages * 2 * kHalf, kParts = (size_t)kWarps * kPart * 4;
+  static constexpr size_t kRoom = kTiles > kParts ? kTiles : kParts;  // parts lie where the tiles lay
   static constexpr size_t kScales = kBits8 ? (size_t)kWarps * kStages * 2 * kTile * 4 : 0;
-  static constexpr size_t kSmem = 1024 + (size_t)kWarps * kStages * 2 * kHalf + kScales;
-  static_assert((size_t)kWarps * kPart * 4 <= (size_t)kWarps * kStages * 2 * kHalf, "parts lie where the tiles lay");
+  static constexpr size_t kSmem = 1024 + kRoom + kScales;
 };
 
 struct AtParams {
@@ -167,7 +171,7 @@ struct AtWarpParts {
   bool began;    // and that item began within the run
   int seq, item; // of the one that ended
   int open_seq, open_item, open_nt;
-  unsigned long long open_at;  // first tile of the open one
+  unsigned open_at;  // first tile of the open one
 };
 
 template <bool kBits8, int kD, int kN>
@@ -175,14 +179,14 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     kv_attend_kernel(const __grid_constant__ AtParams prm) {
   using S = AtShape<kBits8, kD, kN>;
   constexpr int kTile = S::kTile, kWarps = S::kWarps, kStages = S::kStages, kMt = kTile / 16, kSteps = kD / 16;
-  constexpr int kThreads = 32 * kWarps;
+  constexpr int kThreads = 32 * kWarps, kHeads = 8 * kN;
   extern __shared__ uint8_t at_raw[];
   uint8_t *const sm = at_raw + ((1024 - (smem_addr(at_raw) & 1023)) & 1023);
-  float *const s_scales = reinterpret_cast<float *>(sm + (size_t)kWarps * kStages * 2 * S::kHalf);
-  __shared__ uint64_t s_full[kWarps][kStages];
-  __shared__ unsigned s_ok[kWarps][kStages];
-  __shared__ unsigned long long s_pre[kThreads + 1];
+  float *const s_scales = reinterpret_cast<float *>(sm + S::kRoom);
+  __shared__ uint64_t s_keys[kWarps][kStages], s_values[kWarps][kStages], s_join;
+  __shared__ unsigned s_pre[kThreads + 1], s_sums[kWarps];
   __shared__ AtWarpParts s_parts[kWarps];
+  __shared__ float s_m[2 * kWarps][kHeads], s_l[2 * kWarps][kHeads];  // of the warps' parts; then their weights
   __shared__ int s_last[2];
   const KvAttendArgs &a = prm.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -190,7 +194,11 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   const int shift = 31 - __clz(a.c.rows), box = min(a.c.rows, kTile), box_shift = 31 - __clz(box);
   const bool tracer = a.trace && blockIdx.x == 0 && tid == 0;
   if (tracer) trace_min(a.trace, kTrEntry);
-  if (tid < kWarps * kStages) mbar_init(&s_full[0][0] + tid, 1);
+  if (tid < kWarps * kStages) {
+    mbar_init(&s_keys[0][0] + tid, 1);
+    mbar_init(&s_values[0][0] + tid, 1);
+  }
+  if (tid == 0) mbar_init(&s_join, 1);
   fence_mbar_init();
   pdl_wait();
   pdl_launch_dependents();
@@ -201,54 +209,55 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   static_assert((kKvMaxSeqs + kThreads - 1) / kThreads <= 32, "a warp looks through a chunk at once");
   AtCursor<kTile> cur;
   {
-    unsigned long long sum = 0;
+    unsigned sum = 0;
     for (int i = tid * chunk; i < min(n, (tid + 1) * chunk); ++i) {
       cur.seq = i;
       cur.load(a);
-      sum += (unsigned long long)cur.nt * items;
+      sum += (unsigned)cur.nt * items;
     }
-    unsigned long long run = sum;
+    unsigned run = sum;
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
-      const unsigned long long o = __shfl_up_sync(0xffffffffu, run, off);
+      const unsigned o = __shfl_up_sync(0xffffffffu, run, off);
       if (lane >= off) run += o;
     }
+    if (lane == 31) s_sums[warp] = run;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps - 1; ++w)
+      if (w < warp) run += s_sums[w];
     s_pre[tid + 1] = run;
     if (tid == 0) s_pre[0] = 0;
     __syncthreads();
-    unsigned long long before = 0;
-    for (int w = 0; w < warp; ++w) before += s_pre[32 * (w + 1)];
-    __syncthreads();
-    s_pre[tid + 1] = run + before;
-    __syncthreads();
   }
-  const unsigned long long total = s_pre[kThreads];
+  const unsigned total = s_pre[kThreads];
   // as many blocks as have a tile for each warp
-  const unsigned long long want = (total + kWarps - 1) / kWarps;
-  const int blocks = want < gridDim.x ? (int)want : (int)gridDim.x;
+  const int blocks = (int)min((total + kWarps - 1) / kWarps, gridDim.x);
   const bool works = (int)blockIdx.x < blocks;
-  auto block_at = [&](int b) { return total / blocks * b + total % blocks * b / blocks; };  // first tile of block b
-  const unsigned long long bu0 = works ? block_at(blockIdx.x) : 0, bu1 = works ? block_at(blockIdx.x + 1) : 0;
-  const unsigned long long u0 = bu0 + (bu1 - bu0) * warp / kWarps, u1 = bu0 + (bu1 - bu0) * (warp + 1) / kWarps;
+  const unsigned each = works ? total / blocks : 0, rest = works ? total % blocks : 0;
+  auto block_at = [&](int b) { return each * b + rest * b / blocks; };  // first tile of block b
+  const unsigned bu0 = works ? block_at(blockIdx.x) : 0, bu1 = works ? block_at(blockIdx.x + 1) : 0;
+  const unsigned w_each = (bu1 - bu0) / kWarps, w_rest = (bu1 - bu0) % kWarps;
+  const unsigned u0 = bu0 + w_each * warp + w_rest * warp / kWarps;
+  const unsigned u1 = bu0 + w_each * (warp + 1) + w_rest * (warp + 1) / kWarps;
 
   // ---- the warp's first tile
   cur.seq = cur.item = cur.tile = cur.nt = 0;
   if (u0 < u1) {
     int ch = 0;
-    for (int i = lane; i - lane < kThreads; i += 32) {  // chunks that end at or before u0
-      ch += __popc(__ballot_sync(0xffffffffu, i < kThreads && s_pre[i + 1] <= u0));
-    }
+    for (int i = lane; i < kThreads; i += 32) ch += __popc(__ballot_sync(0xffffffffu, s_pre[i + 1] <= u0));
     cur.seq = min(n - 1, ch * chunk + lane);
     cur.load(a);
-    const unsigned long long mine = lane < chunk && ch * chunk + lane < n ? (unsigned long long)cur.nt * items : 0;
-    unsigned long long run = mine;
+    const unsigned mine = lane < chunk && ch * chunk + lane < n ? (unsigned)cur.nt * items : 0;
+    unsigned run = mine;
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
-      const unsigned long long o = __shfl_up_sync(0xffffffffu, run, off);
+      const unsigned o = __shfl_up_sync(0xffffffffu, run, off);
       if (lane >= off) run += o;
     }
-    const int who = __popc(__ballot_sync(0xffffffffu, s_pre[ch] + run <= u0));
-    const unsigned long long left = u0 - s_pre[ch] - __shfl_sync(0xffffffffu, run - mine, who);
+    const unsigned base = s_pre[ch];
+    const int who = __popc(__ballot_sync(0xffffffffu, base + run <= u0));  // lanes whose sequences end before
+    const unsigned left = u0 - base - __shfl_sync(0xffffffffu, run - mine, who);
     cur.seq = ch * chunk + who;
     cur.load(a);
     cur.item = (int)(left / (unsigned)cur.nt);
@@ -260,35 +269,34 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   float *const scales = s_scales + warp * kStages * 2 * kTile;
   const int boxes = kTile / box, columns = (D * (kBits8 ? 1 : 2) + S::kBox - 1) / S::kBox;
   const int rows_all = a.c.n_pages * H * a.c.rows;
+  const uint32_t bytes = (uint32_t)(kTile * S::kBox * columns + (kBits8 ? kTile * 4 : 0));
   bool lost = false, late = false;
-  auto copy = [&](int st) {  // the tile at `is` into stage st
-    if (lane == 0)
-      mbar_arrive_expect_tx(&s_full[warp][st], 2u * (kTile * S::kBox * columns + (kBits8 ? kTile * 4 : 0)));
-    __syncwarp();
+  int row = 0;                  // of the tile at `is`, lane b < boxes its box b
+  uint32_t there[kStages];      // the stages' boxes that are on pages that are there
+  auto find = [&] {             // the rows of the tile at `is`; its boxes that are there
     bool ok = false;
     if (lane < boxes) {
-      const int pos = (is.t0 + is.tile) * kTile + lane * box, kv = is.item / prm.blocks_of;
+      const int pos = (is.t0 + is.tile) * kTile + lane * box;
       const bool need = pos < is.len && pos + box > is.first;
       const int page = need ? __ldg(a.c.table + (size_t)is.seq * a.c.stride + (pos >> shift)) : -1;
       ok = (unsigned)page < (unsigned)a.c.n_pages;
       lost = lost || (need && !ok);
-      const int row = ok ? (page * H + kv) * a.c.rows + (pos & (a.c.rows - 1)) : 0;
-      const int y = ok ? row : rows_all;  // past the end: filled with zeros
-      uint8_t *k = tiles + (size_t)st * 2 * S::kHalf + lane * box * S::kBox;
-      for (int i = 0; i < columns; ++i) {
-        at_tma(k + i * kTile * S::kBox, &prm.k, i * (S::kBox / (kBits8 ? 1 : 2)), y, &s_full[warp][st]);
-        at_tma(k + S::kHalf + i * kTile * S::kBox, &prm.v, i * (S::kBox / (kBits8 ? 1 : 2)), y, &s_full[warp][st]);
-      }
-      if (kBits8) {
-        float *s = scales + st * 2 * kTile + lane * box;
-        bulk_g2s(s, a.c.ks + row, box * 4, &s_full[warp][st]);
-        bulk_g2s(s + kTile, a.c.vs + row, box * 4, &s_full[warp][st]);
-      }
+      row = ok ? (page * H + is.item / prm.blocks_of) * a.c.rows + (pos & (a.c.rows - 1)) : -1;
     }
-    const unsigned oks = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0) s_ok[warp][st] = oks;
-    is.next(a, items);
+    return __ballot_sync(0xffffffffu, ok);
   };
+  auto copy = [&](const CUtensorMap *map, const float *from, uint64_t *bar, int st, int half) {
+    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+    __syncwarp();
+    if (lane < boxes) {
+      uint8_t *to = tiles + (size_t)(2 * st + half) * S::kHalf + lane * box * S::kBox;
+      for (int i = 0; i < columns; ++i)  // (a box that is not there: past the end, filled with zeros)
+        at_tma(to + i * kTile * S::kBox, map, i * (S::kBox / (kBits8 ? 1 : 2)), row >= 0 ? row : rows_all, bar);
+      if (kBits8) bulk_g2s(scales + (2 * st + half) * kTile + lane * box, from + max(row, 0), box * 4, bar);
+    }
+  };
+  auto copy_keys = [&](int st) { copy(&prm.k, a.c.ks, &s_keys[warp][st], st, 0); };
+  auto copy_values = [&](int st) { copy(&prm.v, a.c.vs, &s_values[warp][st], st, 1); };
   // Byte in a half of a stage of the 16-byte piece x of row r, as the copies' swizzle lays it.
   auto place = [&](int r, int x) {
     if (S::kBox == 128) return (x >> 3) * kTile * 128 + r * 128 + (((x & 7) ^ (r & 7)) << 4);
@@ -301,12 +309,12 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   int unit = 1;  // 8 bits: values' weights in units of 2^(unit - 127 - kAtSums)
   auto begin = [&] {
     const int kv = cur.item / prm.blocks_of, h0 = kv * group + cur.item % prm.blocks_of * prm.heads;
-    const int there = min(prm.heads, group - cur.item % prm.blocks_of * prm.heads);
+    const int heads = min(prm.heads, group - cur.item % prm.blocks_of * prm.heads);
     unit = 1;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const uint16_t *from = a.q + (size_t)cur.seq * a.ldq + (size_t)(h0 + 8 * i + g) * D;
-      const bool is_there = 8 * i + g < there;
+      const bool is_there = 8 * i + g < heads;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         q[s][i][0] = q[s][i][1] = 0u;
@@ -353,7 +361,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   // The item's output, written whole.
   auto finish = [&] {
     const int kv = cur.item / prm.blocks_of, part = cur.item % prm.blocks_of * prm.heads, h0 = kv * group + part;
-    const int there = min(prm.heads, group - part);
+    const int heads = min(prm.heads, group - part);
     uint16_t *const out = a.out + (size_t)cur.seq * a.ldo + (size_t)h0 * D;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       for (int j = 0; j < 2; ++j) {
         const float sum = at_rows_sum(l[i][j]);
         const int h = 8 * i + 2 * c + j;
-        if (a.lse && g == 0 && h < there)
+        if (a.lse && g == 0 && h < heads)
           a.lse[(size_t)cur.seq * a.Hq + h0 + h] = m[i][j] * kLn2 + logf(sum);
         f[j] = sum != 0.f ? (kBits8 ? at_pow2(127 - kAtSums) : 1.f) / sum : 0.f;
       }
@@ -376,7 +384,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
         for (int j = 0; j < 4; ++j) v[j] = kBits8 ? o[s][i][j] * f[j & 1] * up : o[s][i][j] * f[j & 1];
         // turned, a lane has head g and dimensions that lie together
         const uint32_t lo = at_turn(at_bf16x2(v[0], v[1])), hi = at_turn(at_bf16x2(v[2], v[3]));
-        if (8 * i + g < there) {
+        if (8 * i + g < heads) {
           if (kBits8) {
             *reinterpret_cast<uint2 *>(to + 16 * s + 4 * c) =
                 make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
@@ -388,23 +396,23 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       }
     }
   };
-  // The state as a part: maxima and sums per head, then the output's sum as the lanes hold it.
-  auto leave = [&](float *to) {
+  // The state as a part: maxima and sums per head, and the output's sum as the lanes hold it.
+  auto leave = [&](float *to, int k) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float sum = at_rows_sum(l[i][j]);
         if (g == 0) {
-          to[8 * i + 2 * c + j] = m[i][j];
-          to[8 * kN + 8 * i + 2 * c + j] = sum;
+          s_m[k][8 * i + 2 * c + j] = m[i][j];
+          s_l[k][8 * i + 2 * c + j] = sum;
         }
       }
       const float up = kBits8 ? at_pow2(unit) : 1.f, down = kBits8 ? at_pow2(127 - kAtSums) : 1.f;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
         if (s < steps)
-          reinterpret_cast<float4 *>(to + 16 * kN)[(s * kN + i) * 32 + lane] =
+          reinterpret_cast<float4 *>(to + 2 * kHeads)[(s * kN + i) * 32 + lane] =
               make_float4(o[s][i][0] * down * up, o[s][i][1] * down * up, o[s][i][2] * down * up, o[s][i][3] * down * up);
     }
   };
@@ -413,11 +421,16 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   float *const my_end = work + (size_t)(blockIdx.x * kWarps + warp) * S::kPart;      // part of an item that ends in my run
   float *const block_parts = work + (size_t)gridDim.x * kWarps * S::kPart;           // [grid][2]
   if (u0 < u1) {
-    __syncwarp();
-#pragma unroll 1
-    for (int i = 0; i < kStages; ++i)
-      if (u0 + i < u1) copy(i);
-    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) {
+      there[i] = 0;
+      if (u0 + i < u1) {
+        there[i] = find();
+        copy_keys(i);
+        copy_values(i);
+        is.next(a, items);
+      }
+    }
   }
   bool ends = false, began = false;
   int end_seq = 0, end_item = 0, st = 0;
@@ -426,25 +439,25 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   const float to_cap = capped ? a.scale / a.softcap : a.scale * kLog2e, cap = a.softcap * kLog2e;
   bool fresh = true;
 #pragma unroll 1
-  for (unsigned long long u = u0; u < u1; ++u) {
+  for (unsigned u = u0; u < u1; ++u) {
     if (fresh) {
       began = cur.tile == 0;
       begin();
       fresh = false;
     }
-    late = __any_sync(0xffffffffu, !mbar_wait(&s_full[warp][st], phase));
-    if (late) {  // the copies under way land, or run out too, before the warp's memory is anyone's again
-      for (int i = 0; i < kStages && u + i < u1; ++i)
-        mbar_wait(&s_full[warp][(st + i) % kStages], phase ^ (st + i >= kStages ? 1u : 0u));
-      break;
-    }
+    const bool more = u + kStages < u1;
     const uint32_t keys = smem_addr(tiles + (size_t)st * 2 * S::kHalf), values = keys + S::kHalf;
     const float *ks = scales + st * 2 * kTile, *vs = ks + kTile;
     // which positions count
     const int p0 = (cur.t0 + cur.tile) * kTile;
+    uint32_t ok = there[0];
+#pragma unroll
+    for (int i = 1; i < kStages; ++i) ok = st == i ? there[i] : ok;
     const unsigned mask = __ballot_sync(
-        0xffffffffu, lane < kTile && p0 + lane >= cur.first && p0 + lane < cur.len && (s_ok[warp][st] >> (lane >> box_shift) & 1u));
+        0xffffffffu, lane < kTile && p0 + lane >= cur.first && p0 + lane < cur.len && (ok >> (lane >> box_shift) & 1u));
     const bool whole = mask == (kTile == 32 ? 0xffffffffu : 0xffffu);
+    late = __any_sync(0xffffffffu, !mbar_wait(&s_keys[warp][st], phase));
+    if (late) break;
 
     // ---- scores of the tile's positions, in units of log 2
     float z[kMt][kN][4];
@@ -498,6 +511,13 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
           z[t][i][j] = v;
         }
     }
+    __syncwarp();  // every lane has read the keys
+    if (more) {
+      const uint32_t boxes_there = find();
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) there[i] = st == i ? boxes_there : there[i];
+      copy_keys(st);
+    }
     // ---- weights
     float up[kN][2], top[kN][2];
     bool grows = false;
@@ -514,6 +534,8 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
         up[i][j] = at_keep(m[i][j], top[i][j]);
         m[i][j] = v;
       }
+    late = __any_sync(0xffffffffu, !mbar_wait(&s_values[warp][st], phase));
+    if (late) break;
     int e = unit;
     if (kBits8) {
       const unsigned most = __reduce_max_sync(
@@ -598,8 +620,11 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
         }
       }
     }
-    __syncwarp();  // every lane has read the stage
-    if (u + kStages < u1) copy(st);
+    __syncwarp();  // every lane has read the values
+    if (more) {
+      copy_values(st);
+      is.next(a, items);
+    }
     if (++st == kStages) {
       st = 0;
       phase ^= 1u;
@@ -609,7 +634,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       if (began) {
         finish();
       } else {
-        leave(my_end);
+        leave(my_end, 2 * warp);
         ends = true;
         end_seq = cur.seq;
         end_item = cur.item;
@@ -618,7 +643,11 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     if (u + 1 < u1) cur.next(a, items);
   }
   if (lane < boxes && lost) set_error(a.err, kErrBadId);
-  if (late && lane == 0) set_error(a.err, kErrTimeout);
+  if (late) {  // the copies under way land, or run out too, before the warp's memory is anyone's again
+    if (lane == 0) set_error(a.err, kErrTimeout);
+    for (int i = 0; i < 4 * kStages; ++i)
+      mbar_wait(i & 1 ? &s_values[warp][i / 4] : &s_keys[warp][i / 4], i >> 1 & 1, 1000000ull);
+  }
 
   // ---- the block's warps join their parts
   const bool open = u0 < u1 && !fresh && !late;
@@ -632,121 +661,140 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     p.open_seq = cur.seq;
     p.open_item = cur.item;
     p.open_nt = cur.nt;
-    p.open_at = u1 - 1 - (unsigned long long)cur.tile;
+    p.open_at = u1 - 1 - (unsigned)cur.tile;
   }
   // the tiles are read: parts take their places.  After a wait that ran out nothing is joined (the error tells).
   const bool joins = !__syncthreads_or(late);
   float *const s_open = reinterpret_cast<float *>(sm);
-  if (open && joins) leave(s_open + (size_t)warp * S::kPart);
+  if (open && joins) leave(s_open + (size_t)warp * S::kPart, 2 * warp + 1);
   __syncthreads();
   // A lane's two heads of a slot of a part, the element's dimension.
   auto write_out = [&](int seq, int item, int slot, const float (&v)[4]) {
     const int ln = slot & 31, i = slot / 32 % kN, s = slot / (32 * kN);
-    const int part = item % prm.blocks_of * prm.heads, there = min(prm.heads, group - part);
+    const int part = item % prm.blocks_of * prm.heads, heads = min(prm.heads, group - part);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int h = 8 * i + 2 * (ln & 3) + (j & 1);
       const int d = 16 * s + (kBits8 ? 2 * (ln >> 2) + (j >> 1) : (ln >> 2) + 8 * (j >> 1));
-      if (h < there)
+      if (h < heads)
         a.out[(size_t)seq * a.ldo + (size_t)(item / prm.blocks_of * group + part + h) * D + d] = float_to_bf16_bits(v[j]);
     }
   };
   auto write_lse = [&](int seq, int item, int h, float top, float sum) {
-    const int part = item % prm.blocks_of * prm.heads, there = min(prm.heads, group - part);
-    if (a.lse && h < there)
+    const int part = item % prm.blocks_of * prm.heads, heads = min(prm.heads, group - part);
+    if (a.lse && h < heads)
       a.lse[(size_t)seq * a.Hq + item / prm.blocks_of * group + part + h] = top * kLn2 + logf(sum);
   };
   const int slots = steps * kN * 32;
-  bool first_part = false, last_part = false;  // of items that other blocks share
-  for (int slot = tid; joins && slot < (slots + kThreads - 1) / kThreads * kThreads; slot += kThreads) {
-    const bool mine = slot < slots;
-    const int i = slot / 32 % kN, h = 8 * i + 2 * (slot & 3);
-    const bool heads = slot < 32 * kN && (slot & 31) < 4;  // this thread writes its heads' maxima and sums too
-    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
-    bool here = false, any = false;  // the item at hand began in this block; there is one
-    auto add = [&](const float *p) {
-      if (!mine) return;
-      const float4 w4 = reinterpret_cast<const float4 *>(p + 16 * kN)[slot];
-      const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-      float k0[2], k1[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float pm = p[h + j], t = fmaxf(M[j], pm), use = t == -INFINITY ? 0.f : t;
-        k0[j] = at_keep(M[j], use);
-        k1[j] = at_keep(pm, use);
-        M[j] = t;
-        L[j] = L[j] * k0[j] + p[8 * kN + h + j] * k1[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = v[j] * k0[j & 1] + w[j] * k1[j & 1];
-    };
-    auto store = [&](float *p) {
-      if (!mine) return;
-      reinterpret_cast<float4 *>(p + 16 * kN)[slot] = make_float4(v[0], v[1], v[2], v[3]);
-      if (heads) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          p[h + j] = M[j];
-          p[8 * kN + h + j] = L[j];
-        }
-      }
-    };
-    auto clear = [&] {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        M[j] = -INFINITY;
-        L[j] = 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = 0.f;
-    };
+  // The parts in their order are, per warp, one that ends an item and one of an item
+  // left open; a run of parts up to one that ends, or to the last, is of one item.
+  // first_part, last_part: parts of items that other blocks share.
+  bool first_part = false, last_part = false;
+  if (joins) {
+    bool here = false, any = false;
     for (int w = 0; w < kWarps; ++w) {
-      const AtWarpParts &p = s_parts[w];
-      if (p.ends) {
-        add(work + (size_t)(blockIdx.x * kWarps + w) * S::kPart);
-        if (here) {
-          if (mine) {
-            const float f[2] = {L[0] != 0.f ? 1.f / L[0] : 0.f, L[1] != 0.f ? 1.f / L[1] : 0.f};
-            const float r[4] = {v[0] * f[0], v[1] * f[1], v[2] * f[0], v[3] * f[1]};
-            write_out(p.seq, p.item, slot, r);
-            if (heads) {
-              write_lse(p.seq, p.item, h, M[0], L[0]);
-              write_lse(p.seq, p.item, h + 1, M[1], L[1]);
-            }
-          }
-        } else {
-          store(block_parts + (size_t)(2 * blockIdx.x) * S::kPart);
-          first_part = true;
-        }
-        clear();
+      if (s_parts[w].ends) {
+        first_part = first_part || !here;
         any = false;
       }
-      if (p.open) {
-        if (p.began) {
-          clear();
-          here = true;
-        }
-        add(s_open + (size_t)w * S::kPart);
+      if (s_parts[w].open) {
+        here = here || s_parts[w].began;
         any = true;
       }
     }
-    if (any) {
-      store(block_parts + (size_t)(2 * blockIdx.x + (here ? 1 : 0)) * S::kPart);
-      if (here)
-        last_part = true;
-      else
-        first_part = true;
+    if (any) (here ? last_part : first_part) = true;
+  }
+  float *const block_part0 = block_parts + (size_t)(2 * blockIdx.x) * S::kPart, *const block_part1 = block_part0 + S::kPart;
+  if (joins && tid < kHeads) {  // a head's maxima and sums: the parts' weights, with 1 / sum where the item ends here
+    const int h = tid;
+    int from = 0;
+    bool here = false;
+    float top = -INFINITY;
+    auto close = [&](int to, bool whole, float *part) {  // parts from .. to
+      const float use = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      for (int k = from; k <= to; ++k) {
+        const bool is_there = k & 1 ? s_parts[k / 2].open : s_parts[k / 2].ends;
+        const float w = is_there ? at_keep(s_m[k][h], use) : 0.f;
+        if (is_there) sum += w * s_l[k][h];
+        s_m[k][h] = w;
+      }
+      if (whole) {
+        const float f = sum != 0.f ? 1.f / sum : 0.f;
+        for (int k = from; k <= to; ++k) s_m[k][h] *= f;
+        write_lse(s_parts[to / 2].seq, s_parts[to / 2].item, h, top, sum);
+      } else {
+        part[h] = top;
+        part[kHeads + h] = sum;
+      }
+      from = to + 1;
+      top = -INFINITY;
+    };
+    for (int w = 0; w < kWarps; ++w) {
+      if (s_parts[w].ends) {
+        top = fmaxf(top, s_m[2 * w][h]);
+        close(2 * w, here, block_part0);
+      }
+      if (s_parts[w].open) {
+        if (s_parts[w].began) {
+          here = true;
+          from = 2 * w + 1;
+        }
+        top = fmaxf(top, s_m[2 * w + 1][h]);
+      }
+    }
+    int w = kWarps - 1;  // the item open at the end of the run, if there is one
+    while (w >= 0 && !s_parts[w].open && !s_parts[w].ends) --w;
+    if (w >= 0 && s_parts[w].open) close(2 * w + 1, false, here ? block_part1 : block_part0);
+  }
+  __syncthreads();
+  if (joins) {
+    for (int slot = tid; slot < slots; slot += kThreads) {
+      const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
+      float4 e[kWarps];  // the parts in the workspace, all on their way at once
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (s_parts[w].ends)
+          e[w] = reinterpret_cast<const float4 *>(work + (size_t)(blockIdx.x * kWarps + w) * S::kPart + 2 * kHeads)[slot];
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      bool here = false, any = false;
+      auto add = [&](const float4 p, int k) {
+        const float w0 = s_m[k][h], w1 = s_m[k][h + 1];
+        v[0] = fmaf(p.x, w0, v[0]);
+        v[1] = fmaf(p.y, w1, v[1]);
+        v[2] = fmaf(p.z, w0, v[2]);
+        v[3] = fmaf(p.w, w1, v[3]);
+      };
+      auto store = [&](float *p) { reinterpret_cast<float4 *>(p + 2 * kHeads)[slot] = make_float4(v[0], v[1], v[2], v[3]); };
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (s_parts[w].ends) {
+          add(e[w], 2 * w);
+          if (here)
+            write_out(s_parts[w].seq, s_parts[w].item, slot, v);
+          else
+            store(block_part0);
+          v[0] = v[1] = v[2] = v[3] = 0.f;
+          any = false;
+        }
+        if (s_parts[w].open) {
+          here = here || s_parts[w].began;
+          any = true;
+          add(reinterpret_cast<const float4 *>(s_open + (size_t)w * S::kPart + 2 * kHeads)[slot], 2 * w + 1);
+        }
+      }
+      if (any) store(here ? block_part1 : block_part0);
     }
   }
 
   // ---- the last block of an item joins the blocks' parts
-  if (works && (first_part || last_part)) {  // (the same for every thread)
+  if (first_part || last_part) {  // (the same for every thread)
     __threadfence();
     __syncthreads();
-    // An item of tiles [at, at + nt) that more than one block has: the first of them, and how many.
-    auto span = [&](unsigned long long at, int nt, int &from, int &count) {
-      auto of = [&](unsigned long long t) {
-        int b = (int)((double)t / (double)total * blocks);
+    // Of the item that a part is of: its first block, and how many have parts.
+    auto span = [&](unsigned at, int nt, int &from, int &count) {
+      auto of = [&](unsigned t) {
+        int b = (int)((float)t / (float)total * (float)blocks);
         b = max(0, min(blocks - 1, b));
         while (b + 1 < blocks && block_at(b + 1) <= t) ++b;
         while (block_at(b) > t) --b;
@@ -756,35 +804,26 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       count = of(at + (unsigned)nt - 1) - from + 1;
     };
     int from[2] = {0, 0}, count[2] = {0, 0}, seq[2] = {0, 0}, item[2] = {0, 0};
-    // the item open at the block's start: it ends in a warp, or is the last one's
-    if (first_part) {
+    if (first_part) {  // of the item open at the block's start: it ends in a warp, or is every warp's
       int w = 0;
       while (w < kWarps - 1 && !s_parts[w].ends) ++w;
-      const bool ended = s_parts[w].ends;
-      int x = w;
-      if (!ended)
-        while (!s_parts[x].open) --x;
-      seq[0] = ended ? s_parts[w].seq : s_parts[x].open_seq;
-      item[0] = ended ? s_parts[w].item : s_parts[x].open_item;
-      AtCursor<kTile> it;
-      it.seq = seq[0];
-      it.load(a);
-      // its first tile: of the sequence's, item by item
-      unsigned long long at;
-      if (ended) {
-        // the block's first tile lies in it: count back from there
-        at = s_pre[seq[0] / chunk];
-        for (int s = seq[0] / chunk * chunk; s < seq[0]; ++s) {
-          AtCursor<kTile> b;
-          b.seq = s;
-          b.load(a);
-          at += (unsigned long long)b.nt * items;
+      if (s_parts[w].ends) {
+        AtCursor<kTile> it;
+        seq[0] = s_parts[w].seq;
+        item[0] = s_parts[w].item;
+        unsigned at = s_pre[seq[0] / chunk];
+        for (it.seq = seq[0] / chunk * chunk; it.seq < seq[0]; ++it.seq) {
+          it.load(a);
+          at += (unsigned)it.nt * items;
         }
-        at += (unsigned long long)it.nt * item[0];
+        it.load(a);
+        span(at + (unsigned)it.nt * item[0], it.nt, from[0], count[0]);
       } else {
-        at = s_parts[x].open_at;
+        while (!s_parts[w].open) --w;
+        seq[0] = s_parts[w].open_seq;
+        item[0] = s_parts[w].open_item;
+        span(s_parts[w].open_at, s_parts[w].open_nt, from[0], count[0]);
       }
-      span(at, it.nt, from[0], count[0]);
     }
     if (last_part) {
       int w = kWarps - 1;
@@ -793,56 +832,96 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       item[1] = s_parts[w].open_item;
       span(s_parts[w].open_at, s_parts[w].open_nt, from[1], count[1]);
     }
-    if (tid == 0) {
-      for (int k = 0; k < 2; ++k) {
-        s_last[k] = 0;
-        if (k == 0 ? !first_part : !last_part) continue;
-        if (atomicAdd(a.tickets + from[k], 1u) + 1u == (unsigned)count[k]) {
+    if (tid < 2) {
+      s_last[tid] = 0;
+      if (tid == 0 ? first_part : last_part) {
+        const int f = tid == 0 ? from[0] : from[1], need = tid == 0 ? count[0] : count[1];
+        if (atomicAdd(a.tickets + f, 1u) + 1u == (unsigned)need) {
           __threadfence();
-          a.tickets[from[k]] = 0u;
-          s_last[k] = 1;
+          a.tickets[f] = 0u;
+          s_last[tid] = 1;
         }
       }
     }
     __syncthreads();
+    uint32_t turn = 0;
     for (int k = 0; k < 2; ++k) {
       if (!s_last[k]) continue;
-      float *const s_w = s_open, *const s_sum = s_open + (size_t)count[k] * 8 * kN;  // weights, then sums and maxima
-      auto part = [&](int b) { return block_parts + (size_t)(2 * (from[k] + b) + (b == 0 ? 1 : 0)) * S::kPart; };
+      // Parts come to shared memory a room full at a time, by bulk copies, while their weights are worked out.
+      const int n_parts = count[k], f = from[k];
+      const uint32_t size = (uint32_t)(2 * kHeads + slots * 4) * 4;  // bytes of a part
+      float *const s_w = reinterpret_cast<float *>(sm), *const s_sum = s_w + n_parts * kHeads;  // weights, 1 / sums
+      const uint32_t head = ((uint32_t)(n_parts + 1) * kHeads * 4 + 127) & ~127u;
+      float *const s_room = reinterpret_cast<float *>(sm + head);
+      const int fit = min(n_parts, (int)((S::kRoom - head) / size));
+      auto part = [&](int b) { return block_parts + (size_t)(2 * (f + b) + (b == 0 ? 1 : 0)) * S::kPart; };
+      auto fetch = [&](int b0) {  // parts b0 .. b0 + fit
+        if (tid == 0) {
+          const int many = min(fit, n_parts - b0);
+          // what other blocks wrote, and this block read here, before the copies read and write
+          asm volatile("fence.proxy.async;" ::: "memory");
+          mbar_arrive_expect_tx(&s_join, (uint32_t)many * size);
+          for (int b = 0; b < many; ++b) bulk_g2s(s_room + (size_t)b * (size / 4), part(b0 + b), size, &s_join);
+        }
+      };
       __syncthreads();
-      for (int h = warp; h < 8 * kN; h += kWarps) {
+      fetch(0);
+      for (int i = tid; i < n_parts * kHeads; i += kThreads) s_w[i] = __ldcg(part(i / kHeads) + i % kHeads);
+      __syncthreads();
+      for (int h = warp; h < kHeads; h += kWarps) {
         float top = -INFINITY, sum = 0.f;
-        for (int b = lane; b < count[k]; b += 32) top = fmaxf(top, __ldcg(part(b) + h));
+        for (int b = lane; b < n_parts; b += 32) top = fmaxf(top, s_w[b * kHeads + h]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
         const float use = top == -INFINITY ? 0.f : top;
-        for (int b = lane; b < count[k]; b += 32) {
-          const float w = at_keep(__ldcg(part(b) + h), use);
-          s_w[b * 8 * kN + h] = w;
-          sum += w * __ldcg(part(b) + 8 * kN + h);
+        for (int b = lane; b < n_parts; b += 32) {
+          const float w = at_keep(s_w[b * kHeads + h], use);
+          s_w[b * kHeads + h] = w;
+          sum += w * __ldcg(part(b) + kHeads + h);
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (lane == 0) {
-          s_sum[h] = sum;
+          s_sum[h] = sum != 0.f ? 1.f / sum : 0.f;
           write_lse(seq[k], item[k], h, top, sum);
         }
       }
       __syncthreads();
-      for (int slot = tid; slot < slots; slot += kThreads) {
-        const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int b = 0; b < count[k]; ++b) {
-          const float4 w4 = __ldcg(reinterpret_cast<const float4 *>(part(b) + 16 * kN) + slot);
-          const float w0 = s_w[b * 8 * kN + h], w1 = s_w[b * 8 * kN + h + 1];
-          v[0] = fmaf(w4.x, w0, v[0]);
-          v[1] = fmaf(w4.y, w1, v[1]);
-          v[2] = fmaf(w4.z, w0, v[2]);
-          v[3] = fmaf(w4.w, w1, v[3]);
+      constexpr int kMine = (kSteps * kN * 32 + kThreads - 1) / kThreads;  // slots of a thread
+      float v[kMine][4];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
+      bool ran_out = false;
+      for (int b0 = 0; b0 < n_parts && !ran_out; b0 += fit) {
+        ran_out = __syncthreads_or(!mbar_wait(&s_join, turn));
+        turn ^= 1u;
+        const int many = ran_out ? 0 : min(fit, n_parts - b0);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int slot = tid + i * kThreads, h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
+          if (slot >= slots) continue;
+#pragma unroll 4
+          for (int b = 0; b < many; ++b) {
+            const float4 p = reinterpret_cast<const float4 *>(s_room + (size_t)b * (size / 4) + 2 * kHeads)[slot];
+            const float2 w = *reinterpret_cast<const float2 *>(s_w + (b0 + b) * kHeads + h);
+            v[i][0] = fmaf(p.x, w.x, v[i][0]);
+            v[i][1] = fmaf(p.y, w.y, v[i][1]);
+            v[i][2] = fmaf(p.z, w.x, v[i][2]);
+            v[i][3] = fmaf(p.w, w.y, v[i][3]);
+          }
         }
-        const float f0 = s_sum[h] != 0.f ? 1.f / s_sum[h] : 0.f, f1 = s_sum[h + 1] != 0.f ? 1.f / s_sum[h + 1] : 0.f;
-        const float r[4] = {v[0] * f0, v[1] * f1, v[2] * f0, v[3] * f1};
+        __syncthreads();
+        if (b0 + fit < n_parts && !ran_out) fetch(b0 + fit);
+      }
+      if (ran_out) {
+        if (tid == 0) set_error(a.err, kErrTimeout);
+        break;
+      }
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int slot = tid + i * kThreads, h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
+        if (slot >= slots) continue;
+        const float r[4] = {v[i][0] * s_sum[h], v[i][1] * s_sum[h + 1], v[i][2] * s_sum[h], v[i][3] * s_sum[h + 1]};
         write_out(seq[k], item[k], slot, r);
       }
     }
@@ -900,7 +979,7 @@ cudaError_t at_size(const KvAttendArgs &a, int n_sm, cudaStream_t st, bool pdl) 
 
 size_t kv_attend_ws_bytes(const KvCache &c, int Hq) {
   const int kN = Hq / c.heads > 8 ? 2 : 1, kD = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
-  return (size_t)kAtMaxGrid * (8 + 2) * (16 * kN + kD / 16 * kN * 128) * 4;
+  return (size_t)kAtMaxGrid * ((kN == 1 ? 12 : 8) + 2) * (16 * kN + kD / 16 * kN * 128) * 4;
 }
 
 cudaError_t kv_attend_set_attributes() {

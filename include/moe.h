@@ -597,7 +597,9 @@ size_t moe_kv_attend_workspace_bytes(const moe_kv_cache *cache, int q_heads);
  *   out      the same with out_stride (strides multiples of 8, 16-byte aligned)
  *   lse      nullable fp32 [n_seqs, q_heads]: L
  *   lengths  int32 [n_seqs]
- *   q_heads  a multiple of kv_heads, up to 64 times as many
+ *   q_heads  a multiple of kv_heads, up to 64 times as many; n_seqs *
+ *            table_stride * page_rows / 16 * kv_heads (for each 16 query heads
+ *            of a key head, or part of them) below 2^31
  *   scale    finite;  softcap 0 or above, finite;  window 0 or above
  *   ws       moe_kv_attend_workspace_bytes(cache, q_heads) bytes, 256-byte aligned
  * A sequence without a position to look at gets zeros and L = -inf.  Positions

@@ -112,6 +112,11 @@ def test_attend_workspace(lib):
         assert n > 0 and n % 256 == 0
     assert lib.moe_kv_attend_workspace_bytes(ctypes.byref(cache()), 3) == 0
     assert lib.moe_kv_attend_workspace_bytes(ctypes.byref(cache()), 0) == 0
+    wide = dict(n_seqs=4096, table_stride=1 << 12, page_rows=256, kv_heads=8)  # 2^31 tiles of 16 positions
+    assert lib.moe_kv_attend_workspace_bytes(ctypes.byref(cache(**wide)), 8) == 0
+    wide["n_seqs"] = 4095
+    assert lib.moe_kv_attend_workspace_bytes(ctypes.byref(cache(**wide)), 128) > 0
+    assert lib.moe_kv_attend_workspace_bytes(ctypes.byref(cache(**wide)), 136) == 0
 
 
 @pytest.mark.parametrize("change,status", [

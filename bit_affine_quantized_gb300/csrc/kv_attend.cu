@@ -78,6 +78,9 @@ __device__ __forceinline__ void at_tma(void *dst, const CUtensorMap *map, int x,
       "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
 }
+__device__ __forceinline__ void at_prefetch(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 __device__ __forceinline__ void at_ldsm(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   __shared__ uint64_t s_keys[kWarps][kStages], s_values[kWarps][kStages], s_join;
   __shared__ unsigned s_pre[kThreads + 1], s_sums[kWarps];
   __shared__ AtWarpParts s_parts[kWarps];
-  __shared__ float s_m[2 * kWarps][kHeads], s_l[2 * kWarps][kHeads];  // of the warps' parts; then their weights
+  __shared__ __align__(16) float s_m[2 * kWarps][kHeads], s_l[2 * kWarps][kHeads];  // of the warps' parts; then their weights
   __shared__ int s_last[2];
   const KvAttendArgs &a = prm.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -198,7 +201,11 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     mbar_init(&s_keys[0][0] + tid, 1);
     mbar_init(&s_values[0][0] + tid, 1);
   }
-  if (tid == 0) mbar_init(&s_join, 1);
+  if (tid == 0) {
+    mbar_init(&s_join, 1);
+    at_prefetch(&prm.k);
+    at_prefetch(&prm.v);
+  }
   fence_mbar_init();
   pdl_wait();
   pdl_launch_dependents();
@@ -271,18 +278,19 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   const int rows_all = a.c.n_pages * H * a.c.rows;
   const uint32_t bytes = (uint32_t)(kTile * S::kBox * columns + (kBits8 ? kTile * 4 : 0));
   bool lost = false, late = false;
-  int row = 0;                  // of the tile at `is`, lane b < boxes its box b
+  int page = 0, row = 0;        // of the tile at `is`, lane b < boxes its box b
+  bool need = false;
   uint32_t there[kStages];      // the stages' boxes that are on pages that are there
+  auto look = [&] {             // asks for the pages of the tile at `is`, well ahead of their use
+    const int pos = (is.t0 + is.tile) * kTile + lane * box;
+    need = lane < boxes && pos < is.len && pos + box > is.first;
+    if (need) page = __ldg(a.c.table + (size_t)is.seq * a.c.stride + (pos >> shift));
+  };
   auto find = [&] {             // the rows of the tile at `is`; its boxes that are there
-    bool ok = false;
-    if (lane < boxes) {
-      const int pos = (is.t0 + is.tile) * kTile + lane * box;
-      const bool need = pos < is.len && pos + box > is.first;
-      const int page = need ? __ldg(a.c.table + (size_t)is.seq * a.c.stride + (pos >> shift)) : -1;
-      ok = (unsigned)page < (unsigned)a.c.n_pages;
-      lost = lost || (need && !ok);
-      row = ok ? (page * H + is.item / prm.blocks_of) * a.c.rows + (pos & (a.c.rows - 1)) : -1;
-    }
+    const bool ok = need && (unsigned)page < (unsigned)a.c.n_pages;
+    const int pos = (is.t0 + is.tile) * kTile + lane * box;
+    lost = lost || (need && !ok);
+    row = ok ? (page * H + is.item / prm.blocks_of) * a.c.rows + (pos & (a.c.rows - 1)) : -1;
     return __ballot_sync(0xffffffffu, ok);
   };
   auto copy = [&](const CUtensorMap *map, const float *from, uint64_t *bar, int st, int half) {
@@ -425,12 +433,14 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     for (int i = 0; i < kStages; ++i) {
       there[i] = 0;
       if (u0 + i < u1) {
+        look();
         there[i] = find();
         copy_keys(i);
         copy_values(i);
         is.next(a, items);
       }
     }
+    if (u0 + kStages < u1) look();
   }
   bool ends = false, began = false;
   int end_seq = 0, end_item = 0, st = 0;
@@ -460,13 +470,13 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     if (late) break;
 
     // ---- scores of the tile's positions, in units of log 2
-    float z[kMt][kN][4];
+    float z[kMt][kN][4], y[kN][4];  // (odd steps apart: two chains of products)
 #pragma unroll
     for (int t = 0; t < kMt; ++t) {
 #pragma unroll
       for (int i = 0; i < kN; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z[t][i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) z[t][i][j] = y[i][j] = 0.f;
       const int r = 16 * t + (lane & 15);
       if (kBits8) {
 #pragma unroll
@@ -482,7 +492,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
             const uint32_t x[4] = {at_codes<0x4140>(w[2 * h]), at_codes<0x4140>(w[2 * h + 1]),
                                    at_codes<0x4342>(w[2 * h]), at_codes<0x4342>(w[2 * h + 1])};
 #pragma unroll
-            for (int i = 0; i < kN; ++i) at_mma<true>(z[t][i], x, q[s + h][i][0], q[s + h][i][1]);
+            for (int i = 0; i < kN; ++i) at_mma<true>(h ? y[i] : z[t][i], x, q[s + h][i][0], q[s + h][i][1]);
           }
         }
       } else {
@@ -492,7 +502,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
           uint32_t w[4];
           at_ldsm(w, keys + place(r, 2 * s + (lane >> 4)));
 #pragma unroll
-          for (int i = 0; i < kN; ++i) at_mma<false>(z[t][i], w, q[s][i][0], q[s][i][1]);
+          for (int i = 0; i < kN; ++i) at_mma<false>(s & 1 ? y[i] : z[t][i], w, q[s][i][0], q[s][i][1]);
         }
       }
       float f[2] = {to_cap, to_cap};
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       for (int i = 0; i < kN; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float v = z[t][i][j] * f[j >> 1];
+          float v = (z[t][i][j] + y[i][j]) * f[j >> 1];
           if (kBits8) v *= qs[i][j & 1];
           if (capped) v = cap * tanhf(v);
           if (!whole && !(mask >> (16 * t + 8 * (j >> 1) + g) & 1u)) v = -INFINITY;
@@ -624,6 +634,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     if (more) {
       copy_values(st);
       is.next(a, items);
+      if (u + kStages + 1 < u1) look();
     }
     if (++st == kStages) {
       st = 0;
@@ -668,16 +679,17 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   float *const s_open = reinterpret_cast<float *>(sm);
   if (open && joins) leave(s_open + (size_t)warp * S::kPart, 2 * warp + 1);
   __syncthreads();
-  // A lane's two heads of a slot of a part, the element's dimension.
-  auto write_out = [&](int seq, int item, int slot, const float (&v)[4]) {
-    const int ln = slot & 31, i = slot / 32 % kN, s = slot / (32 * kN);
-    const int part = item % prm.blocks_of * prm.heads, heads = min(prm.heads, group - part);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int h = 8 * i + 2 * (ln & 3) + (j & 1);
-      const int d = 16 * s + (kBits8 ? 2 * (ln >> 2) + (j >> 1) : (ln >> 2) + 8 * (j >> 1));
-      if (h < heads)
-        a.out[(size_t)seq * a.ldo + (size_t)(item / prm.blocks_of * group + part + h) * D + d] = float_to_bf16_bits(v[j]);
+  // An item's output in bf16, from the sums of a part (divided already) in shared memory.
+  auto write_out = [&](int seq, int item, const float *p) {
+    const int first = item % prm.blocks_of * prm.heads, heads = min(prm.heads, group - first);
+    uint16_t *const out = a.out + (size_t)seq * a.ldo + (size_t)(item / prm.blocks_of * group + first) * D;
+    for (int i = 2 * tid; i < heads * D; i += 2 * kThreads) {
+      const int h = i / D, d = i % D, r = d & 15;
+      const float *f = p + 2 * kHeads + ((d >> 4) * kN + (h >> 3)) * 128 + ((h & 7) >> 1) * 4 + (h & 1);
+      // rows g and g + 8 of a product: dimensions 2 g and 2 g + 1 in 8 bits, else g and g + 8
+      const float lo = kBits8 ? f[(r >> 1) * 16] : f[(r & 7) * 16 + (r >> 3) * 2];
+      const float hi = kBits8 ? f[(r >> 1) * 16 + 2] : f[((r & 7) + 1) * 16 + (r >> 3) * 2];
+      *reinterpret_cast<uint32_t *>(out + i) = at_bf16x2(lo, hi);
     }
   };
   auto write_lse = [&](int seq, int item, int h, float top, float sum) {
@@ -686,105 +698,99 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       a.lse[(size_t)seq * a.Hq + item / prm.blocks_of * group + part + h] = top * kLn2 + logf(sum);
   };
   const int slots = steps * kN * 32;
-  // The parts in their order are, per warp, one that ends an item and one of an item
-  // left open; a run of parts up to one that ends, or to the last, is of one item.
-  // first_part, last_part: parts of items that other blocks share.
-  bool first_part = false, last_part = false;
-  if (joins) {
-    bool here = false, any = false;
-    for (int w = 0; w < kWarps; ++w) {
-      if (s_parts[w].ends) {
-        first_part = first_part || !here;
-        any = false;
-      }
-      if (s_parts[w].open) {
-        here = here || s_parts[w].began;
-        any = true;
-      }
-    }
-    if (any) (here ? last_part : first_part) = true;
-  }
   float *const block_part0 = block_parts + (size_t)(2 * blockIdx.x) * S::kPart, *const block_part1 = block_part0 + S::kPart;
-  if (joins && tid < kHeads) {  // a head's maxima and sums: the parts' weights, with 1 / sum where the item ends here
-    const int h = tid;
-    int from = 0;
-    bool here = false;
-    float top = -INFINITY;
-    auto close = [&](int to, bool whole, float *part) {  // parts from .. to
-      const float use = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      for (int k = from; k <= to; ++k) {
-        const bool is_there = k & 1 ? s_parts[k / 2].open : s_parts[k / 2].ends;
-        const float w = is_there ? at_keep(s_m[k][h], use) : 0.f;
-        if (is_there) sum += w * s_l[k][h];
-        s_m[k][h] = w;
+  // The parts in their order are, per warp, 2 w: one that ends an item, 2 w + 1: one
+  // of an item left open; a run of parts up to one that ends, or to the last, is of
+  // one item.  It was begun in this block if one of them was.
+  static_assert(2 * kWarps <= 32, "a lane per part");
+  const AtWarpParts &lp = s_parts[min(lane / 2, kWarps - 1)];
+  const bool counts = joins && lane < 2 * kWarps;
+  const uint32_t ends_at = __ballot_sync(0xffffffffu, counts && !(lane & 1) && lp.ends);
+  const uint32_t open_at = __ballot_sync(0xffffffffu, counts && (lane & 1) && lp.open);
+  const uint32_t began_at = __ballot_sync(0xffffffffu, counts && (lane & 1) && lp.open && lp.began);
+  const uint32_t all_at = ends_at | open_at;
+  auto run_of = [&](int k) {  // the parts of part k's item
+    const uint32_t before = ends_at & ((1u << k) - 1u), from = ends_at >> k << k;
+    const uint32_t to = from ? (from & -from) : 0x80000000u;  // the one that ends it, or the last
+    return (to | (to - 1u)) & (before ? ~((2u << (31 - __clz(before))) - 1u) : ~0u);
+  };
+  const uint32_t first_run = run_of(0);
+  const bool last_open = open_at > ends_at;  // (the highest of the parts)
+  const uint32_t last_run = last_open ? run_of(31 - __clz(all_at)) : 0u;
+  // of items that other blocks share: the first, not begun here; the last, begun here and open
+  const bool first_part = (first_run & all_at) && !(first_run & began_at), last_part = (last_run & began_at) != 0u;
+  if (joins) {
+    for (int h = warp; h < kHeads; h += kWarps) {  // the parts' weights, with 1 / sum where the item ends here
+      const uint32_t run = run_of(lane);
+      const int from = __ffs(run) - 1, to = 31 - __clz(run);
+      const bool is_there = all_at >> lane & 1u, ended = ends_at >> to & 1u, here = (run & began_at) != 0u;
+      const float mine = is_there ? s_m[min(lane, 2 * kWarps - 1)][h] : -INFINITY;
+      float top = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off *= 2) {
+        const float o = __shfl_down_sync(0xffffffffu, top, off);
+        if (lane + off <= to) top = fmaxf(top, o);
       }
-      if (whole) {
-        const float f = sum != 0.f ? 1.f / sum : 0.f;
-        for (int k = from; k <= to; ++k) s_m[k][h] *= f;
-        write_lse(s_parts[to / 2].seq, s_parts[to / 2].item, h, top, sum);
-      } else {
-        part[h] = top;
-        part[kHeads + h] = sum;
+      top = __shfl_sync(0xffffffffu, top, from);
+      float w = at_keep(mine, top == -INFINITY ? 0.f : top), sum = is_there ? w * s_l[min(lane, 2 * kWarps - 1)][h] : 0.f;
+#pragma unroll
+      for (int off = 1; off < 32; off *= 2) {
+        const float o = __shfl_down_sync(0xffffffffu, sum, off);
+        if (lane + off <= to) sum += o;
       }
-      from = to + 1;
-      top = -INFINITY;
-    };
-    for (int w = 0; w < kWarps; ++w) {
-      if (s_parts[w].ends) {
-        top = fmaxf(top, s_m[2 * w][h]);
-        close(2 * w, here, block_part0);
-      }
-      if (s_parts[w].open) {
-        if (s_parts[w].began) {
-          here = true;
-          from = 2 * w + 1;
+      sum = __shfl_sync(0xffffffffu, sum, from);
+      if (ended && here) w *= sum != 0.f ? 1.f / sum : 0.f;
+      if (is_there) s_m[lane][h] = w;
+      if (lane == from && (run & all_at)) {
+        if (ended && here) {
+          write_lse(s_parts[to / 2].seq, s_parts[to / 2].item, h, top, sum);
+        } else {
+          float *const part = here ? block_part1 : block_part0;
+          part[h] = top;
+          part[kHeads + h] = sum;
         }
-        top = fmaxf(top, s_m[2 * w + 1][h]);
       }
     }
-    int w = kWarps - 1;  // the item open at the end of the run, if there is one
-    while (w >= 0 && !s_parts[w].open && !s_parts[w].ends) --w;
-    if (w >= 0 && s_parts[w].open) close(2 * w + 1, false, here ? block_part1 : block_part0);
   }
   __syncthreads();
-  if (joins) {
-    for (int slot = tid; slot < slots; slot += kThreads) {
-      const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
-      float4 e[kWarps];  // the parts in the workspace, all on their way at once
+  for (int slot = tid; joins && slot < slots; slot += kThreads) {
+    const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
+    float4 e[kWarps];  // the parts in the workspace, all on their way at once
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        if (s_parts[w].ends)
-          e[w] = reinterpret_cast<const float4 *>(work + (size_t)(blockIdx.x * kWarps + w) * S::kPart + 2 * kHeads)[slot];
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      bool here = false, any = false;
-      auto add = [&](const float4 p, int k) {
-        const float w0 = s_m[k][h], w1 = s_m[k][h + 1];
-        v[0] = fmaf(p.x, w0, v[0]);
-        v[1] = fmaf(p.y, w1, v[1]);
-        v[2] = fmaf(p.z, w0, v[2]);
-        v[3] = fmaf(p.w, w1, v[3]);
-      };
-      auto store = [&](float *p) { reinterpret_cast<float4 *>(p + 2 * kHeads)[slot] = make_float4(v[0], v[1], v[2], v[3]); };
+    for (int w = 0; w < kWarps; ++w)
+      if (ends_at >> (2 * w) & 1u)
+        e[w] = reinterpret_cast<const float4 *>(work + (size_t)(blockIdx.x * kWarps + w) * S::kPart + 2 * kHeads)[slot];
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    float *to = block_part0;  // where the sum at hand goes: an item that ends here in place of its last part but one
+    auto add = [&](const float4 p, int k) {
+      const float2 w2 = *reinterpret_cast<const float2 *>(&s_m[k][h]);
+      v[0] = fmaf(p.x, w2.x, v[0]);
+      v[1] = fmaf(p.y, w2.y, v[1]);
+      v[2] = fmaf(p.z, w2.x, v[2]);
+      v[3] = fmaf(p.w, w2.y, v[3]);
+    };
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (s_parts[w].ends) {
-          add(e[w], 2 * w);
-          if (here)
-            write_out(s_parts[w].seq, s_parts[w].item, slot, v);
-          else
-            store(block_part0);
-          v[0] = v[1] = v[2] = v[3] = 0.f;
-          any = false;
-        }
-        if (s_parts[w].open) {
-          here = here || s_parts[w].began;
-          any = true;
-          add(reinterpret_cast<const float4 *>(s_open + (size_t)w * S::kPart + 2 * kHeads)[slot], 2 * w + 1);
-        }
+    for (int w = 0; w < kWarps; ++w) {
+      if (ends_at >> (2 * w) & 1u) {
+        add(e[w], 2 * w);
+        reinterpret_cast<float4 *>(to + 2 * kHeads)[slot] = make_float4(v[0], v[1], v[2], v[3]);
+        v[0] = v[1] = v[2] = v[3] = 0.f;
       }
-      if (any) store(here ? block_part1 : block_part0);
+      if (open_at >> (2 * w + 1) & 1u) {
+        float *const p = s_open + (size_t)w * S::kPart;
+        add(reinterpret_cast<const float4 *>(p + 2 * kHeads)[slot], 2 * w + 1);
+        if (to != block_part0 || (began_at >> (2 * w + 1) & 1u)) to = p;
+      }
     }
+    if (last_open)
+      reinterpret_cast<float4 *>((last_part ? block_part1 : block_part0) + 2 * kHeads)[slot] = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  __syncthreads();
+  for (uint32_t left = ends_at; left; left &= left - 1u) {  // items that warps shared and that began and ended here
+    const int k = __ffs(left) - 1;
+    const uint32_t run = run_of(k) & open_at;
+    if (run_of(k) & began_at)
+      write_out(s_parts[k / 2].seq, s_parts[k / 2].item, s_open + (size_t)((31 - __clz(run)) / 2) * S::kPart);
   }
 
   // ---- the last block of an item joins the blocks' parts
@@ -850,8 +856,9 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       // Parts come to shared memory a room full at a time, by bulk copies, while their weights are worked out.
       const int n_parts = count[k], f = from[k];
       const uint32_t size = (uint32_t)(2 * kHeads + slots * 4) * 4;  // bytes of a part
-      float *const s_w = reinterpret_cast<float *>(sm), *const s_sum = s_w + n_parts * kHeads;  // weights, 1 / sums
-      const uint32_t head = ((uint32_t)(n_parts + 1) * kHeads * 4 + 127) & ~127u;
+      float *const s_w = reinterpret_cast<float *>(sm), *const s_sums_of = s_w + n_parts * kHeads;  // maxima, then weights; sums
+      float *const s_sum = s_sums_of + n_parts * kHeads;                                                // 1 / sum
+      const uint32_t head = ((uint32_t)(2 * n_parts + 1) * kHeads * 4 + 127) & ~127u;
       float *const s_room = reinterpret_cast<float *>(sm + head);
       const int fit = min(n_parts, (int)((S::kRoom - head) / size));
       auto part = [&](int b) { return block_parts + (size_t)(2 * (f + b) + (b == 0 ? 1 : 0)) * S::kPart; };
@@ -866,7 +873,10 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       };
       __syncthreads();
       fetch(0);
-      for (int i = tid; i < n_parts * kHeads; i += kThreads) s_w[i] = __ldcg(part(i / kHeads) + i % kHeads);
+      for (int i = tid; i < 2 * n_parts * kHeads; i += kThreads) {
+        const int b = i / (2 * kHeads), h = i % (2 * kHeads);
+        s_w[(h / kHeads * n_parts + b) * kHeads + h % kHeads] = __ldcg(part(b) + h);
+      }
       __syncthreads();
       for (int h = warp; h < kHeads; h += kWarps) {
         float top = -INFINITY, sum = 0.f;
@@ -877,7 +887,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
         for (int b = lane; b < n_parts; b += 32) {
           const float w = at_keep(s_w[b * kHeads + h], use);
           s_w[b * kHeads + h] = w;
-          sum += w * __ldcg(part(b) + kHeads + h);
+          sum += w * s_sums_of[b * kHeads + h];
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -921,9 +931,11 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       for (int i = 0; i < kMine; ++i) {
         const int slot = tid + i * kThreads, h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
         if (slot >= slots) continue;
-        const float r[4] = {v[i][0] * s_sum[h], v[i][1] * s_sum[h + 1], v[i][2] * s_sum[h], v[i][3] * s_sum[h + 1]};
-        write_out(seq[k], item[k], slot, r);
+        reinterpret_cast<float4 *>(s_room + 2 * kHeads)[slot] =
+            make_float4(v[i][0] * s_sum[h], v[i][1] * s_sum[h + 1], v[i][2] * s_sum[h], v[i][3] * s_sum[h + 1]);
       }
+      __syncthreads();
+      write_out(seq[k], item[k], s_room);
     }
   }
 

@@ -50,7 +50,7 @@ template <bool kBits8, int kD, int kN>
 struct AtShape {
   static constexpr int kRow = kD * (kBits8 ? 1 : 2);   // bytes of a row in shared memory
   static constexpr int kBox = kRow < 128 ? kRow : 128; // bytes of a row in one copy
-  static constexpr int kTile = kRow <= 128 ? 32 : 16;  // positions
+  static constexpr int kTile = kRow <= 256 ? 32 : 16;  // positions
   static constexpr int kHalf = kTile * kRow;           // bytes of a tile's keys, and of its values
   // Warps: as many as the registers of a lane's share of the outputs allow, for a
   // warp waits out its own products and shuffles.
@@ -130,6 +130,11 @@ __device__ __forceinline__ float at_exp2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// cap tanh(x) as cap - 2 cap / (e^(2 x) + 1): within 2^-21 of the cap, which is what
+// matters in an exponent; from infinities +-cap, a NaN stays one.
+__device__ __forceinline__ float at_cap(float x, float cap) {
+  return fmaf(-2.f * cap, __fdividef(1.f, at_exp2(2.f * kLog2e * x) + 1.f), cap);
 }
 // The power of two 2^(e - 127), e in 1 .. 254.
 __device__ __forceinline__ float at_pow2(int e) { return __uint_as_float((unsigned)e << 23); }
@@ -274,9 +279,10 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
 
   uint8_t *const tiles = sm + (size_t)warp * kStages * 2 * S::kHalf;
   float *const scales = s_scales + warp * kStages * 2 * kTile;
-  const int boxes = kTile / box, columns = (D * (kBits8 ? 1 : 2) + S::kBox - 1) / S::kBox;
+  const int boxes = kTile / box;
+  constexpr int kColumns = S::kRow / S::kBox;  // dimensions from D on are copied as zeros
   const int rows_all = a.c.n_pages * H * a.c.rows;
-  const uint32_t bytes = (uint32_t)(kTile * S::kBox * columns + (kBits8 ? kTile * 4 : 0));
+  constexpr uint32_t kBytes = S::kHalf + (kBits8 ? kTile * 4 : 0);
   bool lost = false, late = false;
   int page = 0, row = 0;        // of the tile at `is`, lane b < boxes its box b
   bool need = false;
@@ -294,23 +300,26 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     return __ballot_sync(0xffffffffu, ok);
   };
   auto copy = [&](const CUtensorMap *map, const float *from, uint64_t *bar, int st, int half) {
-    if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+    if (lane == 0) mbar_arrive_expect_tx(bar, kBytes);
     __syncwarp();
     if (lane < boxes) {
       uint8_t *to = tiles + (size_t)(2 * st + half) * S::kHalf + lane * box * S::kBox;
-      for (int i = 0; i < columns; ++i)  // (a box that is not there: past the end, filled with zeros)
-        at_tma(to + i * kTile * S::kBox, map, i * (S::kBox / (kBits8 ? 1 : 2)), row >= 0 ? row : rows_all, bar);
+      const int y = row >= 0 ? row : rows_all;  // (a box that is not there: past the end, filled with zeros)
+#pragma unroll
+      for (int i = 0; i < kColumns; ++i)
+        at_tma(to + i * kTile * S::kBox, map, i * (S::kBox / (kBits8 ? 1 : 2)), y, bar);
       if (kBits8) bulk_g2s(scales + (2 * st + half) * kTile + lane * box, from + max(row, 0), box * 4, bar);
     }
   };
   auto copy_keys = [&](int st) { copy(&prm.k, a.c.ks, &s_keys[warp][st], st, 0); };
   auto copy_values = [&](int st) { copy(&prm.v, a.c.vs, &s_values[warp][st], st, 1); };
-  // Byte in a half of a stage of the 16-byte piece x of row r, as the copies' swizzle lays it.
-  auto place = [&](int r, int x) {
-    if (S::kBox == 128) return (x >> 3) * kTile * 128 + r * 128 + (((x & 7) ^ (r & 7)) << 4);
-    return r * 64 + (((x & 3) ^ ((r >> 1) & 3)) << 4);
-  };
+  // Byte in a half of a stage of the 16-byte piece x + y of row r, x even and y 0 or
+  // 1, as the copies' swizzle lays it: place(r, y) once, then piece(that, x).
+  auto place = [&](int r, int y) { return S::kBox == 128 ? r * 128 + ((y ^ (r & 7)) << 4) : r * 64 + ((y ^ ((r >> 1) & 3)) << 4); };
+  auto piece = [&](uint32_t at, int x) { return (at ^ (uint32_t)((x & 7) << 4)) + (uint32_t)((x >> 3) * kTile * 128); };
 
+  const bool capped = a.softcap > 0.f;
+  const float to_cap = capped ? a.scale / a.softcap : a.scale * kLog2e, cap = a.softcap * kLog2e;
   // ---- state of the item at hand: lane (g, c) has the heads 8 i + 2 c and the one after
   uint32_t q[kSteps][kN][2];
   float m[kN][2], l[kN][2], o[kSteps][kN][4], qs[kN][2];
@@ -353,7 +362,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
           for (int j = 0; j < 2; ++j)
             q[s][i][j] = at_f16x2(__uint_as_float(q[s][i][j] << 16) * down, __uint_as_float(q[s][i][j] & 0xFFFF0000u) * down);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) qs[i][j] = at_pow2(__shfl_sync(0xffffffffu, e, 4 * (2 * c + j)));
+        for (int j = 0; j < 2; ++j) qs[i][j] = at_pow2(__shfl_sync(0xffffffffu, e, 4 * (2 * c + j))) * to_cap;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -445,8 +454,6 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   bool ends = false, began = false;
   int end_seq = 0, end_item = 0, st = 0;
   uint32_t phase = 0;
-  const bool capped = a.softcap > 0.f;
-  const float to_cap = capped ? a.scale / a.softcap : a.scale * kLog2e, cap = a.softcap * kLog2e;
   bool fresh = true;
 #pragma unroll 1
   for (unsigned u = u0; u < u1; ++u) {
@@ -463,9 +470,12 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     uint32_t ok = there[0];
 #pragma unroll
     for (int i = 1; i < kStages; ++i) ok = st == i ? there[i] : ok;
-    const unsigned mask = __ballot_sync(
-        0xffffffffu, lane < kTile && p0 + lane >= cur.first && p0 + lane < cur.len && (ok >> (lane >> box_shift) & 1u));
-    const bool whole = mask == (kTile == 32 ? 0xffffffffu : 0xffffu);
+    constexpr unsigned kAll = kTile == 32 ? 0xffffffffu : 0xffffu;
+    const bool whole = p0 >= cur.first && p0 + kTile <= cur.len && ok == (1u << boxes) - 1u;
+    unsigned mask = kAll;
+    if (!whole)
+      mask = __ballot_sync(0xffffffffu, lane < kTile && p0 + lane >= cur.first && p0 + lane < cur.len &&
+                                            (ok >> (lane >> box_shift) & 1u));
     late = __any_sync(0xffffffffu, !mbar_wait(&s_keys[warp][st], phase));
     if (late) break;
 
@@ -477,18 +487,16 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       for (int i = 0; i < kN; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[t][i][j] = y[i][j] = 0.f;
-      const int r = 16 * t + (lane & 15);
+      const uint32_t rows = keys + place(16 * t + (lane & 15), lane >> 4);
       if (kBits8) {
 #pragma unroll
         for (int s = 0; s < kSteps; s += 2) {
-          if (s >= steps) continue;
           uint32_t w[4];
-          at_ldsm(w, keys + place(r, s + (lane >> 4)));
+          at_ldsm(w, piece(rows, s));
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] ^= 0x80808080u;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (s + h >= steps) continue;
             const uint32_t x[4] = {at_codes<0x4140>(w[2 * h]), at_codes<0x4140>(w[2 * h + 1]),
                                    at_codes<0x4342>(w[2 * h]), at_codes<0x4342>(w[2 * h + 1])};
 #pragma unroll
@@ -498,28 +506,37 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       } else {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          if (s >= steps) continue;
           uint32_t w[4];
-          at_ldsm(w, keys + place(r, 2 * s + (lane >> 4)));
+          at_ldsm(w, piece(rows, 2 * s));
 #pragma unroll
           for (int i = 0; i < kN; ++i) at_mma<false>(s & 1 ? y[i] : z[t][i], w, q[s][i][0], q[s][i][1]);
         }
       }
-      float f[2] = {to_cap, to_cap};
-      if (kBits8) {
-        f[0] *= ks[16 * t + g];
-        f[1] *= ks[16 * t + 8 + g];
-      }
+      const float f[2] = {kBits8 ? ks[16 * t + g] : to_cap, kBits8 ? ks[16 * t + 8 + g] : to_cap};
 #pragma unroll
       for (int i = 0; i < kN; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float v = (z[t][i][j] + y[i][j]) * f[j >> 1];
-          if (kBits8) v *= qs[i][j & 1];
-          if (capped) v = cap * tanhf(v);
-          if (!whole && !(mask >> (16 * t + 8 * (j >> 1) + g) & 1u)) v = -INFINITY;
-          z[t][i][j] = v;
+          z[t][i][j] = (z[t][i][j] + y[i][j]) * f[j >> 1];
+          if (kBits8) z[t][i][j] *= qs[i][j & 1];
         }
+    }
+    if (capped) {
+#pragma unroll
+      for (int t = 0; t < kMt; ++t)
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[t][i][j] = at_cap(z[t][i][j], cap);
+    }
+    if (!whole) {
+#pragma unroll
+      for (int t = 0; t < kMt; ++t)
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!(mask >> (16 * t + 8 * (j >> 1) + g) & 1u)) z[t][i][j] = -INFINITY;
     }
     __syncwarp();  // every lane has read the keys
     if (more) {
@@ -591,17 +608,15 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
           p[i][j] = at_turn(kBits8 ? at_f16x2(w[2 * j] * f[j], w[2 * j + 1] * f[j]) : at_bf16x2(w[2 * j], w[2 * j + 1]));
       }
       if (kBits8) {
-        const int r = 16 * t + (lane & 15);
+        const uint32_t rows = values + place(16 * t + (lane & 15), lane >> 4);
 #pragma unroll
         for (int s = 0; s < kSteps; s += 2) {
-          if (s >= steps) continue;
           uint32_t w[4];
-          at_ldsm_t(w, values + place(r, s + (lane >> 4)));
+          at_ldsm_t(w, piece(rows, s));
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] ^= 0x80808080u;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // rows g and g + 8 of the product are dimensions 2 g and 2 g + 1
-            if (s + h >= steps) continue;
             const uint32_t x[4] = {at_codes<0x4240>(w[2 * h]), at_codes<0x4341>(w[2 * h]),
                                    at_codes<0x4240>(w[2 * h + 1]), at_codes<0x4341>(w[2 * h + 1])};
 #pragma unroll
@@ -609,7 +624,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
           }
         }
       } else {
-        const int r = 16 * t + (lane & 7) + 8 * (lane >> 4);
+        const uint32_t rows = values + place(16 * t + (lane & 7) + 8 * (lane >> 4), lane >> 3 & 1);
         uint32_t keep[2] = {~0u, ~0u};  // rows that do not count may hold anything: nothing of them is multiplied
         if (!whole) {
 #pragma unroll
@@ -620,11 +635,12 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          if (s >= steps) continue;
           uint32_t w[4];
-          at_ldsm_t(w, values + place(r, 2 * s + (lane >> 3 & 1)));
+          at_ldsm_t(w, piece(rows, 2 * s));
+          if (!whole) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] &= keep[j >> 1];
+            for (int j = 0; j < 4; ++j) w[j] &= keep[j >> 1];
+          }
 #pragma unroll
           for (int i = 0; i < kN; ++i) at_mma<false>(o[s][i], w, p[i][0], p[i][1]);
         }

@@ -44,6 +44,7 @@ namespace moe {
 
 namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kAtMaxGrid = 192;  // blocks
 constexpr int kAtSums = 14;  // 8-bit values' weights are held times 2^14
 
 template <bool kBits8, int kD, int kN>
@@ -59,7 +60,9 @@ struct AtShape {
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
   static constexpr int kPart = 16 * kN + kD / 16 * kN * 128;  // floats of a part: maxima, sums, the output's sum
   static constexpr size_t kTiles = (size_t)kWarps * kStages * 2 * kHalf, kParts = (size_t)kWarps * kPart * 4;
-  static constexpr size_t kRoom = kTiles > kParts ? kTiles : kParts;  // parts lie where the tiles lay
+  // Parts lie where the tiles lay: those of items left open, and where there is room those of items that ended.
+  static constexpr bool kBoth = 2 * kParts <= 200 * 1024;
+  static constexpr size_t kAllParts = kBoth ? 2 * kParts : kParts, kRoom = kTiles > kAllParts ? kTiles : kAllParts;
   static constexpr size_t kScales = kBits8 ? (size_t)kWarps * kStages * 2 * kTile * 4 : 0;
   static constexpr size_t kSmem = 1024 + kRoom + kScales;
 };
@@ -78,6 +81,8 @@ __device__ __forceinline__ void at_tma(void *dst, const CUtensorMap *map, int x,
       "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
 }
+// Orders what went before by plain accesses and what comes after by copies.
+__device__ __forceinline__ void at_fence_copies() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void at_prefetch(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -177,9 +182,8 @@ struct AtWarpParts {
   bool ends;     // an item that began before the warp's run ended within it: its part is in the workspace
   bool open;     // the run ends within an item: its part is in shared memory
   bool began;    // and that item began within the run
-  int seq, item; // of the one that ended
-  int open_seq, open_item, open_nt;
-  unsigned open_at;  // first tile of the open one
+  int seq[2], item[2], nt[2];  // of the one that ended, the open one
+  unsigned at[2];              // their first tiles
 };
 
 template <bool kBits8, int kD, int kN>
@@ -192,10 +196,10 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   uint8_t *const sm = at_raw + ((1024 - (smem_addr(at_raw) & 1023)) & 1023);
   float *const s_scales = reinterpret_cast<float *>(sm + S::kRoom);
   __shared__ uint64_t s_keys[kWarps][kStages], s_values[kWarps][kStages], s_join;
-  __shared__ unsigned s_pre[kThreads + 1], s_sums[kWarps];
+  __shared__ unsigned s_pre[kThreads + 1], s_sums[kWarps + 1];
   __shared__ AtWarpParts s_parts[kWarps];
   __shared__ __align__(16) float s_m[2 * kWarps][kHeads], s_l[2 * kWarps][kHeads];  // of the warps' parts; then their weights
-  __shared__ int s_last[2];
+  __shared__ int s_last[2], s_count[2], s_from[2];
   const KvAttendArgs &a = prm.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int D = a.c.D, steps = D / 16, H = a.c.heads, group = a.Hq / H, items = H * prm.blocks_of;
@@ -233,12 +237,19 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       const unsigned o = __shfl_up_sync(0xffffffffu, run, off);
       if (lane >= off) run += o;
     }
-    if (lane == 31) s_sums[warp] = run;
+    if (lane == 31) s_sums[warp + 1] = run;
     __syncthreads();
+    if (warp == 0) {  // over the warps
+      unsigned all = lane > 0 && lane <= kWarps ? s_sums[lane] : 0;
 #pragma unroll
-    for (int w = 0; w < kWarps - 1; ++w)
-      if (w < warp) run += s_sums[w];
-    s_pre[tid + 1] = run;
+      for (int off = 1; off < 32; off *= 2) {
+        const unsigned o = __shfl_up_sync(0xffffffffu, all, off);
+        if (lane >= off) all += o;
+      }
+      if (lane <= kWarps) s_sums[lane] = all;
+    }
+    __syncthreads();
+    s_pre[tid + 1] = run + s_sums[warp];
     if (tid == 0) s_pre[0] = 0;
     __syncthreads();
   }
@@ -256,8 +267,9 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   // ---- the warp's first tile
   cur.seq = cur.item = cur.tile = cur.nt = 0;
   if (u0 < u1) {
-    int ch = 0;
-    for (int i = lane; i < kThreads; i += 32) ch += __popc(__ballot_sync(0xffffffffu, s_pre[i + 1] <= u0));
+    // the chunk: of which warp, then of which lane
+    int ch = 32 * __popc(__ballot_sync(0xffffffffu, lane < kWarps && s_sums[min(lane, kWarps - 1) + 1] <= u0));
+    ch += __popc(__ballot_sync(0xffffffffu, s_pre[ch + lane + 1] <= u0));
     cur.seq = min(n - 1, ch * chunk + lane);
     cur.load(a);
     const unsigned mine = lane < chunk && ch * chunk + lane < n ? (unsigned)cur.nt * items : 0;
@@ -452,7 +464,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     if (u0 + kStages < u1) look();
   }
   bool ends = false, began = false;
-  int end_seq = 0, end_item = 0, st = 0;
+  int st = 0;
   uint32_t phase = 0;
   bool fresh = true;
 #pragma unroll 1
@@ -663,8 +675,13 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       } else {
         leave(my_end, 2 * warp);
         ends = true;
-        end_seq = cur.seq;
-        end_item = cur.item;
+        if (lane == 0) {
+          AtWarpParts &p = s_parts[warp];
+          p.seq[0] = cur.seq;
+          p.item[0] = cur.item;
+          p.nt[0] = cur.nt;
+          p.at[0] = u + 1 - (unsigned)cur.nt;
+        }
       }
     }
     if (u + 1 < u1) cur.next(a, items);
@@ -683,13 +700,12 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     p.ends = ends;
     p.open = open;
     p.began = began;
-    p.seq = end_seq;
-    p.item = end_item;
-    p.open_seq = cur.seq;
-    p.open_item = cur.item;
-    p.open_nt = cur.nt;
-    p.open_at = u1 - 1 - (unsigned)cur.tile;
+    p.seq[1] = cur.seq;
+    p.item[1] = cur.item;
+    p.nt[1] = cur.nt;
+    p.at[1] = u1 - 1 - (unsigned)cur.tile;
   }
+  at_fence_copies();
   // the tiles are read: parts take their places.  After a wait that ran out nothing is joined (the error tells).
   const bool joins = !__syncthreads_or(late);
   float *const s_open = reinterpret_cast<float *>(sm);
@@ -735,7 +751,20 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   const uint32_t last_run = last_open ? run_of(31 - __clz(all_at)) : 0u;
   // of items that other blocks share: the first, not begun here; the last, begun here and open
   const bool first_part = (first_run & all_at) && !(first_run & began_at), last_part = (last_run & began_at) != 0u;
+  uint32_t turn = 0;  // of s_join
+  const uint32_t size = (uint32_t)(2 * kHeads + slots * 4) * 4;  // bytes of a part
+  float *const s_ends = s_open + kWarps * S::kPart;
+  const bool fetches = S::kBoth && ends_at != 0u;
+  if (fetches && tid == 0) {
+    at_fence_copies();
+    mbar_arrive_expect_tx(&s_join, size * (uint32_t)__popc(ends_at));
+    for (uint32_t left = ends_at; left; left &= left - 1u) {
+      const int w = (__ffs(left) - 1) / 2;
+      bulk_g2s(s_ends + (size_t)w * S::kPart, work + (size_t)(blockIdx.x * kWarps + w) * S::kPart, size, &s_join);
+    }
+  }
   if (joins) {
+#pragma unroll 1
     for (int h = warp; h < kHeads; h += kWarps) {  // the parts' weights, with 1 / sum where the item ends here
       const uint32_t run = run_of(lane);
       const int from = __ffs(run) - 1, to = 31 - __clz(run);
@@ -759,7 +788,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       if (is_there) s_m[lane][h] = w;
       if (lane == from && (run & all_at)) {
         if (ended && here) {
-          write_lse(s_parts[to / 2].seq, s_parts[to / 2].item, h, top, sum);
+          write_lse(s_parts[to / 2].seq[0], s_parts[to / 2].item[0], h, top, sum);
         } else {
           float *const part = here ? block_part1 : block_part0;
           part[h] = top;
@@ -768,190 +797,155 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
       }
     }
   }
-  __syncthreads();
-  for (int slot = tid; joins && slot < slots; slot += kThreads) {
+  const bool came = !fetches || mbar_wait(&s_join, turn);
+  if (fetches) turn ^= 1u;
+  const bool whole_parts = !__syncthreads_or(!came);
+  if (!whole_parts && tid == 0) set_error(a.err, kErrTimeout);
+#pragma unroll 1
+  for (int slot = tid; whole_parts && slot < slots; slot += kThreads) {
     const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
-    float4 e[kWarps];  // the parts in the workspace, all on their way at once
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (ends_at >> (2 * w) & 1u)
-        e[w] = reinterpret_cast<const float4 *>(work + (size_t)(blockIdx.x * kWarps + w) * S::kPart + 2 * kHeads)[slot];
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    float *to = block_part0;  // where the sum at hand goes: an item that ends here in place of its last part but one
-    auto add = [&](const float4 p, int k) {
-      const float2 w2 = *reinterpret_cast<const float2 *>(&s_m[k][h]);
-      v[0] = fmaf(p.x, w2.x, v[0]);
-      v[1] = fmaf(p.y, w2.y, v[1]);
-      v[2] = fmaf(p.z, w2.x, v[2]);
-      v[3] = fmaf(p.w, w2.y, v[3]);
-    };
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (ends_at >> (2 * w) & 1u) {
-        add(e[w], 2 * w);
-        reinterpret_cast<float4 *>(to + 2 * kHeads)[slot] = make_float4(v[0], v[1], v[2], v[3]);
-        v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll 1
+    for (uint32_t left = all_at; left;) {
+      const uint32_t run = run_of(__ffs(left) - 1) & all_at;
+      left &= ~run;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (uint32_t m = run; m; m &= m - 1u) {
+        const int k = __ffs(m) - 1, w = k / 2;
+        const float *p = k & 1 ? s_open + (size_t)w * S::kPart
+                               : S::kBoth ? s_ends + (size_t)w * S::kPart : work + (size_t)(blockIdx.x * kWarps + w) * S::kPart;
+        const float4 f = reinterpret_cast<const float4 *>(p + 2 * kHeads)[slot];
+        const float2 w2 = *reinterpret_cast<const float2 *>(&s_m[k][h]);
+        v.x = fmaf(f.x, w2.x, v.x);
+        v.y = fmaf(f.y, w2.y, v.y);
+        v.z = fmaf(f.z, w2.x, v.z);
+        v.w = fmaf(f.w, w2.y, v.w);
       }
-      if (open_at >> (2 * w + 1) & 1u) {
-        float *const p = s_open + (size_t)w * S::kPart;
-        add(reinterpret_cast<const float4 *>(p + 2 * kHeads)[slot], 2 * w + 1);
-        if (to != block_part0 || (began_at >> (2 * w + 1) & 1u)) to = p;
-      }
+      // an item that began and ends here: to its last open part's place
+      const bool here = (run & began_at) != 0u, ended = (run & ends_at) != 0u;
+      float *const to = !here ? block_part0 : ended ? s_open + (size_t)((31 - __clz(run & open_at)) / 2) * S::kPart : block_part1;
+      reinterpret_cast<float4 *>(to + 2 * kHeads)[slot] = v;
     }
-    if (last_open)
-      reinterpret_cast<float4 *>((last_part ? block_part1 : block_part0) + 2 * kHeads)[slot] = make_float4(v[0], v[1], v[2], v[3]);
   }
   __syncthreads();
-  for (uint32_t left = ends_at; left; left &= left - 1u) {  // items that warps shared and that began and ended here
+#pragma unroll 1
+  for (uint32_t left = ends_at; left && whole_parts; left &= left - 1u) {  // items that warps shared and that began and ended here
     const int k = __ffs(left) - 1;
-    const uint32_t run = run_of(k) & open_at;
-    if (run_of(k) & began_at)
-      write_out(s_parts[k / 2].seq, s_parts[k / 2].item, s_open + (size_t)((31 - __clz(run)) / 2) * S::kPart);
+    const uint32_t run = run_of(k);
+    if (run & began_at)
+      write_out(s_parts[k / 2].seq[0], s_parts[k / 2].item[0], s_open + (size_t)((31 - __clz(run & open_at)) / 2) * S::kPart);
   }
 
   // ---- the last block of an item joins the blocks' parts
-  if (first_part || last_part) {  // (the same for every thread)
+  if ((first_part || last_part) && whole_parts) {  // (the same for every thread)
+    at_fence_copies();
     __threadfence();
     __syncthreads();
-    // Of the item that a part is of: its first block, and how many have parts.
-    auto span = [&](unsigned at, int nt, int &from, int &count) {
-      auto of = [&](unsigned t) {
-        int b = (int)((float)t / (float)total * (float)blocks);
-        b = max(0, min(blocks - 1, b));
-        while (b + 1 < blocks && block_at(b + 1) <= t) ++b;
-        while (block_at(b) > t) --b;
-        return b;
-      };
-      from = of(at);
-      count = of(at + (unsigned)nt - 1) - from + 1;
-    };
-    int from[2] = {0, 0}, count[2] = {0, 0}, seq[2] = {0, 0}, item[2] = {0, 0};
-    if (first_part) {  // of the item open at the block's start: it ends in a warp, or is every warp's
-      int w = 0;
-      while (w < kWarps - 1 && !s_parts[w].ends) ++w;
-      if (s_parts[w].ends) {
-        AtCursor<kTile> it;
-        seq[0] = s_parts[w].seq;
-        item[0] = s_parts[w].item;
-        unsigned at = s_pre[seq[0] / chunk];
-        for (it.seq = seq[0] / chunk * chunk; it.seq < seq[0]; ++it.seq) {
-          it.load(a);
-          at += (unsigned)it.nt * items;
-        }
-        it.load(a);
-        span(at + (unsigned)it.nt * item[0], it.nt, from[0], count[0]);
-      } else {
-        while (!s_parts[w].open) --w;
-        seq[0] = s_parts[w].open_seq;
-        item[0] = s_parts[w].open_item;
-        span(s_parts[w].open_at, s_parts[w].open_nt, from[0], count[0]);
-      }
-    }
-    if (last_part) {
-      int w = kWarps - 1;
-      while (!s_parts[w].began || !s_parts[w].open) --w;
-      seq[1] = s_parts[w].open_seq;
-      item[1] = s_parts[w].open_item;
-      span(s_parts[w].open_at, s_parts[w].open_nt, from[1], count[1]);
-    }
+    const int first_k = 31 - __clz(first_run & all_at), last_k = 31 - __clz(last_run & all_at);  // a part that tells the item
     if (tid < 2) {
       s_last[tid] = 0;
       if (tid == 0 ? first_part : last_part) {
-        const int f = tid == 0 ? from[0] : from[1], need = tid == 0 ? count[0] : count[1];
-        if (atomicAdd(a.tickets + f, 1u) + 1u == (unsigned)need) {
+        const int k = tid == 0 ? first_k : last_k;
+        const AtWarpParts &p = s_parts[k / 2];
+        // the blocks of its first and its last tile: the largest b with total * b / blocks <= tile
+        auto of = [&](unsigned t) { return (int)((((unsigned long long)t + 1) * (unsigned)blocks - 1) / total); };
+        const int from = of(p.at[k & 1]), count = of(p.at[k & 1] + (unsigned)p.nt[k & 1] - 1) - from + 1;
+        s_from[tid] = from;
+        s_count[tid] = count;
+        if (atomicAdd(a.tickets + from, 1u) + 1u == (unsigned)count) {
           __threadfence();
-          a.tickets[f] = 0u;
+          a.tickets[from] = 0u;
           s_last[tid] = 1;
         }
       }
     }
     __syncthreads();
-    uint32_t turn = 0;
-    for (int k = 0; k < 2; ++k) {
-      if (!s_last[k]) continue;
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      if (!s_last[which]) continue;
       // Parts come to shared memory a room full at a time, by bulk copies, while their weights are worked out.
-      const int n_parts = count[k], f = from[k];
-      const uint32_t size = (uint32_t)(2 * kHeads + slots * 4) * 4;  // bytes of a part
-      float *const s_w = reinterpret_cast<float *>(sm), *const s_sums_of = s_w + n_parts * kHeads;  // maxima, then weights; sums
-      float *const s_sum = s_sums_of + n_parts * kHeads;                                                // 1 / sum
-      const uint32_t head = ((uint32_t)(2 * n_parts + 1) * kHeads * 4 + 127) & ~127u;
-      float *const s_room = reinterpret_cast<float *>(sm + head);
-      const int fit = min(n_parts, (int)((S::kRoom - head) / size));
+      const int n_parts = s_count[which], f = s_from[which];
+      float *const s_w = reinterpret_cast<float *>(sm), *const s_sum = s_w + n_parts * kHeads;  // weights, 1 / sums
+      const uint32_t head = ((uint32_t)(n_parts + 1) * kHeads * 4 + 127) & ~127u;
+      float *const s_out = reinterpret_cast<float *>(sm + head), *const s_room = s_out + size / 4;  // the sum; parts
+      const int fit = min(n_parts, (int)((S::kRoom - head) / size) - 1);
       auto part = [&](int b) { return block_parts + (size_t)(2 * (f + b) + (b == 0 ? 1 : 0)) * S::kPart; };
-      auto fetch = [&](int b0) {  // parts b0 .. b0 + fit
-        if (tid == 0) {
-          const int many = min(fit, n_parts - b0);
-          // what other blocks wrote, and this block read here, before the copies read and write
-          asm volatile("fence.proxy.async;" ::: "memory");
-          mbar_arrive_expect_tx(&s_join, (uint32_t)many * size);
-          for (int b = 0; b < many; ++b) bulk_g2s(s_room + (size_t)b * (size / 4), part(b0 + b), size, &s_join);
-        }
-      };
       __syncthreads();
-      fetch(0);
-      for (int i = tid; i < 2 * n_parts * kHeads; i += kThreads) {
-        const int b = i / (2 * kHeads), h = i % (2 * kHeads);
-        s_w[(h / kHeads * n_parts + b) * kHeads + h % kHeads] = __ldcg(part(b) + h);
-      }
-      __syncthreads();
-      for (int h = warp; h < kHeads; h += kWarps) {
-        float top = -INFINITY, sum = 0.f;
-        for (int b = lane; b < n_parts; b += 32) top = fmaxf(top, s_w[b * kHeads + h]);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float use = top == -INFINITY ? 0.f : top;
-        for (int b = lane; b < n_parts; b += 32) {
-          const float w = at_keep(s_w[b * kHeads + h], use);
-          s_w[b * kHeads + h] = w;
-          sum += w * s_sums_of[b * kHeads + h];
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) {
-          s_sum[h] = sum != 0.f ? 1.f / sum : 0.f;
-          write_lse(seq[k], item[k], h, top, sum);
-        }
-      }
-      __syncthreads();
-      constexpr int kMine = (kSteps * kN * 32 + kThreads - 1) / kThreads;  // slots of a thread
-      float v[kMine][4];
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0.f;
       bool ran_out = false;
+#pragma unroll 1
       for (int b0 = 0; b0 < n_parts && !ran_out; b0 += fit) {
+        const int many = min(fit, n_parts - b0);
+        if (warp == 0) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&s_join, (uint32_t)many * size);
+          }
+          __syncwarp();
+          for (int b = lane; b < many; b += 32) {
+            at_fence_copies();  // what other blocks wrote, and this one read here
+            bulk_g2s(s_room + (size_t)b * (size / 4), part(b0 + b), size, &s_join);
+          }
+        }
+        if (b0 == 0) {
+#pragma unroll 1
+          for (int h = warp; h < kHeads; h += kWarps) {
+            constexpr int kLane = kAtMaxGrid / 32;  // parts of a lane
+            float top = -INFINITY, sum = 0.f, m1[kLane], l1[kLane];
+#pragma unroll
+            for (int i = 0; i < kLane; ++i) {
+              const int b = lane + 32 * i;
+              m1[i] = b < n_parts ? __ldcg(part(b) + h) : -INFINITY;
+              l1[i] = b < n_parts ? __ldcg(part(b) + kHeads + h) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kLane; ++i) top = fmaxf(top, m1[i]);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float use = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int i = 0; i < kLane; ++i) {
+              const float w = at_keep(m1[i], use);
+              if (lane + 32 * i < n_parts) s_w[(lane + 32 * i) * kHeads + h] = w;
+              sum += w * l1[i];
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            if (lane == 0) {
+              const AtWarpParts &p = s_parts[(which ? last_k : first_k) / 2];
+              const int o = (which ? last_k : first_k) & 1;
+              s_sum[h] = sum != 0.f ? 1.f / sum : 0.f;
+              write_lse(p.seq[o], p.item[o], h, top, sum);
+            }
+          }
+        }
         ran_out = __syncthreads_or(!mbar_wait(&s_join, turn));
         turn ^= 1u;
-        const int many = ran_out ? 0 : min(fit, n_parts - b0);
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int slot = tid + i * kThreads, h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
-          if (slot >= slots) continue;
+#pragma unroll 1
+        for (int slot = tid; slot < slots && !ran_out; slot += kThreads) {
+          const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          float4 *const to = reinterpret_cast<float4 *>(s_out + 2 * kHeads) + slot;
+          if (b0) v = *to;
 #pragma unroll 4
           for (int b = 0; b < many; ++b) {
             const float4 p = reinterpret_cast<const float4 *>(s_room + (size_t)b * (size / 4) + 2 * kHeads)[slot];
             const float2 w = *reinterpret_cast<const float2 *>(s_w + (b0 + b) * kHeads + h);
-            v[i][0] = fmaf(p.x, w.x, v[i][0]);
-            v[i][1] = fmaf(p.y, w.y, v[i][1]);
-            v[i][2] = fmaf(p.z, w.x, v[i][2]);
-            v[i][3] = fmaf(p.w, w.y, v[i][3]);
+            v.x = fmaf(p.x, w.x, v.x);
+            v.y = fmaf(p.y, w.y, v.y);
+            v.z = fmaf(p.z, w.x, v.z);
+            v.w = fmaf(p.w, w.y, v.w);
           }
+          const float f0 = b0 + many < n_parts ? 1.f : s_sum[h], f1 = b0 + many < n_parts ? 1.f : s_sum[h + 1];
+          *to = make_float4(v.x * f0, v.y * f1, v.z * f0, v.w * f1);
         }
         __syncthreads();
-        if (b0 + fit < n_parts && !ran_out) fetch(b0 + fit);
       }
       if (ran_out) {
         if (tid == 0) set_error(a.err, kErrTimeout);
         break;
       }
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int slot = tid + i * kThreads, h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
-        if (slot >= slots) continue;
-        reinterpret_cast<float4 *>(s_room + 2 * kHeads)[slot] =
-            make_float4(v[i][0] * s_sum[h], v[i][1] * s_sum[h + 1], v[i][2] * s_sum[h], v[i][3] * s_sum[h + 1]);
-      }
-      __syncthreads();
-      write_out(seq[k], item[k], s_room);
+      const AtWarpParts &p = s_parts[(which ? last_k : first_k) / 2];
+      const int o = (which ? last_k : first_k) & 1;
+      write_out(p.seq[o], p.item[o], s_out);
     }
   }
 
@@ -965,8 +959,6 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   }
   if (a.trace && tid == 0) trace_max(a.trace, kTrExit);
 }
-
-constexpr int kAtMaxGrid = 192;
 
 template <bool kBits8, int kD, int kN>
 cudaError_t at_launch(const KvAttendArgs &a, int n_sm, cudaStream_t st, bool pdl) {

@@ -29,6 +29,7 @@ struct moe_handle {
   int qdense_clusters[moe::kQdenseMaxCluster + 1];  // clusters that fit the device, by their blocks
   bool logits_ready;          // and for the logits kernel
   bool attend_ready;          // and for the attention's
+  bool sample_ready;          // and for the sampling's
   bool prefill_dense;         // multi-token calls may run dense slots on the tensor cores (tcgen05)
   // failure-detection hook, consumed by the next fused single-token launch
   int skip_block_next;                  // -1: none
@@ -1122,6 +1123,10 @@ int moe_sample(moe_handle *h, const float *logits, size_t logits_stride, int n_r
   for (const void *p : p4)
     if (!aligned(p, 4)) return MOE_ERR_INVALID_ARG;
   if (!on_device(h)) return MOE_ERR_INVALID_ARG;
+  if (!h->sample_ready) {
+    if (moe::sample_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    h->sample_ready = true;
+  }
   moe::SampleArgs a;
   a.logits = logits;
   a.ld = logits_stride;

@@ -333,9 +333,11 @@ struct SampleArgs {
   int32_t *tokens;            // [T]
   float *logprobs;            // nullable [T]
   int T, V;
+  int cluster, per;           // blocks of a row, tokens of a block (set by the launcher)
   unsigned *err;
   unsigned long long *trace;
 };
+cudaError_t sample_set_attributes();
 cudaError_t launch_sample(const SampleArgs &a, int n_sm, cudaStream_t st, bool pdl);
 
 // smem budgets (bytes) for a given shape; 0 = shape not supported by that kernel

@@ -3,10 +3,28 @@
 //
 // The three filters keep a first part of the tokens in the order of their logits
 // (the lower id first of equal ones), so what remains is told by one key: the
-// logit as an ordered integer, then the complement of the id.  The key is found
-// bit by bit, a count and a sum over the row for each; the token by bisection
-// over the ids.  Sums are of weights in fixed point, 64 bits: whatever their
-// order they are the same, and to 2^-34 of a weight or better.
+// logit as an ordered integer, then the complement of the id.  Nothing is sorted;
+// the key is found by histograms, and the token by a running sum over the ids.
+//
+// A cluster of up to 16 blocks has a row, each block a run of its tokens in
+// shared memory, so that every logit is read once.  While the logits land every
+// thread takes the maximum of its own; from these maxima alone follow bounds
+// below which no token can remain:
+//   top-k:  some block has k threads with a maximum above a value, or every block
+//           has k / blocks such threads: k tokens lie above it;
+//   top-p:  the tokens of less than (1 - p) S / V each have less than (1 - p) S
+//           together, for S any lower bound of the sum (here of the maxima).
+// The tokens above the bound are few: for a small k they go to the first block's
+// list at once, else a histogram of their distance to the maximum (512 bins, a
+// count and a sum each, refined by 9 bits where needed) says in which bin the cut
+// falls, and a list takes what lies above its lower end, or in the bin alone.
+// What is in a list is ranked by comparing all pairs.  Where a bin cannot be
+// refined (many equal logits) the key is found bit by bit.
+//
+// Weights e^((l - M) / T) are summed in fixed point, 64 bits: any order gives the
+// same sums, to 2^-34 of a weight of 1 or better.  A weight is within 2^-21 of its
+// value: the argument's rounding errors are carried along (a difference's and a
+// product's), what is left is the exponential's.
 #include <math.h>
 
 #include "kernels.h"
@@ -14,133 +32,689 @@
 namespace moe {
 
 namespace {
-constexpr int kSmThreads = 1024;
+typedef unsigned long long u64;
+constexpr int kSmThreads = 512, kSmWarps = kSmThreads / 32;
+constexpr int kSmCluster = 16;       // blocks of a row, at most
+constexpr int kSmSeg = 16384;        // tokens of a block that leave room for another block on the SM
+constexpr int kSmSegMax = 49152;     // that fit shared memory at all; rows of more are read again in every pass
+constexpr int kSmChunk = 4096;       // tokens of a bulk copy
+constexpr int kSmBins = kSmThreads;  // a thread per bin
+constexpr int kSmBits = 27;          // of a token's distance to the maximum: three times 9
+constexpr int kSmList = kSmThreads;  // a thread per token of the list
 
-// Orders floats above -inf as unsigned integers (both zeros the same), 0 for what does not count.
+// Orders floats above -inf as unsigned integers (both zeros the same); 0 for -inf.
 __device__ __forceinline__ unsigned sm_key(float f) {
-  if (!(f < INFINITY) || f == -INFINITY) return 0u;
+  if (f == -INFINITY) return 0u;
   const unsigned u = __float_as_uint(f + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-
 __device__ __forceinline__ float sm_value(unsigned k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
+__device__ __forceinline__ u64 sm_full(float f, int id) { return ((u64)sm_key(f) << 32) | (0xFFFFFFFFu - (unsigned)id); }
+__device__ __forceinline__ int sm_id(u64 k) { return (int)(0xFFFFFFFFu - (unsigned)k); }
 
-__device__ unsigned long long sm_sum(unsigned long long v) {
-  __shared__ unsigned long long s[33];
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    unsigned long long t = 0;
-    for (int i = 0; i < kSmThreads / 32; ++i) t += s[i];
-    s[32] = t;
-  }
-  __syncthreads();
-  return s[32];
+// ---- the other blocks' shared memory
+__device__ __forceinline__ uint32_t sm_far(const void *p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void sm_put(uint32_t at, u64 v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory"); }
+__device__ __forceinline__ void sm_put(uint32_t at, unsigned v) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
+__device__ __forceinline__ void sm_put(uint32_t at, float v) { sm_put(at, __float_as_uint(v)); }
+__device__ __forceinline__ unsigned sm_get(uint32_t at) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ u64 sm_get64(uint32_t at) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned sm_count(uint32_t at, unsigned n) {
+  unsigned v;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(v) : "r"(at), "r"(n) : "memory");
+  return v;
+}
+// Every thread of the cluster's blocks, which run at the same time.
+__device__ __forceinline__ void sm_meet() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kSmThreads) sample_kernel(const SampleArgs a) {
-  __shared__ unsigned long long s_best;
-  const int tid = threadIdx.x, row = blockIdx.x;
-  const bool tracer = a.trace && row == 0 && tid == 0;
+struct SmWeight {
+  float top, c, c_lo, one;  // the maximum; log2(e) / temperature in two parts; the unit
+  __device__ __forceinline__ u64 operator()(float l) const {
+    const float d = l - top, y = d * c;
+    if (!(y > -70.f)) return 0;
+    const float b = d - l, e = (l - (d - b)) + (-top - b);        // what the difference lost
+    const float lo = fmaf(d, c, -y) + fmaf(d, c_lo, e * c);       // and the product
+    float w;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(w) : "f"(y));
+    return __float2ull_rn(fmaf(w, lo * 0.69314718f, w) * one);
+  }
+};
+
+__device__ __forceinline__ u64 sm_warp_sum(u64 v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ u64 sm_warp_scan(u64 v, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off *= 2) {
+    const u64 o = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += o;
+  }
+  return v;
+}
+
+// What a block tells the others of its tokens.
+struct SmTold {
+  float top, least, cut_all, cut_part, sum, bad;
+};
+// What the first block tells all.
+struct SmCut {
+  u64 above, mass;    // tokens above the bin, and their sum
+  u64 in, in_mass;    // in it
+  u64 all;            // sum of what remained before this cut
+  unsigned bin;
+};
+
+// kHeld: the block's tokens lie in shared memory.
+template <bool kHeld>
+__global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const SampleArgs a) {
+  extern __shared__ __align__(16) float seg[];
+  __shared__ u64 s_mass[kSmBins], s_list[kSmList], s_weight[kSmList], s_warp[kSmWarps], s_far[kSmCluster], s_one[4];
+  __shared__ unsigned s_cnt[kSmBins], s_n;
+  __shared__ uint64_t s_bar[(kSmSegMax + kSmChunk) / kSmChunk + 1];
+  __shared__ float s_red[3][kSmWarps];
+  __shared__ SmTold s_told[kSmCluster];
+  __shared__ SmCut s_cut;
+  __shared__ double s_least;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = a.cluster, row = blockIdx.x / C, rank = blockIdx.x % C, V = a.V;
+  const bool tracer = a.trace && blockIdx.x == 0 && tid == 0;
   if (tracer) trace_min(a.trace, kTrEntry);
-  if (tid == 0) s_best = 0;
+  const int per = a.per, n = max(0, min(per, V - rank * per));  // (per: a multiple of 4)
+  const float *const from = a.logits + (size_t)row * a.ld + (size_t)rank * per;
+  // Place j of the run is token j - skew, so that places of four are 16 bytes in memory as well.
+  const int skew = (int)((reinterpret_cast<uintptr_t>(from) >> 2) & 3), id0 = rank * per - skew;
+  const int places = (skew + n + 3) & ~3, quads = n > 0 ? places / 4 : 0;
+  const int in0 = skew ? 4 : 0, in1 = (skew + n) & ~3;  // whole fours
+  const int chunks = kHeld && in1 > in0 ? (in1 + kSmChunk - 1) / kSmChunk : 0;
+  if (tid < chunks) mbar_init(&s_bar[tid], 1);
+  fence_mbar_init();
+  s_cnt[tid] = 0u;
+  s_mass[tid] = 0;
+  if (tid == 0) s_n = 0u;
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
   if (tracer) trace_min(a.trace, kTrWaited);
-  const float *l = a.logits + (size_t)row * a.ld;
-  const float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
-  __syncthreads();
-  unsigned long long best = 0;
-  bool bad = false;
-  for (int i = tid; i < a.V; i += kSmThreads) {
-    const unsigned k = sm_key(l[i]);
-    bad |= !(l[i] < INFINITY);
-    if (k) best = max(best, ((unsigned long long)k << 32) | (0xFFFFFFFFu - (unsigned)i));
+  if (kHeld && tid < chunks) {
+    const int j0 = max(in0, tid * kSmChunk), j1 = min(in1, (tid + 1) * kSmChunk);
+    mbar_arrive_expect_tx(&s_bar[tid], (uint32_t)(j1 - j0) * 4);
+    bulk_g2s(seg + j0, from + (j0 - skew), (uint32_t)(j1 - j0) * 4, &s_bar[tid]);
   }
-  atomicMax(&s_best, best);
+  if (kHeld && tid >= 32 && tid < 40 && n > 0) {  // the places at the ends that are not whole fours
+    const int j = tid < 36 ? tid - 32 : places - 4 + tid - 36;
+    if (j < in0 || j >= in1) seg[j] = j >= skew && j < skew + n ? __ldcg(from + (j - skew)) : -INFINITY;
+  }
+  // the row's filters; a greedy row is one of top-k 1
+  const float temp0 = a.temperature ? __ldg(a.temperature + row) : 1.f;
+  const bool greedy = !(temp0 > 0.f);
+  const float temp = greedy ? 1.f : temp0, given = __ldg(a.uniform + row);
+  const float min_p = a.min_p ? fminf(__ldg(a.min_p + row), 1.f) : 0.f;
+  const float top_p0 = a.top_p ? __ldg(a.top_p + row) : 1.f;
+  int top_k = a.top_k ? __ldg(a.top_k + row) : 0;
+  if (greedy || top_p0 <= 0.f) top_k = 1;
+  if (top_k <= 0 || top_k >= V) top_k = 0;
+  const bool cut_p = top_p0 < 1.f && top_p0 > 0.f;
+  const bool has_min = (a.min_p ? __ldg(a.min_p + row) : 0.f) > 0.f;
+  const double top_p = (double)top_p0, u = given > 0.f ? (double)given : 0.0;
+  if (tid == 64) s_least = has_min ? (double)temp * log((double)min_p) : 0.0;
+  const double slope = fmin(1.4426950408889634 / (double)temp, 3.0e38);
+  SmWeight weight;
+  weight.c = (float)slope;
+  weight.c_lo = (float)(slope - (double)weight.c);
+  weight.one = (float)(1ull << (__clz(V) + 31));  // V weights of 1 stay below 2^63
+  __syncthreads();
+
+  auto quad = [&](int i) {  // four places
+    if (kHeld) return reinterpret_cast<const float4 *>(seg)[i];
+    const int j = 4 * i;
+    float4 f;
+    if (j >= in0 && j < in1) {
+      f = __ldcg(reinterpret_cast<const float4 *>(from + (j - skew)));
+    } else {
+      f.x = j >= skew && j < skew + n ? __ldcg(from + (j - skew)) : -INFINITY;
+      f.y = j + 1 >= skew && j + 1 < skew + n ? __ldcg(from + (j + 1 - skew)) : -INFINITY;
+      f.z = j + 2 >= skew && j + 2 < skew + n ? __ldcg(from + (j + 2 - skew)) : -INFINITY;
+      f.w = j + 3 >= skew && j + 3 < skew + n ? __ldcg(from + (j + 3 - skew)) : -INFINITY;
+    }
+    f.x = f.x < INFINITY ? f.x : -INFINITY;
+    f.y = f.y < INFINITY ? f.y : -INFINITY;
+    f.z = f.z < INFINITY ? f.z : -INFINITY;
+    f.w = f.w < INFINITY ? f.w : -INFINITY;
+    return f;
+  };
+
+  // ---- the block's largest and least logit, its threads' maxima
+  float mine = -INFINITY, least = INFINITY;
+  bool bad = false, late = false;
+  auto take = [&](float4 f, int i) {
+    float *v = &f.x;
+    float t = -INFINITY;
+    bool odd = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool fine = v[k] < INFINITY;  // NaN and +inf are not for the token
+      odd = odd || !fine;
+      v[k] = fine ? v[k] : -INFINITY;
+      t = fmaxf(t, v[k]);
+      least = fminf(least, v[k] > -INFINITY ? v[k] : INFINITY);
+    }
+    mine = fmaxf(mine, t);
+    if (odd) {
+      bad = true;
+      if (kHeld) reinterpret_cast<float4 *>(seg)[i] = f;
+    }
+  };
+  if (kHeld) {
+    for (int q = 0; q < max(chunks, 1); ++q) {
+      if (q < chunks) late = late || !mbar_wait(&s_bar[q], 0);
+      for (int i = q * (kSmChunk / 4) + tid; i < min(quads, (q + 1 < chunks ? q + 1 : 1 << 20) * (kSmChunk / 4)); i += kSmThreads)
+        take(reinterpret_cast<const float4 *>(seg)[i], i);
+    }
+  } else {
+    for (int i = tid; i < quads; i += kSmThreads) {
+      const int j = 4 * i;
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = j + k >= skew && j + k < skew + n ? __ldcg(from + (j + k - skew)) : -INFINITY;
+      take(make_float4(v[0], v[1], v[2], v[3]), i);
+    }
+  }
   if (bad) set_error(a.err, kErrNonFinite);
+  if (late) set_error(a.err, kErrTimeout);
+  auto block_max = [&](float v, int k) {  // of one value per thread; k: its place
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    if (lane == 0) s_red[k][warp] = v;
+  };
+  auto of_warps = [&](int k) {
+    float v = s_red[k][lane & (kSmWarps - 1)];
+#pragma unroll
+    for (int off = kSmWarps / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+  };
+  block_max(mine, 0);
+  block_max(-least, 1);
+  block_max(mine > -INFINITY ? -mine : -INFINITY, 2);
   __syncthreads();
-  best = s_best;
-  int token = best ? (int)(0xFFFFFFFFu - (unsigned)best) : -1;
-  float logprob = best ? 0.f : -INFINITY;
-  if (best && temp > 0.f) {
-    const float top = sm_value((unsigned)(best >> 32));
-    const double inv = fmin(1.0 / (double)temp, 1e300);
-    const double one = (double)(1ull << (__clz(a.V) + 31));  // V weights of 1 stay below 2^63
-    auto weight = [&](float f) { return (unsigned long long)__double2ll_rn(exp(((double)f - (double)top) * inv) * one); };
-    // full keys; those from `low` on remain
-    auto key = [&](int i) {
-      const unsigned k = sm_key(l[i]);
-      return k ? ((unsigned long long)k << 32) | (0xFFFFFFFFu - (unsigned)i) : 0ull;
-    };
-    unsigned long long low = 1;
-    const float mp = a.min_p ? __ldg(a.min_p + row) : 0.f;
-    if (mp > 0.f) {
-      const double least = (double)temp * log((double)fminf(mp, 1.f));
-      unsigned long long k = ~0ull;
-      for (int i = tid; i < a.V; i += kSmThreads)
-        if (key(i) && (double)l[i] - (double)top >= least) k = min(k, key(i));
-      for (int off = 16; off > 0; off >>= 1) k = min(k, __shfl_xor_sync(0xffffffffu, k, off));
-      __shared__ unsigned long long s_low;
-      if (tid == 0) s_low = ~0ull;
+  const float block_top = of_warps(0), low_max = -of_warps(2);  // (of the threads that have a token)
+  {
+    SmTold told = {block_top, -of_warps(1), -INFINITY, -INFINITY, 0.f, 0.f};
+    const float wide = block_top - low_max;
+    if (top_k > 0 && block_top > -INFINITY && wide < 1e37f) {
+      // a histogram of the threads' maxima: the values that k, or k / C, of them reach
+      const float f = wide > 0.f ? fminf((kSmBins - 1) / wide, 1e30f) : 0.f;
+      if (mine > -INFINITY) atomicAdd(&s_cnt[min(kSmBins - 1, (int)((block_top - mine) * f))], 1u);
       __syncthreads();
-      if ((tid & 31) == 0) atomicMin(&s_low, k);
-      __syncthreads();
-      low = s_low;
-    }
-    const int top_k = a.top_k ? __ldg(a.top_k + row) : 0;
-    auto find = [&](auto enough) {  // the largest key whose tokens from it on are enough
-      unsigned long long k = 0;
-      for (int b = 63; b >= 0; --b) {
-        const unsigned long long t = k | (1ull << b);
-        if (t <= low || enough(t)) k = t;
+      unsigned run = s_cnt[tid];
+#pragma unroll
+      for (int off = 1; off < 32; off *= 2) {
+        const unsigned o = __shfl_up_sync(0xffffffffu, run, off);
+        if (lane >= off) run += o;
       }
-      return max(k, low);
-    };
-    if (top_k > 0)
-      low = find([&](unsigned long long t) {
-        unsigned long long n = 0;
-        for (int i = tid; i < a.V; i += kSmThreads) n += key(i) >= t;
-        return sm_sum(n) >= (unsigned long long)top_k;
-      });
-    auto mass = [&](unsigned long long t, int ids) {
-      unsigned long long n = 0;
-      for (int i = tid; i < ids; i += kSmThreads)
-        if (key(i) >= t) n += weight(l[i]);
-      return sm_sum(n);
-    };
-    const float p = a.top_p ? __ldg(a.top_p + row) : 1.f;
-    if (p < 1.f) {
-      const double share = (double)p * (double)mass(low, a.V);
-      low = find([&](unsigned long long t) { return t <= best && (double)mass(t, a.V) >= share; });
+      if (lane == 31) s_warp[warp] = run;
+      __syncthreads();
+      const unsigned own = s_cnt[tid];
+      for (int w = 0; w < warp; ++w) run += (unsigned)s_warp[w];
+      // a bin's lower end, and what fp32 may have moved
+      const float edge = f > 0.f ? block_top - (tid + 1.01f) / f - 1e-6f * (fabsf(block_top) + wide) : block_top;
+      const unsigned part = (unsigned)((top_k + C - 1) / C);
+      if (run >= (unsigned)top_k && run - own < (unsigned)top_k) s_one[0] = __float_as_uint(edge);
+      if (run >= part && run - own < part) s_one[1] = __float_as_uint(edge);
+      if (tid == kSmThreads - 1) s_one[2] = run;
+      __syncthreads();
+      if (s_one[2] >= (unsigned)top_k) told.cut_all = __uint_as_float((unsigned)s_one[0]);
+      if (s_one[2] >= part) told.cut_part = __uint_as_float((unsigned)s_one[1]);
+      s_cnt[tid] = 0u;
+    } else if (cut_p) {
+      float e = mine > -INFINITY ? exp2f((mine - block_top) * weight.c) : 0.f;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
+      __syncthreads();
+      if (lane == 0) s_red[0][warp] = e;
+      __syncthreads();
+      for (int w = 0; w < kSmWarps; ++w) told.sum += s_red[0][w];
     }
-    const float given = __ldg(a.uniform + row);
-    const double u = given > 0.f ? (double)given : 0.0, all = (double)mass(low, a.V), goal = u * all;
-    int from = 0, to = a.V;  // the running sum is above the goal at `to` ids, not at `from`
-    while (to - from > 1) {
-      const int mid = from + (to - from) / 2;
-      if ((double)mass(low, mid) > goal || (u >= 1.0 && mass(low, mid) == mass(low, a.V)))
-        to = mid;
-      else
-        from = mid;
+    if (tid < C) {
+      const uint32_t to = sm_far(&s_told[rank], tid);
+      sm_put(to, told.top);
+      sm_put(to + 4, told.least);
+      sm_put(to + 8, told.cut_all);
+      sm_put(to + 12, told.cut_part);
+      sm_put(to + 16, told.sum);
     }
-    token = to - 1;
-    logprob = (float)(((double)l[token] - (double)top) * inv - log(all / one));
   }
-  if (tid == 0) {
-    a.tokens[row] = token;
-    if (a.logprobs) a.logprobs[row] = logprob;
-    if (a.trace) trace_max(a.trace, kTrExit);
+  sm_meet();
+  // ---- what every block knows now
+  float top = -INFINITY, bottom = INFINITY, cut_all = -INFINITY, cut_part = INFINITY, sum = 0.f;
+  for (int r = 0; r < C; ++r) {
+    top = fmaxf(top, s_told[r].top);
+    bottom = fminf(bottom, s_told[r].least);
+    cut_all = fmaxf(cut_all, s_told[r].cut_all);
+    cut_part = fminf(cut_part, s_told[r].cut_part);
   }
+  if (top == -INFINITY) {
+    if (rank == 0 && tid == 0) {
+      a.tokens[row] = -1;
+      if (a.logprobs) a.logprobs[row] = -INFINITY;
+      if (a.trace) trace_max(a.trace, kTrExit);
+    }
+    return;
+  }
+  for (int r = 0; r < C && !has_min; ++r)
+    if (s_told[r].top > -INFINITY) sum += s_told[r].sum * exp2f((s_told[r].top - top) * weight.c);
+  if (has_min) sum = 1.f;  // (maxima below min-p do not count: the largest does)
+  weight.top = top;
+  // min-p: the least logit with l - top >= temperature * ln(min_p), in 64 bits
+  float low = bottom;
+  if (has_min) {
+    float f = (float)((double)top + s_least);
+    f = (double)f - (double)top >= s_least ? f : nextafterf(f, INFINITY);
+    const float g = nextafterf(f, -INFINITY);
+    f = (double)g - (double)top >= s_least ? g : f;
+    low = fmaxf(low, f);
+  }
+  const uint32_t first_n = sm_far(&s_n, 0), first_list = sm_far(s_list, 0);
+
+  auto write = [&](u64 key, u64 all) {  // one thread
+    const float l = sm_value((unsigned)(key >> 32));
+    a.tokens[row] = sm_id(key);
+    if (a.logprobs)
+      a.logprobs[row] = greedy ? 0.f : (float)(((double)l - (double)top) / (double)temp - log((double)all / (double)weight.one));
+  };
+  // The running sum that the token's has to reach.
+  auto goal_of = [&](u64 all) {
+    const double g = u * (double)all;
+    return u >= 1.0 || g >= (double)all ? all : min(all, (u64)g + 1);
+  };
+  // The tokens that `yes` names go to the first block's list, as far as it reaches; s_n there counts them.
+  auto gather = [&](auto yes) {
+    for (int i = tid; i - lane < quads; i += kSmThreads) {
+      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (i < quads) f = quad(i);
+      const float v[4] = {f.x, f.y, f.z, f.w};
+      bool is[4];
+      int many = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        is[k] = v[k] >= low && v[k] > -INFINITY && yes(v[k], id0 + 4 * i + k);
+        many += is[k];
+      }
+      if (__any_sync(0xffffffffu, many > 0) && many > 0) {
+        unsigned at = sm_count(first_n, (unsigned)many);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (is[k]) {
+            if (at < (unsigned)kSmList) sm_put(first_list + 8 * at, sm_full(v[k], id0 + 4 * i + k));
+            ++at;
+          }
+      }
+    }
+  };
+  // Over the block: the sum of one value per thread.
+  auto block_sum = [&](u64 v) {
+    v = sm_warp_sum(v);
+    __syncthreads();
+    if (lane == 0) s_warp[warp] = v;
+    __syncthreads();
+    u64 t = 0;
+#pragma unroll
+    for (int w = 0; w < kSmWarps; ++w) t += s_warp[w];
+    return t;
+  };
+  // The first block alone: the list has every token that may remain.
+  auto finish = [&](int count, int k, u64 all) {
+    const u64 key = tid < count ? s_list[tid] : 0, w = tid < count ? weight(sm_value((unsigned)(key >> 32))) : 0;
+    s_weight[tid] = w;
+    if (tid == 0) s_one[3] = ~0ull;
+    __syncthreads();
+    u64 upto = 0;
+    int place = 0;
+    if (tid < count) {
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) {
+        const bool is = s_list[i] >= key;
+        place += is;
+        upto += is ? s_weight[i] : 0;
+      }
+    }
+    bool stays = tid < count && (k == 0 || place <= k);
+    if (k > 0) all = block_sum(stays ? w : 0);
+    if (cut_p) stays = stays && (place == 1 || (double)(upto - w) < top_p * (double)all);
+    all = block_sum(stays ? w : 0);
+    __syncthreads();
+    s_weight[tid] = stays ? w : 0;
+    __syncthreads();
+    const u64 goal = goal_of(all);
+    if (stays) {
+      u64 run = 0;
+#pragma unroll 4
+      for (int i = 0; i < count; ++i) run += (unsigned)s_list[i] >= (unsigned)key ? s_weight[i] : 0;  // (a lower id: a larger complement)
+      if (run >= goal) atomicMin(&s_one[3], (u64)(unsigned)sm_id(key));
+    }
+    __syncthreads();
+    if (stays && (u64)(unsigned)sm_id(key) == s_one[3]) write(key, all);
+  };
+
+  u64 tau = (u64)sm_key(low) << 32;  // what remains: keys from here on
+  bool done = false;
+  // ---- a small k: every token above the bound to the first block
+  float cut_k = fmaxf(low, top_k > 0 ? fmaxf(cut_all, cut_part == INFINITY ? -INFINITY : cut_part) : low);
+  if (top_k > 0 && top_k <= kSmList / 4) {
+    gather([&](float v, int) { return v >= cut_k; });
+    sm_meet();
+    const unsigned count = sm_get(first_n);
+    if (count <= (unsigned)kSmList) {
+      // the other blocks are done; the first stays while they may look into its memory
+      asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+      if (rank != 0) return;
+      finish((int)count, top_k, 0);
+      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+      if (tid == 0 && a.trace) trace_max(a.trace, kTrExit);
+      return;
+    }
+    sm_meet();
+    if (tid == 0) s_n = 0u;
+    sm_meet();
+  }
+
+  // Sum over the cluster; every thread of every block calls it.
+  auto cluster_sum = [&](u64 v) {
+    const u64 t = block_sum(v);
+    if (tid < C) sm_put(sm_far(&s_far[rank], tid), t);
+    sm_meet();
+    u64 all = 0;
+    for (int r = 0; r < C; ++r) all += s_far[r];
+    sm_meet();
+    return all;
+  };
+
+  // ---- the cuts, one after the other
+  u64 all = 0;  // sum of what remains, where known
+  bool known = false;
+#pragma unroll 1
+  for (int stage = 0; stage < 2 && !done; ++stage) {
+    const bool by_count = stage == 0;
+    if (by_count ? top_k == 0 : !cut_p) continue;
+    // the bound below which nothing remains
+    float cut = low;
+    if (by_count) {
+      cut = cut_k;
+    } else if (known) {
+      cut = fmaxf(low, sm_value((unsigned)(tau >> 32)));
+    } else {
+      const float least_w = (float)((1.0 - top_p) * 0.99 * (double)sum / (double)V);
+      const float f = top + (log2f(least_w) - 0.01f) / weight.c;
+      if (f < top) cut = fmaxf(low, f - 1e-6f * (fabsf(top) + fabsf(f)));
+    }
+    const float wide = top - cut, scale = wide > 0.f ? fminf((float)((1 << kSmBits) - 256) / wide, 3e38f) : 0.f;
+    auto far_of = [&](float v) { return (unsigned)fminf((top - v) * scale, (float)((1 << kSmBits) - 1)); };
+    unsigned prefix = 0;
+    double need = by_count ? (double)top_k : known ? top_p * (double)all : 0.0;
+    u64 above = 0, above_mass = 0;  // what lies above the bin at hand
+    bool found = false;
+#pragma unroll 1
+    for (int level = 1; level <= 3 && !found; ++level) {
+      const int shift = kSmBits - 9 * level;
+      u64 rest = 0;
+      for (int i = tid; i < quads; i += kSmThreads) {
+        const float4 f = quad(i);
+        const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (!(v[k] >= low) || v[k] == -INFINITY) continue;
+          if (v[k] >= cut) {
+            const unsigned y = far_of(v[k]) >> shift;
+            if (y >> 9 == prefix && sm_full(v[k], id0 + 4 * i + k) >= tau) {
+              const u64 w = weight(v[k]);
+              atomicAdd(&s_cnt[y & 511u], 1u);
+              if (w) atomicAdd(&s_mass[y & 511u], w);
+            }
+          } else if (!by_count && !known && level == 1) {
+            rest += weight(v[k]);
+          }
+        }
+      }
+      rest = block_sum(rest);
+      if (tid == 0) sm_put(sm_far(&s_far[rank], 0), rest);
+      sm_meet();
+      if (rank == 0) {  // the bin in which the cut falls
+        u64 cnt = 0, mass = 0, tail = 0;
+#pragma unroll 4
+        for (int r = 0; r < C; ++r) {
+          cnt += sm_get(sm_far(&s_cnt[tid], r));
+          mass += sm_get64(sm_far(&s_mass[tid], r));
+        }
+        for (int r = 0; r < C; ++r) tail += s_far[r];
+        u64 cr = sm_warp_scan(cnt, lane), mr = sm_warp_scan(mass, lane);
+        __syncthreads();
+        if (lane == 31) {
+          s_warp[warp] = mr;
+          s_list[warp] = cr;
+        }
+        __syncthreads();
+        u64 whole_m = 0, whole_c = 0;
+        for (int w = 0; w < kSmWarps; ++w) {
+          if (w == warp) {
+            mr += whole_m;
+            cr += whole_c;
+          }
+          whole_m += s_warp[w];
+          whole_c += s_list[w];
+        }
+        // (at w == warp the sums of the warps before were added)
+        const u64 total = !by_count && !known && level == 1 ? whole_m + tail : all;
+        const double want = by_count ? need : (level == 1 && !known ? top_p * (double)total : need);
+        const bool reached = by_count ? (double)(above + cr) >= want : (double)(above_mass + mr) >= want;
+        const bool before = by_count ? (double)(above + cr - cnt) >= want : (double)(above_mass + mr - mass) >= want;
+        if ((reached && !before) || (tid == kSmThreads - 1 && !reached)) {
+          for (int r = 0; r < C; ++r) {
+            const uint32_t to = sm_far(&s_cut, r);
+            sm_put(to, above + cr - cnt);
+            sm_put(to + 8, above_mass + mr - mass);
+            sm_put(to + 16, cnt);
+            sm_put(to + 24, mass);
+            sm_put(to + 32, total);
+            sm_put(to + 40, (unsigned)tid);
+          }
+        }
+      }
+      sm_meet();
+      above = s_cut.above;
+      above_mass = s_cut.mass;
+      if (!by_count && !known) {
+        all = s_cut.all;
+        known = true;
+        need = top_p * (double)all;
+      }
+      prefix = prefix << 9 | s_cut.bin;
+      const u64 in = s_cut.in;
+      s_cnt[tid] = 0u;
+      s_mass[tid] = 0;
+      __syncthreads();
+      if (above + in <= (u64)kSmList && (!by_count || top_k > 0)) {  // all that may remain fits the list
+        gather([&](float v, int id) { return v >= cut && far_of(v) >> shift <= prefix && sm_full(v, id) >= tau; });
+        sm_meet();
+        if (rank == 0) finish((int)(above + in), by_count ? top_k : 0, all);
+        done = found = true;
+      } else if (in <= (u64)kSmList) {
+        gather([&](float v, int id) { return v >= cut && far_of(v) >> shift == prefix && sm_full(v, id) >= tau; });
+        sm_meet();
+        if (rank == 0) {
+          const u64 key = tid < (int)in ? s_list[tid] : 0, w = tid < (int)in ? weight(sm_value((unsigned)(key >> 32))) : 0;
+          s_weight[tid] = w;
+          __syncthreads();
+          u64 upto = 0;
+          u64 place = 0;
+          if (tid < (int)in)
+            for (int i = 0; i < (int)in; ++i) {
+              const bool is = s_list[i] >= key;
+              place += is;
+              upto += is ? s_weight[i] : 0;
+            }
+          // the last that stays: the place k, or the one whose sum reaches the share
+          const bool last = tid < (int)in && (by_count ? above + place == (u64)top_k
+                                                       : (double)(above_mass + upto) >= need && (double)(above_mass + upto - w) < need);
+          // (none reaches it where the share is the whole sum to fp64's last bit: then the least key stays)
+          const bool none = __syncthreads_or(last) == 0;
+          if (last || (none && tid < (int)in && place == in)) {
+            for (int r = 0; r < C; ++r) {
+              const uint32_t to = sm_far(&s_cut, r);
+              sm_put(to, key);
+              sm_put(to + 8, above_mass + upto);
+            }
+          }
+          if (tid == 0) s_n = 0u;
+        }
+        sm_meet();
+        tau = s_cut.above;
+        if (by_count) {
+          all = s_cut.mass;
+          known = true;
+        }
+        found = true;
+        sm_meet();
+      }
+    }
+    if (!found) {  // many equal logits: the largest key from which on there is enough, bit by bit
+      u64 k = 0;
+#pragma unroll 1
+      for (int b = 63; b >= 0; --b) {
+        const u64 t = k | (1ull << b);
+        u64 part = 0;
+        if (t > tau) {  // (else everything that remains lies above it, which is enough)
+          for (int i = tid; i < quads; i += kSmThreads) {
+            const float4 f = quad(i);
+            const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (v[j] > -INFINITY && sm_full(v[j], id0 + 4 * i + j) >= t) part += by_count ? 1 : weight(v[j]);
+          }
+          if ((double)cluster_sum(part) >= need) k = t;
+        } else {
+          k = t;
+        }
+      }
+      tau = max(tau, k);
+      if (by_count) {
+        u64 part = 0;
+        for (int i = tid; i < quads; i += kSmThreads) {
+          const float4 f = quad(i);
+          const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (v[j] > -INFINITY && sm_full(v[j], id0 + 4 * i + j) >= tau) part += weight(v[j]);
+        }
+        all = cluster_sum(part);
+        known = true;
+      }
+    }
+  }
+
+  // ---- the token: running sums over blocks, warps, lanes
+  if (!done) {
+    const float tau_v = sm_value((unsigned)(tau >> 32));
+    const int q0 = (int)((long long)quads * warp / kSmWarps), q1 = (int)((long long)quads * (warp + 1) / kSmWarps);
+    auto kept = [&](float v, int id) -> u64 {
+      return v >= tau_v && v > -INFINITY && sm_full(v, id) >= tau ? weight(v) : 0;
+    };
+    u64 part = 0;
+    for (int i = q0 + lane; i < q1; i += 32) {
+      const float4 f = quad(i);
+      const int id = id0 + 4 * i;
+      part += kept(f.x, id) + kept(f.y, id + 1) + kept(f.z, id + 2) + kept(f.w, id + 3);
+    }
+    const u64 own = block_sum(part);
+    if (tid < C) sm_put(sm_far(&s_far[rank], tid), own);
+    sm_meet();
+    u64 before = 0, whole = 0;
+    for (int r = 0; r < C; ++r) {
+      if (r < rank) before += s_far[r];
+      whole += s_far[r];
+    }
+    const u64 goal = goal_of(whole);
+    if (before < goal && before + own >= goal) {  // it is this block's
+      int w = 0;
+      while (w < kSmWarps - 1 && before + s_warp[w] < goal) before += s_warp[w++];
+      if (warp == w) {
+        bool seen = false;
+        for (int i0 = q0; i0 < q1 && !seen; i0 += 32) {
+          float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          if (i0 + lane < q1) f = quad(i0 + lane);
+          const int id = id0 + 4 * (i0 + lane);
+          const u64 w4[4] = {kept(f.x, id), kept(f.y, id + 1), kept(f.z, id + 2), kept(f.w, id + 3)};
+          const u64 mine4 = w4[0] + w4[1] + w4[2] + w4[3], run = sm_warp_scan(mine4, lane);
+          const unsigned hit = __ballot_sync(0xffffffffu, before + run >= goal);
+          if (hit) {
+            seen = true;
+            if (lane == __ffs(hit) - 1) {
+              u64 at = before + run - mine4;
+              const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const bool was = at >= goal;
+                at += w4[k];
+                if (!was && at >= goal) write(sm_full(v[k], id + k), whole);
+              }
+            }
+          }
+          before += __shfl_sync(0xffffffffu, run, 31);
+        }
+      }
+    }
+  }
+  if (a.trace && tid == 0) trace_max(a.trace, kTrExit);  // (no block looks into another's memory past the last meeting)
 }
 }  // namespace
 
-cudaError_t launch_sample(const SampleArgs &a, int n_sm, cudaStream_t st, bool pdl) {
-  return launch_k(sample_kernel, dim3((unsigned)a.T), dim3(kSmThreads), 0, st, pdl, a);
+cudaError_t sample_set_attributes() {
+  const void *k[2] = {(const void *)sample_kernel<true>, (const void *)sample_kernel<false>};
+  for (const void *f : k) {
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && f == k[0])
+      e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSmSegMax + 8) * 4);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_sample(const SampleArgs &a0, int n_sm, cudaStream_t st, bool pdl) {
+  SampleArgs a = a0;
+  a.cluster = 1;
+  while (a.cluster < kSmCluster && (a.V + a.cluster - 1) / a.cluster > kSmSeg) a.cluster *= 2;
+  a.per = ((a.V + a.cluster - 1) / a.cluster + 3) & ~3;
+  const bool held = a.per <= kSmSegMax;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.T * a.cluster));
+  cfg.blockDim = dim3(kSmThreads);
+  cfg.dynamicSmemBytes = held ? (size_t)(a.per + 8) * 4 : 0;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, held ? sample_kernel<true> : sample_kernel<false>, a);
 }
 
 }  // namespace moe

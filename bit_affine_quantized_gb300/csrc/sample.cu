@@ -110,14 +110,26 @@ __device__ __forceinline__ u64 sm_warp_scan(u64 v, int lane) {
   return v;
 }
 
+// f * n rounded down, or up, for 0 <= f < 1: exact, in integers (64-bit floating point is scarce on this chip).
+__device__ __forceinline__ u64 sm_share(float f, u64 n, bool up) {
+  const unsigned b = __float_as_uint(f), e = b >> 23;
+  const u64 m = e ? (b & 0x7FFFFFu) | 0x800000u : b & 0x7FFFFFu;  // f = m 2^-shift
+  const int shift = 150 - (int)(e ? e : 1u);                        // 24 .. 149
+  const u64 lo = m * n, hi = __umul64hi(m, n);
+  if (shift >= 128) return up && (lo | hi) ? 1 : 0;
+  const u64 q = shift >= 64 ? hi >> (shift - 64) : hi << (64 - shift) | lo >> shift;
+  const u64 left = shift >= 64 ? lo | (shift > 64 ? hi & ((1ull << (shift - 64)) - 1) : 0) : lo & ((1ull << shift) - 1);
+  return q + (up && left ? 1 : 0);
+}
+
 // What a block tells the others of its tokens.
 struct SmTold {
   float top, least, cut_all, cut_part, sum, bad;
 };
-// What the first block tells all.
+// Where a cut falls.
 struct SmCut {
   u64 above, mass;    // tokens above the bin, and their sum
-  u64 in, in_mass;    // in it
+  u64 in;             // in it
   u64 all;            // sum of what remained before this cut
   unsigned bin;
 };
@@ -126,13 +138,15 @@ struct SmCut {
 template <bool kHeld>
 __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) float seg[];
-  __shared__ u64 s_mass[kSmBins], s_list[kSmList], s_weight[kSmList], s_warp[kSmWarps], s_far[kSmCluster], s_one[4];
-  __shared__ unsigned s_cnt[kSmBins], s_n;
+  __shared__ u64 s_mass[kSmBins], s_list[kSmList], s_weight[kSmList], s_warp[kSmWarps], s_warp_cnt[kSmWarps], s_far[kSmCluster], s_one[4];
+  __shared__ u64 s_all_mass[kSmBins];                 // of the row: the blocks' bins added up
+  __shared__ unsigned s_cnt[kSmBins], s_all_cnt[kSmBins], s_n, s_own, s_base;
   __shared__ uint64_t s_bar[(kSmSegMax + kSmChunk) / kSmChunk + 1];
   __shared__ float s_red[3][kSmWarps];
   __shared__ SmTold s_told[kSmCluster];
   __shared__ SmCut s_cut;
   __shared__ double s_least;
+  __shared__ float s_slope[2], s_low;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.cluster, row = blockIdx.x / C, rank = blockIdx.x % C, V = a.V;
   const bool tracer = a.trace && blockIdx.x == 0 && tid == 0;
@@ -148,7 +162,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   fence_mbar_init();
   s_cnt[tid] = 0u;
   s_mass[tid] = 0;
-  if (tid == 0) s_n = 0u;
+  if (tid == 0) s_n = s_own = 0u;
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
@@ -173,14 +187,18 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   if (top_k <= 0 || top_k >= V) top_k = 0;
   const bool cut_p = top_p0 < 1.f && top_p0 > 0.f;
   const bool has_min = (a.min_p ? __ldg(a.min_p + row) : 0.f) > 0.f;
-  const double top_p = (double)top_p0, u = given > 0.f ? (double)given : 0.0;
-  if (tid == 64) s_least = has_min ? (double)temp * log((double)min_p) : 0.0;
-  const double slope = fmin(1.4426950408889634 / (double)temp, 3.0e38);
+  const float u = given > 0.f ? given : 0.f;
+  if (tid == 64) {  // 64-bit floating point by one thread, while the logits land
+    const double slope = fmin(1.4426950408889634 / (double)temp, 3.0e38);
+    s_slope[0] = (float)slope;
+    s_slope[1] = (float)(slope - (double)(float)slope);
+    s_least = has_min ? (double)temp * log((double)min_p) : 0.0;
+  }
   SmWeight weight;
-  weight.c = (float)slope;
-  weight.c_lo = (float)(slope - (double)weight.c);
-  weight.one = (float)(1ull << (__clz(V) + 31));  // V weights of 1 stay below 2^63
+  weight.one = __uint_as_float((unsigned)(127 + 31 + __clz(V)) << 23);  // 2^(31 + clz): V weights of 1 stay below 2^63
   __syncthreads();
+  weight.c = s_slope[0];
+  weight.c_lo = s_slope[1];
 
   auto quad = [&](int i) {  // four places
     if (kHeld) return reinterpret_cast<const float4 *>(seg)[i];
@@ -303,13 +321,14 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   }
   sm_meet();
   // ---- what every block knows now
-  float top = -INFINITY, bottom = INFINITY, cut_all = -INFINITY, cut_part = INFINITY, sum = 0.f;
-  for (int r = 0; r < C; ++r) {
-    top = fmaxf(top, s_told[r].top);
-    bottom = fminf(bottom, s_told[r].least);
-    cut_all = fmaxf(cut_all, s_told[r].cut_all);
-    cut_part = fminf(cut_part, s_told[r].cut_part);
-  }
+  const SmTold &of = s_told[min(lane, C - 1)];
+  auto lanes_max = [&](float v) {
+#pragma unroll
+    for (int off = kSmCluster / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return __shfl_sync(0xffffffffu, v, 0);
+  };
+  const float their_top = of.top, top = lanes_max(their_top), bottom = -lanes_max(-of.least);
+  const float cut_all = lanes_max(of.cut_all), cut_part = -lanes_max(-of.cut_part);
   if (top == -INFINITY) {
     if (rank == 0 && tid == 0) {
       a.tokens[row] = -1;
@@ -318,55 +337,72 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     }
     return;
   }
-  for (int r = 0; r < C && !has_min; ++r)
-    if (s_told[r].top > -INFINITY) sum += s_told[r].sum * exp2f((s_told[r].top - top) * weight.c);
-  if (has_min) sum = 1.f;  // (maxima below min-p do not count: the largest does)
+  float sum = 1.f;  // a lower bound of the sum (with min-p: of the largest alone, the others may not count)
+  if (cut_p && !has_min) {
+    sum = lane < C && their_top > -INFINITY ? of.sum * exp2f((their_top - top) * weight.c) : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  }
   weight.top = top;
   // min-p: the least logit with l - top >= temperature * ln(min_p), in 64 bits
   float low = bottom;
   if (has_min) {
-    float f = (float)((double)top + s_least);
-    f = (double)f - (double)top >= s_least ? f : nextafterf(f, INFINITY);
-    const float g = nextafterf(f, -INFINITY);
-    f = (double)g - (double)top >= s_least ? g : f;
-    low = fmaxf(low, f);
+    if (tid == 0) {
+      float f = (float)((double)top + s_least);
+      f = (double)f - (double)top >= s_least ? f : nextafterf(f, INFINITY);
+      const float g = nextafterf(f, -INFINITY);
+      s_low = (double)g - (double)top >= s_least ? g : f;
+    }
+    __syncthreads();
+    low = fmaxf(low, s_low);
   }
   const uint32_t first_n = sm_far(&s_n, 0), first_list = sm_far(s_list, 0);
 
   auto write = [&](u64 key, u64 all) {  // one thread
     const float l = sm_value((unsigned)(key >> 32));
     a.tokens[row] = sm_id(key);
-    if (a.logprobs)
-      a.logprobs[row] = greedy ? 0.f : (float)(((double)l - (double)top) / (double)temp - log((double)all / (double)weight.one));
+    // (the sum is at least the token's weight: of a part of 1 no more than fp32 holds is lost)
+    if (a.logprobs) a.logprobs[row] = greedy ? 0.f : __fdiv_rn(l - top, temp) - logf(__ull2float_rn(all) / weight.one);
   };
   // The running sum that the token's has to reach.
-  auto goal_of = [&](u64 all) {
-    const double g = u * (double)all;
-    return u >= 1.0 || g >= (double)all ? all : min(all, (u64)g + 1);
+  auto goal_of = [&](u64 all) { return u >= 1.f ? all : min(all, sm_share(u, all, false) + 1); };
+  auto value = [&](int j) {  // of place j, 0 .. 4 quads
+    if (kHeld) return seg[j];
+    const float v = j >= skew && j < skew + n ? __ldcg(from + (j - skew)) : -INFINITY;
+    return v < INFINITY ? v : -INFINITY;
   };
-  // The tokens that `yes` names go to the first block's list, as far as it reaches; s_n there counts them.
-  auto gather = [&](auto yes) {
-    for (int i = tid; i - lane < quads; i += kSmThreads) {
-      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (i < quads) f = quad(i);
-      const float v[4] = {f.x, f.y, f.z, f.w};
-      bool is[4];
-      int many = 0;
+  // Quads first, first + step, .. below end: `look` at every value, which says whether `each` is for it.  A
+  // lane goes through its own picks: where they are few, a warp's turns are the most that one lane has.
+  auto sweep = [&](int first, int end, int step, auto look, auto each) {
+    for (int i0 = first; i0 < end; i0 += 8 * step) {
+      unsigned picks = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        is[k] = v[k] >= low && v[k] > -INFINITY && yes(v[k], id0 + 4 * i + k);
-        many += is[k];
+      for (int q = 0; q < 8; ++q) {
+        const int i = i0 + q * step;
+        if (i >= end) continue;
+        const float4 f = quad(i);
+        picks |= ((look(f.x) ? 1u : 0u) | (look(f.y) ? 2u : 0u) | (look(f.z) ? 4u : 0u) | (look(f.w) ? 8u : 0u)) << (4 * q);
       }
-      if (__any_sync(0xffffffffu, many > 0) && many > 0) {
-        unsigned at = sm_count(first_n, (unsigned)many);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (is[k]) {
-            if (at < (unsigned)kSmList) sm_put(first_list + 8 * at, sm_full(v[k], id0 + 4 * i + k));
-            ++at;
-          }
+      for (; picks; picks &= picks - 1u) {
+        const int b = __ffs(picks) - 1, j = 4 * (i0 + (b >> 2) * step) + (b & 3);
+        each(value(j), id0 + j);
       }
     }
+  };
+  // The tokens from `bound` on that `yes` names go to the first block's list, as far as it reaches; s_n there
+  // counts them.  (The list's order varies; nothing depends on it.)
+  auto gather = [&](float bound, auto yes) {
+    sweep(tid, quads, kSmThreads, [&](float v) { return v >= bound && v > -INFINITY; }, [&](float v, int id) {
+      if (!yes(v, id)) return;
+      const unsigned at = atomicAdd(&s_own, 1u);
+      if (at < (unsigned)kSmList) s_weight[at] = sm_full(v, id);
+    });
+    __syncthreads();
+    const unsigned many = s_own;
+    if (tid == 0 && many) s_base = sm_count(first_n, many);
+    __syncthreads();
+    if (tid < many && s_base + tid < (unsigned)kSmList) sm_put(first_list + 8 * (s_base + tid), s_weight[tid]);
+    if (tid == 0) s_own = 0u;
   };
   // Over the block: the sum of one value per thread.
   auto block_sum = [&](u64 v) {
@@ -397,7 +433,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     }
     bool stays = tid < count && (k == 0 || place <= k);
     if (k > 0) all = block_sum(stays ? w : 0);
-    if (cut_p) stays = stays && (place == 1 || (double)(upto - w) < top_p * (double)all);
+    if (cut_p) stays = stays && (place == 1 || upto - w < sm_share(top_p0, all, true));
     all = block_sum(stays ? w : 0);
     __syncthreads();
     s_weight[tid] = stays ? w : 0;
@@ -416,9 +452,9 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   u64 tau = (u64)sm_key(low) << 32;  // what remains: keys from here on
   bool done = false;
   // ---- a small k: every token above the bound to the first block
-  float cut_k = fmaxf(low, top_k > 0 ? fmaxf(cut_all, cut_part == INFINITY ? -INFINITY : cut_part) : low);
-  if (top_k > 0 && top_k <= kSmList / 4) {
-    gather([&](float v, int) { return v >= cut_k; });
+  float cut_k = fmaxf(low, top_k > 0 ? fmaxf(cut_all, cut_part) : low);
+  if (top_k > 0 && top_k <= kSmList / 2) {
+    gather(cut_k, [&](float, int) { return true; });
     sm_meet();
     const unsigned count = sm_get(first_n);
     if (count <= (unsigned)kSmList) {
@@ -460,102 +496,106 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     } else if (known) {
       cut = fmaxf(low, sm_value((unsigned)(tau >> 32)));
     } else {
-      const float least_w = (float)((1.0 - top_p) * 0.99 * (double)sum / (double)V);
+      const float least_w = (1.f - top_p0) * 0.99f * sum / (float)V;
       const float f = top + (log2f(least_w) - 0.01f) / weight.c;
       if (f < top) cut = fmaxf(low, f - 1e-6f * (fabsf(top) + fabsf(f)));
     }
     const float wide = top - cut, scale = wide > 0.f ? fminf((float)((1 << kSmBits) - 256) / wide, 3e38f) : 0.f;
     auto far_of = [&](float v) { return (unsigned)fminf((top - v) * scale, (float)((1 << kSmBits) - 1)); };
     unsigned prefix = 0;
-    double need = by_count ? (double)top_k : known ? top_p * (double)all : 0.0;
+    u64 need = by_count ? (u64)top_k : known ? sm_share(top_p0, all, true) : 0;
     u64 above = 0, above_mass = 0;  // what lies above the bin at hand
     bool found = false;
 #pragma unroll 1
     for (int level = 1; level <= 3 && !found; ++level) {
       const int shift = kSmBits - 9 * level;
-      u64 rest = 0;
-      for (int i = tid; i < quads; i += kSmThreads) {
-        const float4 f = quad(i);
-        const float v[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (!(v[k] >= low) || v[k] == -INFINITY) continue;
-          if (v[k] >= cut) {
-            const unsigned y = far_of(v[k]) >> shift;
-            if (y >> 9 == prefix && sm_full(v[k], id0 + 4 * i + k) >= tau) {
-              const u64 w = weight(v[k]);
+      const bool tail = !by_count && !known && level == 1;
+      float rest_w = 0.f;  // below the bound: each weight is less than the share of one of V in 1 - p
+      sweep(tid, quads, kSmThreads,
+            [&](float v) {
+              if (tail) {
+                float e;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((v - top) * weight.c));
+                rest_w += v < cut && v >= low ? e : 0.f;
+              }
+              return v >= cut;
+            },
+            [&](float v, int id) {
+              const unsigned y = far_of(v) >> shift;
+              if (y >> 9 != prefix || sm_full(v, id) < tau) return;
+              const u64 w = weight(v);
               atomicAdd(&s_cnt[y & 511u], 1u);
               if (w) atomicAdd(&s_mass[y & 511u], w);
-            }
-          } else if (!by_count && !known && level == 1) {
-            rest += weight(v[k]);
-          }
-        }
+            });
+      u64 rest = __float2ull_rn(rest_w * weight.one);
+      if (tail) {
+        rest = block_sum(rest);
+        if (tid < C) sm_put(sm_far(&s_far[rank], tid), rest);
       }
-      rest = block_sum(rest);
-      if (tid == 0) sm_put(sm_far(&s_far[rank], 0), rest);
       sm_meet();
-      if (rank == 0) {  // the bin in which the cut falls
-        u64 cnt = 0, mass = 0, tail = 0;
-#pragma unroll 4
-        for (int r = 0; r < C; ++r) {
-          cnt += sm_get(sm_far(&s_cnt[tid], r));
-          mass += sm_get64(sm_far(&s_mass[tid], r));
+      {  // a block adds up its part of the bins over the blocks, a thread per bin and block, and tells all
+        const int b = rank * (kSmBins / C) + tid / C, r = tid % C;
+        unsigned cnt = sm_get(sm_far(&s_cnt[b], r));
+        u64 mass = sm_get64(sm_far(&s_mass[b], r));
+        for (int off = C / 2; off > 0; off >>= 1) {
+          cnt += __shfl_xor_sync(0xffffffffu, cnt, off);
+          mass += __shfl_xor_sync(0xffffffffu, mass, off);
         }
-        for (int r = 0; r < C; ++r) tail += s_far[r];
+        sm_put(sm_far(&s_all_cnt[b], r), cnt);
+        sm_put(sm_far(&s_all_mass[b], r), mass);
+      }
+      sm_meet();
+      {  // the bin in which the cut falls, in every block alike
+        const u64 cnt = s_all_cnt[tid], mass = s_all_mass[tid];
+        s_cnt[tid] = 0u;
+        s_mass[tid] = 0;
+        u64 rest_all = 0;
+        for (int r = 0; r < C && tail; ++r) rest_all += s_far[r];
         u64 cr = sm_warp_scan(cnt, lane), mr = sm_warp_scan(mass, lane);
-        __syncthreads();
         if (lane == 31) {
           s_warp[warp] = mr;
-          s_list[warp] = cr;
+          s_warp_cnt[warp] = cr;
         }
         __syncthreads();
-        u64 whole_m = 0, whole_c = 0;
+        u64 whole_m = 0, my_m = 0, my_c = 0;
+#pragma unroll
         for (int w = 0; w < kSmWarps; ++w) {
-          if (w == warp) {
-            mr += whole_m;
-            cr += whole_c;
-          }
+          my_m += w < warp ? s_warp[w] : 0;
+          my_c += w < warp ? s_warp_cnt[w] : 0;
           whole_m += s_warp[w];
-          whole_c += s_list[w];
         }
-        // (at w == warp the sums of the warps before were added)
-        const u64 total = !by_count && !known && level == 1 ? whole_m + tail : all;
-        const double want = by_count ? need : (level == 1 && !known ? top_p * (double)total : need);
-        const bool reached = by_count ? (double)(above + cr) >= want : (double)(above_mass + mr) >= want;
-        const bool before = by_count ? (double)(above + cr - cnt) >= want : (double)(above_mass + mr - mass) >= want;
+        mr += my_m;
+        cr += my_c;
+        const u64 total = tail ? whole_m + rest_all : all;
+        const u64 want = by_count || known ? need : sm_share(top_p0, total, true);
+        const bool reached = (by_count ? above + cr : above_mass + mr) >= want;
+        const bool before = (by_count ? above + cr - cnt : above_mass + mr - mass) >= want;
         if ((reached && !before) || (tid == kSmThreads - 1 && !reached)) {
-          for (int r = 0; r < C; ++r) {
-            const uint32_t to = sm_far(&s_cut, r);
-            sm_put(to, above + cr - cnt);
-            sm_put(to + 8, above_mass + mr - mass);
-            sm_put(to + 16, cnt);
-            sm_put(to + 24, mass);
-            sm_put(to + 32, total);
-            sm_put(to + 40, (unsigned)tid);
-          }
+          s_cut.above = above + cr - cnt;
+          s_cut.mass = above_mass + mr - mass;
+          s_cut.in = cnt;
+          s_cut.all = total;
+          s_cut.bin = tid;
         }
+        __syncthreads();
       }
-      sm_meet();
       above = s_cut.above;
       above_mass = s_cut.mass;
       if (!by_count && !known) {
         all = s_cut.all;
         known = true;
-        need = top_p * (double)all;
+        need = sm_share(top_p0, all, true);
       }
       prefix = prefix << 9 | s_cut.bin;
       const u64 in = s_cut.in;
-      s_cnt[tid] = 0u;
-      s_mass[tid] = 0;
-      __syncthreads();
+      __syncthreads();  // (s_cut is free again)
       if (above + in <= (u64)kSmList && (!by_count || top_k > 0)) {  // all that may remain fits the list
-        gather([&](float v, int id) { return v >= cut && far_of(v) >> shift <= prefix && sm_full(v, id) >= tau; });
+        gather(cut, [&](float v, int id) { return far_of(v) >> shift <= prefix && sm_full(v, id) >= tau; });
         sm_meet();
         if (rank == 0) finish((int)(above + in), by_count ? top_k : 0, all);
         done = found = true;
       } else if (in <= (u64)kSmList) {
-        gather([&](float v, int id) { return v >= cut && far_of(v) >> shift == prefix && sm_full(v, id) >= tau; });
+        gather(cut, [&](float v, int id) { return far_of(v) >> shift == prefix && sm_full(v, id) >= tau; });
         sm_meet();
         if (rank == 0) {
           const u64 key = tid < (int)in ? s_list[tid] : 0, w = tid < (int)in ? weight(sm_value((unsigned)(key >> 32))) : 0;
@@ -571,7 +611,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
             }
           // the last that stays: the place k, or the one whose sum reaches the share
           const bool last = tid < (int)in && (by_count ? above + place == (u64)top_k
-                                                       : (double)(above_mass + upto) >= need && (double)(above_mass + upto - w) < need);
+                                                       : above_mass + upto >= need && above_mass + upto - w < need);
           // (none reaches it where the share is the whole sum to fp64's last bit: then the least key stays)
           const bool none = __syncthreads_or(last) == 0;
           if (last || (none && tid < (int)in && place == in)) {
@@ -600,14 +640,10 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
         const u64 t = k | (1ull << b);
         u64 part = 0;
         if (t > tau) {  // (else everything that remains lies above it, which is enough)
-          for (int i = tid; i < quads; i += kSmThreads) {
-            const float4 f = quad(i);
-            const float v[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (v[j] > -INFINITY && sm_full(v[j], id0 + 4 * i + j) >= t) part += by_count ? 1 : weight(v[j]);
-          }
-          if ((double)cluster_sum(part) >= need) k = t;
+          const float bound = sm_value((unsigned)(t >> 32));
+          sweep(tid, quads, kSmThreads, [&](float v) { return !(v < bound) && v > -INFINITY; },
+                [&](float v, int id) { part += sm_full(v, id) < t ? 0 : by_count ? 1 : weight(v); });
+          if (cluster_sum(part) >= need) k = t;
         } else {
           k = t;
         }
@@ -615,13 +651,9 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       tau = max(tau, k);
       if (by_count) {
         u64 part = 0;
-        for (int i = tid; i < quads; i += kSmThreads) {
-          const float4 f = quad(i);
-          const float v[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (v[j] > -INFINITY && sm_full(v[j], id0 + 4 * i + j) >= tau) part += weight(v[j]);
-        }
+        const float bound = sm_value((unsigned)(tau >> 32));
+        sweep(tid, quads, kSmThreads, [&](float v) { return v >= bound; },
+              [&](float v, int id) { part += sm_full(v, id) >= tau ? weight(v) : 0; });
         all = cluster_sum(part);
         known = true;
       }
@@ -636,11 +668,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       return v >= tau_v && v > -INFINITY && sm_full(v, id) >= tau ? weight(v) : 0;
     };
     u64 part = 0;
-    for (int i = q0 + lane; i < q1; i += 32) {
-      const float4 f = quad(i);
-      const int id = id0 + 4 * i;
-      part += kept(f.x, id) + kept(f.y, id + 1) + kept(f.z, id + 2) + kept(f.w, id + 3);
-    }
+    sweep(q0 + lane, q1, 32, [&](float v) { return v >= tau_v && v > -INFINITY; }, [&](float v, int id) { part += kept(v, id); });
     const u64 own = block_sum(part);
     if (tid < C) sm_put(sm_far(&s_far[rank], tid), own);
     sm_meet();

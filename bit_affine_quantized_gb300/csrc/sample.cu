@@ -18,7 +18,7 @@
 // list at once, else a histogram of their distance to the maximum (512 bins, a
 // count and a sum each, refined by 9 bits where needed) says in which bin the cut
 // falls, and a list takes what lies above its lower end, or in the bin alone.
-// What is in a list is ranked by comparing all pairs.  Where a bin cannot be
+// What is in a list is sorted.  Where a bin cannot be
 // refined (many equal logits) the key is found bit by bit.
 //
 // Weights e^((l - M) / T) are summed in fixed point, 64 bits: any order gives the
@@ -61,16 +61,14 @@ __device__ __forceinline__ uint32_t sm_far(const void *p, int rank) {
   return r;
 }
 __device__ __forceinline__ void sm_put(uint32_t at, u64 v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory"); }
+__device__ __forceinline__ void sm_put(uint32_t at, u64 a, u64 b) {
+  asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(at), "l"(a), "l"(b) : "memory");
+}
 __device__ __forceinline__ void sm_put(uint32_t at, unsigned v) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); }
 __device__ __forceinline__ void sm_put(uint32_t at, float v) { sm_put(at, __float_as_uint(v)); }
 __device__ __forceinline__ unsigned sm_get(uint32_t at) {
   unsigned v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ u64 sm_get64(uint32_t at) {
-  u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
   return v;
 }
 __device__ __forceinline__ unsigned sm_count(uint32_t at, unsigned n) {
@@ -101,6 +99,12 @@ __device__ __forceinline__ u64 sm_warp_sum(u64 v) {
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
 }
+// Over the 16 lanes of a half warp.
+__device__ __forceinline__ u64 sm_half_sum(u64 v) {
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
 __device__ __forceinline__ u64 sm_warp_scan(u64 v, int lane) {
 #pragma unroll
   for (int off = 1; off < 32; off *= 2) {
@@ -126,21 +130,26 @@ __device__ __forceinline__ u64 sm_share(float f, u64 n, bool up) {
 struct SmTold {
   float top, least, cut_all, cut_part, sum, bad;
 };
-// Where a cut falls.
+struct __align__(16) SmBin {
+  u64 mass, count;
+};
+
+// Where a cut falls: the least key that stays, the sum down to it.
 struct SmCut {
-  u64 above, mass;    // tokens above the bin, and their sum
-  u64 in;             // in it
-  u64 all;            // sum of what remained before this cut
-  unsigned bin;
+  u64 key, mass;
 };
 
 // kHeld: the block's tokens lie in shared memory.
 template <bool kHeld>
 __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) float seg[];
-  __shared__ u64 s_mass[kSmBins], s_list[kSmList], s_weight[kSmList], s_warp[kSmWarps], s_warp_cnt[kSmWarps], s_far[kSmCluster], s_one[4];
-  __shared__ u64 s_all_mass[kSmBins];                 // of the row: the blocks' bins added up
-  __shared__ unsigned s_cnt[kSmBins], s_all_cnt[kSmBins], s_n, s_own, s_base;
+  // A bin's sum as three sums of 16 bits of a weight each (the last of what is left), for shared memory adds 32
+  // bits at once and 64 by trial only; rows that are not held have more tokens than the 16 bits allow for.
+  __shared__ unsigned s_m[3][kSmBins];
+  __shared__ u64 s_mass[kHeld ? 1 : kSmBins], s_list[kSmList], s_weight[kSmList], s_warp[kSmWarps], s_far[kSmCluster], s_one[4];
+  __shared__ SmBin s_wide[kSmCluster][32], s_fine[kSmCluster][16];  // the blocks' bins: 16 at a time, then one by one
+  __shared__ u64 s_sums[2][32];
+  __shared__ unsigned s_cnt[kSmBins], s_n, s_own, s_base;
   __shared__ uint64_t s_bar[(kSmSegMax + kSmChunk) / kSmChunk + 1];
   __shared__ float s_red[3][kSmWarps];
   __shared__ SmTold s_told[kSmCluster];
@@ -160,8 +169,12 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   const int chunks = kHeld && in1 > in0 ? (in1 + kSmChunk - 1) / kSmChunk : 0;
   if (tid < chunks) mbar_init(&s_bar[tid], 1);
   fence_mbar_init();
-  s_cnt[tid] = 0u;
-  s_mass[tid] = 0;
+  auto clear_bins = [&] {
+    s_cnt[tid] = 0u;
+    s_m[0][tid] = s_m[1][tid] = s_m[2][tid] = 0u;
+    if (!kHeld) s_mass[tid] = 0;
+  };
+  clear_bins();
   if (tid == 0) s_n = s_own = 0u;
   __syncthreads();
   pdl_wait();
@@ -300,7 +313,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       __syncthreads();
       if (s_one[2] >= (unsigned)top_k) told.cut_all = __uint_as_float((unsigned)s_one[0]);
       if (s_one[2] >= part) told.cut_part = __uint_as_float((unsigned)s_one[1]);
-      s_cnt[tid] = 0u;
+      clear_bins();
     } else if (cut_p) {
       float e = mine > -INFINITY ? exp2f((mine - block_top) * weight.c) : 0.f;
 #pragma unroll
@@ -415,38 +428,74 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     for (int w = 0; w < kSmWarps; ++w) t += s_warp[w];
     return t;
   };
+  // Running sum over the block, of one value per thread.
+  auto block_scan = [&](u64 v) {
+    const u64 own = sm_warp_scan(v, lane);
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = own;
+    __syncthreads();
+    u64 before = 0;
+#pragma unroll
+    for (int w = 0; w < kSmWarps - 1; ++w) before += w < warp ? s_warp[w] : 0;
+    return own + before;
+  };
+  // Sorts `count` keys, one per thread (0: none), the largest first; s_list is its own to use.  Few by their ranks, four
+  // threads to a key, more by a bitonic network (100 of them: 0.5 us against 1.5; 512: 10 against 4).
+  auto sort = [&](u64 key, int count) {
+    if (count <= kSmThreads / 4) {
+      __syncthreads();
+      s_list[tid] = key;
+      __syncthreads();
+      const u64 mine = s_list[tid / 4];
+      int place = 0;
+#pragma unroll 4
+      for (int i = tid % 4; i < count; i += 4) place += s_list[i] > mine;
+      place += __shfl_xor_sync(0xffffffffu, place, 1);
+      place += __shfl_xor_sync(0xffffffffu, place, 2);
+      __syncthreads();
+      if (tid / 4 < count && tid % 4 == 0) s_list[place] = mine;
+      __syncthreads();
+      return tid < count ? s_list[tid] : 0;
+    }
+    const int size = count <= 32 ? 32 : 1 << (32 - __clz(count - 1));
+#pragma unroll 1
+    for (int k = 2; k <= size; k *= 2)
+#pragma unroll 1
+      for (int j = k / 2; j > 0; j /= 2) {
+        u64 other;
+        if (j < 32) {
+          other = __shfl_xor_sync(0xffffffffu, key, j);
+        } else {
+          __syncthreads();
+          s_list[tid] = key;
+          __syncthreads();
+          other = s_list[tid ^ j];
+        }
+        const bool larger = ((tid & j) == 0) == ((tid & k) == 0);  // this thread keeps the larger
+        key = tid >= size ? 0 : larger ? (key > other ? key : other) : (key < other ? key : other);
+      }
+    return key;
+  };
   // The first block alone: the list has every token that may remain.
   auto finish = [&](int count, int k, u64 all) {
-    const u64 key = tid < count ? s_list[tid] : 0, w = tid < count ? weight(sm_value((unsigned)(key >> 32))) : 0;
-    s_weight[tid] = w;
-    if (tid == 0) s_one[3] = ~0ull;
-    __syncthreads();
-    u64 upto = 0;
-    int place = 0;
-    if (tid < count) {
-#pragma unroll 4
-      for (int i = 0; i < count; ++i) {
-        const bool is = s_list[i] >= key;
-        place += is;
-        upto += is ? s_weight[i] : 0;
-      }
+    u64 key = sort(tid < count ? s_list[tid] : 0, count);
+    const u64 w = key ? weight(sm_value((unsigned)(key >> 32))) : 0, upto = block_scan(w);
+    bool stays = key != 0 && (k == 0 || tid < k);
+    if (k > 0) {
+      if (tid == min(k, count) - 1) s_one[0] = upto;
+      __syncthreads();
+      all = s_one[0];
     }
-    bool stays = tid < count && (k == 0 || place <= k);
-    if (k > 0) all = block_sum(stays ? w : 0);
-    if (cut_p) stays = stays && (place == 1 || upto - w < sm_share(top_p0, all, true));
-    all = block_sum(stays ? w : 0);
+    if (cut_p) stays = stays && (tid == 0 || upto - w < sm_share(top_p0, all, true));
+    const int many = __syncthreads_count(stays);  // (a first part of the order)
+    if (tid == many - 1) s_one[1] = upto;
     __syncthreads();
-    s_weight[tid] = stays ? w : 0;
-    __syncthreads();
+    all = s_one[1];
     const u64 goal = goal_of(all);
-    if (stays) {
-      u64 run = 0;
-#pragma unroll 4
-      for (int i = 0; i < count; ++i) run += (unsigned)s_list[i] >= (unsigned)key ? s_weight[i] : 0;  // (a lower id: a larger complement)
-      if (run >= goal) atomicMin(&s_one[3], (u64)(unsigned)sm_id(key));
-    }
-    __syncthreads();
-    if (stays && (u64)(unsigned)sm_id(key) == s_one[3]) write(key, all);
+    key = sort(stays ? key << 32 | key >> 32 : 0, many);  // by the ids
+    key = key << 32 | key >> 32;
+    const u64 w2 = key ? weight(sm_value((unsigned)(key >> 32))) : 0, run = block_scan(w2);
+    if (run >= goal && run - w2 < goal) write(key, all);
   };
 
   u64 tau = (u64)sm_key(low) << 32;  // what remains: keys from here on
@@ -502,6 +551,11 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     }
     const float wide = top - cut, scale = wide > 0.f ? fminf((float)((1 << kSmBits) - 256) / wide, 3e38f) : 0.f;
     auto far_of = [&](float v) { return (unsigned)fminf((top - v) * scale, (float)((1 << kSmBits) - 1)); };
+    // about the largest and the least value at a distance, and a little over
+    auto value_at = [&](unsigned y, float over) {
+      const float d = scale > 0.f ? (float)y / scale : 0.f;
+      return top - d + over * (1e-6f * (fabsf(top) + d) + 1e-30f);
+    };
     unsigned prefix = 0;
     u64 need = by_count ? (u64)top_k : known ? sm_share(top_p0, all, true) : 0;
     u64 above = 0, above_mass = 0;  // what lies above the bin at hand
@@ -525,92 +579,77 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
               if (y >> 9 != prefix || sm_full(v, id) < tau) return;
               const u64 w = weight(v);
               atomicAdd(&s_cnt[y & 511u], 1u);
-              if (w) atomicAdd(&s_mass[y & 511u], w);
+              if (kHeld) {
+                atomicAdd(&s_m[0][y & 511u], (unsigned)w & 0xFFFFu);
+                atomicAdd(&s_m[1][y & 511u], (unsigned)w >> 16);
+                if (w >> 32) atomicAdd(&s_m[2][y & 511u], (unsigned)(w >> 32));
+              } else if (w) {
+                atomicAdd(&s_mass[y & 511u], w);
+              }
             });
       u64 rest = __float2ull_rn(rest_w * weight.one);
       if (tail) {
         rest = block_sum(rest);
         if (tid < C) sm_put(sm_far(&s_far[rank], tid), rest);
       }
-      sm_meet();
-      {  // a block adds up its part of the bins over the blocks, a thread per bin and block, and tells all
-        const int b = rank * (kSmBins / C) + tid / C, r = tid % C;
-        unsigned cnt = sm_get(sm_far(&s_cnt[b], r));
-        u64 mass = sm_get64(sm_far(&s_mass[b], r));
-        for (int off = C / 2; off > 0; off >>= 1) {
-          cnt += __shfl_xor_sync(0xffffffffu, cnt, off);
-          mass += __shfl_xor_sync(0xffffffffu, mass, off);
-        }
-        sm_put(sm_far(&s_all_cnt[b], r), cnt);
-        sm_put(sm_far(&s_all_mass[b], r), mass);
+      __syncthreads();
+      // The bin in which the cut falls: every block learns the others' bins 16 at a time, then the 16 that matter.
+      auto mass_of = [&](int b) { return kHeld ? s_m[0][b] + ((u64)s_m[1][b] << 16) + ((u64)s_m[2][b] << 32) : s_mass[b]; };
+      const int half = tid / 16, peer = tid % 16;
+      {
+        const u64 cnt = sm_half_sum(s_cnt[tid]), mass = sm_half_sum(mass_of(tid));
+        if (peer < C) sm_put(sm_far(&s_wide[rank][half], peer), mass, cnt);
       }
       sm_meet();
-      {  // the bin in which the cut falls, in every block alike
-        const u64 cnt = s_all_cnt[tid], mass = s_all_mass[tid];
-        s_cnt[tid] = 0u;
-        s_mass[tid] = 0;
-        u64 rest_all = 0;
-        for (int r = 0; r < C && tail; ++r) rest_all += s_far[r];
-        u64 cr = sm_warp_scan(cnt, lane), mr = sm_warp_scan(mass, lane);
-        if (lane == 31) {
-          s_warp[warp] = mr;
-          s_warp_cnt[warp] = cr;
+      unsigned bin = 0;
+      u64 in = 0;
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        SmBin b = {0, 0};
+        if (peer < C && (part == 0 || half < 16)) b = part == 0 ? s_wide[peer][half] : s_fine[peer][half];
+        const u64 m16 = sm_half_sum(b.mass), c16 = sm_half_sum(b.count);
+        if (peer == 0) {
+          s_sums[0][half] = m16;
+          s_sums[1][half] = c16;
         }
         __syncthreads();
-        u64 whole_m = 0, my_m = 0, my_c = 0;
-#pragma unroll
-        for (int w = 0; w < kSmWarps; ++w) {
-          my_m += w < warp ? s_warp[w] : 0;
-          my_c += w < warp ? s_warp_cnt[w] : 0;
-          whole_m += s_warp[w];
+        const u64 mass = s_sums[0][lane], cnt = s_sums[1][lane], mr = sm_warp_scan(mass, lane), cr = sm_warp_scan(cnt, lane);
+        if (part == 0 && tail) {
+          all = __shfl_sync(0xffffffffu, mr, 31);
+          for (int r = 0; r < C; ++r) all += s_far[r];
+          known = true;
+          need = sm_share(top_p0, all, true);
         }
-        mr += my_m;
-        cr += my_c;
-        const u64 total = tail ? whole_m + rest_all : all;
-        const u64 want = by_count || known ? need : sm_share(top_p0, total, true);
-        const bool reached = (by_count ? above + cr : above_mass + mr) >= want;
-        const bool before = (by_count ? above + cr - cnt : above_mass + mr - mass) >= want;
-        if ((reached && !before) || (tid == kSmThreads - 1 && !reached)) {
-          s_cut.above = above + cr - cnt;
-          s_cut.mass = above_mass + mr - mass;
-          s_cut.in = cnt;
-          s_cut.all = total;
-          s_cut.bin = tid;
+        const unsigned hit = __ballot_sync(0xffffffffu, (by_count ? above + cr : above_mass + mr) >= need);
+        const int at = hit ? __ffs(hit) - 1 : part == 0 ? 31 : 15;  // (fewer than are needed: all of them)
+        above += __shfl_sync(0xffffffffu, cr - cnt, at);
+        above_mass += __shfl_sync(0xffffffffu, mr - mass, at);
+        in = __shfl_sync(0xffffffffu, cnt, at);
+        bin = 16 * bin + (unsigned)at;
+        if (part == 0) {
+          const int f = 16 * at + (half & 15);
+          if (half < 16 && peer < C) sm_put(sm_far(&s_fine[rank][half], peer), mass_of(f), (u64)s_cnt[f]);
+          sm_meet();
         }
-        __syncthreads();
       }
-      above = s_cut.above;
-      above_mass = s_cut.mass;
-      if (!by_count && !known) {
-        all = s_cut.all;
-        known = true;
-        need = sm_share(top_p0, all, true);
-      }
-      prefix = prefix << 9 | s_cut.bin;
-      const u64 in = s_cut.in;
-      __syncthreads();  // (s_cut is free again)
-      if (above + in <= (u64)kSmList && (!by_count || top_k > 0)) {  // all that may remain fits the list
-        gather(cut, [&](float v, int id) { return far_of(v) >> shift <= prefix && sm_full(v, id) >= tau; });
+      __syncthreads();
+      clear_bins();
+      prefix = prefix << 9 | bin;
+      const float bin_low = prefix == (1u << (9 * level)) - 1u || !(wide < 1e37f) ? cut : fmaxf(cut, value_at((prefix + 1) << shift, -1.f));
+      if (above + in <= (u64)kSmList) {  // all that may remain fits the list
+        gather(bin_low, [&](float v, int id) { return far_of(v) >> shift <= prefix && sm_full(v, id) >= tau; });
         sm_meet();
         if (rank == 0) finish((int)(above + in), by_count ? top_k : 0, all);
         done = found = true;
       } else if (in <= (u64)kSmList) {
-        gather(cut, [&](float v, int id) { return far_of(v) >> shift == prefix && sm_full(v, id) >= tau; });
+        const float bin_high = wide < 1e37f ? value_at(prefix << shift, 1.f) : INFINITY;
+        gather(bin_low, [&](float v, int id) { return v <= bin_high && far_of(v) >> shift == prefix && sm_full(v, id) >= tau; });
         sm_meet();
         if (rank == 0) {
-          const u64 key = tid < (int)in ? s_list[tid] : 0, w = tid < (int)in ? weight(sm_value((unsigned)(key >> 32))) : 0;
-          s_weight[tid] = w;
-          __syncthreads();
-          u64 upto = 0;
-          u64 place = 0;
-          if (tid < (int)in)
-            for (int i = 0; i < (int)in; ++i) {
-              const bool is = s_list[i] >= key;
-              place += is;
-              upto += is ? s_weight[i] : 0;
-            }
+          const u64 key = sort(tid < (int)in ? s_list[tid] : 0, (int)in);
+          const u64 w = key ? weight(sm_value((unsigned)(key >> 32))) : 0, upto = block_scan(w), place = tid + 1;
           // the last that stays: the place k, or the one whose sum reaches the share
-          const bool last = tid < (int)in && (by_count ? above + place == (u64)top_k
+          const bool last = key != 0 && (by_count ? above + place == (u64)top_k
                                                        : above_mass + upto >= need && above_mass + upto - w < need);
           // (none reaches it where the share is the whole sum to fp64's last bit: then the least key stays)
           const bool none = __syncthreads_or(last) == 0;
@@ -624,13 +663,13 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
           if (tid == 0) s_n = 0u;
         }
         sm_meet();
-        tau = s_cut.above;
+        tau = s_cut.key;
         if (by_count) {
           all = s_cut.mass;
           known = true;
         }
         found = true;
-        sm_meet();
+        __syncthreads();  // (s_cut is free again)
       }
     }
     if (!found) {  // many equal logits: the largest key from which on there is enough, bit by bit

@@ -287,7 +287,7 @@ struct KvAppendArgs {
   const int32_t *seq, *pos;   // [T]; seq nullable
   const float *freq;          // [rot / 2]
   int T, Hq, rot;
-  int parts;                  // blocks per row (set by the launcher)
+  int per, parts;             // rows of a block, blocks of as many rows (set by the launcher)
   unsigned *err;
   unsigned long long *trace;
 };

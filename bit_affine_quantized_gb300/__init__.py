@@ -356,19 +356,18 @@ def make_logit_rules(history=None, history_len=None, prompt_len=None, repetition
 def _heads(t, what: str, n_rows: int, heads: int, dim: int, dev: int):
     """Device address and row stride of bf16 rows on device dev: a tensor of at
     least n_rows x heads x dim, or x (heads * dim), whose rows may lie apart."""
-    if t is None:
-        return None, 0
-    shape, stride, width = t.shape, t.stride(), heads * dim
-    if t.get_device() != dev or t.dtype not in (_DTYPES or _fill_dtypes())["b16"]:
-        raise ValueError(f"{what}: bf16 values on CUDA device {dev} are wanted, {t.dtype} on {t.device} given")
-    if len(shape) == 3:
-        fits = shape[1] == heads and shape[2] == dim and stride[2] == 1 and (heads == 1 or stride[1] == dim)
-    else:
-        fits = len(shape) == 2 and shape[1] == width and stride[1] == 1
-    if not fits or shape[0] < n_rows:
-        raise ValueError(f"{what}: {tuple(shape)} with strides {stride} given, at least {n_rows} rows of {heads} x {dim} "
-                         f"adjacent values are wanted")
-    return t.data_ptr(), stride[0] if shape[0] > 1 else width
+    stride = t.stride()
+    if t.get_device() == dev and t.dtype in _DTYPES["b16"]:
+        if len(stride) == 3:
+            n, h, d = t.shape
+            if h == heads and d == dim and stride[2] == 1 and (stride[1] == dim or h == 1) and n >= n_rows:
+                return t.data_ptr(), stride[0] if n > 1 else heads * dim
+        elif len(stride) == 2:
+            n, w = t.shape
+            if w == heads * dim and stride[1] == 1 and n >= n_rows:
+                return t.data_ptr(), stride[0] if n > 1 else w
+    raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} with strides {stride} on {t.device} given, at least {n_rows} bf16 "
+                     f"rows of {heads} x {dim} adjacent values on CUDA device {max(dev, 0)} are wanted")
 
 
 def make_kv_cache(k, v, table, k_scales=None, v_scales=None) -> KvCache:
@@ -649,14 +648,17 @@ class Moe:
         [T, kv_heads, head_dim], or with the last two dimensions as one; rows may
         lie apart, as the parts of one projection's output do."""
         dev, types = self._on_device("cache", cache.device), _DTYPES or _fill_dtypes()
-        T, H, D = positions.numel(), cache.kv_heads, cache.head_dim
-        q_heads = 0 if q is None else q.shape[1] if q.dim() == 3 else q.shape[-1] // D
-        (qp, lq), (kp, lk) = _heads(q, "q", T, q_heads, D, dev), _heads(k, "k", T, H, D, dev)
-        (vp, lv), (op, lo) = _heads(v, "v", T, H, D, dev), _heads(q_out, "q_out", T, q_heads, D, dev)
+        T, H, D, i32 = positions.numel(), cache.kv_heads, cache.head_dim, types["i32"]
+        (kp, lk), (vp, lv) = _heads(k, "k", T, H, D, dev), _heads(v, "v", T, H, D, dev)
+        if q is None or q_out is None:  # (the call refuses one without the other)
+            q_heads, qp, lq, op, lo = 0, _ptr(q), 0, _ptr(q_out), 0
+        else:
+            q_heads = q.shape[1] if q.dim() == 3 else q.shape[-1] // D
+            (qp, lq), (op, lo) = _heads(q, "q", T, q_heads, D, dev), _heads(q_out, "q_out", T, q_heads, D, dev)
         rot = 0 if inv_freq is None else 2 * inv_freq.numel()
         st = self.lib.moe_kv_append(self.h, qp, lq, q_heads, kp, lk, vp, lv, T,
-                                    _data(seqs, "seqs", types["i32"], T, dev),
-                                    _data(positions, "positions", types["i32"], T, dev), ctypes.byref(cache),
+                                    None if seqs is None else _data(seqs, "seqs", i32, T, dev),
+                                    _data(positions, "positions", i32, T, dev), ctypes.byref(cache),
                                     _data(inv_freq, "inv_freq", types["f32"], rot // 2, dev), rot, op, lo,
                                     _stream(stream, dev))
         if st:
@@ -667,7 +669,8 @@ class Moe:
         positions (moe_kv_read; seqs None: row t is of sequence t)."""
         dev, types = self._on_device("cache", cache.device), _DTYPES or _fill_dtypes()
         T, H, D = positions.numel(), cache.kv_heads, cache.head_dim
-        (kp, lk), (vp, lv) = _heads(k_out, "k_out", T, H, D, dev), _heads(v_out, "v_out", T, H, D, dev)
+        kp, lk = (None, 0) if k_out is None else _heads(k_out, "k_out", T, H, D, dev)
+        vp, lv = (None, 0) if v_out is None else _heads(v_out, "v_out", T, H, D, dev)
         st = self.lib.moe_kv_read(self.h, ctypes.byref(cache), _data(seqs, "seqs", types["i32"], T, dev),
                                   _data(positions, "positions", types["i32"], T, dev), T, kp, lk, vp, lv,
                                   _stream(stream, dev))

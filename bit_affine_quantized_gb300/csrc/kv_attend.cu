@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   extern __shared__ uint8_t at_raw[];
   uint8_t *const sm = at_raw + ((1024 - (smem_addr(at_raw) & 1023)) & 1023);
   float *const s_scales = reinterpret_cast<float *>(sm + S::kRoom);
-  __shared__ uint64_t s_keys[kWarps][kStages], s_values[kWarps][kStages], s_join;
-  __shared__ unsigned s_pre[kThreads + 1], s_sums[kWarps + 1];
+  __shared__ uint64_t s_keys[kWarps][kStages], s_values[kWarps][kStages], s_join, s_heads;
+  __shared__ unsigned s_pre[kThreads + 1], s_sums[kWarps + 1], s_start[kWarps + 1];
   __shared__ AtWarpParts s_parts[kWarps];
   __shared__ __align__(16) float s_m[2 * kWarps][kHeads], s_l[2 * kWarps][kHeads];  // of the warps' parts; then their weights
   __shared__ int s_last[2], s_count[2], s_from[2];
@@ -206,12 +206,13 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   const int shift = 31 - __clz(a.c.rows), box = min(a.c.rows, kTile), box_shift = 31 - __clz(box);
   const bool tracer = a.trace && blockIdx.x == 0 && tid == 0;
   if (tracer) trace_min(a.trace, kTrEntry);
-  if (tid < kWarps * kStages) {
-    mbar_init(&s_keys[0][0] + tid, 1);
-    mbar_init(&s_values[0][0] + tid, 1);
+  if (lane < kStages) {  // (a warp's own: no other waits on them)
+    mbar_init(&s_keys[warp][lane], 1);
+    mbar_init(&s_values[warp][lane], 1);
   }
   if (tid == 0) {
     mbar_init(&s_join, 1);
+    mbar_init(&s_heads, 1);
     at_prefetch(&prm.k);
     at_prefetch(&prm.v);
   }
@@ -220,40 +221,46 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   pdl_launch_dependents();
   if (tracer) trace_min(a.trace, kTrWaited);
 
-  // ---- the list of tiles: prefix sums over chunks of sequences, one per thread
+  // ---- the list of tiles: prefix sums over the sequences, up to 32 by every warp, more
+  // by chunks of sequences, one per thread
   const int n = a.c.n_seqs, chunk = (n + kThreads - 1) / kThreads;
   static_assert((kKvMaxSeqs + kThreads - 1) / kThreads <= 32, "a warp looks through a chunk at once");
   AtCursor<kTile> cur;
-  {
-    unsigned sum = 0;
-    for (int i = tid * chunk; i < min(n, (tid + 1) * chunk); ++i) {
-      cur.seq = i;
-      cur.load(a);
-      sum += (unsigned)cur.nt * items;
-    }
-    unsigned run = sum;
+  auto tiles_of = [&](int seq, bool is) {  // and the sequence in the cursor
+    cur.seq = seq;
+    cur.load(a);
+    return is ? (unsigned)cur.nt * items : 0u;
+  };
+  auto scan = [&](unsigned v) {
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
-      const unsigned o = __shfl_up_sync(0xffffffffu, run, off);
-      if (lane >= off) run += o;
+      const unsigned o = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += o;
     }
-    if (lane == 31) s_sums[warp + 1] = run;
+    return v;
+  };
+  unsigned total, mine = 0, run = 0;  // of a lane's sequence, and up to it
+  if (n <= 32) {
+    mine = tiles_of(min(lane, n - 1), lane < n);
+    run = scan(mine);
+    total = __shfl_sync(0xffffffffu, run, 31);
+    __syncwarp();
+  } else {
+    unsigned sum = 0;
+    for (int i = tid * chunk; i < min(n, (tid + 1) * chunk); ++i) sum += tiles_of(i, true);
+    sum = scan(sum);
+    if (lane == 31) s_sums[warp + 1] = sum;
     __syncthreads();
     if (warp == 0) {  // over the warps
-      unsigned all = lane > 0 && lane <= kWarps ? s_sums[lane] : 0;
-#pragma unroll
-      for (int off = 1; off < 32; off *= 2) {
-        const unsigned o = __shfl_up_sync(0xffffffffu, all, off);
-        if (lane >= off) all += o;
-      }
+      const unsigned all = scan(lane > 0 && lane <= kWarps ? s_sums[lane] : 0);
       if (lane <= kWarps) s_sums[lane] = all;
     }
     __syncthreads();
-    s_pre[tid + 1] = run + s_sums[warp];
+    s_pre[tid + 1] = sum + s_sums[warp];
     if (tid == 0) s_pre[0] = 0;
     __syncthreads();
+    total = s_pre[kThreads];
   }
-  const unsigned total = s_pre[kThreads];
   // as many blocks as have a tile for each warp
   const int blocks = (int)min((total + kWarps - 1) / kWarps, gridDim.x);
   const bool works = (int)blockIdx.x < blocks;
@@ -261,32 +268,51 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   auto block_at = [&](int b) { return each * b + rest * b / blocks; };  // first tile of block b
   const unsigned bu0 = works ? block_at(blockIdx.x) : 0, bu1 = works ? block_at(blockIdx.x + 1) : 0;
   const unsigned w_each = (bu1 - bu0) / kWarps, w_rest = (bu1 - bu0) % kWarps;
-  const unsigned u0 = bu0 + w_each * warp + w_rest * warp / kWarps;
-  const unsigned u1 = bu0 + w_each * (warp + 1) + w_rest * (warp + 1) / kWarps;
+  unsigned u0 = bu0 + w_each * warp + w_rest * warp / kWarps;
+  unsigned u1 = bu0 + w_each * (warp + 1) + w_rest * (warp + 1) / kWarps;
 
   // ---- the warp's first tile
-  cur.seq = cur.item = cur.tile = cur.nt = 0;
-  if (u0 < u1) {
-    // the chunk: of which warp, then of which lane
-    int ch = 32 * __popc(__ballot_sync(0xffffffffu, lane < kWarps && s_sums[min(lane, kWarps - 1) + 1] <= u0));
-    ch += __popc(__ballot_sync(0xffffffffu, s_pre[ch + lane + 1] <= u0));
-    cur.seq = min(n - 1, ch * chunk + lane);
-    cur.load(a);
-    const unsigned mine = lane < chunk && ch * chunk + lane < n ? (unsigned)cur.nt * items : 0;
-    unsigned run = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off *= 2) {
-      const unsigned o = __shfl_up_sync(0xffffffffu, run, off);
-      if (lane >= off) run += o;
+  auto locate = [&](unsigned u) {
+    int ch = 0;
+    unsigned base = 0, m = mine, r = run;
+    if (n > 32) {  // the chunk: of which warp, then of which lane
+      ch = 32 * __popc(__ballot_sync(0xffffffffu, lane < kWarps && s_sums[min(lane, kWarps - 1) + 1] <= u));
+      ch += __popc(__ballot_sync(0xffffffffu, s_pre[ch + lane + 1] <= u));
+      m = tiles_of(min(n - 1, ch * chunk + lane), lane < chunk && ch * chunk + lane < n);
+      r = scan(m);
+      base = s_pre[ch];
     }
-    const unsigned base = s_pre[ch];
-    const int who = __popc(__ballot_sync(0xffffffffu, base + run <= u0));  // lanes whose sequences end before
-    const unsigned left = u0 - base - __shfl_sync(0xffffffffu, run - mine, who);
-    cur.seq = ch * chunk + who;
+    const int who = __popc(__ballot_sync(0xffffffffu, base + r <= u));  // lanes whose sequences end before
+    const unsigned left = u - base - __shfl_sync(0xffffffffu, r - m, who);
+    cur.seq = (n > 32 ? ch * chunk : 0) + who;
     cur.load(a);
     cur.item = (int)(left / (unsigned)cur.nt);
     cur.tile = (int)(left % (unsigned)cur.nt);
+  };
+  // Short items stay whole: where they have four tiles or fewer on average, a run that would begin within an item of
+  // so few begins with the next (256 sequences of 64 positions: XX us, cut anywhere 27).
+  constexpr int kShort = 4;
+  if (total != 0 && total <= kShort * (unsigned)items * n) {
+    if (warp == kWarps - 1) {  // where the next block begins
+      unsigned end = bu1;
+      if (works && bu1 < total) {
+        locate(bu1);
+        if (cur.tile != 0 && cur.nt <= kShort) end += cur.nt - cur.tile;
+      }
+      if (lane == 0) s_start[kWarps] = end;
+    }
+    unsigned start = u0;
+    if (works && u0 < total) {
+      locate(u0);
+      if (cur.tile != 0 && cur.nt <= kShort) start += cur.nt - cur.tile;
+    }
+    if (lane == 0) s_start[warp] = start;
+    __syncthreads();
+    u0 = start;
+    u1 = s_start[warp + 1];
   }
+  cur.seq = cur.item = cur.tile = cur.nt = 0;
+  if (u0 < u1) locate(u0);
   AtCursor<kTile> is = cur;  // of the next tile to copy
 
   uint8_t *const tiles = sm + (size_t)warp * kStages * 2 * S::kHalf;
@@ -751,202 +777,200 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   const uint32_t last_run = last_open ? run_of(31 - __clz(all_at)) : 0u;
   // of items that other blocks share: the first, not begun here; the last, begun here and open
   const bool first_part = (first_run & all_at) && !(first_run & began_at), last_part = (last_run & began_at) != 0u;
-  uint32_t turn = 0;  // of s_join
-  const uint32_t size = (uint32_t)(2 * kHeads + slots * 4) * 4;  // bytes of a part
-  float *const s_ends = s_open + kWarps * S::kPart;
-  const bool fetches = S::kBoth && ends_at != 0u;
-  if (fetches && tid == 0) {
-    at_fence_copies();
-    mbar_arrive_expect_tx(&s_join, size * (uint32_t)__popc(ends_at));
-    for (uint32_t left = ends_at; left; left &= left - 1u) {
-      const int w = (__ffs(left) - 1) / 2;
-      bulk_g2s(s_ends + (size_t)w * S::kPart, work + (size_t)(blockIdx.x * kWarps + w) * S::kPart, size, &s_join);
+  if (all_at != 0u) {
+    uint32_t turn = 0, heads_turn = 0;  // of s_join, s_heads
+    const uint32_t size = (uint32_t)(2 * kHeads + slots * 4) * 4;  // bytes of a part
+    float *const s_ends = s_open + kWarps * S::kPart;
+    const bool fetches = S::kBoth && ends_at != 0u;
+    if (fetches && tid == 0) {
+      at_fence_copies();
+      mbar_arrive_expect_tx(&s_join, size * (uint32_t)__popc(ends_at));
+      for (uint32_t left = ends_at; left; left &= left - 1u) {
+        const int w = (__ffs(left) - 1) / 2;
+        bulk_g2s(s_ends + (size_t)w * S::kPart, work + (size_t)(blockIdx.x * kWarps + w) * S::kPart, size, &s_join);
+      }
     }
-  }
-  if (joins) {
+    if (joins) {
 #pragma unroll 1
-    for (int h = warp; h < kHeads; h += kWarps) {  // the parts' weights, with 1 / sum where the item ends here
-      const uint32_t run = run_of(lane);
-      const int from = __ffs(run) - 1, to = 31 - __clz(run);
-      const bool is_there = all_at >> lane & 1u, ended = ends_at >> to & 1u, here = (run & began_at) != 0u;
-      const float mine = is_there ? s_m[min(lane, 2 * kWarps - 1)][h] : -INFINITY;
-      float top = mine;
+      for (int h = warp; h < kHeads; h += kWarps) {  // the parts' weights, with 1 / sum where the item ends here
+        const uint32_t run = run_of(lane);
+        const int from = __ffs(run) - 1, to = 31 - __clz(run);
+        const bool is_there = all_at >> lane & 1u, ended = ends_at >> to & 1u, here = (run & began_at) != 0u;
+        const float mine = is_there ? s_m[min(lane, 2 * kWarps - 1)][h] : -INFINITY;
+        float top = mine;
 #pragma unroll
-      for (int off = 1; off < 32; off *= 2) {
-        const float o = __shfl_down_sync(0xffffffffu, top, off);
-        if (lane + off <= to) top = fmaxf(top, o);
-      }
-      top = __shfl_sync(0xffffffffu, top, from);
-      float w = at_keep(mine, top == -INFINITY ? 0.f : top), sum = is_there ? w * s_l[min(lane, 2 * kWarps - 1)][h] : 0.f;
+        for (int off = 1; off < 32; off *= 2) {
+          const float o = __shfl_down_sync(0xffffffffu, top, off);
+          if (lane + off <= to) top = fmaxf(top, o);
+        }
+        top = __shfl_sync(0xffffffffu, top, from);
+        float w = at_keep(mine, top == -INFINITY ? 0.f : top), sum = is_there ? w * s_l[min(lane, 2 * kWarps - 1)][h] : 0.f;
 #pragma unroll
-      for (int off = 1; off < 32; off *= 2) {
-        const float o = __shfl_down_sync(0xffffffffu, sum, off);
-        if (lane + off <= to) sum += o;
-      }
-      sum = __shfl_sync(0xffffffffu, sum, from);
-      if (ended && here) w *= sum != 0.f ? 1.f / sum : 0.f;
-      if (is_there) s_m[lane][h] = w;
-      if (lane == from && (run & all_at)) {
-        if (ended && here) {
-          write_lse(s_parts[to / 2].seq[0], s_parts[to / 2].item[0], h, top, sum);
-        } else {
-          float *const part = here ? block_part1 : block_part0;
-          part[h] = top;
-          part[kHeads + h] = sum;
+        for (int off = 1; off < 32; off *= 2) {
+          const float o = __shfl_down_sync(0xffffffffu, sum, off);
+          if (lane + off <= to) sum += o;
+        }
+        sum = __shfl_sync(0xffffffffu, sum, from);
+        if (ended && here) w *= sum != 0.f ? 1.f / sum : 0.f;
+        if (is_there) s_m[lane][h] = w;
+        if (lane == from && (run & all_at)) {
+          if (ended && here) {
+            write_lse(s_parts[to / 2].seq[0], s_parts[to / 2].item[0], h, top, sum);
+          } else {
+            float *const part = here ? block_part1 : block_part0;
+            part[h] = top;
+            part[kHeads + h] = sum;
+          }
         }
       }
     }
-  }
-  const bool came = !fetches || mbar_wait(&s_join, turn);
-  if (fetches) turn ^= 1u;
-  const bool whole_parts = !__syncthreads_or(!came);
-  if (!whole_parts && tid == 0) set_error(a.err, kErrTimeout);
+    const bool came = !fetches || mbar_wait(&s_join, turn);
+    if (fetches) turn ^= 1u;
+    const bool whole_parts = !__syncthreads_or(!came);
+    if (!whole_parts && tid == 0) set_error(a.err, kErrTimeout);
 #pragma unroll 1
-  for (int slot = tid; whole_parts && slot < slots; slot += kThreads) {
-    const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
+    for (int slot = tid; whole_parts && slot < slots; slot += kThreads) {
+      const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
 #pragma unroll 1
-    for (uint32_t left = all_at; left;) {
-      const uint32_t run = run_of(__ffs(left) - 1) & all_at;
-      left &= ~run;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (uint32_t left = all_at; left;) {
+        const uint32_t run = run_of(__ffs(left) - 1) & all_at;
+        left &= ~run;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (uint32_t m = run; m; m &= m - 1u) {
-        const int k = __ffs(m) - 1, w = k / 2;
-        const float *p = k & 1 ? s_open + (size_t)w * S::kPart
-                               : S::kBoth ? s_ends + (size_t)w * S::kPart : work + (size_t)(blockIdx.x * kWarps + w) * S::kPart;
-        const float4 f = reinterpret_cast<const float4 *>(p + 2 * kHeads)[slot];
-        const float2 w2 = *reinterpret_cast<const float2 *>(&s_m[k][h]);
-        v.x = fmaf(f.x, w2.x, v.x);
-        v.y = fmaf(f.y, w2.y, v.y);
-        v.z = fmaf(f.z, w2.x, v.z);
-        v.w = fmaf(f.w, w2.y, v.w);
+        for (uint32_t m = run; m; m &= m - 1u) {
+          const int k = __ffs(m) - 1, w = k / 2;
+          const float *p = k & 1 ? s_open + (size_t)w * S::kPart
+                                 : S::kBoth ? s_ends + (size_t)w * S::kPart : work + (size_t)(blockIdx.x * kWarps + w) * S::kPart;
+          const float4 f = reinterpret_cast<const float4 *>(p + 2 * kHeads)[slot];
+          const float2 w2 = *reinterpret_cast<const float2 *>(&s_m[k][h]);
+          v.x = fmaf(f.x, w2.x, v.x);
+          v.y = fmaf(f.y, w2.y, v.y);
+          v.z = fmaf(f.z, w2.x, v.z);
+          v.w = fmaf(f.w, w2.y, v.w);
+        }
+        // an item that began and ends here: to its last open part's place
+        const bool here = (run & began_at) != 0u, ended = (run & ends_at) != 0u;
+        float *const to = !here ? block_part0 : ended ? s_open + (size_t)((31 - __clz(run & open_at)) / 2) * S::kPart : block_part1;
+        reinterpret_cast<float4 *>(to + 2 * kHeads)[slot] = v;
       }
-      // an item that began and ends here: to its last open part's place
-      const bool here = (run & began_at) != 0u, ended = (run & ends_at) != 0u;
-      float *const to = !here ? block_part0 : ended ? s_open + (size_t)((31 - __clz(run & open_at)) / 2) * S::kPart : block_part1;
-      reinterpret_cast<float4 *>(to + 2 * kHeads)[slot] = v;
     }
-  }
-  __syncthreads();
+    __syncthreads();
 #pragma unroll 1
-  for (uint32_t left = ends_at; left && whole_parts; left &= left - 1u) {  // items that warps shared and that began and ended here
-    const int k = __ffs(left) - 1;
-    const uint32_t run = run_of(k);
-    if (run & began_at)
-      write_out(s_parts[k / 2].seq[0], s_parts[k / 2].item[0], s_open + (size_t)((31 - __clz(run & open_at)) / 2) * S::kPart);
-  }
+    for (uint32_t left = ends_at; left && whole_parts; left &= left - 1u) {  // items that warps shared and that began and ended here
+      const int k = __ffs(left) - 1;
+      const uint32_t run = run_of(k);
+      if (run & began_at)
+        write_out(s_parts[k / 2].seq[0], s_parts[k / 2].item[0], s_open + (size_t)((31 - __clz(run & open_at)) / 2) * S::kPart);
+    }
 
-  // ---- the last block of an item joins the blocks' parts
-  if ((first_part || last_part) && whole_parts) {  // (the same for every thread)
-    at_fence_copies();
-    __threadfence();
-    __syncthreads();
-    const int first_k = 31 - __clz(first_run & all_at), last_k = 31 - __clz(last_run & all_at);  // a part that tells the item
-    if (tid < 2) {
-      s_last[tid] = 0;
-      if (tid == 0 ? first_part : last_part) {
-        const int k = tid == 0 ? first_k : last_k;
-        const AtWarpParts &p = s_parts[k / 2];
-        // the blocks of its first and its last tile: the largest b with total * b / blocks <= tile
-        auto of = [&](unsigned t) { return (int)((((unsigned long long)t + 1) * (unsigned)blocks - 1) / total); };
-        const int from = of(p.at[k & 1]), count = of(p.at[k & 1] + (unsigned)p.nt[k & 1] - 1) - from + 1;
-        s_from[tid] = from;
-        s_count[tid] = count;
-        if (atomicAdd(a.tickets + from, 1u) + 1u == (unsigned)count) {
-          __threadfence();
-          a.tickets[from] = 0u;
-          s_last[tid] = 1;
-        }
-      }
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      if (!s_last[which]) continue;
-      // Parts come to shared memory a room full at a time, by bulk copies, while their weights are worked out.
-      const int n_parts = s_count[which], f = s_from[which];
-      float *const s_w = reinterpret_cast<float *>(sm), *const s_sum = s_w + n_parts * kHeads;  // weights, 1 / sums
-      const uint32_t head = ((uint32_t)(n_parts + 1) * kHeads * 4 + 127) & ~127u;
-      float *const s_out = reinterpret_cast<float *>(sm + head), *const s_room = s_out + size / 4;  // the sum; parts
-      const int fit = min(n_parts, (int)((S::kRoom - head) / size) - 1);
-      auto part = [&](int b) { return block_parts + (size_t)(2 * (f + b) + (b == 0 ? 1 : 0)) * S::kPart; };
+    // ---- the last block of an item joins the blocks' parts
+    if ((first_part || last_part) && whole_parts) {  // (the same for every thread)
+      at_fence_copies();
+      __threadfence();
       __syncthreads();
-      bool ran_out = false;
-#pragma unroll 1
-      for (int b0 = 0; b0 < n_parts && !ran_out; b0 += fit) {
-        const int many = min(fit, n_parts - b0);
-        if (warp == 0) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&s_join, (uint32_t)many * size);
-          }
-          __syncwarp();
-          for (int b = lane; b < many; b += 32) {
-            at_fence_copies();  // what other blocks wrote, and this one read here
-            bulk_g2s(s_room + (size_t)b * (size / 4), part(b0 + b), size, &s_join);
-          }
-        }
-        if (b0 == 0) {
-#pragma unroll 1
-          for (int h = warp; h < kHeads; h += kWarps) {
-            constexpr int kLane = kAtMaxGrid / 32;  // parts of a lane
-            float top = -INFINITY, sum = 0.f, m1[kLane], l1[kLane];
-#pragma unroll
-            for (int i = 0; i < kLane; ++i) {
-              const int b = lane + 32 * i;
-              m1[i] = b < n_parts ? __ldcg(part(b) + h) : -INFINITY;
-              l1[i] = b < n_parts ? __ldcg(part(b) + kHeads + h) : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < kLane; ++i) top = fmaxf(top, m1[i]);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float use = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int i = 0; i < kLane; ++i) {
-              const float w = at_keep(m1[i], use);
-              if (lane + 32 * i < n_parts) s_w[(lane + 32 * i) * kHeads + h] = w;
-              sum += w * l1[i];
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (lane == 0) {
-              const AtWarpParts &p = s_parts[(which ? last_k : first_k) / 2];
-              const int o = (which ? last_k : first_k) & 1;
-              s_sum[h] = sum != 0.f ? 1.f / sum : 0.f;
-              write_lse(p.seq[o], p.item[o], h, top, sum);
-            }
+      const int first_k = 31 - __clz(first_run & all_at), last_k = 31 - __clz(last_run & all_at);  // a part that tells the item
+      if (tid < 2) {
+        s_last[tid] = 0;
+        if (tid == 0 ? first_part : last_part) {
+          const int k = tid == 0 ? first_k : last_k;
+          const AtWarpParts &p = s_parts[k / 2];
+          // the blocks of its first and its last tile: the largest b with total * b / blocks <= tile
+          auto of = [&](unsigned t) { return (int)((((unsigned long long)t + 1) * (unsigned)blocks - 1) / total); };
+          const int from = of(p.at[k & 1]), count = of(p.at[k & 1] + (unsigned)p.nt[k & 1] - 1) - from + 1;
+          s_from[tid] = from;
+          s_count[tid] = count;
+          if (atomicAdd(a.tickets + from, 1u) + 1u == (unsigned)count) {
+            __threadfence();
+            a.tickets[from] = 0u;
+            s_last[tid] = 1;
           }
         }
-        ran_out = __syncthreads_or(!mbar_wait(&s_join, turn));
-        turn ^= 1u;
+      }
+      __syncthreads();
 #pragma unroll 1
-        for (int slot = tid; slot < slots && !ran_out; slot += kThreads) {
-          const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          float4 *const to = reinterpret_cast<float4 *>(s_out + 2 * kHeads) + slot;
-          if (b0) v = *to;
-#pragma unroll 4
-          for (int b = 0; b < many; ++b) {
-            const float4 p = reinterpret_cast<const float4 *>(s_room + (size_t)b * (size / 4) + 2 * kHeads)[slot];
-            const float2 w = *reinterpret_cast<const float2 *>(s_w + (b0 + b) * kHeads + h);
-            v.x = fmaf(p.x, w.x, v.x);
-            v.y = fmaf(p.y, w.y, v.y);
-            v.z = fmaf(p.z, w.x, v.z);
-            v.w = fmaf(p.w, w.y, v.w);
-          }
-          const float f0 = b0 + many < n_parts ? 1.f : s_sum[h], f1 = b0 + many < n_parts ? 1.f : s_sum[h + 1];
-          *to = make_float4(v.x * f0, v.y * f1, v.z * f0, v.w * f1);
-        }
+      for (int which = 0; which < 2; ++which) {
+        if (!s_last[which]) continue;
+        // Parts come to shared memory a room full at a time, by bulk copies, while their weights are worked out.
+        const int n_parts = s_count[which], f = s_from[which];
+        // the parts' maxima, then weights, and sums; 1 / sum
+        float *const s_stat = reinterpret_cast<float *>(sm), *const s_sum = s_stat + n_parts * 2 * kHeads;
+        const uint32_t head = ((uint32_t)(2 * n_parts + 1) * kHeads * 4 + 127) & ~127u;
+        float *const s_out = reinterpret_cast<float *>(sm + head), *const s_room = s_out + size / 4;  // the sum; parts
+        const int fit = min(n_parts, (int)((S::kRoom - head) / size) - 1);
+        auto part = [&](int b) { return block_parts + (size_t)(2 * (f + b) + (b == 0 ? 1 : 0)) * S::kPart; };
         __syncthreads();
+        bool ran_out = false;
+#pragma unroll 1
+        for (int b0 = 0; b0 < n_parts && !ran_out; b0 += fit) {
+          const int many = min(fit, n_parts - b0);
+          if (warp == 0) {
+            if (lane == 0) {
+              if (b0 == 0) mbar_arrive_expect_tx(&s_heads, (uint32_t)n_parts * (2 * kHeads * 4));
+              mbar_arrive_expect_tx(&s_join, (uint32_t)many * size);
+            }
+            __syncwarp();
+            at_fence_copies();  // what other blocks wrote, and this one read here
+            if (b0 == 0)
+              for (int b = lane; b < n_parts; b += 32) bulk_g2s(s_stat + b * 2 * kHeads, part(b), 2 * kHeads * 4, &s_heads);
+            for (int b = lane; b < many; b += 32) bulk_g2s(s_room + (size_t)b * (size / 4), part(b0 + b), size, &s_join);
+          }
+          if (b0 == 0) {
+            ran_out = !mbar_wait(&s_heads, heads_turn);
+            heads_turn ^= 1u;
+#pragma unroll 1
+            for (int h = warp; h < kHeads; h += kWarps) {
+              float top = -INFINITY, sum = 0.f;
+              for (int b = lane; b < n_parts; b += 32) top = fmaxf(top, s_stat[b * 2 * kHeads + h]);
+#pragma unroll
+              for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+              const float use = top == -INFINITY ? 0.f : top;
+              for (int b = lane; b < n_parts; b += 32) {
+                const float w = at_keep(s_stat[b * 2 * kHeads + h], use);
+                s_stat[b * 2 * kHeads + h] = w;
+                sum += w * s_stat[b * 2 * kHeads + kHeads + h];
+              }
+#pragma unroll
+              for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+              if (lane == 0) {
+                const AtWarpParts &p = s_parts[(which ? last_k : first_k) / 2];
+                const int o = (which ? last_k : first_k) & 1;
+                s_sum[h] = sum != 0.f ? 1.f / sum : 0.f;
+                write_lse(p.seq[o], p.item[o], h, top, sum);
+              }
+            }
+          }
+          ran_out = __syncthreads_or(ran_out || !mbar_wait(&s_join, turn));
+          turn ^= 1u;
+#pragma unroll 1
+          for (int slot = tid; slot < slots && !ran_out; slot += kThreads) {
+            const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 *const to = reinterpret_cast<float4 *>(s_out + 2 * kHeads) + slot;
+            if (b0) v = *to;
+#pragma unroll 4
+            for (int b = 0; b < many; ++b) {
+              const float4 p = reinterpret_cast<const float4 *>(s_room + (size_t)b * (size / 4) + 2 * kHeads)[slot];
+              const float2 w = *reinterpret_cast<const float2 *>(s_stat + (b0 + b) * 2 * kHeads + h);
+              v.x = fmaf(p.x, w.x, v.x);
+              v.y = fmaf(p.y, w.y, v.y);
+              v.z = fmaf(p.z, w.x, v.z);
+              v.w = fmaf(p.w, w.y, v.w);
+            }
+            const float f0 = b0 + many < n_parts ? 1.f : s_sum[h], f1 = b0 + many < n_parts ? 1.f : s_sum[h + 1];
+            *to = make_float4(v.x * f0, v.y * f1, v.z * f0, v.w * f1);
+          }
+          __syncthreads();
+        }
+        if (ran_out) {
+          if (tid == 0) set_error(a.err, kErrTimeout);
+          break;
+        }
+        const AtWarpParts &p = s_parts[(which ? last_k : first_k) / 2];
+        const int o = (which ? last_k : first_k) & 1;
+        write_out(p.seq[o], p.item[o], s_out);
       }
-      if (ran_out) {
-        if (tid == 0) set_error(a.err, kErrTimeout);
-        break;
-      }
-      const AtWarpParts &p = s_parts[(which ? last_k : first_k) / 2];
-      const int o = (which ? last_k : first_k) & 1;
-      write_out(p.seq[o], p.item[o], s_out);
     }
+
   }
 
   // ---- sequences without a position to look at

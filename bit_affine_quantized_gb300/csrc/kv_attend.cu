@@ -81,8 +81,9 @@ __device__ __forceinline__ void at_tma(void *dst, const CUtensorMap *map, int x,
       "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
 }
-// Orders what went before by plain accesses and what comes after by copies.
-__device__ __forceinline__ void at_fence_copies() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void at_copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void at_prefetch(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   extern __shared__ uint8_t at_raw[];
   uint8_t *const sm = at_raw + ((1024 - (smem_addr(at_raw) & 1023)) & 1023);
   float *const s_scales = reinterpret_cast<float *>(sm + S::kRoom);
-  __shared__ uint64_t s_keys[kWarps][kStages], s_values[kWarps][kStages], s_join, s_heads;
+  __shared__ uint64_t s_keys[kWarps][kStages], s_values[kWarps][kStages];
   __shared__ unsigned s_pre[kThreads + 1], s_sums[kWarps + 1], s_start[kWarps + 1];
   __shared__ AtWarpParts s_parts[kWarps];
   __shared__ __align__(16) float s_m[2 * kWarps][kHeads], s_l[2 * kWarps][kHeads];  // of the warps' parts; then their weights
@@ -211,8 +212,6 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     mbar_init(&s_values[warp][lane], 1);
   }
   if (tid == 0) {
-    mbar_init(&s_join, 1);
-    mbar_init(&s_heads, 1);
     at_prefetch(&prm.k);
     at_prefetch(&prm.v);
   }
@@ -731,7 +730,6 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     p.nt[1] = cur.nt;
     p.at[1] = u1 - 1 - (unsigned)cur.tile;
   }
-  at_fence_copies();
   // the tiles are read: parts take their places.  After a wait that ran out nothing is joined (the error tells).
   const bool joins = !__syncthreads_or(late);
   float *const s_open = reinterpret_cast<float *>(sm);
@@ -778,16 +776,13 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   // of items that other blocks share: the first, not begun here; the last, begun here and open
   const bool first_part = (first_run & all_at) && !(first_run & began_at), last_part = (last_run & began_at) != 0u;
   if (all_at != 0u) {
-    uint32_t turn = 0, heads_turn = 0;  // of s_join, s_heads
-    const uint32_t size = (uint32_t)(2 * kHeads + slots * 4) * 4;  // bytes of a part
     float *const s_ends = s_open + kWarps * S::kPart;
-    const bool fetches = S::kBoth && ends_at != 0u;
-    if (fetches && tid == 0) {
-      at_fence_copies();
-      mbar_arrive_expect_tx(&s_join, size * (uint32_t)__popc(ends_at));
+    if (S::kBoth) {  // the parts in the workspace, on their way while the weights are worked out
+#pragma unroll 1
       for (uint32_t left = ends_at; left; left &= left - 1u) {
-        const int w = (__ffs(left) - 1) / 2;
-        bulk_g2s(s_ends + (size_t)w * S::kPart, work + (size_t)(blockIdx.x * kWarps + w) * S::kPart, size, &s_join);
+        const size_t at = (size_t)((__ffs(left) - 1) / 2) * S::kPart + 2 * kHeads;
+        for (int slot = tid; slot < slots; slot += kThreads)
+          at_copy16(s_ends + at + 4 * slot, work + (size_t)(blockIdx.x * kWarps) * S::kPart + at + 4 * slot);
       }
     }
     if (joins) {
@@ -824,12 +819,10 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
         }
       }
     }
-    const bool came = !fetches || mbar_wait(&s_join, turn);
-    if (fetches) turn ^= 1u;
-    const bool whole_parts = !__syncthreads_or(!came);
-    if (!whole_parts && tid == 0) set_error(a.err, kErrTimeout);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
 #pragma unroll 1
-    for (int slot = tid; whole_parts && slot < slots; slot += kThreads) {
+    for (int slot = tid; slot < slots; slot += kThreads) {
       const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
 #pragma unroll 1
       for (uint32_t left = all_at; left;) {
@@ -839,9 +832,10 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
 #pragma unroll 4
         for (uint32_t m = run; m; m &= m - 1u) {
           const int k = __ffs(m) - 1, w = k / 2;
-          const float *p = k & 1 ? s_open + (size_t)w * S::kPart
-                                 : S::kBoth ? s_ends + (size_t)w * S::kPart : work + (size_t)(blockIdx.x * kWarps + w) * S::kPart;
-          const float4 f = reinterpret_cast<const float4 *>(p + 2 * kHeads)[slot];
+          const float *const in = (k & 1 ? s_open : s_ends) + (size_t)w * S::kPart + 2 * kHeads;
+          const float *const ws = work + (size_t)(blockIdx.x * kWarps + w) * S::kPart + 2 * kHeads;
+          const float4 f = (k & 1) || S::kBoth ? reinterpret_cast<const float4 *>(in)[slot]
+                                               : __ldcg(reinterpret_cast<const float4 *>(ws) + slot);
           const float2 w2 = *reinterpret_cast<const float2 *>(&s_m[k][h]);
           v.x = fmaf(f.x, w2.x, v.x);
           v.y = fmaf(f.y, w2.y, v.y);
@@ -856,7 +850,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     }
     __syncthreads();
 #pragma unroll 1
-    for (uint32_t left = ends_at; left && whole_parts; left &= left - 1u) {  // items that warps shared and that began and ended here
+    for (uint32_t left = ends_at; left; left &= left - 1u) {  // items that warps shared and that began and ended here
       const int k = __ffs(left) - 1;
       const uint32_t run = run_of(k);
       if (run & began_at)
@@ -864,8 +858,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     }
 
     // ---- the last block of an item joins the blocks' parts
-    if ((first_part || last_part) && whole_parts) {  // (the same for every thread)
-      at_fence_copies();
+    if (first_part || last_part) {  // (the same for every thread)
       __threadfence();
       __syncthreads();
       const int first_k = 31 - __clz(first_run & all_at), last_k = 31 - __clz(last_run & all_at);  // a part that tells the item
@@ -890,83 +883,66 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
 #pragma unroll 1
       for (int which = 0; which < 2; ++which) {
         if (!s_last[which]) continue;
-        // Parts come to shared memory a room full at a time, by bulk copies, while their weights are worked out.
         const int n_parts = s_count[which], f = s_from[which];
-        // the parts' maxima, then weights, and sums; 1 / sum
+        // the parts' maxima, then weights, and sums; 1 / sum; the output's sum
         float *const s_stat = reinterpret_cast<float *>(sm), *const s_sum = s_stat + n_parts * 2 * kHeads;
-        const uint32_t head = ((uint32_t)(2 * n_parts + 1) * kHeads * 4 + 127) & ~127u;
-        float *const s_out = reinterpret_cast<float *>(sm + head), *const s_room = s_out + size / 4;  // the sum; parts
-        const int fit = min(n_parts, (int)((S::kRoom - head) / size) - 1);
+        float *const s_out = s_sum + 2 * kHeads;
         auto part = [&](int b) { return block_parts + (size_t)(2 * (f + b) + (b == 0 ? 1 : 0)) * S::kPart; };
-        __syncthreads();
-        bool ran_out = false;
-#pragma unroll 1
-        for (int b0 = 0; b0 < n_parts && !ran_out; b0 += fit) {
-          const int many = min(fit, n_parts - b0);
-          if (warp == 0) {
-            if (lane == 0) {
-              if (b0 == 0) mbar_arrive_expect_tx(&s_heads, (uint32_t)n_parts * (2 * kHeads * 4));
-              mbar_arrive_expect_tx(&s_join, (uint32_t)many * size);
-            }
-            __syncwarp();
-            at_fence_copies();  // what other blocks wrote, and this one read here
-            if (b0 == 0)
-              for (int b = lane; b < n_parts; b += 32) bulk_g2s(s_stat + b * 2 * kHeads, part(b), 2 * kHeads * 4, &s_heads);
-            for (int b = lane; b < many; b += 32) bulk_g2s(s_room + (size_t)b * (size / 4), part(b0 + b), size, &s_join);
-          }
-          if (b0 == 0) {
-            ran_out = !mbar_wait(&s_heads, heads_turn);
-            heads_turn ^= 1u;
-#pragma unroll 1
-            for (int h = warp; h < kHeads; h += kWarps) {
-              float top = -INFINITY, sum = 0.f;
-              for (int b = lane; b < n_parts; b += 32) top = fmaxf(top, s_stat[b * 2 * kHeads + h]);
-#pragma unroll
-              for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-              const float use = top == -INFINITY ? 0.f : top;
-              for (int b = lane; b < n_parts; b += 32) {
-                const float w = at_keep(s_stat[b * 2 * kHeads + h], use);
-                s_stat[b * 2 * kHeads + h] = w;
-                sum += w * s_stat[b * 2 * kHeads + kHeads + h];
-              }
-#pragma unroll
-              for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-              if (lane == 0) {
-                const AtWarpParts &p = s_parts[(which ? last_k : first_k) / 2];
-                const int o = (which ? last_k : first_k) & 1;
-                s_sum[h] = sum != 0.f ? 1.f / sum : 0.f;
-                write_lse(p.seq[o], p.item[o], h, top, sum);
-              }
-            }
-          }
-          ran_out = __syncthreads_or(ran_out || !mbar_wait(&s_join, turn));
-          turn ^= 1u;
-#pragma unroll 1
-          for (int slot = tid; slot < slots && !ran_out; slot += kThreads) {
-            const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            float4 *const to = reinterpret_cast<float4 *>(s_out + 2 * kHeads) + slot;
-            if (b0) v = *to;
-#pragma unroll 4
-            for (int b = 0; b < many; ++b) {
-              const float4 p = reinterpret_cast<const float4 *>(s_room + (size_t)b * (size / 4) + 2 * kHeads)[slot];
-              const float2 w = *reinterpret_cast<const float2 *>(s_stat + (b0 + b) * 2 * kHeads + h);
-              v.x = fmaf(p.x, w.x, v.x);
-              v.y = fmaf(p.y, w.y, v.y);
-              v.z = fmaf(p.z, w.x, v.z);
-              v.w = fmaf(p.w, w.y, v.w);
-            }
-            const float f0 = b0 + many < n_parts ? 1.f : s_sum[h], f1 = b0 + many < n_parts ? 1.f : s_sum[h + 1];
-            *to = make_float4(v.x * f0, v.y * f1, v.z * f0, v.w * f1);
-          }
-          __syncthreads();
-        }
-        if (ran_out) {
-          if (tid == 0) set_error(a.err, kErrTimeout);
-          break;
-        }
         const AtWarpParts &p = s_parts[(which ? last_k : first_k) / 2];
         const int o = (which ? last_k : first_k) & 1;
+        // sixteen parts' share of a slot at a time, the first of them before the weights are known
+        constexpr int kAhead = 16;
+        float4 v[kAhead];
+        auto fetch = [&](int slot, int b0) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+            if (b0 + i < n_parts) v[i] = __ldcg(reinterpret_cast<const float4 *>(part(b0 + i) + 2 * kHeads) + slot);
+        };
+        __syncthreads();
+        for (int i = tid; i < n_parts * 2 * kHeads; i += kThreads) s_stat[i] = __ldcg(part(i / (2 * kHeads)) + i % (2 * kHeads));
+        if (tid < slots) fetch(tid, 0);
+        __syncthreads();
+#pragma unroll 1
+        for (int h = warp; h < kHeads; h += kWarps) {
+          float top = -INFINITY, sum = 0.f;
+          for (int b = lane; b < n_parts; b += 32) top = fmaxf(top, s_stat[b * 2 * kHeads + h]);
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const float use = top == -INFINITY ? 0.f : top;
+          for (int b = lane; b < n_parts; b += 32) {
+            const float w = at_keep(s_stat[b * 2 * kHeads + h], use);
+            s_stat[b * 2 * kHeads + h] = w;
+            sum += w * s_stat[b * 2 * kHeads + kHeads + h];
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+          if (lane == 0) {
+            s_sum[h] = sum != 0.f ? 1.f / sum : 0.f;
+            write_lse(p.seq[o], p.item[o], h, top, sum);
+          }
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int slot = tid; slot < slots; slot += kThreads) {
+          const int h = 8 * (slot / 32 % kN) + 2 * (slot & 3);
+          float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int b0 = 0; b0 < n_parts; b0 += kAhead) {
+            if (slot != tid || b0 != 0) fetch(slot, b0);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+              if (b0 + i >= n_parts) continue;
+              const float2 w = *reinterpret_cast<const float2 *>(s_stat + (b0 + i) * 2 * kHeads + h);
+              t.x = fmaf(v[i].x, w.x, t.x);
+              t.y = fmaf(v[i].y, w.y, t.y);
+              t.z = fmaf(v[i].z, w.x, t.z);
+              t.w = fmaf(v[i].w, w.y, t.w);
+            }
+          }
+          const float f0 = s_sum[h], f1 = s_sum[h + 1];
+          reinterpret_cast<float4 *>(s_out + 2 * kHeads)[slot] = make_float4(t.x * f0, t.y * f1, t.z * f0, t.w * f1);
+        }
+        __syncthreads();
         write_out(p.seq[o], p.item[o], s_out);
       }
     }

@@ -159,3 +159,31 @@ def test_attention_of_one_sequence_many_times(moe):
                 c[6] = out
             assert torch.equal(out, c[6])  # bit by bit
     assert error(moe) == bq.MOE_OK
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+def test_rows_behind_the_last_sequence(moe, bits8):
+    """Outputs of more rows than there are sequences: those behind the last stay as they were."""
+    lengths = [30, 0, 5]
+    cache = Cache(90, lengths, 2, 64, 16, bits8)
+    q = bf16(np.random.default_rng(9).standard_normal((5, 4, 64)))
+    out, lse = torch.full((5, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((5, 4), 7.0, device="cuda")
+    ws = torch.empty(moe.kv_attend_workspace_bytes(cache.c, 4), dtype=torch.uint8, device="cuda")
+    moe.kv_attend(dev(q), i32(lengths + [9, 9]), cache.c, out, ws, scale=0.1, lse=lse)
+    assert error(moe) == bq.MOE_OK
+    check_attend(cache, q[:3], lengths, 0.1, 0.0, 0, out[:3], lse)
+    assert bool((out[3:] == 7).all()) and bool((lse[3:] == 7).all())
+
+
+def test_workspace_behind_its_size_is_left_alone(moe):
+    """The call writes no byte past the size that it asks for, on shapes that use all kinds of parts."""
+    for lengths, H, group, D, bits8 in (([60000, 9], 1, 16, 256, False), ([3000] * 40, 2, 8, 128, True), ([700] * 90, 3, 1, 64, True)):
+        cache = Cache(91, lengths, H, D, 64, bits8)
+        n = moe.kv_attend_workspace_bytes(cache.c, H * group)
+        ws = torch.full((n + 4096,), 85, dtype=torch.uint8, device="cuda")
+        q = dev(np.ones((len(lengths), H * group, D)))
+        moe.kv_attend(q, i32(lengths), cache.c, torch.empty_like(q), ws[:n], scale=0.1)
+        assert error(moe) == bq.MOE_OK and bool((ws[n:] == 85).all())
+        with pytest.raises(bq.MoeError) as e:
+            moe.kv_attend(q, i32(lengths), cache.c, torch.empty_like(q), ws[:n - 1], scale=0.1)
+        assert e.value.status == bq.MOE_ERR_WORKSPACE

@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   auto piece = [&](uint32_t at, int x) { return (at ^ (uint32_t)((x & 7) << 4)) + (uint32_t)((x >> 3) * kTile * 128); };
 
   const bool capped = a.softcap > 0.f;
-  const float to_cap = capped ? a.scale / a.softcap : a.scale * kLog2e, cap = a.softcap * kLog2e;
+  const float most = 3e38f;  // (finite: a score of 0 stays one)
+  const float to_cap = fminf(fmaxf(capped ? a.scale / a.softcap : a.scale * kLog2e, -most), most), cap = a.softcap * kLog2e;
   // ---- state of the item at hand: lane (g, c) has the heads 8 i + 2 c and the one after
   uint32_t q[kSteps][kN][2];
   float m[kN][2], l[kN][2], o[kSteps][kN][4], qs[kN][2];

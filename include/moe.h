@@ -576,8 +576,9 @@ int moe_kv_append(moe_handle *h, const void *q, size_t q_stride, int q_heads, co
  *   k_out, v_out  nullable bf16 [n_rows, kv_heads, head_dim] with strides of
  *                 multiples of 8 values from row to row, 16-byte aligned; not
  *                 both null
- * A row of a negative position is left as it was; one that is not there is all
- * zeros and records MOE_ERR_BAD_EXPERT_ID. */
+ * Outputs must not overlap the cache or each other.  A row of a negative
+ * position is left as it was; one that is not there is all zeros and records
+ * MOE_ERR_BAD_EXPERT_ID. */
 int moe_kv_read(moe_handle *h, const moe_kv_cache *cache, const int32_t *row_seq, const int32_t *row_pos, int n_rows,
                 void *k_out, size_t k_stride, void *v_out, size_t v_stride, moe_stream_t stream);
 
@@ -602,7 +603,8 @@ size_t moe_kv_attend_workspace_bytes(const moe_kv_cache *cache, int q_heads);
  *            of a key head, or part of them) below 2^31
  *   scale    finite;  softcap 0 or above, finite;  window 0 or above
  *   ws       moe_kv_attend_workspace_bytes(cache, q_heads) bytes, 256-byte aligned
- * A sequence without a position to look at gets zeros and L = -inf.  Positions
+ * Outputs must not overlap inputs (a query is read by several blocks).  A
+ * sequence without a position to look at gets zeros and L = -inf.  Positions
  * of a page that is not there are left out, and one among those looked at
  * records MOE_ERR_BAD_EXPERT_ID; what the cache holds from the length on, or
  * ahead of the window, does not matter.  Sums and statistics are fp32; a weight
@@ -640,7 +642,9 @@ typedef struct {
  *             remaining weights (0 for a greedy row; -inf with token -1)
  * u counts as 0 below 0 or NaN, and as the last remaining token from 1 on.  A
  * NaN filter is off, a NaN temperature is greedy.  A NaN or +inf among the
- * logits counts as -inf and records MOE_ERR_NONFINITE. */
+ * logits counts as -inf and records MOE_ERR_NONFINITE.  The sums are exact over
+ * weights within 2^-21 of their values, the same whatever their order.  Nothing
+ * but the error stays in the handle: calls may overlap. */
 int moe_sample(moe_handle *h, const float *logits, size_t logits_stride, int n_rows, int vocab,
                const moe_sample_rules *rules, int32_t *tokens, float *logprobs, moe_stream_t stream);
 

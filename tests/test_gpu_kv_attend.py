@@ -92,6 +92,17 @@ def test_caps_and_windows(moe, bits8, softcap, window, scale):
 
 
 @pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("scale,softcap", [(1e10, 1e-30), (3e38, 0.0), (3e38, 1e-3), (-3e38, 2.0)])
+def test_scores_of_zero_at_any_scale(moe, bits8, scale, softcap):
+    """Queries of zeros: every score is 0 however large the factors are, the output the mean of the values."""
+    cache = Cache(35, [77, 3], 2, 64, 16, bits8)
+    q = np.zeros((2, 4, 64))
+    out, lse = run(moe, cache, dev(q), i32([77, 3]), scale, softcap)
+    assert moe.get_error() == bq.MOE_OK
+    check(cache, q, [77, 3], 0.0, 0.0, 0, out, lse)
+
+
+@pytest.mark.parametrize("bits8", [False, True])
 def test_a_long_sequence(moe, bits8):
     """One head's positions go to many blocks, next to sequences of a few."""
     lengths = [70001, 3, 0, 20000]

@@ -30,6 +30,7 @@ struct moe_handle {
   bool logits_ready;          // and for the logits kernel
   bool attend_ready;          // and for the attention's
   bool sample_ready;          // and for the sampling's
+  int sample_clusters[moe::kSampleMaxCluster + 1];  // clusters that fit the device, by their blocks
   bool prefill_dense;         // multi-token calls may run dense slots on the tensor cores (tcgen05)
   // failure-detection hook, consumed by the next fused single-token launch
   int skip_block_next;                  // -1: none
@@ -1124,7 +1125,7 @@ int moe_sample(moe_handle *h, const float *logits, size_t logits_stride, int n_r
     if (!aligned(p, 4)) return MOE_ERR_INVALID_ARG;
   if (!on_device(h)) return MOE_ERR_INVALID_ARG;
   if (!h->sample_ready) {
-    if (moe::sample_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    if (moe::sample_set_attributes(h->sample_clusters) != cudaSuccess) return MOE_ERR_CUDA;
     h->sample_ready = true;
   }
   moe::SampleArgs a;
@@ -1141,7 +1142,7 @@ int moe_sample(moe_handle *h, const float *logits, size_t logits_stride, int n_r
   a.V = vocab;
   a.err = h->dwords;
   a.trace = take_trace(h, 1);
-  return cuda_status(moe::launch_sample(a, h->n_sm, (cudaStream_t)stream, h->pdl));
+  return cuda_status(moe::launch_sample(a, h->sample_clusters, (cudaStream_t)stream, h->pdl));
 }
 
 int moe_embed(moe_handle *h, const int32_t *ids, int n, const moe_head_weights *w, void *out, moe_stream_t stream) {

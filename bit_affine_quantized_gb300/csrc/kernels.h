@@ -337,8 +337,10 @@ struct SampleArgs {
   unsigned *err;
   unsigned long long *trace;
 };
-cudaError_t sample_set_attributes();
-cudaError_t launch_sample(const SampleArgs &a, int n_sm, cudaStream_t st, bool pdl);
+constexpr int kSampleMaxCluster = 16;
+// clusters[c], c <= kSampleMaxCluster: clusters of c blocks that the device holds at once
+cudaError_t sample_set_attributes(int *clusters);
+cudaError_t launch_sample(const SampleArgs &a, const int *clusters, cudaStream_t st, bool pdl);
 
 // smem budgets (bytes) for a given shape; 0 = shape not supported by that kernel
 size_t router_smem(const Dims &d, int tb);

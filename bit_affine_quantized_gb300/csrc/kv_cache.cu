@@ -25,6 +25,12 @@
 // the first r dimensions, or two neighbours behind them; D / 16 threads have a
 // head's row, and its maximum goes round them by shuffles.  All loads of a
 // thread's two units are on their way before the first is used.
+//
+// 4096 rows of 16 query and 2 x 8 key and value heads of 256, turned: 23.7 us in
+// bf16 (134 MB, 5.7 TB/s), 28 in 8 bits (117 MB, 4.2 TB/s: the issue slots are 72 %
+// used, 346 instructions a unit and warp); 31 and 25 with four units a thread, 32 and
+// 27 with one.  The angles' table read across its banks and 64-bit floating point per
+// row cost 10 us of it.
 #include <math.h>
 
 #include "kernels.h"

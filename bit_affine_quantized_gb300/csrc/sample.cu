@@ -17,9 +17,18 @@
 // The tokens above the bound are few: for a small k they go to the first block's
 // list at once, else a histogram of their distance to the maximum (512 bins, a
 // count and a sum each, refined by 9 bits where needed) says in which bin the cut
-// falls, and a list takes what lies above its lower end, or in the bin alone.
-// What is in a list is sorted.  Where a bin cannot be
-// refined (many equal logits) the key is found bit by bit.
+// falls, and a list takes what lies above its lower end, or in the bin alone.  The
+// blocks tell each other their bins 16 at a time, then the 16 in question.  A list
+// is sorted.  Where a bin cannot be refined (many equal logits) the key is found
+// bit by bit.
+//
+// What bounds it: the row's chain of phases (landing, maxima, histogram, two
+// meetings, list, sort, the running sum), each 0.5 to 4 us with the SM mostly
+// waiting (issue slots 30 % used), times the rounds of clusters; of the logits'
+// bytes alone 64 x 262144 would take 10 us.  One row of 262144: top-k 12.5 us,
+// top-p 0.9 24, no filter 15; 64 rows: 42, 122, 74.  What made it: the same with
+// 64-bit floating point in every thread 137 us instead of 105 (mixed filters), bins
+// read out of the other blocks' memory one by one 105 instead of 85.
 //
 // Weights e^((l - M) / T) are summed in fixed point, 64 bits: any order gives the
 // same sums, to 2^-34 of a weight of 1 or better.  A weight is within 2^-21 of its
@@ -34,8 +43,9 @@ namespace moe {
 namespace {
 typedef unsigned long long u64;
 constexpr int kSmThreads = 512, kSmWarps = kSmThreads / 32;
-constexpr int kSmCluster = 16;       // blocks of a row, at most
-constexpr int kSmSeg = 16384;        // tokens of a block that leave room for another block on the SM
+constexpr int kSmCluster = kSampleMaxCluster;  // blocks of a row, at most
+constexpr int kSmSeg = 22528;        // tokens of a block that leave room for another block on the SM
+constexpr int kSmFew = 4096;         // tokens of a block where blocks are plenty: 8 a thread
 constexpr int kSmSegMax = 49152;     // that fit shared memory at all; rows of more are read again in every pass
 constexpr int kSmChunk = 4096;       // tokens of a bulk copy
 constexpr int kSmBins = kSmThreads;  // a thread per bin
@@ -143,13 +153,17 @@ struct SmCut {
 template <bool kHeld>
 __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) float seg[];
-  // A bin's sum as three sums of 16 bits of a weight each (the last of what is left), for shared memory adds 32
-  // bits at once and 64 by trial only; rows that are not held have more tokens than the 16 bits allow for.
-  __shared__ unsigned s_m[3][kSmBins];
-  __shared__ u64 s_mass[kHeld ? 1 : kSmBins], s_list[kSmList], s_weight[kSmList], s_warp[kSmWarps], s_far[kSmCluster], s_one[4];
+  // The bins, then, when they are read, the lists: the row's (the first block's is used) and the block's own.  A
+  // bin's sum is three sums of 16 bits of a weight each (the last of what is left), for shared memory adds 32 bits
+  // at once and 64 by trial only; rows that are not held have more tokens than the 16 bits allow for.
+  __shared__ __align__(16) unsigned s_space[4][kSmBins];
+  unsigned *const s_cnt = s_space[0], (*const s_m)[kSmBins] = s_space + 1;
+  u64 *const s_list = reinterpret_cast<u64 *>(s_space[0]), *const s_own_list = reinterpret_cast<u64 *>(s_space[2]);
+  static_assert(kSmList * 8 <= 2 * kSmBins * 4, "a list in the place of two of the arrays");
+  __shared__ u64 s_mass[kHeld ? 1 : kSmBins], s_warp[kSmWarps], s_far[kSmCluster], s_one[4];
   __shared__ SmBin s_wide[kSmCluster][32], s_fine[kSmCluster][16];  // the blocks' bins: 16 at a time, then one by one
   __shared__ u64 s_sums[2][32];
-  __shared__ unsigned s_cnt[kSmBins], s_n, s_own, s_base;
+  __shared__ unsigned s_n, s_own, s_base;
   __shared__ uint64_t s_bar[(kSmSegMax + kSmChunk) / kSmChunk + 1];
   __shared__ float s_red[3][kSmWarps];
   __shared__ SmTold s_told[kSmCluster];
@@ -313,7 +327,6 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       __syncthreads();
       if (s_one[2] >= (unsigned)top_k) told.cut_all = __uint_as_float((unsigned)s_one[0]);
       if (s_one[2] >= part) told.cut_part = __uint_as_float((unsigned)s_one[1]);
-      clear_bins();
     } else if (cut_p) {
       float e = mine > -INFINITY ? exp2f((mine - block_top) * weight.c) : 0.f;
 #pragma unroll
@@ -408,13 +421,13 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     sweep(tid, quads, kSmThreads, [&](float v) { return v >= bound && v > -INFINITY; }, [&](float v, int id) {
       if (!yes(v, id)) return;
       const unsigned at = atomicAdd(&s_own, 1u);
-      if (at < (unsigned)kSmList) s_weight[at] = sm_full(v, id);
+      if (at < (unsigned)kSmList) s_own_list[at] = sm_full(v, id);
     });
     __syncthreads();
     const unsigned many = s_own;
     if (tid == 0 && many) s_base = sm_count(first_n, many);
     __syncthreads();
-    if (tid < many && s_base + tid < (unsigned)kSmList) sm_put(first_list + 8 * (s_base + tid), s_weight[tid]);
+    if (tid < many && s_base + tid < (unsigned)kSmList) sm_put(first_list + 8 * (s_base + tid), s_own_list[tid]);
     if (tid == 0) s_own = 0u;
   };
   // Over the block: the sum of one value per thread.
@@ -564,6 +577,8 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     for (int level = 1; level <= 3 && !found; ++level) {
       const int shift = kSmBits - 9 * level;
       const bool tail = !by_count && !known && level == 1;
+      clear_bins();
+      __syncthreads();
       float rest_w = 0.f;  // below the bound: each weight is less than the share of one of V in 1 - p
       sweep(tid, quads, kSmThreads,
             [&](float v) {
@@ -632,8 +647,6 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
           sm_meet();
         }
       }
-      __syncthreads();
-      clear_bins();
       prefix = prefix << 9 | bin;
       const float bin_low = prefix == (1u << (9 * level)) - 1u || !(wide < 1e37f) ? cut : fmaxf(cut, value_at((prefix + 1) << shift, -1.f));
       if (above + in <= (u64)kSmList) {  // all that may remain fits the list
@@ -751,35 +764,56 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
 }
 }  // namespace
 
-cudaError_t sample_set_attributes() {
+// The launch of a row's cluster of `cluster` blocks with `per` tokens each, T rows.
+namespace {
+void sm_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int T, int cluster, size_t smem) {
+  cfg.gridDim = dim3((unsigned)(T * cluster));
+  cfg.blockDim = dim3(kSmThreads);
+  cfg.dynamicSmemBytes = smem;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+}
+size_t sm_bytes(int per) { return (size_t)(per + 8) * 4; }
+}  // namespace
+
+cudaError_t sample_set_attributes(int *clusters) {
   const void *k[2] = {(const void *)sample_kernel<true>, (const void *)sample_kernel<false>};
-  for (const void *f : k) {
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && f == k[0])
-      e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSmSegMax + 8) * 4);
-    if (e != cudaSuccess) return e;
+  cudaError_t e;
+  for (const void *f : k)
+    if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1))) return e;
+  if ((e = cudaFuncSetAttribute(k[0], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm_bytes(kSmSegMax)))) return e;
+  for (int c = 1; c <= kSmCluster; ++c) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    sm_config(cfg, attr, 1, c, sm_bytes(kSmSeg));
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters[c], sample_kernel<true>, &cfg))) return e;
   }
   return cudaSuccess;
 }
 
-cudaError_t launch_sample(const SampleArgs &a0, int n_sm, cudaStream_t st, bool pdl) {
+// A row's blocks: as many as leave every thread 8 tokens, up to 16, where all rows run
+// at once so; with more rows the most with which they still do, or the fewest that
+// hold the row two blocks to an SM.  (Of clusters of 16 the device holds 16 at once,
+// of clusters of 12 24: 64 x 262144 with mixed filters took 82 us and takes 79, one
+// row 13 with 16 blocks; 17 x 32000 with 16384 tokens a block 21, with 4096 17.)
+cudaError_t launch_sample(const SampleArgs &a0, const int *clusters, cudaStream_t st, bool pdl) {
   SampleArgs a = a0;
-  a.cluster = 1;
-  while (a.cluster < kSmCluster && (a.V + a.cluster - 1) / a.cluster > kSmSeg) a.cluster *= 2;
-  a.per = ((a.V + a.cluster - 1) / a.cluster + 3) & ~3;
+  const int least = (a.V + kSmSeg - 1) / kSmSeg;
+  int c = (a.V + kSmFew - 1) / kSmFew;
+  c = c < kSmCluster ? c : kSmCluster;
+  while (c > 1 && c > least && clusters[c] < a.T) --c;
+  a.cluster = c;
+  a.per = ((a.V + c - 1) / c + 3) & ~3;
   const bool held = a.per <= kSmSegMax;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.T * a.cluster));
-  cfg.blockDim = dim3(kSmThreads);
-  cfg.dynamicSmemBytes = held ? (size_t)(a.per + 8) * 4 : 0;
-  cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.cluster;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  sm_config(cfg, attr, a.T, c, held ? sm_bytes(a.per) : 0);
+  cfg.stream = st;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, held ? sample_kernel<true> : sample_kernel<false>, a);
 }

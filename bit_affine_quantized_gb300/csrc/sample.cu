@@ -95,12 +95,11 @@ struct SmWeight {
   float top, c, c_lo, one;  // the maximum; log2(e) / temperature in two parts; the unit
   __device__ __forceinline__ u64 operator()(float l) const {
     const float d = l - top, y = d * c;
-    if (!(y > -70.f)) return 0;
     const float b = d - l, e = (l - (d - b)) + (-top - b);        // what the difference lost
     const float lo = fmaf(d, c, -y) + fmaf(d, c_lo, e * c);       // and the product
     float w;
     asm("ex2.approx.f32 %0, %1;" : "=f"(w) : "f"(y));
-    return __float2ull_rn(fmaf(w, lo * 0.69314718f, w) * one);
+    return y > -70.f ? __float2ull_rn(fmaf(w, lo * 0.69314718f, w) * one) : 0;
   }
 };
 
@@ -397,9 +396,11 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     const float v = j >= skew && j < skew + n ? __ldcg(from + (j - skew)) : -INFINITY;
     return v < INFINITY ? v : -INFINITY;
   };
-  // Quads first, first + step, .. below end: `look` at every value, which says whether `each` is for it.  A
-  // lane goes through its own picks: where they are few, a warp's turns are the most that one lane has.
-  auto sweep = [&](int first, int end, int step, auto look, auto each) {
+  // Quads first, first + step, .. below end: `look` at every value, which says whether it is to go through `make`
+  // and what that makes of it through `put`.  A lane goes through its own picks, kPicks at a time: where they are
+  // few, a warp's turns are the most that one lane has; where they are many, there is something to overlap.
+  auto sweep = [&](int first, int end, int step, auto look, auto make, auto put) {
+    constexpr int kPicks = 2;
     for (int i0 = first; i0 < end; i0 += 8 * step) {
       unsigned picks = 0;
 #pragma unroll
@@ -409,20 +410,37 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
         const float4 f = quad(i);
         picks |= ((look(f.x) ? 1u : 0u) | (look(f.y) ? 2u : 0u) | (look(f.z) ? 4u : 0u) | (look(f.w) ? 8u : 0u)) << (4 * q);
       }
-      for (; picks; picks &= picks - 1u) {
-        const int b = __ffs(picks) - 1, j = 4 * (i0 + (b >> 2) * step) + (b & 3);
-        each(value(j), id0 + j);
+      while (picks) {
+        float v[kPicks];
+        int id[kPicks];
+        bool is[kPicks];
+#pragma unroll
+        for (int k = 0; k < kPicks; ++k) {  // (none left: the last again, to no avail)
+          is[k] = picks != 0u;
+          const int b = is[k] ? __ffs(picks) - 1 : 0, j = is[k] ? 4 * (i0 + (b >> 2) * step) + (b & 3) : id[0] - id0;
+          picks &= picks - 1u;
+          v[k] = value(j);
+          id[k] = id0 + j;
+        }
+        decltype(make(0.f, 0)) made[kPicks];
+#pragma unroll
+        for (int k = 0; k < kPicks; ++k) made[k] = make(v[k], id[k]);
+#pragma unroll
+        for (int k = 0; k < kPicks; ++k)
+          if (is[k]) put(made[k]);
       }
     }
   };
   // The tokens from `bound` on that `yes` names go to the first block's list, as far as it reaches; s_n there
   // counts them.  (The list's order varies; nothing depends on it.)
   auto gather = [&](float bound, auto yes) {
-    sweep(tid, quads, kSmThreads, [&](float v) { return v >= bound && v > -INFINITY; }, [&](float v, int id) {
-      if (!yes(v, id)) return;
-      const unsigned at = atomicAdd(&s_own, 1u);
-      if (at < (unsigned)kSmList) s_own_list[at] = sm_full(v, id);
-    });
+    sweep(tid, quads, kSmThreads, [&](float v) { return v >= bound && v > -INFINITY; },
+          [&](float v, int id) -> u64 { return yes(v, id) ? sm_full(v, id) : 0; },
+          [&](u64 key) {
+            if (key == 0) return;
+            const unsigned at = atomicAdd(&s_own, 1u);
+            if (at < (unsigned)kSmList) s_own_list[at] = key;
+          });
     __syncthreads();
     const unsigned many = s_own;
     if (tid == 0 && many) s_base = sm_count(first_n, many);
@@ -569,6 +587,8 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       const float d = scale > 0.f ? (float)y / scale : 0.f;
       return top - d + over * (1e-6f * (fabsf(top) + d) + 1e-30f);
     };
+    const bool by_key = (unsigned)tau != 0u;  // (else tau is a value's first key: values tell)
+    auto outside = [&](float v, int id) { return by_key && sm_full(v, id) < tau; };
     unsigned prefix = 0;
     u64 need = by_count ? (u64)top_k : known ? sm_share(top_p0, all, true) : 0;
     u64 above = 0, above_mass = 0;  // what lies above the bin at hand
@@ -591,15 +611,18 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
             },
             [&](float v, int id) {
               const unsigned y = far_of(v) >> shift;
-              if (y >> 9 != prefix || sm_full(v, id) < tau) return;
-              const u64 w = weight(v);
-              atomicAdd(&s_cnt[y & 511u], 1u);
+              return SmBin{weight(v), y >> 9 != prefix || outside(v, id) ? (u64)kSmBins : (u64)(y & 511u)};
+            },
+            [&](const SmBin &b) {  // (the sum and the bin)
+              if (b.count == kSmBins) return;
+              const u64 w = b.mass;
+              atomicAdd(&s_cnt[b.count], 1u);
               if (kHeld) {
-                atomicAdd(&s_m[0][y & 511u], (unsigned)w & 0xFFFFu);
-                atomicAdd(&s_m[1][y & 511u], (unsigned)w >> 16);
-                if (w >> 32) atomicAdd(&s_m[2][y & 511u], (unsigned)(w >> 32));
+                atomicAdd(&s_m[0][b.count], (unsigned)w & 0xFFFFu);
+                atomicAdd(&s_m[1][b.count], (unsigned)w >> 16);
+                if (w >> 32) atomicAdd(&s_m[2][b.count], (unsigned)(w >> 32));
               } else if (w) {
-                atomicAdd(&s_mass[y & 511u], w);
+                atomicAdd(&s_mass[b.count], w);
               }
             });
       u64 rest = __float2ull_rn(rest_w * weight.one);
@@ -650,13 +673,13 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       prefix = prefix << 9 | bin;
       const float bin_low = prefix == (1u << (9 * level)) - 1u || !(wide < 1e37f) ? cut : fmaxf(cut, value_at((prefix + 1) << shift, -1.f));
       if (above + in <= (u64)kSmList) {  // all that may remain fits the list
-        gather(bin_low, [&](float v, int id) { return far_of(v) >> shift <= prefix && sm_full(v, id) >= tau; });
+        gather(bin_low, [&](float v, int id) { return far_of(v) >> shift <= prefix && !outside(v, id); });
         sm_meet();
         if (rank == 0) finish((int)(above + in), by_count ? top_k : 0, all);
         done = found = true;
       } else if (in <= (u64)kSmList) {
         const float bin_high = wide < 1e37f ? value_at(prefix << shift, 1.f) : INFINITY;
-        gather(bin_low, [&](float v, int id) { return v <= bin_high && far_of(v) >> shift == prefix && sm_full(v, id) >= tau; });
+        gather(bin_low, [&](float v, int id) { return v <= bin_high && far_of(v) >> shift == prefix && !outside(v, id); });
         sm_meet();
         if (rank == 0) {
           const u64 key = sort(tid < (int)in ? s_list[tid] : 0, (int)in);
@@ -694,7 +717,8 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
         if (t > tau) {  // (else everything that remains lies above it, which is enough)
           const float bound = sm_value((unsigned)(t >> 32));
           sweep(tid, quads, kSmThreads, [&](float v) { return !(v < bound) && v > -INFINITY; },
-                [&](float v, int id) { part += sm_full(v, id) < t ? 0 : by_count ? 1 : weight(v); });
+                [&](float v, int id) -> u64 { return sm_full(v, id) < t ? 0 : by_count ? 1 : weight(v); },
+                [&](u64 w) { part += w; });
           if (cluster_sum(part) >= need) k = t;
         } else {
           k = t;
@@ -705,7 +729,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
         u64 part = 0;
         const float bound = sm_value((unsigned)(tau >> 32));
         sweep(tid, quads, kSmThreads, [&](float v) { return v >= bound; },
-              [&](float v, int id) { part += sm_full(v, id) >= tau ? weight(v) : 0; });
+              [&](float v, int id) -> u64 { return sm_full(v, id) >= tau ? weight(v) : 0; }, [&](u64 w) { part += w; });
         all = cluster_sum(part);
         known = true;
       }
@@ -715,12 +739,14 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   // ---- the token: running sums over blocks, warps, lanes
   if (!done) {
     const float tau_v = sm_value((unsigned)(tau >> 32));
+    const bool by_key = (unsigned)tau != 0u;
     const int q0 = (int)((long long)quads * warp / kSmWarps), q1 = (int)((long long)quads * (warp + 1) / kSmWarps);
     auto kept = [&](float v, int id) -> u64 {
-      return v >= tau_v && v > -INFINITY && sm_full(v, id) >= tau ? weight(v) : 0;
+      return v >= tau_v && v > -INFINITY && (!by_key || sm_full(v, id) >= tau) ? weight(v) : 0;
     };
     u64 part = 0;
-    sweep(q0 + lane, q1, 32, [&](float v) { return v >= tau_v && v > -INFINITY; }, [&](float v, int id) { part += kept(v, id); });
+    sweep(q0 + lane, q1, 32, [&](float v) { return v >= tau_v && v > -INFINITY; }, kept,
+          [&](u64 w) { part += w; });
     const u64 own = block_sum(part);
     if (tid < C) sm_put(sm_far(&s_far[rank], tid), own);
     sm_meet();

@@ -62,13 +62,15 @@ constexpr int kAtSums = 14;  // 8-bit values' weights are held times 2^14
 
 template <bool kBits8, int kD, int kN>
 struct AtShape {
-  static constexpr int kRow = kD * (kBits8 ? 1 : 2);   // bytes of a row in shared memory
-  static constexpr int kBox = kRow < 128 ? kRow : 128; // bytes of a row in one copy
+  static constexpr int kBytes = kD * (kBits8 ? 1 : 2);
+  static constexpr int kBox = kBytes <= 64 ? 64 : 128;  // bytes of a row in one copy
+  static constexpr int kRow = (kBytes + kBox - 1) / kBox * kBox;  // and in shared memory
   static constexpr int kTile = kRow <= 256 ? 32 : 16;  // positions
   static constexpr int kHalf = kTile * kRow;           // bytes of a tile's keys, and of its values
   // Warps: as many as the registers of a lane's share of the outputs allow, for a
-  // warp waits out its own products and shuffles.
-  static constexpr int kWarps = kN == 1 ? 12 : 8;
+  // warp waits out its own products and shuffles (heads of 64 in 8 bits, 47 sequences of 16384: 95 us with 16 warps, 106
+  // with 12; with 16 queries a head 126 with 12, 147 with 8; heads of 128 and 16 queries 103 with 8, 119 with 12, spilled).
+  static constexpr int kWarps = kN == 1 ? (kD == 64 ? 16 : 12) : (kD == 64 && kBits8 ? 12 : 8);
   static constexpr int kFit = (int)(200 * 1024 / ((size_t)kWarps * 2 * kHalf));
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
   static constexpr int kPart = 16 * kN + kD / 16 * kN * 128;  // floats of a part: maxima, sums, the output's sum
@@ -1006,22 +1008,27 @@ cudaError_t at_attribute() {
 template <bool kBits8, int kN>
 cudaError_t at_size(const KvAttendArgs &a, int n_sm, cudaStream_t st, bool pdl) {
   if (a.c.D <= 64) return at_launch<kBits8, 64, kN>(a, n_sm, st, pdl);
+  // the products of 8-bit rows bound what memory bounds in bf16: two sizes more (192 in place of 256, 15 sequences of
+  // 16384 x 4: 74 us instead of 78, with 16 queries a head 93 instead of 131; 80 in place of 128: 130 instead of 149)
+  if (kBits8 && a.c.D <= 96) return at_launch<true, 96, kN>(a, n_sm, st, pdl);
   if (a.c.D <= 128) return at_launch<kBits8, 128, kN>(a, n_sm, st, pdl);
+  if (kBits8 && a.c.D <= 192) return at_launch<true, 192, kN>(a, n_sm, st, pdl);
   return at_launch<kBits8, 256, kN>(a, n_sm, st, pdl);
 }
 }  // namespace
 
 size_t kv_attend_ws_bytes(const KvCache &c, int Hq) {
   const int kN = Hq / c.heads > 8 ? 2 : 1, kD = c.D <= 64 ? 64 : c.D <= 128 ? 128 : 256;
-  return (size_t)kAtMaxGrid * ((kN == 1 ? 12 : 8) + 2) * (16 * kN + kD / 16 * kN * 128) * 4;
+  return (size_t)kAtMaxGrid * (16 + 2) * (16 * kN + kD / 16 * kN * 128) * 4;
 }
 
 cudaError_t kv_attend_set_attributes() {
-  const cudaError_t e[12] = {
+  const cudaError_t e[16] = {
       at_attribute<false, 64, 1>(), at_attribute<false, 128, 1>(), at_attribute<false, 256, 1>(),
       at_attribute<false, 64, 2>(), at_attribute<false, 128, 2>(), at_attribute<false, 256, 2>(),
       at_attribute<true, 64, 1>(),  at_attribute<true, 128, 1>(),  at_attribute<true, 256, 1>(),
-      at_attribute<true, 64, 2>(),  at_attribute<true, 128, 2>(),  at_attribute<true, 256, 2>()};
+      at_attribute<true, 64, 2>(),  at_attribute<true, 128, 2>(),  at_attribute<true, 256, 2>(),
+      at_attribute<true, 96, 1>(),  at_attribute<true, 192, 1>(),  at_attribute<true, 96, 2>(), at_attribute<true, 192, 2>()};
   for (const cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;

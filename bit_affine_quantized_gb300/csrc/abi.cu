@@ -299,7 +299,7 @@ bool kv_rows(const void *p, size_t stride, size_t width) {
 
 moe::KvCache kv_cache(const moe_kv_cache *c) {
   return moe::KvCache{(uint8_t *)c->k, (uint8_t *)c->v, c->k_scales,  c->v_scales, c->table,       c->n_pages,
-                      c->kv_heads,     c->page_rows,    c->head_dim, c->n_seqs,   c->table_stride};
+                      c->kv_heads,     c->page_rows,    c->head_dim, c->n_seqs,   c->table_stride, __builtin_ctz(c->page_rows)};
 }
 
 int check_qdense(const moe_qdense_weights *w) {

@@ -271,13 +271,14 @@ struct KvCache {
   float *ks, *vs;             // [n_pages, heads, rows]; null: bf16
   const int32_t *table;       // [n_seqs, stride]
   int n_pages, heads, rows, D, n_seqs, stride;
+  int log_rows;               // rows = 2^log_rows
 };
 // Row of the pages, over all pages, of head 0 of a position (the heads' rows lie
 // `rows` apart); -1 for a sequence, a position or a page that is not there.
 __device__ __forceinline__ long long kv_row(const KvCache &c, int seq, int pos) {
-  if ((unsigned)seq >= (unsigned)c.n_seqs || pos < 0 || pos / c.rows >= c.stride) return -1;
-  const int page = __ldg(c.table + (size_t)seq * c.stride + pos / c.rows);
-  return (unsigned)page < (unsigned)c.n_pages ? (long long)page * c.heads * c.rows + pos % c.rows : -1;
+  if ((unsigned)seq >= (unsigned)c.n_seqs || pos < 0 || pos >> c.log_rows >= c.stride) return -1;
+  const int page = __ldg(c.table + (size_t)seq * c.stride + (pos >> c.log_rows));
+  return (unsigned)page < (unsigned)c.n_pages ? (long long)page * c.heads * c.rows + (pos & (c.rows - 1)) : -1;
 }
 struct KvAppendArgs {
   KvCache c;

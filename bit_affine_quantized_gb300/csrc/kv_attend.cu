@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   const KvAttendArgs &a = prm.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   const int D = a.c.D, steps = D / 16, H = a.c.heads, group = a.Hq / H, items = H * prm.blocks_of;
-  const int shift = 31 - __clz(a.c.rows), box = min(a.c.rows, kTile), box_shift = 31 - __clz(box);
+  const int shift = a.c.log_rows, box = min(a.c.rows, kTile), box_shift = 31 - __clz(box);
   const bool tracer = a.trace && blockIdx.x == 0 && tid == 0;
   if (tracer) trace_min(a.trace, kTrEntry);
   if (lane < kStages) {  // (a warp's own: no other waits on them)

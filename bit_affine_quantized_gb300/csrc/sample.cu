@@ -51,6 +51,7 @@ constexpr int kSmChunk = 4096;       // tokens of a bulk copy
 constexpr int kSmBins = kSmThreads;  // a thread per bin
 constexpr int kSmBits = 27;          // of a token's distance to the maximum: three times 9
 constexpr int kSmList = kSmThreads;  // a thread per token of the list
+constexpr int kSmSorted = kSmThreads / 4;  // tokens of a short one, which four threads each rank
 
 // Orders floats above -inf as unsigned integers (both zeros the same); 0 for -inf.
 __device__ __forceinline__ unsigned sm_key(float f) {
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   // Sorts `count` keys, one per thread (0: none), the largest first; s_list is its own to use.  Few by their ranks, four
   // threads to a key, more by a bitonic network (100 of them: 0.5 us against 1.5; 512: 10 against 4).
   auto sort = [&](u64 key, int count) {
-    if (count <= kSmThreads / 4) {
+    if (count <= kSmSorted) {
       __syncthreads();
       s_list[tid] = key;
       __syncthreads();
@@ -672,7 +673,8 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       }
       prefix = prefix << 9 | bin;
       const float bin_low = prefix == (1u << (9 * level)) - 1u || !(wide < 1e37f) ? cut : fmaxf(cut, value_at((prefix + 1) << shift, -1.f));
-      if (above + in <= (u64)kSmList) {  // all that may remain fits the list
+      // all that may remain is a list: a short one, or a longer that saves the second cut
+      if (above + in <= (u64)(by_count && cut_p ? kSmList : kSmSorted)) {
         gather(bin_low, [&](float v, int id) { return far_of(v) >> shift <= prefix && !outside(v, id); });
         sm_meet();
         if (rank == 0) finish((int)(above + in), by_count ? top_k : 0, all);

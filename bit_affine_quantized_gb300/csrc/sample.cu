@@ -99,7 +99,7 @@ struct SmWeight {
     const float b = d - l, e = (l - (d - b)) + (-top - b);        // what the difference lost
     const float lo = fmaf(d, c, -y) + fmaf(d, c_lo, e * c);       // and the product
     float w;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(w) : "f"(y));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(y));
     return y > -70.f ? __float2ull_rn(fmaf(w, lo * 0.69314718f, w) * one) : 0;
   }
 };
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   // Quads first, first + step, .. below end: `look` at every value, which says whether it is to go through `make`
   // and what that makes of it through `put`.  A lane goes through its own picks, kPicks at a time: where they are
   // few, a warp's turns are the most that one lane has; where they are many, there is something to overlap.
-  auto sweep = [&](int first, int end, int step, auto look, auto make, auto put) {
+  auto sweep = [&](bool many, int first, int end, int step, auto look, auto make, auto put) {
     constexpr int kPicks = 2;
     for (int i0 = first; i0 < end; i0 += 8 * step) {
       unsigned picks = 0;
@@ -410,6 +410,18 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
         if (i >= end) continue;
         const float4 f = quad(i);
         picks |= ((look(f.x) ? 1u : 0u) | (look(f.y) ? 2u : 0u) | (look(f.z) ? 4u : 0u) | (look(f.w) ? 8u : 0u)) << (4 * q);
+      }
+      if (many && __any_sync(__activemask(), __popc(picks) >= 16)) {
+#pragma unroll 1
+        for (int q = 0; q < 8 && picks >> (4 * q); ++q) {
+          const float4 f = quad(i0 + q * step);
+          const int id = id0 + 4 * (i0 + q * step);
+          const decltype(make(0.f, 0)) made[4] = {make(f.x, id), make(f.y, id + 1), make(f.z, id + 2), make(f.w, id + 3)};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (picks >> (4 * q + k) & 1u) put(made[k]);
+        }
+        continue;
       }
       while (picks) {
         float v[kPicks];
@@ -435,7 +447,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   // The tokens from `bound` on that `yes` names go to the first block's list, as far as it reaches; s_n there
   // counts them.  (The list's order varies; nothing depends on it.)
   auto gather = [&](float bound, auto yes) {
-    sweep(tid, quads, kSmThreads, [&](float v) { return v >= bound && v > -INFINITY; },
+    sweep(false, tid, quads, kSmThreads, [&](float v) { return v >= bound && v > -INFINITY; },
           [&](float v, int id) -> u64 { return yes(v, id) ? sm_full(v, id) : 0; },
           [&](u64 key) {
             if (key == 0) return;
@@ -472,7 +484,8 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     return own + before;
   };
   // Sorts `count` keys, one per thread (0: none), the largest first; s_list is its own to use.  Few by their ranks, four
-  // threads to a key, more by a bitonic network (100 of them: 0.5 us against 1.5; 512: 10 against 4).
+  // threads to a key; more by sorting each warp's 32 and a search for the place among every other warp's (top-k 50, then
+  // the drawn order, of lists of 200 of 262144: 10.9 us a call, with a bitonic network over the block 12.5).
   auto sort = [&](u64 key, int count) {
     if (count <= kSmSorted) {
       __syncthreads();
@@ -489,24 +502,31 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       __syncthreads();
       return tid < count ? s_list[tid] : 0;
     }
-    const int size = count <= 32 ? 32 : 1 << (32 - __clz(count - 1));
-#pragma unroll 1
-    for (int k = 2; k <= size; k *= 2)
-#pragma unroll 1
+#pragma unroll
+    for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
       for (int j = k / 2; j > 0; j /= 2) {
-        u64 other;
-        if (j < 32) {
-          other = __shfl_xor_sync(0xffffffffu, key, j);
-        } else {
-          __syncthreads();
-          s_list[tid] = key;
-          __syncthreads();
-          other = s_list[tid ^ j];
-        }
-        const bool larger = ((tid & j) == 0) == ((tid & k) == 0);  // this thread keeps the larger
-        key = tid >= size ? 0 : larger ? (key > other ? key : other) : (key < other ? key : other);
+        const u64 other = __shfl_xor_sync(0xffffffffu, key, j);
+        const bool larger = ((lane & j) == 0) == ((lane & k) == 0);  // this thread keeps the larger
+        key = larger ? (key > other ? key : other) : (key < other ? key : other);
       }
-    return key;
+    __syncthreads();
+    s_list[tid] = key;
+    __syncthreads();
+    int place = lane;
+#pragma unroll 4
+    for (int w = 0; 32 * w < count; ++w) {  // how many of a warp's 32 are larger
+      const u64 *run = s_list + 32 * w;
+      int n = 0;
+#pragma unroll
+      for (int step = 16; step > 0; step /= 2) n += run[n + step - 1] > key ? step : 0;
+      n += run[n] > key;
+      place += w != warp ? n : 0;
+    }
+    __syncthreads();
+    if (key) s_list[place] = key;
+    __syncthreads();
+    return tid < count ? s_list[tid] : 0;
   };
   // The first block alone: the list has every token that may remain.
   auto finish = [&](int count, int k, u64 all) {
@@ -594,6 +614,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     u64 need = by_count ? (u64)top_k : known ? sm_share(top_p0, all, true) : 0;
     u64 above = 0, above_mass = 0;  // what lies above the bin at hand
     bool found = false;
+    float lo = cut, hi = INFINITY;  // what the bin at hand may hold, and a little over
 #pragma unroll 1
     for (int level = 1; level <= 3 && !found; ++level) {
       const int shift = kSmBits - 9 * level;
@@ -601,14 +622,14 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       clear_bins();
       __syncthreads();
       float rest_w = 0.f;  // below the bound: each weight is less than the share of one of V in 1 - p
-      sweep(tid, quads, kSmThreads,
+      sweep(true, tid, quads, kSmThreads,
             [&](float v) {
               if (tail) {
                 float e;
                 asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((v - top) * weight.c));
                 rest_w += v < cut && v >= low ? e : 0.f;
               }
-              return v >= cut;
+              return v >= lo && v <= hi;
             },
             [&](float v, int id) {
               const unsigned y = far_of(v) >> shift;
@@ -672,16 +693,16 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
         }
       }
       prefix = prefix << 9 | bin;
-      const float bin_low = prefix == (1u << (9 * level)) - 1u || !(wide < 1e37f) ? cut : fmaxf(cut, value_at((prefix + 1) << shift, -1.f));
+      lo = prefix == (1u << (9 * level)) - 1u || !(wide < 1e37f) ? cut : fmaxf(cut, value_at((prefix + 1) << shift, -1.f));
+      hi = wide < 1e37f ? value_at(prefix << shift, 1.f) : INFINITY;
       // all that may remain is a list: a short one, or a longer that saves the second cut
       if (above + in <= (u64)(by_count && cut_p ? kSmList : kSmSorted)) {
-        gather(bin_low, [&](float v, int id) { return far_of(v) >> shift <= prefix && !outside(v, id); });
+        gather(lo, [&](float v, int id) { return far_of(v) >> shift <= prefix && !outside(v, id); });
         sm_meet();
         if (rank == 0) finish((int)(above + in), by_count ? top_k : 0, all);
         done = found = true;
       } else if (in <= (u64)kSmList) {
-        const float bin_high = wide < 1e37f ? value_at(prefix << shift, 1.f) : INFINITY;
-        gather(bin_low, [&](float v, int id) { return v <= bin_high && far_of(v) >> shift == prefix && !outside(v, id); });
+        gather(lo, [&](float v, int id) { return v <= hi && far_of(v) >> shift == prefix && !outside(v, id); });
         sm_meet();
         if (rank == 0) {
           const u64 key = sort(tid < (int)in ? s_list[tid] : 0, (int)in);
@@ -718,7 +739,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
         u64 part = 0;
         if (t > tau) {  // (else everything that remains lies above it, which is enough)
           const float bound = sm_value((unsigned)(t >> 32));
-          sweep(tid, quads, kSmThreads, [&](float v) { return !(v < bound) && v > -INFINITY; },
+          sweep(false, tid, quads, kSmThreads, [&](float v) { return !(v < bound) && v > -INFINITY; },
                 [&](float v, int id) -> u64 { return sm_full(v, id) < t ? 0 : by_count ? 1 : weight(v); },
                 [&](u64 w) { part += w; });
           if (cluster_sum(part) >= need) k = t;
@@ -730,7 +751,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       if (by_count) {
         u64 part = 0;
         const float bound = sm_value((unsigned)(tau >> 32));
-        sweep(tid, quads, kSmThreads, [&](float v) { return v >= bound; },
+        sweep(false, tid, quads, kSmThreads, [&](float v) { return v >= bound; },
               [&](float v, int id) -> u64 { return sm_full(v, id) >= tau ? weight(v) : 0; }, [&](u64 w) { part += w; });
         all = cluster_sum(part);
         known = true;
@@ -747,7 +768,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       return v >= tau_v && v > -INFINITY && (!by_key || sm_full(v, id) >= tau) ? weight(v) : 0;
     };
     u64 part = 0;
-    sweep(q0 + lane, q1, 32, [&](float v) { return v >= tau_v && v > -INFINITY; }, kept,
+    sweep(true, q0 + lane, q1, 32, [&](float v) { return v >= tau_v && v > -INFINITY; }, kept,
           [&](u64 w) { part += w; });
     const u64 own = block_sum(part);
     if (tid < C) sm_put(sm_far(&s_far[rank], tid), own);
@@ -761,30 +782,25 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     if (before < goal && before + own >= goal) {  // it is this block's
       int w = 0;
       while (w < kSmWarps - 1 && before + s_warp[w] < goal) before += s_warp[w++];
-      if (warp == w) {
-        bool seen = false;
-        for (int i0 = q0; i0 < q1 && !seen; i0 += 32) {
-          float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-          if (i0 + lane < q1) f = quad(i0 + lane);
-          const int id = id0 + 4 * (i0 + lane);
-          const u64 w4[4] = {kept(f.x, id), kept(f.y, id + 1), kept(f.z, id + 2), kept(f.w, id + 3)};
-          const u64 mine4 = w4[0] + w4[1] + w4[2] + w4[3], run = sm_warp_scan(mine4, lane);
-          const unsigned hit = __ballot_sync(0xffffffffu, before + run >= goal);
-          if (hit) {
-            seen = true;
-            if (lane == __ffs(hit) - 1) {
-              u64 at = before + run - mine4;
-              const float v[4] = {f.x, f.y, f.z, f.w};
+      const int end = (int)((long long)quads * (w + 1) / kSmWarps);
+      for (int i0 = (int)((long long)quads * w / kSmWarps); i0 < end && before < goal; i0 += kSmThreads) {
+        float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (i0 + tid < end) f = quad(i0 + tid);
+        const int id = id0 + 4 * (i0 + tid);
+        const u64 w4[4] = {kept(f.x, id), kept(f.y, id + 1), kept(f.z, id + 2), kept(f.w, id + 3)};
+        const u64 mine4 = w4[0] + w4[1] + w4[2] + w4[3], run = block_scan(mine4);
+        u64 at = before + run - mine4;
+        if (at < goal && before + run >= goal) {
+          const float v[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const bool was = at >= goal;
-                at += w4[k];
-                if (!was && at >= goal) write(sm_full(v[k], id + k), whole);
-              }
-            }
+          for (int k = 0; k < 4; ++k) {
+            const bool was = at >= goal;
+            at += w4[k];
+            if (!was && at >= goal) write(sm_full(v[k], id + k), whole);
           }
-          before += __shfl_sync(0xffffffffu, run, 31);
         }
+#pragma unroll
+        for (int k = 0; k < kSmWarps; ++k) before += s_warp[k];
       }
     }
   }

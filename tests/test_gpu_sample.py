@@ -191,6 +191,31 @@ def test_values_close_together(moe):
     check(l, tokens, logp, u, None, k)
 
 
+@pytest.mark.parametrize("V", [600, 40000])
+def test_lists_of_every_length(moe, V):
+    ks = [1, 2, 31, 32, 33, 63, 65, 127, 128, 129, 160, 255, 256, 257, 300, 479, 511, 512, 513]
+    g = np.random.default_rng(V + 1)
+    k, p, u = (np.array(c) for c in zip(*itertools.product(ks, (1.0, 0.9), (0.0, 0.37, 0.999))))
+    logits = g.standard_normal((len(k), V)) * 2
+    tokens, logp = draw(moe, logits, u, None, k, p)
+    assert moe.get_error() == bq.MOE_OK
+    check(logits, tokens, logp, u, None, k, p)
+
+
+@pytest.mark.parametrize("V", [3000, 50000])
+@pytest.mark.parametrize("few", [2, 7, 11])
+def test_cuts_among_close_values(moe, V, few):
+    """A few tokens far above, the others within 2^-few of each other: the cut lies in one bin of the first histogram."""
+    g = np.random.default_rng(V + few)
+    k, p, u = (np.array(c) for c in zip(*itertools.product((0, V // 9, V - 20), (1.0, 0.8, 0.3), (0.01, 0.5, 0.99))))
+    logits = g.random((len(k), V)) * 2.0 ** -few
+    logits[:, 5:V:V // 10] += 50
+    temp = np.full(len(k), 10.0)  # (a far one counts as much as e^5 others)
+    tokens, logp = draw(moe, logits, u, temp, k, p)
+    assert moe.get_error() == bq.MOE_OK
+    check(logits, tokens, logp, u, temp, k, p)
+
+
 def test_shares_follow_the_weights(moe):
     """A thousand even random numbers pick each token as often as its weight says."""
     w = np.array([0.1, 0.0, 0.4, 0.25, 0.05, 0.2])

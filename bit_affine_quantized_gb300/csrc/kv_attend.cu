@@ -254,14 +254,17 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     return v;
   };
   unsigned total, mine = 0, run = 0;  // of a lane's sequence, and up to it
+  constexpr int kWhole = 4;
+  bool fits;  // no item has more tiles than that for every warp
   if (n <= 32) {
     mine = tiles_of(min(lane, n - 1), lane < n);
     run = scan(mine);
     total = __shfl_sync(0xffffffffu, run, 31);
-    __syncwarp();
+    fits = __all_sync(0xffffffffu, mine <= (unsigned)(kWhole * kWarps * items));
   } else {
     unsigned sum = 0;
     for (int i = tid * chunk; i < min(n, (tid + 1) * chunk); ++i) sum += tiles_of(i, true);
+    const unsigned own = sum;
     sum = scan(sum);
     if (lane == 31) s_sums[warp + 1] = sum;
     __syncthreads();
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     __syncthreads();
     s_pre[tid + 1] = sum + s_sums[warp];
     if (tid == 0) s_pre[0] = 0;
-    __syncthreads();
+    fits = __syncthreads_and(own <= (unsigned)(kWhole * kWarps * items));
     total = s_pre[kThreads];
   }
   // as many blocks as have a tile for each warp
@@ -280,11 +283,15 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   const bool works = (int)blockIdx.x < blocks;
   const unsigned each = works ? total / blocks : 0, rest = works ? total % blocks : 0;
   auto block_at = [&](int b) { return each * b + rest * b / blocks; };  // first tile of block b
-  const unsigned bu0 = works ? block_at(blockIdx.x) : 0, bu1 = works ? block_at(blockIdx.x + 1) : 0;
-  const unsigned w_each = (bu1 - bu0) / kWarps, w_rest = (bu1 - bu0) % kWarps;
-  unsigned u0 = bu0 + w_each * warp + w_rest * warp / kWarps;
-  unsigned u1 = bu0 + w_each * (warp + 1) + w_rest * (warp + 1) / kWarps;
-
+  unsigned bu0 = works ? block_at(blockIdx.x) : 0, bu1 = works ? block_at(blockIdx.x + 1) : 0;
+  const bool whole_items = fits && n * items <= (int)gridDim.x;
+  if (whole_items) {
+    const int s = (int)blockIdx.x / items;
+    const unsigned all = n <= 32 ? __shfl_sync(0xffffffffu, mine, s & 31) : s < n ? s_pre[s + 1] - s_pre[s] : 0;
+    const unsigned before = n <= 32 ? __shfl_sync(0xffffffffu, run - mine, s & 31) : s < n ? s_pre[s] : 0, nt = all / items;
+    bu0 = s < n ? before + (blockIdx.x - s * items) * nt : 0;
+    bu1 = s < n ? bu0 + nt : 0;
+  }
   // ---- the warp's first tile
   auto locate = [&](unsigned u) {
     int ch = 0;
@@ -303,10 +310,27 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     cur.item = (int)(left / (unsigned)cur.nt);
     cur.tile = (int)(left % (unsigned)cur.nt);
   };
+  constexpr int kShort = 4;
+  const bool is_short = !whole_items && total != 0 && total <= kShort * (unsigned)items * n;
+  if (fits && !whole_items && !is_short) {
+    if (warp < 2) {
+      unsigned at = warp == 0 ? bu0 : bu1;
+      if (works && at < total) {
+        locate(at);
+        if (cur.tile != 0) at += cur.nt - cur.tile;
+      }
+      if (lane == 0) s_start[warp] = at;
+    }
+    __syncthreads();
+    bu0 = s_start[0];
+    bu1 = s_start[1];
+  }
+  const unsigned w_each = (bu1 - bu0) / kWarps, w_rest = (bu1 - bu0) % kWarps;
+  unsigned u0 = bu0 + w_each * warp + w_rest * warp / kWarps;
+  unsigned u1 = bu0 + w_each * (warp + 1) + w_rest * (warp + 1) / kWarps;
   // Short items stay whole: where they have four tiles or fewer on average, a run that would begin within an item of
   // so few begins with the next (256 sequences of 64 positions: 20 us, cut anywhere 27).
-  constexpr int kShort = 4;
-  if (total != 0 && total <= kShort * (unsigned)items * n) {
+  if (is_short) {
     if (warp == kWarps - 1) {  // where the next block begins
       unsigned end = bu1;
       if (works && bu1 < total) {

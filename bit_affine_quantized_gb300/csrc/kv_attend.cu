@@ -32,19 +32,18 @@
 // queries stay as they are and weights are rounded to bf16.
 //
 // An item (a sequence's key head) that one warp has whole is written at once.
-// Where warps share one, the block joins its warps' parts; where blocks do, each
-// leaves a part in the workspace, and the last of them, by a counter, joins them
-// in the order of the blocks: the result does not depend on who was last.
+// Where warps share one, the block joins its warps' parts; where blocks share a long
+// one, each leaves a part in the workspace, and the last of them, by a counter,
+// joins them in the order of the blocks: the result does not depend on who was last.
 //
 // What it takes (us of a call in a CUDA graph; 152 blocks):
 //   32 sequences of up to 32768, 4 x 128, eight queries a head, 8 bits: 116, 738 MB
 //   at 6.4 TB/s; 16 of 32768 in bf16 with pages of 16: 164, 1074 MB at 6.5.
-//   64 sequences, window 1024, 8 x 256, 8 bits: 71 (272 MB: 41 at the copy rate): the
-//   memory's part ends after 40 to 48, block by block; then the slowest warp (3 to
-//   6), the warps' parts of 8 KB (4), the counter (1.5), the blocks' parts (4).
+//   64 sequences, window 1024, 8 x 256, 8 bits: 67 (272 MB: 41 at the copy rate): three
+//   or four whole items a block, then the slowest warp (3 to 6) and the warps' parts (4).
 //   One sequence of 4096, 8 x 256, bf16: 18 (5): lengths and first tiles 2.5, one or
 //   two tiles a warp 2.5 to 4, the joins 8.
-//   256 sequences of 64, 8 x 128, bf16: 20 (11), short items whole (cut anywhere 27).
+//   256 sequences of 64, 8 x 128, bf16: 20 (11); 16 of 500, 8 x 64: 7.4 (1.6).
 // Tiles of 16 positions for rows of 256 bytes: window 1024 75 us instead of 71; eight
 // warps a block: the 32 sequences 140 instead of 120; scores and outputs in one
 // chain of products, with their loops' trip counts from the head's size: 146.
@@ -254,8 +253,14 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     return v;
   };
   unsigned total, mine = 0, run = 0;  // of a lane's sequence, and up to it
+  // Parts that blocks share cost 5 us, so items stay whole where that costs less.  An item of kWhole tiles a warp or
+  // fewer is no longer to a block than its join, to which the others' idling adds: where all are (fits), each of them
+  // has a block, or more of them the even cuts between blocks moved to an item's end (the same cut anywhere, us: 8
+  // sequences of up to 100, 4 x 128, 8 bits, 7.7 instead of 13.1; 32 of 1500 in bf16 17.9, 22.9; 128 of 600, 8 x 128,
+  // 45, 50; window 1024 of 64, 67, 70; but 57 of 1500, 4 x 128, 8 bits, 27.3 instead of 26.7).  With 8 tiles a warp 23
+  // of up to 1999, 3 x 80, take 16.5 instead of 15.4, one of 2000 15.3 instead of 12.4.
   constexpr int kWhole = 4;
-  bool fits;  // no item has more tiles than that for every warp
+  bool fits;
   if (n <= 32) {
     mine = tiles_of(min(lane, n - 1), lane < n);
     run = scan(mine);
@@ -310,16 +315,21 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
     cur.item = (int)(left / (unsigned)cur.nt);
     cur.tile = (int)(left % (unsigned)cur.nt);
   };
-  constexpr int kShort = 4;
-  const bool is_short = !whole_items && total != 0 && total <= kShort * (unsigned)items * n;
+  // Short items stay whole in a warp too, up to kShort tiles, where they have 6 on average and fill all warps, or 2.5: a
+  // run that would begin within one begins with the next (256 sequences of 64, 8 x 128: 20 us, cut anywhere 27; 256 of
+  // 180 41.5, whole in the block alone 45.5; with few items the other way: 64 of up to 360, 4 x 128, 13.6, and 23 so).
+  constexpr int kShort = 8;
+  const unsigned many = (unsigned)(items * n);
+  const bool is_short = !whole_items && total != 0 && 2ull * total <= (unsigned long long)many * (many >= gridDim.x * kWarps ? 12 : 5);
+  auto next_start = [&](unsigned u, int limit) {  // tile u, or the next item's first where u is within one of few
+    locate(u);
+    return cur.tile != 0 && cur.nt <= limit ? u + (cur.nt - cur.tile) : u;
+  };
+  const int block_limit = fits ? kWhole * kWarps : kShort;
   if (fits && !whole_items && !is_short) {
     if (warp < 2) {
-      unsigned at = warp == 0 ? bu0 : bu1;
-      if (works && at < total) {
-        locate(at);
-        if (cur.tile != 0) at += cur.nt - cur.tile;
-      }
-      if (lane == 0) s_start[warp] = at;
+      const unsigned at = warp == 0 ? bu0 : bu1, to = works && at < total ? next_start(at, block_limit) : at;
+      if (lane == 0) s_start[warp] = to;
     }
     __syncthreads();
     bu0 = s_start[0];
@@ -328,26 +338,16 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   const unsigned w_each = (bu1 - bu0) / kWarps, w_rest = (bu1 - bu0) % kWarps;
   unsigned u0 = bu0 + w_each * warp + w_rest * warp / kWarps;
   unsigned u1 = bu0 + w_each * (warp + 1) + w_rest * (warp + 1) / kWarps;
-  // Short items stay whole: where they have four tiles or fewer on average, a run that would begin within an item of
-  // so few begins with the next (256 sequences of 64 positions: 20 us, cut anywhere 27).
   if (is_short) {
     if (warp == kWarps - 1) {  // where the next block begins
-      unsigned end = bu1;
-      if (works && bu1 < total) {
-        locate(bu1);
-        if (cur.tile != 0 && cur.nt <= kShort) end += cur.nt - cur.tile;
-      }
+      const unsigned end = works && bu1 < total ? next_start(bu1, block_limit) : bu1;
       if (lane == 0) s_start[kWarps] = end;
     }
-    unsigned start = u0;
-    if (works && u0 < total) {
-      locate(u0);
-      if (cur.tile != 0 && cur.nt <= kShort) start += cur.nt - cur.tile;
-    }
+    const unsigned start = works && u0 < total ? next_start(u0, warp == 0 ? block_limit : kShort) : u0;
     if (lane == 0) s_start[warp] = start;
     __syncthreads();
-    u0 = start;
-    u1 = s_start[warp + 1];
+    u0 = max(start, s_start[0]);  // (the block's own begins with an item that the warps would cut)
+    u1 = max(s_start[warp + 1], s_start[0]);
   }
   cur.seq = cur.item = cur.tile = cur.nt = 0;
   if (u0 < u1) locate(u0);

@@ -609,9 +609,10 @@ size_t moe_kv_attend_workspace_bytes(const moe_kv_cache *cache, int q_heads);
  * records MOE_ERR_BAD_EXPERT_ID; what the cache holds from the length on, or
  * ahead of the window, does not matter.  Sums and statistics are fp32; a weight
  * e^(z - max) is rounded once, to bf16 with a bf16 cache and to fp16 (with its
- * value row's scale) with an 8-bit one.  Finished-block counters live in the
- * handle, so calls on one handle must not overlap on the GPU; calls that may
- * run at the same time need a handle and a workspace each. */
+ * value row's scale) with an 8-bit one, where a weight and scale below 2^-28 of
+ * the largest keep fewer bits (2^-39 of the largest scale).  Finished-block
+ * counters live in the handle, so calls on one handle must not overlap on the
+ * GPU; calls that may run at the same time need a handle and a workspace each. */
 int moe_kv_attend(moe_handle *h, const void *q, size_t q_stride, const moe_kv_cache *cache, const int32_t *lengths,
                   int q_heads, float scale, float softcap, int window, void *out, size_t out_stride, float *lse,
                   void *ws, size_t ws_bytes, moe_stream_t stream);

@@ -6,6 +6,11 @@ values' magnitudes and S the sum of magnitudes behind a score:
   a score's error                32 * 2^-22 S + 2^-22 |z|: fp32 sums in at most 16 steps of 16 products and
                                  the factors; capped scores 2^-20 of the cap more; a weight changes by as much
   sums over positions, joins     2^-17 of A
+  a small weight (8 bits)        a weight times its row's scale is held as fp16 in units of U 2^-14, U the power of two
+                                 at or below the largest scale s: below fp16's normal numbers (2^-14) it is off by up
+                                 to half of 2^-24, times 2^-14 U <= 2^-14 s: 2^-39 s.  Times a code of up to 127, over
+                                 the positions, divided by a sum of weights of 1 or more: positions 2^-39 127 s, and
+                                 127 s is the largest magnitude of a value, as every row has a code of 127
   the output's rounding          half a step of bf16"""
 import numpy as np
 import pytest
@@ -52,6 +57,8 @@ def check(cache, q, lengths, scale, softcap, window, out, lse, heads=None):
                 continue
             z = 32 * 2.0 ** -22 * size + 2.0 ** -22 * max(size, abs(wl)) + 2.0 ** -20 * softcap
             tol = mean * (weight + 2 * z + 2.0 ** -17) + BF16 * np.abs(want) * 1.01 + 1e-37
+            if cache.bits8:
+                tol = tol + len(pos) * 2.0 ** -39 * np.abs(v[:, h // group]).max()
             off = np.abs(got[s, h] - want)
             assert np.all(off <= tol), (s, h, float((off / tol).max()))
             assert abs(got_lse[s, h] - wl) <= z + 2.0 ** -17 + 2.0 ** -22 * abs(wl), (s, h, got_lse[s, h], wl)
@@ -113,6 +120,25 @@ def test_a_long_sequence(moe, bits8):
     check(cache, q, lengths, 0.2, 0.0, 0, out, lse)
     again, _ = run(moe, cache, dev(q), i32(lengths), 0.2)
     assert torch.equal(out, again)  # bit by bit
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("n,H,most,few", [(40, 2, 500, ()), (100, 2, 900, ()), (150, 1, 1500, (0,)), (700, 3, 190, ()),
+                                          (700, 3, 120, (6000,)), (60, 4, 60, (1400, 1900)), (300, 1, 40, (1500, 0, 1400)),
+                                          (31, 5, 64, (700,)), (152, 1, 1, ()), (153, 1, 33, ())])
+def test_how_sequences_share_the_blocks(moe, bits8, n, H, most, few):
+    """Items that a block or a warp has whole, beside longer ones that are cut."""
+    g = np.random.default_rng(n + most)
+    lengths = g.integers(0, most + 1, n)
+    for i, L in enumerate(few):
+        lengths[(i + 1) * n // (len(few) + 1)] = L
+    cache = Cache(45, lengths, H, 64, 16, bits8)
+    q = queries(46, n, 2 * H, 64)
+    out, lse = run(moe, cache, dev(q), i32(lengths), 0.15)
+    assert moe.get_error() == bq.MOE_OK
+    check(cache, q, lengths, 0.15, 0.0, 0, out, lse, heads=(0, 2 * H - 1))
+    again, _ = run(moe, cache, dev(q), i32(lengths), 0.15)
+    assert torch.equal(out, again)
 
 
 @pytest.mark.parametrize("bits8", [False, True])

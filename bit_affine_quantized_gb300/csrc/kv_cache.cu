@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kKvThreads, 5) kv_append_kernel(const KvAppend
 // A block has the rows that its threads take at once; D / 16 threads (of a power of
 // two) have a head's key or value, 16 values each.  Small threads, many of them:
 // 32768 rows of 8 x 128 in 8 bits took 47 us with two units a thread, 52 with four,
-// 41 so (201 MB, 4.9 TB/s); units of 8 values, with twice the look-ups, 75.
+// 39 so (201 MB, 5.2 TB/s); units of 8 values, with twice the look-ups, 75.
 template <bool kBits8>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvReadArgs a) {
   const int tid = threadIdx.x, row0 = blockIdx.x * a.per, rows = min(a.per, a.T - row0);

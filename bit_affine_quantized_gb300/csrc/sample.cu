@@ -25,10 +25,11 @@
 // What bounds it: the row's chain of phases (landing, maxima, histogram, two
 // meetings, list, sort, the running sum), each 0.5 to 4 us with the SM mostly
 // waiting (issue slots 30 % used), times the rounds of clusters; of the logits'
-// bytes alone 64 x 262144 would take 10 us.  One row of 262144: top-k 12.5 us,
-// top-p 0.9 24, no filter 15; 64 rows: 42, 122, 74.  What made it: the same with
-// 64-bit floating point in every thread 137 us instead of 105 (mixed filters), bins
-// read out of the other blocks' memory one by one 105 instead of 85.
+// bytes alone 64 x 262144 would take 10 us.  One row of 262144: top-k 50 10.8 us,
+// top-p 0.9 22.6, no filter 13.6; 64 rows: 39, 106, 67; top-p 0.9 of flat rows, of
+// which most tokens stay, 204.  What made it (64 x 262144, mixed filters): 64-bit
+// floating point in every thread 137 us instead of 105, bins read out of the other
+// blocks' memory one by one 105 instead of 85.
 //
 // Weights e^((l - M) / T) are summed in fixed point, 64 bits: any order gives the
 // same sums, to 2^-34 of a weight of 1 or better.  A weight is within 2^-21 of its
@@ -399,7 +400,9 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   };
   // Quads first, first + step, .. below end: `look` at every value, which says whether it is to go through `make`
   // and what that makes of it through `put`.  A lane goes through its own picks, kPicks at a time: where they are
-  // few, a warp's turns are the most that one lane has; where they are many, there is something to overlap.
+  // few, a warp's turns are the most that one lane has; where they are many, there is something to overlap.  With `many`
+  // a warp of which a lane picks half or more goes through the quads in their order, without a search for the next
+  // (64 x 262144 without a filter 67.5 us instead of 70, top-p 0.9 of flat rows 227 instead of 237).
   auto sweep = [&](bool many, int first, int end, int step, auto look, auto make, auto put) {
     constexpr int kPicks = 2;
     for (int i0 = first; i0 < end; i0 += 8 * step) {
@@ -695,7 +698,8 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       prefix = prefix << 9 | bin;
       lo = prefix == (1u << (9 * level)) - 1u || !(wide < 1e37f) ? cut : fmaxf(cut, value_at((prefix + 1) << shift, -1.f));
       hi = wide < 1e37f ? value_at(prefix << shift, 1.f) : INFINITY;
-      // all that may remain is a list: a short one, or a longer that saves the second cut
+      // all that may remain is a list: a short one, or a longer that saves the second cut (400 by top-k, then top-p,
+      // 64 x 262144: 77 us instead of 118; but top-p of 64 x 16000 20.2 us with short ones, 21.6 with any)
       if (above + in <= (u64)(by_count && cut_p ? kSmList : kSmSorted)) {
         gather(lo, [&](float v, int id) { return far_of(v) >> shift <= prefix && !outside(v, id); });
         sm_meet();
@@ -841,7 +845,7 @@ cudaError_t sample_set_attributes(int *clusters) {
 // A row's blocks: as many as leave every thread 8 tokens, up to 16, where all rows run
 // at once so; with more rows the most with which they still do, or the fewest that
 // hold the row two blocks to an SM.  (Of clusters of 16 the device holds 16 at once,
-// of clusters of 12 24: 64 x 262144 with mixed filters took 82 us and takes 79, one
+// of clusters of 12 24: 64 x 262144 with mixed filters took 82 us and took 79 so, one
 // row 13 with 16 blocks; 17 x 32000 with 16384 tokens a block 21, with 4096 17.)
 cudaError_t launch_sample(const SampleArgs &a0, const int *clusters, cudaStream_t st, bool pdl) {
   SampleArgs a = a0;

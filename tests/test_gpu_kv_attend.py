@@ -287,6 +287,38 @@ def test_graphs_that_share_a_workspace(moe, bits8):
             check(job["cache"], job["q"], lengths, 0.1, 0.0, 0, job["out"], job["lse"])
 
 
+@pytest.mark.parametrize("bits8", [False, True])
+def test_a_graph_whose_lengths_change(moe, bits8):
+    """Replays in which the blocks share the items in another way each time: all empty, short, one long, all long."""
+    H, n, most = 2, 90, 1900
+    cache = Cache(47, np.full(n, most), H, 64, 16, bits8)
+    q = queries(48, n, 2 * H, 64)
+    out, lse = torch.empty((n, 2 * H, 64), dtype=torch.bfloat16, device="cuda"), torch.empty((n, 2 * H), device="cuda")
+    ws = torch.empty(moe.kv_attend_workspace_bytes(cache.c, 2 * H), dtype=torch.uint8, device="cuda")
+    dq, held = dev(q), torch.zeros(n, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            moe.kv_attend(dq, held, cache.c, out, ws, scale=0.15, lse=lse)
+    r = np.random.default_rng(49)
+    long = r.integers(0, 50, n)
+    long[37] = most
+    few = np.zeros(n, int)
+    few[[3, 80]] = 1700, 40
+    for lengths in (np.zeros(n, int), r.integers(0, 65, n), long, few, np.full(n, most), r.integers(0, 400, n), np.zeros(n, int), long):
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        held.copy_(i32(lengths))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert moe.get_error() == bq.MOE_OK
+        check(cache, q, lengths, 0.15, 0.0, 0, out, lse, heads=(1, 2))
+
+
 def test_two_handles_on_two_streams():
     """A handle and a workspace each: calls that may run at the same time."""
     bq.build_library()

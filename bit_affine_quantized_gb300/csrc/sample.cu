@@ -89,8 +89,11 @@ __device__ __forceinline__ unsigned sm_count(uint32_t at, unsigned n) {
   return v;
 }
 // Every thread of the cluster's blocks, which run at the same time.
+__device__ __forceinline__ void sm_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void sm_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void sm_meet() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+  sm_arrive();
+  sm_wait();
 }
 
 struct SmWeight {
@@ -192,6 +195,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   clear_bins();
   if (tid == 0) s_n = s_own = 0u;
   __syncthreads();
+  sm_arrive();  // this block runs; a block that does not run yet has no memory to write to
   pdl_wait();
   pdl_launch_dependents();
   if (tracer) trace_min(a.trace, kTrWaited);
@@ -337,6 +341,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       __syncthreads();
       for (int w = 0; w < kSmWarps; ++w) told.sum += s_red[0][w];
     }
+    sm_wait();  // the others run (they had the logits' landing to begin in)
     if (tid < C) {
       const uint32_t to = sm_far(&s_told[rank], tid);
       sm_put(to, told.top);
@@ -563,10 +568,10 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     const unsigned count = sm_get(first_n);
     if (count <= (unsigned)kSmList) {
       // the other blocks are done; the first stays while they may look into its memory
-      asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+      sm_arrive();
       if (rank != 0) return;
       finish((int)count, top_k, 0);
-      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+      sm_wait();
       if (tid == 0 && a.trace) trace_max(a.trace, kTrExit);
       return;
     }

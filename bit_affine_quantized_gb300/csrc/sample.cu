@@ -670,7 +670,8 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       }
       sm_meet();
       unsigned bin = 0;
-      u64 in = 0;
+      u64 in = 0, in_mass = 0;
+      bool few = false;  // fewer remain than are needed
 #pragma unroll 1
       for (int part = 0; part < 2; ++part) {
         SmBin b = {0, 0};
@@ -689,10 +690,12 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
           need = sm_share(top_p0, all, true);
         }
         const unsigned hit = __ballot_sync(0xffffffffu, (by_count ? above + cr : above_mass + mr) >= need);
-        const int at = hit ? __ffs(hit) - 1 : part == 0 ? 31 : 15;  // (fewer than are needed: all of them)
+        few = few || hit == 0u;
+        const int at = hit ? __ffs(hit) - 1 : part == 0 ? 31 : 15;  // (few: the last bin, so that all are counted)
         above += __shfl_sync(0xffffffffu, cr - cnt, at);
         above_mass += __shfl_sync(0xffffffffu, mr - mass, at);
         in = __shfl_sync(0xffffffffu, cnt, at);
+        in_mass = __shfl_sync(0xffffffffu, mass, at);
         bin = 16 * bin + (unsigned)at;
         if (part == 0) {
           const int f = 16 * at + (half & 15);
@@ -710,6 +713,9 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
         sm_meet();
         if (rank == 0) finish((int)(above + in), by_count ? top_k : 0, all);
         done = found = true;
+      } else if (few) {  // all of them stay (by the count alone: a part of the sum is there); the last bin may be empty
+        all = above_mass + in_mass;
+        known = found = true;
       } else if (in <= (u64)kSmList) {
         gather(lo, [&](float v, int id) { return v <= hi && far_of(v) >> shift == prefix && !outside(v, id); });
         sm_meet();
@@ -719,9 +725,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
           // the last that stays: the place k, or the one whose sum reaches the share
           const bool last = key != 0 && (by_count ? above + place == (u64)top_k
                                                        : above_mass + upto >= need && above_mass + upto - w < need);
-          // (none reaches it where the share is the whole sum to fp64's last bit: then the least key stays)
-          const bool none = __syncthreads_or(last) == 0;
-          if (last || (none && tid < (int)in && place == in)) {
+          if (last) {  // (one thread: the bin is the one in which the count, or the sum, passes what is needed)
             for (int r = 0; r < C; ++r) {
               const uint32_t to = sm_far(&s_cut, r);
               sm_put(to, key);

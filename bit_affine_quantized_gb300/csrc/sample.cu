@@ -142,7 +142,7 @@ __device__ __forceinline__ u64 sm_share(float f, u64 n, bool up) {
 
 // What a block tells the others of its tokens.
 struct SmTold {
-  float top, least, cut_all, cut_part, sum, bad;
+  float top, least, cut_all, cut_part, sum, lost;  // lost: 1 where its tokens did not land in time
 };
 struct __align__(16) SmBin {
   u64 mass, count;
@@ -274,7 +274,10 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   };
   if (kHeld) {
     for (int q = 0; q < max(chunks, 1); ++q) {
-      if (q < chunks) late = late || !mbar_wait(&s_bar[q], 0);
+      if (q < chunks && !mbar_wait(&s_bar[q], 0)) {
+        late = true;
+        break;
+      }
       for (int i = q * (kSmChunk / 4) + tid; i < min(quads, (q + 1 < chunks ? q + 1 : 1 << 20) * (kSmChunk / 4)); i += kSmThreads)
         take(reinterpret_cast<const float4 *>(seg)[i], i);
     }
@@ -288,7 +291,6 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     }
   }
   if (bad) set_error(a.err, kErrNonFinite);
-  if (late) set_error(a.err, kErrTimeout);
   auto block_max = [&](float v, int k) {  // of one value per thread; k: its place
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
@@ -303,10 +305,14 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   block_max(mine, 0);
   block_max(-least, 1);
   block_max(mine > -INFINITY ? -mine : -INFINITY, 2);
-  __syncthreads();
+  const bool lost = __syncthreads_or(late) != 0;
+  if (lost) {  // the copies under way land, or run out too, before the block's memory is anyone's again
+    if (tid == 0) set_error(a.err, kErrTimeout);
+    for (int q = 0; q < chunks; ++q) mbar_wait(&s_bar[q], 0, 1000000ull);
+  }
   const float block_top = of_warps(0), low_max = -of_warps(2);  // (of the threads that have a token)
   {
-    SmTold told = {block_top, -of_warps(1), -INFINITY, -INFINITY, 0.f, 0.f};
+    SmTold told = {block_top, -of_warps(1), -INFINITY, -INFINITY, 0.f, lost ? 1.f : 0.f};
     const float wide = block_top - low_max;
     if (top_k > 0 && block_top > -INFINITY && wide < 1e37f) {
       // a histogram of the threads' maxima: the values that k, or k / C, of them reach
@@ -349,6 +355,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       sm_put(to + 8, told.cut_all);
       sm_put(to + 12, told.cut_part);
       sm_put(to + 16, told.sum);
+      sm_put(to + 20, told.lost);
     }
   }
   sm_meet();
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   };
   const float their_top = of.top, top = lanes_max(their_top), bottom = -lanes_max(-of.least);
   const float cut_all = lanes_max(of.cut_all), cut_part = -lanes_max(-of.cut_part);
-  if (top == -INFINITY) {
+  if (top == -INFINITY || lanes_max(of.lost) > 0.f) {  // (the same for all blocks: they leave together)
     if (rank == 0 && tid == 0) {
       a.tokens[row] = -1;
       if (a.logprobs) a.logprobs[row] = -INFINITY;

@@ -643,7 +643,8 @@ typedef struct {
  *             remaining weights (0 for a greedy row; -inf with token -1)
  * u counts as 0 below 0 or NaN, and as the last remaining token from 1 on.  A
  * NaN filter is off, a NaN temperature is greedy.  A NaN or +inf among the
- * logits counts as -inf and records MOE_ERR_NONFINITE.  The sums are exact over
+ * logits counts as -inf and records MOE_ERR_NONFINITE.  A row whose logits did
+ * not land in time gets token -1 and records MOE_ERR_TIMEOUT.  The sums are exact over
  * weights within 2^-21 of their values, the same whatever their order.  Nothing
  * but the error stays in the handle: calls may overlap. */
 int moe_sample(moe_handle *h, const float *logits, size_t logits_stride, int n_rows, int vocab,

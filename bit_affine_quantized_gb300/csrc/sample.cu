@@ -25,15 +25,16 @@
 // What bounds it: the row's chain of phases (landing, maxima, histogram, two
 // meetings, list, sort, the running sum), each 0.5 to 4 us with the SM mostly
 // waiting (issue slots 30 % used), times the rounds of clusters; of the logits'
-// bytes alone 64 x 262144 would take 10 us.  One row of 262144: top-k 50 10.8 us,
-// top-p 0.9 22.6, no filter 13.6; 64 rows: 39, 106, 67; top-p 0.9 of flat rows, of
-// which most tokens stay, 204.  What made it (64 x 262144, mixed filters): 64-bit
+// bytes alone 64 x 262144 would take 10 us.  One row of 262144: top-k 50 11.0 us,
+// top-p 0.9 25.2, no filter 13.8; 64 rows: 40, 118, 69; top-p 0.9 of flat rows, of
+// which most tokens stay, 209.  What made it (64 x 262144, mixed filters): 64-bit
 // floating point in every thread 137 us instead of 105, bins read out of the other
 // blocks' memory one by one 105 instead of 85.
 //
-// Weights e^((l - M) / T) are summed in fixed point, 64 bits: any order gives the
-// same sums, to 2^-34 of a weight of 1 or better.  A weight is within 2^-21 of its
-// value: the argument's rounding errors are carried along (a difference's and a
+// Weights e^((l - M) / T) are summed in fixed point, 64 bits: any order, and any
+// number of blocks, gives the same sums.  The unit is 2^-34 of a weight of 1 for the
+// most tokens, 2^-44 for 262144.  A weight is within 2^-21 of its value before that
+// rounding: the argument's rounding errors are carried along (a difference's and a
 // product's), what is left is the exponential's.
 #include <math.h>
 
@@ -98,14 +99,15 @@ __device__ __forceinline__ void sm_meet() {
 
 struct SmWeight {
   float top, c, c_lo, one;  // the maximum; log2(e) / temperature in two parts; the unit
-  __device__ __forceinline__ u64 operator()(float l) const {
+  __device__ __forceinline__ float units(float l) const {
     const float d = l - top, y = d * c;
     const float b = d - l, e = (l - (d - b)) + (-top - b);        // what the difference lost
     const float lo = fmaf(d, c, -y) + fmaf(d, c_lo, e * c);       // and the product
     float w;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(y));
-    return y > -70.f ? __float2ull_rn(fmaf(w, lo * 0.69314718f, w) * one) : 0;
+    return y > -70.f ? fmaf(w, lo * 0.69314718f, w) * one : 0.f;
   }
+  __device__ __forceinline__ u64 operator()(float l) const { return __float2ull_rn(units(l)); }
 };
 
 __device__ __forceinline__ u64 sm_warp_sum(u64 v) {
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
   // and what that makes of it through `put`.  A lane goes through its own picks, kPicks at a time: where they are
   // few, a warp's turns are the most that one lane has; where they are many, there is something to overlap.  With `many`
   // a warp of which a lane picks half or more goes through the quads in their order, without a search for the next
-  // (64 x 262144 without a filter 67.5 us instead of 70, top-p 0.9 of flat rows 227 instead of 237).
+  // (64 x 262144 without a filter 67.5 us instead of 70, top-p 0.9 of flat rows, then, 227 instead of 237).
   auto sweep = [&](bool many, int first, int end, int step, auto look, auto make, auto put) {
     constexpr int kPicks = 2;
     for (int i0 = first; i0 < end; i0 += 8 * step) {
@@ -607,14 +609,16 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
     if (by_count ? top_k == 0 : !cut_p) continue;
     // the bound below which nothing remains
     float cut = low;
+    bool narrow = false;  // weights below it fit 32 bits
     if (by_count) {
       cut = cut_k;
     } else if (known) {
       cut = fmaxf(low, sm_value((unsigned)(tau >> 32)));
     } else {
-      const float least_w = (1.f - top_p0) * 0.99f * sum / (float)V;
+      const float least_w = (1.f - top_p0) * 0.99f * sum / (float)V - 1.f / weight.one;  // (what rounding to units may add)
       const float f = top + (log2f(least_w) - 0.01f) / weight.c;
       if (f < top) cut = fmaxf(low, f - 1e-6f * (fabsf(top) + fabsf(f)));
+      narrow = f < top && least_w * weight.one < 0x1p31f;
     }
     const float wide = top - cut, scale = wide > 0.f ? fminf((float)((1 << kSmBits) - 256) / wide, 3e38f) : 0.f;
     auto far_of = [&](float v) { return (unsigned)fminf((top - v) * scale, (float)((1 << kSmBits) - 1)); };
@@ -636,14 +640,24 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
       const bool tail = !by_count && !known && level == 1;
       clear_bins();
       __syncthreads();
-      float rest_w = 0.f;  // below the bound: each weight is less than the share of one of V in 1 - p
+      // Below the bound each weight is less than the share of one of V in 1 - p.  They are summed as all the others are,
+      // for which tokens lie below it follows from how many blocks the row has, and the sum must not: 64 x 262144 with
+      // top-p 0.9 and temperature 1 141 us, where fp32 sums of plain exponentials took 131 and were off by 2^-15 at 2^25
+      // tokens; with every weight to 64 bits, not 32 where they fit, and within the sweep below, 156.
+      u64 rest = 0;
+      auto add_below = [&](auto whole) {
+        for (int i = tid; i < quads; i += kSmThreads) {
+          const float4 f = quad(i);
+          const float v[4] = {f.x, f.y, f.z, f.w};
+          if (!(fminf(fminf(f.x, f.y), fminf(f.z, f.w)) < cut)) continue;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) rest += whole(v[k] < cut && v[k] >= low ? weight.units(v[k]) : 0.f);
+        }
+      };
+      if (tail && narrow) add_below([](float w) { return __float2uint_rn(w); });
+      if (tail && !narrow) add_below([](float w) -> u64 { return __float2ull_rn(w); });
       sweep(true, tid, quads, kSmThreads,
             [&](float v) {
-              if (tail) {
-                float e;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((v - top) * weight.c));
-                rest_w += v < cut && v >= low ? e : 0.f;
-              }
               return v >= lo && v <= hi;
             },
             [&](float v, int id) {
@@ -662,7 +676,6 @@ __global__ void __launch_bounds__(kSmThreads, kHeld ? 2 : 1) sample_kernel(const
                 atomicAdd(&s_mass[b.count], w);
               }
             });
-      u64 rest = __float2ull_rn(rest_w * weight.one);
       if (tail) {
         rest = block_sum(rest);
         if (tid < C) sm_put(sm_far(&s_far[rank], tid), rest);

@@ -644,9 +644,12 @@ typedef struct {
  * u counts as 0 below 0 or NaN, and as the last remaining token from 1 on.  A
  * NaN filter is off, a NaN temperature is greedy.  A NaN or +inf among the
  * logits counts as -inf and records MOE_ERR_NONFINITE.  A row whose logits did
- * not land in time gets token -1 and records MOE_ERR_TIMEOUT.  The sums are exact over
- * weights within 2^-21 of their values, the same whatever their order.  Nothing
- * but the error stays in the handle: calls may overlap. */
+ * not land in time gets token -1 and records MOE_ERR_TIMEOUT.  The sums are exact
+ * over weights within 2^-21 of their values, rounded to whole units of
+ * 2^-(31 + the leading zeros of vocab's 32 bits) of the largest (2^-44 for
+ * 262144 tokens, 2^-34 for the most), the same whatever their order and
+ * whatever else is in the call.  Nothing but the error stays in the handle:
+ * calls may overlap. */
 int moe_sample(moe_handle *h, const float *logits, size_t logits_stride, int n_rows, int vocab,
                const moe_sample_rules *rules, int32_t *tokens, float *logprobs, moe_stream_t stream);
 

@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
           for (int j = 0; j < 2; ++j)
             q[s][i][j] = at_f16x2(__uint_as_float(q[s][i][j] << 16) * down, __uint_as_float(q[s][i][j] & 0xFFFF0000u) * down);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) qs[i][j] = at_pow2(__shfl_sync(0xffffffffu, e, 4 * (2 * c + j))) * factor;
+        for (int j = 0; j < 2; ++j)  // (finite, as the factor is)
+          qs[i][j] = fminf(fmaxf(at_pow2(__shfl_sync(0xffffffffu, e, 4 * (2 * c + j))) * factor, -most), most);
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {

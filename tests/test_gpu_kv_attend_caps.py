@@ -69,3 +69,18 @@ def test_large_scores_under_large_caps(moe, bits8):  # noqa: F811
                 assert abs(got_lse[s, h] - first) <= 2.0 ** -12 * abs(first)
                 # the output's rounding, and the weight's: of 1 none, of 1 times a row's scale half a step of fp16
                 assert np.all(np.abs(got[s, h] - v[z.argmax(), 0]) <= (BF16 + 2.0 ** -11) * np.abs(v[z.argmax(), 0]) * 1.01 + 1e-6)
+
+
+@pytest.mark.parametrize("bits8", [False, True])
+@pytest.mark.parametrize("scale,softcap", [(3e38, 0.0), (-3e38, 0.0), (3e38, 1e-3), (1e30, 5.0), (3e38, 3e38)])
+@pytest.mark.parametrize("size", [1.0, 40.0, 2.0 ** 100])
+def test_scores_of_zero_of_large_queries(moe, bits8, scale, softcap, size):  # noqa: F811
+    """Keys of zeros: every score is 0, whatever the query and the factors; the output is the mean of the values."""
+    lengths = [77, 3]
+    cache = Cache(40, lengths, 2, 64, 16, bits8)
+    cache.k[:] = 0.0
+    cache.upload()
+    q = queries(41, 2, 4, 64) * size
+    out, lse = run(moe, cache, dev(q), i32(lengths), scale, softcap)
+    assert moe.get_error() == bq.MOE_OK
+    check(cache, q, lengths, 0.0, 0.0, out, lse)

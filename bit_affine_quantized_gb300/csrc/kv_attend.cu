@@ -31,6 +31,14 @@
 // to 2^-16 of the head's largest value, to 2^-25 of it below).  With a bf16 cache
 // queries stay as they are and weights are rounded to bf16.
 //
+// Weights have 16 bits in the second product because the tensor cores take no more
+// of an operand whose other side is a row of the cache as it lies; the sum of the
+// weights, which divides, is of fp32 ones.  A weight is off by half a step on its own,
+// one up, one down, so an output's error stays below that of its own rounding:
+// against 64 bits 1.7e-3 (of the outputs' size) for one sequence of 4096 in bf16 and for
+// a window in 8 bits, 1.1e-3 for 23 ragged ones, with weights in fp32 the same to two
+// digits.  (The two sides differ by 7e-4 to 1.2e-3: values near a rounding border.)
+//
 // An item (a sequence's key head) that one warp has whole is written at once.
 // Where warps share one, the block joins its warps' parts; where blocks share a long
 // one, each leaves a part in the workspace, and the last of them, by a counter,

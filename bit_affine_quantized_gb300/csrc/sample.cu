@@ -20,7 +20,9 @@
 // falls, and a list takes what lies above its lower end, or in the bin alone.  The
 // blocks tell each other their bins 16 at a time, then the 16 in question.  A list
 // is sorted.  Where a bin cannot be refined (many equal logits) the key is found
-// bit by bit.
+// bit by bit, a sweep and two meetings each: rows of 262144 equal logits, top-p 0.5,
+// take 393 us for one, 2450 for 64; a few hundred likely tokens, values rounded to
+// bf16, 144 for 64 with top-p 0.9 (142 not rounded).
 //
 // What bounds it: the row's chain of phases (landing, maxima, histogram, two
 // meetings, list, sort, the running sum), each 0.5 to 4 us with the SM mostly

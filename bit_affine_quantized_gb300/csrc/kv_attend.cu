@@ -274,9 +274,9 @@ __global__ void __launch_bounds__(32 * AtShape<kBits8, kD, kN>::kWarps, 1)
   // fewer is no longer to a block than its join, to which the others' idling adds: where all are (fits), each of them
   // has a block, or more of them the even cuts between blocks moved to an item's end (the same cut anywhere, us: 8
   // sequences of up to 100, 4 x 128, 8 bits, 7.7 instead of 13.1; 32 of 1500 in bf16 17.9, 22.9; 128 of 600, 8 x 128,
-  // 45, 50; window 1024 of 64, 67, 70; 1000 of up to 1500,
-  // 2 x 128, bf16, 167, 172; 4000 of up to 400, 1 x 64, 8 bits, 55, 62; but 57 of 1500, 4 x 128, 8 bits, 27.3 instead of 26.7).  With 8 tiles a warp 23
-  // of up to 1999, 3 x 80, take 16.5 instead of 15.4, one of 2000 15.3 instead of 12.4.
+  // 45, 50; window 1024 of 64, 67, 70; 1000 of up to 1500, 2 x 128, bf16, 167, 172; 4000 of up to 400, 1 x 64, 8 bits, 55,
+  // 62; but 57 of 1500, 4 x 128, 8 bits, 27.3 instead of 26.7).  With 8 tiles a warp 23 of up to 1999, 3 x 80, take 16.5
+  // instead of 15.4, one of 2000 15.3 instead of 12.4.
   constexpr int kWhole = 4;
   bool fits;
   if (n <= 32) {
